@@ -80,7 +80,8 @@ extern "C" {
 #define MOE_STATUS_COUNT_MISMATCH 4 /* offsets disagree with the histogram of topk_idx */
 #define MOE_STATUS_TIMEOUT 8        /* a pipeline wait gave up (kernel returned early) */
 
-/* ABI version of this header (major * 100 + minor). */
+/* ABI version of this header (major * 100 + minor): changes with the calls
+ * declared so far; calls that are added leave it as it is. */
 int moe_abi_version(void);
 
 /* Text of the last error returned to the calling host thread ("" if none). */
@@ -417,6 +418,89 @@ int moe_route_topk_bwd(const float* d_w, const float* topk_w, const int32_t* top
                        const void* x, const float* Wr, const float* dx_acc, int T, int H, int E,
                        int k, float* dWr, void* dx, int accumulate, void* ws, size_t ws_bytes,
                        void* stream);
+
+/* A1 + A2 that also keeps the router's logits, and B5 with a further gradient
+ * of them: how the balance loss below joins the layer.
+ *   moe_route_topk_logits:     moe_route_topk_chunks, writing logits fp32 [T,E]
+ *                              (bias included); every other output is the same.
+ *   moe_route_topk_logits_bwd: moe_route_topk_bwd with dlogits fp32 [T,E] added
+ *                              to the scattered dl before both contractions:
+ *                              dWr[h,e] = sum_t x[t,h] (dl + dlogits)[t,e],
+ *                              dx[t,h]  = dx_acc[t,h] + sum_e (dl + dlogits)[t,e] Wr[h,e].
+ * Workspaces as for moe_route_topk_chunks and moe_route_topk_bwd. */
+int moe_route_topk_logits(const void* x, const float* Wr, const float* bias, int T, int H, int E, int k,
+                          int ep_size, int32_t* topk_idx, float* topk_w, int32_t* counts, int32_t* offsets,
+                          int32_t* rank_offsets, int32_t* chunk_prefix, float* logits, void* ws, size_t ws_bytes,
+                          void* stream);
+int moe_route_topk_logits_bwd(const float* d_w, const float* topk_w, const int32_t* topk_idx, const float* dlogits,
+                              const void* x, const float* Wr, const float* dx_acc, int T, int H, int E, int k,
+                              float* dWr, void* dx, int accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Load-balance loss and router z-loss (no counterpart on the pages).
+ *
+ * The T tokens are num_seg packed sequences: sequence q holds tokens
+ * [seg_offsets[q], seg_offsets[q+1]); NULL with num_seg = 1 is one sequence
+ * of all tokens.  Tokens before the first and after the last offset, and
+ * tokens whose mask byte is 0 (mask uint8 [T], NULL: none), take no part:
+ * their logits are not read and their dlogits are 0.  With m_t = 1 for the
+ * tokens that take part, p_t = softmax(logits[t]), n_q = sum m_t, n = sum n_q:
+ *   counts[q,e]   = slots of q's tokens routed to e (topk_idx)   int32 [num_seg,E]
+ *   tokens[q]     = n_q                                          int32 [num_seg]
+ *   prob_sum[q,e] = sum m_t p[t,e]                               fp32  [num_seg,E]
+ *   loss[0] = 1/n sum_q E/(k n_q) sum_e counts[q,e] prob_sum[q,e]   (1 when balanced)
+ *   loss[1] = 1/n sum_t m_t lse(logits[t])^2
+ * and, when dlogits is not NULL, the gradient of
+ * balance_coef loss[0] + z_coef loss[1] in the logits (the counts carry none):
+ *   dlogits[t,e] = m_t p[t,e] (balance_coef E/(k n_q n) (counts[q,e] - sum_j counts[q,j] p[t,j])
+ *                              + z_coef 2/n lse(logits[t]))         fp32 [T,E]
+ * A sequence without tokens adds nothing; n = 0 gives zeros.
+ *
+ * moe_balance_loss_bwd computes dlogits alone, from the counts and tokens of
+ * an earlier moe_balance_loss, each coefficient multiplied by the upstream
+ * gradient dloss[0], dloss[1] (fp32 [2] on the device, NULL: 1).
+ * Limits: E <= 1024, k <= min(E,32), num_seg <= 1024, T*k < 2^31. */
+size_t moe_balance_loss_workspace_size(int T, int E, int num_seg);
+int moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask, int T, int E, int k,
+                     int num_seg, const int32_t* seg_offsets, int32_t* counts, int32_t* tokens, float* prob_sum,
+                     float* loss, float balance_coef, float z_coef, float* dlogits, void* ws, size_t ws_bytes,
+                     void* stream);
+int moe_balance_loss_bwd(const float* logits, const uint8_t* mask, int T, int E, int k, int num_seg,
+                         const int32_t* seg_offsets, const int32_t* counts, const int32_t* tokens, float balance_coef,
+                         float z_coef, const float* dloss, float* dlogits, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Dropout from a counter-based generator (no counterpart on the pages).  The
+ * mask is never stored: the backward computes it again from the same rng.
+ *
+ * rng: two 64-bit words on the device, {seed, offset}.  Element i of the
+ * tensor (row-major) belongs to block i/8, whose 128 random bits are
+ * Philox4x32-10 of key seed and counter offset + i/8 (as a 64-bit number in
+ * the counter's two low words); it has the (i%8)-th 16 bits of them, lowest
+ * first.  With drop = round(65536 p), 0 <= p <= 1, it stays when its bits are
+ * >= drop, scaled by 65536/(65536 - drop), and is 0 otherwise:
+ *   D(v)_i = keep_i ? v_i * 65536/(65536 - drop) : 0
+ * A call on n elements uses ceil(n/8) counters: calls that are to be
+ * independent advance offset by at least that.
+ *
+ * moe_dropout: out = residual + D(x), n elements, fp32 arithmetic, rounded
+ *   once; fp32 = 0: bf16 tensors, 1: fp32 tensors.  residual may be NULL (0);
+ *   out may be x or residual.  The gradient of x is the same call on dout
+ *   without a residual, that of the residual is dout.
+ * moe_combine_dropout: moe_combine with dropout and a residual,
+ *   y[t] = residual[t] + D(sum_j topk_w[t,j] y_perm[row_of_slot[t,j]])   -> bf16 [T,H]
+ *   residual bf16 [T,H] or NULL; y may be residual.
+ * moe_combine_dropout_bwd: its backward, with g = D(dy) in fp32:
+ *   dy_perm[row(t,j)] = topk_w[t,j] g[t]                      -> bf16
+ *   d_w[t,j]          = sum_h g[t,h] y_perm[row(t,j),h]       (fp32)
+ *   (the residual's gradient is dy). */
+int moe_dropout(const void* x, const void* residual, long long n, int fp32, double p, const int64_t* rng, void* out,
+                void* stream);
+int moe_combine_dropout(const void* y_perm, const float* topk_w, const int32_t* row_of_slot, const void* residual,
+                        int T, int H, int k, double p, const int64_t* rng, void* y, void* stream);
+int moe_combine_dropout_bwd(const void* dy, const void* y_perm, const float* topk_w, const int32_t* row_of_slot,
+                            int T, int H, int k, double p, const int64_t* rng, void* dy_perm, float* d_w,
+                            void* stream);
 
 /* Persistent-grid limit of the grouped GEMMs (no counterpart on the pages).
  * Every grouped GEMM kernel (the forward, backward and router-backward

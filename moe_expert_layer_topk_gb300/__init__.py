@@ -30,11 +30,15 @@ __all__ = ["lib", "MoEError", "LIB_PATH", "ENTRY_POINTS",
            "moe_dispatch_bwd", "moe_route_topk_bwd",
            "moe_route_topk_workspace_size", "moe_dispatch_workspace_size",
            "moe_route_topk_bwd_workspace_size", "moe_grouped_gemm_bwd_workspace_size",
+           "moe_route_topk_logits", "moe_route_topk_logits_bwd",
+           "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_balance_loss_bwd",
+           "moe_dropout", "moe_combine_dropout", "moe_combine_dropout_bwd",
            "moe_read_device_status", "moe_abi_version", "moe_probe_fma", "moe_set_gemm_sm_limit", "sm_count"]
 
 LIB_PATH: Path = _build_mod.LIB
 
 _P, _I, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_L, _F, _D = ctypes.c_longlong, ctypes.c_float, ctypes.c_double
 
 # name -> (argtypes, restype); mirrors include/moe_topk.h
 # the ABI version of include/moe_topk.h these signatures follow
@@ -75,6 +79,14 @@ ENTRY_POINTS = {
     "moe_dispatch_bwd": ([_P, _P, _I, _I, _I, _P, _P], _I),
     "moe_route_topk_bwd_workspace_size": ([_I, _I, _I], _Z),
     "moe_route_topk_bwd": ([_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _I, _P, _Z, _P], _I),
+    "moe_route_topk_logits": ([_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P], _I),
+    "moe_route_topk_logits_bwd": ([_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _I, _P, _Z, _P], _I),
+    "moe_balance_loss_workspace_size": ([_I, _I, _I], _Z),
+    "moe_balance_loss": ([_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _F, _F, _P, _P, _Z, _P], _I),
+    "moe_balance_loss_bwd": ([_P, _P, _I, _I, _I, _I, _P, _P, _P, _F, _F, _P, _P, _P], _I),
+    "moe_dropout": ([_P, _P, _L, _I, _D, _P, _P, _P], _I),
+    "moe_combine_dropout": ([_P, _P, _P, _P, _I, _I, _I, _D, _P, _P, _P], _I),
+    "moe_combine_dropout_bwd": ([_P, _P, _P, _P, _I, _I, _I, _D, _P, _P, _P, _P], _I),
     "moe_probe_fma": ([_I, _I, _I, _P, ctypes.POINTER(ctypes.c_longlong), _P], _I),
     "moe_set_gemm_sm_limit": ([_I, ctypes.POINTER(ctypes.c_int)], _I),
 }
@@ -323,6 +335,61 @@ def moe_route_topk_bwd(d_w, topk_w, topk_idx, x, Wr, dx_acc, T, H, E, k, dWr, dx
     _call("moe_route_topk_bwd", _ptr(d_w), _ptr(topk_w), _ptr(topk_idx), _ptr(x), _ptr(Wr),
           _ptr(dx_acc), T, H, E, k, _ptr(dWr), _ptr(dx), int(accumulate), _ptr(ws), _nbytes(ws),
           _stream(stream))
+
+
+def moe_route_topk_logits(x, Wr, bias, T, H, E, k, ep_size, topk_idx, topk_w, counts, offsets, rank_offsets,
+                          chunk_prefix, logits, ws, stream=None):
+    _call("moe_route_topk_logits", _ptr(x), _ptr(Wr), _ptr(bias), T, H, E, k, ep_size, _ptr(topk_idx),
+          _ptr(topk_w), _ptr(counts), _ptr(offsets), _ptr(rank_offsets), _ptr(chunk_prefix), _ptr(logits),
+          _ptr(ws), _nbytes(ws), _stream(stream))
+
+
+def moe_route_topk_logits_bwd(d_w, topk_w, topk_idx, dlogits, x, Wr, dx_acc, T, H, E, k, dWr, dx, accumulate=0,
+                              ws=None, stream=None):
+    _call("moe_route_topk_logits_bwd", _ptr(d_w), _ptr(topk_w), _ptr(topk_idx), _ptr(dlogits), _ptr(x),
+          _ptr(Wr), _ptr(dx_acc), T, H, E, k, _ptr(dWr), _ptr(dx), int(accumulate), _ptr(ws), _nbytes(ws),
+          _stream(stream))
+
+
+def moe_balance_loss_workspace_size(T, E, num_seg=1) -> int:
+    return lib().moe_balance_loss_workspace_size(T, E, num_seg)
+
+
+def moe_balance_loss(logits, topk_idx, mask, T, E, k, num_seg, seg_offsets, counts, tokens, prob_sum, loss,
+                     balance_coef, z_coef, dlogits, ws, stream=None):
+    _call("moe_balance_loss", _ptr(logits), _ptr(topk_idx), _ptr(mask), T, E, k, num_seg, _ptr(seg_offsets),
+          _ptr(counts), _ptr(tokens), _ptr(prob_sum), _ptr(loss), balance_coef, z_coef, _ptr(dlogits), _ptr(ws),
+          _nbytes(ws), _stream(stream))
+
+
+def moe_balance_loss_bwd(logits, mask, T, E, k, num_seg, seg_offsets, counts, tokens, balance_coef, z_coef, dloss,
+                         dlogits, stream=None):
+    _call("moe_balance_loss_bwd", _ptr(logits), _ptr(mask), T, E, k, num_seg, _ptr(seg_offsets), _ptr(counts),
+          _ptr(tokens), balance_coef, z_coef, _ptr(dloss), _ptr(dlogits), _stream(stream))
+
+
+def _dropout_type(x, out) -> int:
+    """0 for bf16 tensors, 1 for fp32 ones."""
+    if x.dtype != out.dtype or x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("x and out must both be bf16 or both fp32")
+    return int(x.dtype == torch.float32)
+
+
+def moe_dropout(x, residual, n, p, rng, out, stream=None):
+    """out = residual + D(x) over n elements, bf16 or fp32 by x's type; rng: int64 [2] {seed, offset}."""
+    if residual is not None and residual.dtype != x.dtype:
+        raise ValueError("residual must have x's type")
+    _call("moe_dropout", _ptr(x), _ptr(residual), n, _dropout_type(x, out), p, _ptr(rng), _ptr(out), _stream(stream))
+
+
+def moe_combine_dropout(y_perm, topk_w, row_of_slot, residual, T, H, k, p, rng, y, stream=None):
+    _call("moe_combine_dropout", _ptr(y_perm), _ptr(topk_w), _ptr(row_of_slot), _ptr(residual), T, H, k, p,
+          _ptr(rng), _ptr(y), _stream(stream))
+
+
+def moe_combine_dropout_bwd(dy, y_perm, topk_w, row_of_slot, T, H, k, p, rng, dy_perm, d_w, stream=None):
+    _call("moe_combine_dropout_bwd", _ptr(dy), _ptr(y_perm), _ptr(topk_w), _ptr(row_of_slot), T, H, k, p,
+          _ptr(rng), _ptr(dy_perm), _ptr(d_w), _stream(stream))
 
 
 def moe_set_gemm_sm_limit(max_sms: int) -> int:

@@ -1,0 +1,356 @@
+// Dropout whose mask is computed from a counter and never stored: alone, in
+// the weighted combine (with the residual added), and in the combine's
+// backward.
+//
+// Mask: Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers:
+// as easy as 1, 2, 3", SC 2011), key = rng[0], 64-bit counter = rng[1] + i/8
+// for element i of the tensor in row-major order.  One evaluation's 128 bits
+// are eight 16-bit numbers, one per element of a 16-byte bf16 vector, so a
+// thread evaluates the generator once per vector it already holds and the
+// backward recomputes the same bits from the same (key, counter).  Sixteen
+// bits an element halve the generator's work against 32; the drop
+// probability is the multiple of 2^-16 nearest to p, and the scale
+// 65536/(65536 - drop) is that probability's own, so the expectation is
+// exact.
+//
+// A dropped element is selected away, not multiplied by zero: an infinity or
+// a NaN under the mask does not reach the output.
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+// drop counts 16-bit numbers: element i stays when its number is >= drop.
+struct DropParams {
+  uint32_t drop;  // 0..65536
+  float scale;    // 65536 / (65536 - drop), 0 when everything is dropped
+};
+
+struct PhiloxKey {
+  uint32_t k0, k1;
+  unsigned long long base;  // counter of the tensor's first eight elements
+};
+
+__device__ __forceinline__ PhiloxKey load_key(const unsigned long long* rng) {
+  const unsigned long long s = __ldg(rng), o = __ldg(rng + 1);
+  return {(uint32_t)s, (uint32_t)(s >> 32), o};
+}
+
+// The eight 16-bit numbers of elements 8b .. 8b+7, two to a word, lowest first.
+__device__ __forceinline__ uint4 philox8(const PhiloxKey& k, unsigned long long b) {
+  const unsigned long long ctr = k.base + b;
+  uint32_t c0 = (uint32_t)ctr, c1 = (uint32_t)(ctr >> 32), c2 = 0, c3 = 0;
+  uint32_t k0 = k.k0, k1 = k.k1;
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const unsigned long long p0 = (unsigned long long)0xD2511F53u * c0;
+    const unsigned long long p1 = (unsigned long long)0xCD9E8D57u * c2;
+    c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
+    c1 = (uint32_t)p1;
+    c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
+    c3 = (uint32_t)p0;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return make_uint4(c0, c1, c2, c3);
+}
+
+// Bit i: element 8b + i stays.
+__device__ __forceinline__ uint32_t keep_bits(const PhiloxKey& k, unsigned long long b, uint32_t drop) {
+  const uint4 w = philox8(k, b);
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m |= (uint32_t)((v[i] & 0xFFFFu) >= drop) << (2 * i);
+    m |= (uint32_t)((v[i] >> 16) >= drop) << (2 * i + 1);
+  }
+  return m;
+}
+
+// ------------------------------------------------------------- elementwise
+// out = residual + D(x), fp32 arithmetic, one rounding.  Thread = eight
+// elements (one generator block); the last, partial block element by element.
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<__nv_bfloat16> {
+  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&f)[8]) {
+    unpack8(*reinterpret_cast<const uint4*>(p), f);
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
+    *reinterpret_cast<uint4*>(p) = pack8(f);
+  }
+  static __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  static __device__ __forceinline__ __nv_bfloat16 round(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct Vec8<float> {
+  static __device__ __forceinline__ void load(const float* p, float (&f)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  }
+  static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+  static __device__ __forceinline__ float one(const float* p) { return *p; }
+  static __device__ __forceinline__ float round(float v) { return v; }
+};
+
+// x may be out (every element is read before it is written by its thread).
+template <typename T>
+__global__ void __launch_bounds__(256) dropout_kernel(const T* x, const T* residual, long long n, DropParams dp,
+                                                      const unsigned long long* __restrict__ rng, T* out) {
+  pdl_wait();
+  pdl_trigger();
+  const PhiloxKey key = load_key(rng);
+  const long long nb = (n + 7) / 8;
+  for (long long b = blockIdx.x * (long long)blockDim.x + threadIdx.x; b < nb; b += (long long)gridDim.x * blockDim.x) {
+    if (8 * b + 8 <= n) {
+      float v[8], r[8];
+      Vec8<T>::load(x + 8 * b, v);
+      if (residual) Vec8<T>::load(residual + 8 * b, r);
+      const uint32_t keep = keep_bits(key, b, dp.drop);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = (keep >> i) & 1u ? v[i] * dp.scale : 0.f;
+        v[i] = residual ? r[i] + d : d;
+      }
+      Vec8<T>::store(out + 8 * b, v);
+    } else {
+      const uint32_t keep = keep_bits(key, b, dp.drop);
+      for (long long i = 8 * b; i < n; ++i) {
+        const float d = (keep >> (int)(i - 8 * b)) & 1u ? Vec8<T>::one(x + i) * dp.scale : 0.f;
+        out[i] = Vec8<T>::round(residual ? Vec8<T>::one(residual + i) + d : d);
+      }
+    }
+  }
+}
+
+// ----------------------------------------------------------------- combine
+// Thread = one 16-byte vector (8 columns) of one token: k independent row
+// loads, the fp32 sum over the slots in order, dropout on that sum, the
+// residual, one bf16 rounding.
+__global__ void __launch_bounds__(256) combine_dropout_kernel(
+    const __nv_bfloat16* __restrict__ y_perm, const float* __restrict__ topk_w,
+    const int32_t* __restrict__ row_of_slot, const __nv_bfloat16* residual, int T, int H, int k, int R,
+    DropParams dp, const unsigned long long* __restrict__ rng, __nv_bfloat16* y, int* status) {
+  pdl_wait();
+  pdl_trigger();
+  const PhiloxKey key = load_key(rng);
+  const int nvec = H / 8;
+  const size_t total = (size_t)T * nvec;
+  for (size_t gid = blockIdx.x * (size_t)blockDim.x + threadIdx.x; gid < total;
+       gid += (size_t)gridDim.x * blockDim.x) {
+    const int t = (int)(gid / nvec), v = (int)(gid % nvec);
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < k; j0 += 8) {
+      uint4 buf[8];
+      float wv[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int j = j0 + u;
+        buf[u] = make_uint4(0, 0, 0, 0);
+        wv[u] = 0.f;
+        if (j < k) {
+          const int row = __ldg(row_of_slot + (size_t)t * k + j);
+          if (row >= 0 && row < R) {
+            buf[u] = __ldg(reinterpret_cast<const uint4*>(y_perm + (size_t)row * H) + v);
+            wv[u] = __ldg(topk_w + (size_t)t * k + j);
+          } else {
+            set_status(status, MOE_STATUS_BAD_INDEX);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (j0 + u < k) {
+          float f[8];
+          unpack8(buf[u], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i] = __fmaf_rn(wv[u], f[i], acc[i]);
+        }
+      }
+    }
+    const uint32_t keep = keep_bits(key, gid, dp.drop);
+    float res[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (residual) unpack8(*(reinterpret_cast<const uint4*>(residual) + gid), res);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = res[i] + ((keep >> i) & 1u ? acc[i] * dp.scale : 0.f);
+    reinterpret_cast<uint4*>(y)[gid] = pack8(acc);
+  }
+}
+
+// bf16 element pairs of a vector with the dropped ones replaced by zero
+__device__ __forceinline__ uint4 select8(uint4 v, uint32_t keep) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] &= ((keep >> (2 * i)) & 1u ? 0xFFFFu : 0u) | ((keep >> (2 * i + 1)) & 1u ? 0xFFFF0000u : 0u);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Warp per token: the token's dy row with its dropped elements zeroed sits in
+// registers; for every slot the warp writes dy_perm[row] = (w scale) dy[t] and
+// reduces dy[t] . y_perm[row]; the scale is applied to the sum once.
+__global__ void __launch_bounds__(256) combine_dropout_bwd_kernel(
+    const __nv_bfloat16* __restrict__ dy, const __nv_bfloat16* __restrict__ y_perm,
+    const float* __restrict__ topk_w, const int32_t* __restrict__ row_of_slot, int T, int H, int k, int R,
+    DropParams dp, const unsigned long long* __restrict__ rng, __nv_bfloat16* __restrict__ dy_perm,
+    float* __restrict__ d_w, int* status) {
+  pdl_wait();
+  pdl_trigger();
+  const PhiloxKey key = load_key(rng);
+  const int lane = threadIdx.x & 31;
+  const int nvec = H / 8;
+  const int nw = (int)((gridDim.x * blockDim.x) >> 5);
+  for (int t = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5); t < T; t += nw) {
+    int my_row = lane < k ? __ldg(row_of_slot + (size_t)t * k + lane) : -1;
+    const float my_w = lane < k ? __ldg(topk_w + (size_t)t * k + lane) * dp.scale : 0.f;
+    if (lane < k && (my_row < 0 || my_row >= R)) {
+      set_status(status, MOE_STATUS_BAD_INDEX);
+      my_row = -1;
+    }
+    float my_dw = 0.f;
+    for (int v0 = 0; v0 < nvec; v0 += 256) {
+      uint4 gp[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int v = v0 + u * 32 + lane;
+        gp[u] = v < nvec ? __ldg(reinterpret_cast<const uint4*>(dy + (size_t)t * H) + v) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int v = v0 + u * 32 + lane;
+        if (v < nvec) gp[u] = select8(gp[u], keep_bits(key, (unsigned long long)t * nvec + v, dp.drop));
+      }
+      for (int j = 0; j < k; ++j) {
+        const int row = __shfl_sync(0xffffffffu, my_row, j);
+        const float w = __shfl_sync(0xffffffffu, my_w, j);
+        if (row < 0) continue;  // uniform across the warp
+        uint4 yb[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int v = v0 + u * 32 + lane;
+          yb[u] = v < nvec ? __ldg(reinterpret_cast<const uint4*>(y_perm + (size_t)row * H) + v)
+                           : make_uint4(0, 0, 0, 0);
+        }
+        float p = 0.f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int v = v0 + u * 32 + lane;
+          float g[8], yv[8], o[8];
+          unpack8(gp[u], g);
+          unpack8(yb[u], yv);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            o[i] = w * g[i];
+            p = __fmaf_rn(g[i], yv[i], p);
+          }
+          if (v < nvec) reinterpret_cast<uint4*>(dy_perm + (size_t)row * H)[v] = pack8(o);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) p += __shfl_xor_sync(0xffffffffu, p, off);
+        if (lane == j) my_dw += p;
+      }
+    }
+    if (lane < k) d_w[(size_t)t * k + lane] = my_dw * dp.scale;
+  }
+}
+
+// --------------------------------------------------------------- host side
+
+int drop_params(const char* fn, double p, const void* rng, DropParams* dp) {
+  if (!(p >= 0.0 && p <= 1.0)) return fail(MOE_ERR_INVALID_ARG, "%s: need 0 <= p <= 1", fn);
+  if (!rng) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer argument", fn);
+  if (!aligned16(rng)) return fail(MOE_ERR_ALIGNMENT, "%s: rng must be 16-byte aligned", fn);
+  dp->drop = (uint32_t)(p * 65536.0 + 0.5);
+  dp->scale = dp->drop < 65536u ? (float)(65536.0 / (65536.0 - dp->drop)) : 0.f;
+  return MOE_OK;
+}
+
+int grid_for(size_t work, int per_block, int per_sm) {
+  const size_t b = (work + per_block - 1) / per_block;
+  const size_t cap = (size_t)(sm_count() > 0 ? sm_count() : 148) * per_sm;
+  return (int)(b < cap ? (b > 0 ? b : 1) : cap);
+}
+
+int check_combine(const char* fn, int T, int H, int k) {
+  if (T < 0 || H <= 0 || k <= 0) return fail(MOE_ERR_INVALID_ARG, "%s: need T>=0, H>0, k>0", fn);
+  if (H % 64 != 0 || k > kMaxTopK || (long long)T * k >= (1ll << 31))
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: need H%%64==0, k<=32, T*k<2^31", fn);
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_dropout(const void* x, const void* residual, long long n, int fp32, double p, const int64_t* rng, void* out,
+                void* stream) {
+  clear_error();
+  const char* fn = "moe_dropout";
+  DropParams dp;
+  if (n < 0 || (fp32 != 0 && fp32 != 1)) return fail(MOE_ERR_INVALID_ARG, "%s: need n>=0, fp32 0 or 1", fn);
+  if (n == 0) return MOE_OK;
+  if (int rc = drop_params(fn, p, rng, &dp)) return rc;
+  if (!x || !out) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer argument", fn);
+  if (!aligned16(x) || !aligned16(out) || (residual && !aligned16(residual)))
+    return fail(MOE_ERR_ALIGNMENT, "%s: x, residual and out must be 16-byte aligned", fn);
+  const int grid = grid_for((size_t)(n + 7) / 8, 256, 16);
+  const auto* r = reinterpret_cast<const unsigned long long*>(rng);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (fp32)
+    launch_pdl(dropout_kernel<float>, grid, 256, 0, s, static_cast<const float*>(x),
+               static_cast<const float*>(residual), n, dp, r, static_cast<float*>(out));
+  else
+    launch_pdl(dropout_kernel<__nv_bfloat16>, grid, 256, 0, s, static_cast<const __nv_bfloat16*>(x),
+               static_cast<const __nv_bfloat16*>(residual), n, dp, r, static_cast<__nv_bfloat16*>(out));
+  return check_launch(fn);
+}
+
+int moe_combine_dropout(const void* y_perm, const float* topk_w, const int32_t* row_of_slot, const void* residual,
+                        int T, int H, int k, double p, const int64_t* rng, void* y, void* stream) {
+  clear_error();
+  const char* fn = "moe_combine_dropout";
+  DropParams dp;
+  if (int rc = check_combine(fn, T, H, k)) return rc;
+  if (T == 0) return MOE_OK;
+  if (int rc = drop_params(fn, p, rng, &dp)) return rc;
+  if (!y_perm || !topk_w || !row_of_slot || !y) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer argument", fn);
+  if (!aligned16(y_perm) || !aligned16(y) || (residual && !aligned16(residual)))
+    return fail(MOE_ERR_ALIGNMENT, "%s: y_perm, residual and y must be 16-byte aligned", fn);
+  const size_t work = (size_t)T * (H / 8);
+  launch_pdl(combine_dropout_kernel, grid_for(work, 256, 16), 256, 0, static_cast<cudaStream_t>(stream),
+             static_cast<const __nv_bfloat16*>(y_perm), topk_w, row_of_slot,
+             static_cast<const __nv_bfloat16*>(residual), T, H, k, T * k, dp,
+             reinterpret_cast<const unsigned long long*>(rng), static_cast<__nv_bfloat16*>(y), status_word());
+  return check_launch(fn);
+}
+
+int moe_combine_dropout_bwd(const void* dy, const void* y_perm, const float* topk_w, const int32_t* row_of_slot,
+                            int T, int H, int k, double p, const int64_t* rng, void* dy_perm, float* d_w,
+                            void* stream) {
+  clear_error();
+  const char* fn = "moe_combine_dropout_bwd";
+  DropParams dp;
+  if (int rc = check_combine(fn, T, H, k)) return rc;
+  if (T == 0) return MOE_OK;
+  if (int rc = drop_params(fn, p, rng, &dp)) return rc;
+  if (!dy || !y_perm || !topk_w || !row_of_slot || !dy_perm || !d_w)
+    return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer argument", fn);
+  if (!aligned16(dy) || !aligned16(y_perm) || !aligned16(dy_perm))
+    return fail(MOE_ERR_ALIGNMENT, "%s: dy, y_perm and dy_perm must be 16-byte aligned", fn);
+  launch_pdl(combine_dropout_bwd_kernel, grid_for((size_t)T * 32, 256, 16), 256, 0, static_cast<cudaStream_t>(stream),
+             static_cast<const __nv_bfloat16*>(dy), static_cast<const __nv_bfloat16*>(y_perm), topk_w, row_of_slot, T,
+             H, k, T * k, dp, reinterpret_cast<const unsigned long long*>(rng),
+             static_cast<__nv_bfloat16*>(dy_perm), d_w, status_word());
+  return check_launch(fn);
+}
+
+}  // extern "C"

@@ -254,16 +254,6 @@ __global__ void __launch_bounds__(256, kE4M3 ? 4 : 1) dispatch_kernel(
 // ------------------------------------------------------------------ combine
 // Thread = one 16-byte vector (8 columns) of one token; k independent row
 // loads, fp32 accumulation in slot order, one bf16 rounding.
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  f[0] = bf16lo(v.x); f[1] = bf16hi(v.x); f[2] = bf16lo(v.y); f[3] = bf16hi(v.y);
-  f[4] = bf16lo(v.z); f[5] = bf16hi(v.z); f[6] = bf16lo(v.w); f[7] = bf16hi(v.w);
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
-}
-
 template <bool kWeighted, bool kF32Out>
 __global__ void __launch_bounds__(256) gather_sum_kernel(const __nv_bfloat16* __restrict__ src,
                                                          const float* __restrict__ topk_w,

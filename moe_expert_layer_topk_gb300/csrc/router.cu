@@ -232,7 +232,8 @@ __global__ void __launch_bounds__(256) router_topk_kernel(const float* __restric
                                                           const float* __restrict__ bias, int T,
                                                           int E, int k, int32_t* __restrict__ topk_idx,
                                                           float* __restrict__ topk_w,
-                                                          int32_t* __restrict__ chunk_cnt, int nchunk) {
+                                                          int32_t* __restrict__ chunk_cnt, int nchunk,
+                                                          float* __restrict__ logits) {
   pdl_wait();
   pdl_trigger();
   extern __shared__ int chist[];  // [E] slots of this chunk per expert
@@ -269,6 +270,11 @@ __global__ void __launch_bounds__(256) router_topk_kernel(const float* __restric
         const int e = lane + 32 * q;
         if (e < E) v[q] = __fadd_rn(v[q], __ldg(bias + e));
       }
+    }
+    if (logits) {  // kept for the balance loss and its gradient
+#pragma unroll
+      for (int q = 0; q < kNQ; ++q)
+        if (lane + 32 * q < E) logits[(size_t)t * E + lane + 32 * q] = v[q];
     }
     uint32_t taken = 0;
 #pragma unroll
@@ -406,7 +412,7 @@ __device__ __forceinline__ void split_bf16(float v, __nv_bfloat16& hi, __nv_bflo
 
 __global__ void __launch_bounds__(256) router_bwd_dl_kernel(
     const float* __restrict__ d_w, const float* __restrict__ topk_w,
-    const int32_t* __restrict__ topk_idx, int T, int E, int Ep, int k,
+    const int32_t* __restrict__ topk_idx, const float* __restrict__ dlogits, int T, int E, int Ep, int k,
     __nv_bfloat16* __restrict__ dl2, __nv_bfloat16* __restrict__ dl3, int* status) {
   pdl_wait();
   pdl_trigger();
@@ -415,7 +421,7 @@ __global__ void __launch_bounds__(256) router_bwd_dl_kernel(
   const int t = blockIdx.x * 8 + warp;
   if (t >= T) return;
   float* row = rowbuf + (size_t)warp * Ep;
-  for (int e = lane; e < Ep; e += 32) row[e] = 0.f;
+  for (int e = lane; e < Ep; e += 32) row[e] = dlogits && e < E ? __ldg(dlogits + (size_t)t * E + e) : 0.f;
   __syncwarp();
   const float w = lane < k ? topk_w[(size_t)t * k + lane] : 0.f;
   const float g = lane < k ? d_w[(size_t)t * k + lane] : 0.f;
@@ -425,7 +431,7 @@ __global__ void __launch_bounds__(256) router_bwd_dl_kernel(
   if (lane < k) {
     const int e = topk_idx[(size_t)t * k + lane];
     if (e >= 0 && e < E)
-      row[e] = w * (g - s);
+      row[e] = dlogits ? row[e] + w * (g - s) : w * (g - s);
     else
       set_status(status, MOE_STATUS_BAD_INDEX);
   }
@@ -558,7 +564,7 @@ namespace {
 // totals), counts / offsets / EP-rank ranges.
 int route_impl(const char* fn, const void* x, const float* Wr, const float* bias, int T, int H, int E, int k,
                int ep_size, int32_t* topk_idx, float* topk_w, int32_t* counts, int32_t* offsets,
-               int32_t* rank_offsets, int32_t* chunk, void* ws, cudaStream_t s) {
+               int32_t* rank_offsets, int32_t* chunk, float* logits, void* ws, cudaStream_t s) {
   float* part = static_cast<float*>(ws);
   int32_t* totals = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + route_part_bytes(T, H, E));
   const int nchunk = route_nchunk(T);
@@ -603,17 +609,23 @@ int route_impl(const char* fn, const void* x, const float* Wr, const float* bias
     const int nq = (E + 31) / 32;
     const size_t hs = sizeof(int) * (size_t)E;
     if (nq <= 1)
-      launch_pdl(router_topk_kernel<1>, nchunk, 256, hs, s, part, nblk_h, bias, T, E, k, topk_idx, topk_w, chunk, nchunk);
+      launch_pdl(router_topk_kernel<1>, nchunk, 256, hs, s, part, nblk_h, bias, T, E, k, topk_idx, topk_w, chunk, nchunk,
+                 logits);
     else if (nq <= 2)
-      launch_pdl(router_topk_kernel<2>, nchunk, 256, hs, s, part, nblk_h, bias, T, E, k, topk_idx, topk_w, chunk, nchunk);
+      launch_pdl(router_topk_kernel<2>, nchunk, 256, hs, s, part, nblk_h, bias, T, E, k, topk_idx, topk_w, chunk, nchunk,
+                 logits);
     else if (nq <= 4)
-      launch_pdl(router_topk_kernel<4>, nchunk, 256, hs, s, part, nblk_h, bias, T, E, k, topk_idx, topk_w, chunk, nchunk);
+      launch_pdl(router_topk_kernel<4>, nchunk, 256, hs, s, part, nblk_h, bias, T, E, k, topk_idx, topk_w, chunk, nchunk,
+                 logits);
     else if (nq <= 8)
-      launch_pdl(router_topk_kernel<8>, nchunk, 256, hs, s, part, nblk_h, bias, T, E, k, topk_idx, topk_w, chunk, nchunk);
+      launch_pdl(router_topk_kernel<8>, nchunk, 256, hs, s, part, nblk_h, bias, T, E, k, topk_idx, topk_w, chunk, nchunk,
+                 logits);
     else if (nq <= 16)
-      launch_pdl(router_topk_kernel<16>, nchunk, 256, hs, s, part, nblk_h, bias, T, E, k, topk_idx, topk_w, chunk, nchunk);
+      launch_pdl(router_topk_kernel<16>, nchunk, 256, hs, s, part, nblk_h, bias, T, E, k, topk_idx, topk_w, chunk, nchunk,
+                 logits);
     else
-      launch_pdl(router_topk_kernel<32>, nchunk, 256, hs, s, part, nblk_h, bias, T, E, k, topk_idx, topk_w, chunk, nchunk);
+      launch_pdl(router_topk_kernel<32>, nchunk, 256, hs, s, part, nblk_h, bias, T, E, k, topk_idx, topk_w, chunk, nchunk,
+                 logits);
     if (int rc = check_launch("route: top-k kernel")) return rc;
   }
   // with no token every total is 0 (the scan runs over no chunk)
@@ -656,7 +668,7 @@ int moe_route_topk(const void* x, const float* Wr, const float* bias, int T, int
     return rc;
   int32_t* chunk = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + route_ws_bytes(T, H, E, false));
   return route_impl(fn, x, Wr, bias, T, H, E, k, ep_size, topk_idx, topk_w, counts, offsets, rank_offsets,
-                    chunk, ws, static_cast<cudaStream_t>(stream));
+                    chunk, nullptr, ws, static_cast<cudaStream_t>(stream));
 }
 
 int moe_route_topk_chunks(const void* x, const float* Wr, const float* bias, int T, int H, int E, int k,
@@ -670,7 +682,22 @@ int moe_route_topk_chunks(const void* x, const float* Wr, const float* bias, int
     return rc;
   if (T > 0 && !chunk_prefix) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer argument", fn);
   return route_impl(fn, x, Wr, bias, T, H, E, k, ep_size, topk_idx, topk_w, counts, offsets, rank_offsets,
-                    chunk_prefix, ws, static_cast<cudaStream_t>(stream));
+                    chunk_prefix, nullptr, ws, static_cast<cudaStream_t>(stream));
+}
+
+int moe_route_topk_logits(const void* x, const float* Wr, const float* bias, int T, int H, int E, int k,
+                          int ep_size, int32_t* topk_idx, float* topk_w, int32_t* counts, int32_t* offsets,
+                          int32_t* rank_offsets, int32_t* chunk_prefix, float* logits, void* ws, size_t ws_bytes,
+                          void* stream) {
+  clear_error();
+  const char* fn = "moe_route_topk_logits";
+  if (int rc = route_check(fn, x, Wr, bias, T, H, E, k, ep_size, topk_idx, topk_w, counts, offsets, rank_offsets,
+                           ws, ws_bytes, T >= 0 && H > 0 && E > 0 ? route_ws_bytes(T, H, E, false) : 0))
+    return rc;
+  if (T > 0 && (!chunk_prefix || !logits)) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer argument", fn);
+  if (!aligned16(logits)) return fail(MOE_ERR_ALIGNMENT, "%s: logits must be 16-byte aligned", fn);
+  return route_impl(fn, x, Wr, bias, T, H, E, k, ep_size, topk_idx, topk_w, counts, offsets, rank_offsets,
+                    chunk_prefix, logits, ws, static_cast<cudaStream_t>(stream));
 }
 
 size_t moe_route_topk_bwd_workspace_size(int T, int H, int E) {
@@ -678,25 +705,29 @@ size_t moe_route_topk_bwd_workspace_size(int T, int H, int E) {
   return bwd_layout(T, H, E).total;
 }
 
-int moe_route_topk_bwd(const float* d_w, const float* topk_w, const int32_t* topk_idx,
-                       const void* x, const float* Wr, const float* dx_acc, int T, int H, int E,
-                       int k, float* dWr, void* dx, int accumulate, void* ws, size_t ws_bytes,
-                       void* stream) {
-  clear_error();
+}  // extern "C"
+
+namespace moe {
+namespace {
+
+// dlogits: a further gradient of the logits, or null.
+int route_bwd_impl(const char* fn, const float* d_w, const float* topk_w, const int32_t* topk_idx,
+                   const float* dlogits, const void* x, const float* Wr, const float* dx_acc, int T, int H, int E,
+                   int k, float* dWr, void* dx, int accumulate, void* ws, size_t ws_bytes, void* stream) {
   if (T < 0 || H <= 0 || E <= 0 || k <= 0)
-    return fail(MOE_ERR_INVALID_ARG, "moe_route_topk_bwd: need T>=0, H>0, E>0, k>0");
+    return fail(MOE_ERR_INVALID_ARG, "%s: need T>=0, H>0, E>0, k>0", fn);
   if (E > kMaxExperts || k > kMaxTopK || k > E || H % 64 != 0 || (long long)T * k >= (1ll << 31))
     return fail(MOE_ERR_UNSUPPORTED_SHAPE,
-                "moe_route_topk_bwd: need E<=1024, k<=min(E,32), H%%64==0 (E=%d k=%d H=%d)", E, k, H);
+                "%s: need E<=1024, k<=min(E,32), H%%64==0 (E=%d k=%d H=%d)", fn, E, k, H);
   if (!dWr || !ws || (T > 0 && (!d_w || !topk_w || !topk_idx || !x || !Wr || !dx_acc || !dx)))
-    return fail(MOE_ERR_INVALID_ARG, "moe_route_topk_bwd: NULL pointer argument");
-  if (!aligned16(x) || !aligned16(Wr) || !aligned16(dx_acc) || !aligned16(dWr) || !aligned16(dx) ||
+    return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer argument", fn);
+  if (!aligned16(x) || !aligned16(Wr) || !aligned16(dx_acc) || !aligned16(dWr) || !aligned16(dx) || !aligned16(dlogits) ||
       (reinterpret_cast<uintptr_t>(ws) & 127u))
     return fail(MOE_ERR_ALIGNMENT,
-                "moe_route_topk_bwd: tensors must be 16-byte and ws 128-byte aligned");
+                "%s: tensors must be 16-byte and ws 128-byte aligned", fn);
   const BwdLayout L = bwd_layout(T, H, E);
   if (ws_bytes < L.total)
-    return fail(MOE_ERR_WORKSPACE, "moe_route_topk_bwd: workspace %zu < %zu bytes", ws_bytes, L.total);
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, L.total);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* base = static_cast<char*>(ws);
   auto* dl2 = reinterpret_cast<__nv_bfloat16*>(base + L.dl2);
@@ -709,26 +740,50 @@ int moe_route_topk_bwd(const float* d_w, const float* topk_w, const int32_t* top
   if (T == 0) {  // no token: dWr gets a zero sum, dx is empty
     if (!accumulate) {
       cudaError_t e = cudaMemsetAsync(dWr, 0, sizeof(float) * (size_t)H * E, s);
-      if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "moe_route_topk_bwd: %s", cudaGetErrorString(e));
+      if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
     }
     return MOE_OK;
   }
   launch_pdl(router_bwd_dl_kernel, (T + 7) / 8, 256, sizeof(float) * 8 * L.Ep, s, 
-      d_w, topk_w, topk_idx, T, E, L.Ep, k, dl2, dl3, status);
-  if (int rc = check_launch("moe_route_topk_bwd: dl kernel")) return rc;
+      d_w, topk_w, topk_idx, dlogits, T, E, L.Ep, k, dl2, dl3, status);
+  if (int rc = check_launch(fn, "dl kernel")) return rc;
   const size_t nwr = (size_t)H * L.Ep;
   launch_pdl(router_bwd_wr_kernel, (int)((nwr + 255) / 256 < 4096 ? (nwr + 255) / 256 : 4096), 256, 0, s, 
       Wr, H, E, L.Ep, wr3);
-  if (int rc = check_launch("moe_route_topk_bwd: Wr split kernel")) return rc;
+  if (int rc = check_launch(fn, "Wr split kernel")) return rc;
   launch_pdl(split_table_kernel, 1, 128, 0, s, seg, L.S, T);
-  if (int rc = check_launch("moe_route_topk_bwd: split table")) return rc;
+  if (int rc = check_launch(fn, "split table")) return rc;
   // dx = bf16(dx_acc + dl . Wr^T)
   if (int rc = launch_dense_add_bf16(dl3, wr3, dx_acc, dx, T, H, 3 * L.Ep, s)) return rc;
   // split-K partials of x^T . [dl_hi | dl_lo]
   if (int rc = launch_dw_split(x, dl2, T, H, 2 * L.Ep, seg, L.S, part, base + L.maps, s)) return rc;
   const size_t nred = (size_t)H * E;
   launch_pdl(router_bwd_reduce_kernel, (int)((nred + 255) / 256 < 4096 ? (nred + 255) / 256 : 4096), 256, 0, s, part, L.S, H, E, L.Ep, dWr, accumulate);
-  return check_launch("moe_route_topk_bwd: reduce kernel");
+  return check_launch(fn, "reduce kernel");
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" {
+
+int moe_route_topk_bwd(const float* d_w, const float* topk_w, const int32_t* topk_idx,
+                       const void* x, const float* Wr, const float* dx_acc, int T, int H, int E,
+                       int k, float* dWr, void* dx, int accumulate, void* ws, size_t ws_bytes,
+                       void* stream) {
+  clear_error();
+  return route_bwd_impl("moe_route_topk_bwd", d_w, topk_w, topk_idx, nullptr, x, Wr, dx_acc, T, H, E, k, dWr, dx,
+                        accumulate, ws, ws_bytes, stream);
+}
+
+int moe_route_topk_logits_bwd(const float* d_w, const float* topk_w, const int32_t* topk_idx, const float* dlogits,
+                              const void* x, const float* Wr, const float* dx_acc, int T, int H, int E, int k,
+                              float* dWr, void* dx, int accumulate, void* ws, size_t ws_bytes, void* stream) {
+  clear_error();
+  const char* fn = "moe_route_topk_logits_bwd";
+  if (T > 0 && !dlogits) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer argument", fn);
+  return route_bwd_impl(fn, d_w, topk_w, topk_idx, dlogits, x, Wr, dx_acc, T, H, E, k, dWr, dx, accumulate, ws,
+                        ws_bytes, stream);
 }
 
 }  // extern "C"
