@@ -502,6 +502,42 @@ int moe_combine_dropout_bwd(const void* dy, const void* y_perm, const float* top
                             int T, int H, int k, double p, const int64_t* rng, void* dy_perm, float* d_w,
                             void* stream);
 
+/* ------------------------------------------------------------------------
+ * A projection shared by all requests plus a low-rank adapter for each
+ * request (no counterpart on the pages): many fine-tuned adapters served, or
+ * trained, over one set of weights.
+ *
+ * The T rows are num_seg requests: request i holds rows [seg_offsets[i],
+ * seg_offsets[i+1]) and uses adapter a = seg_adapter[i], or none when that is
+ * -1; rows outside every request use none.  A request may have any number of
+ * rows, one or none among them; several may share an adapter.
+ *   y[t]  = W x[t] + B[a] v[t],       v[t] = scale[a] A[a] x[t]          -> bf16 [T,N]
+ * W bf16 [N,K]; A bf16 [num_adapters,r,K]; B bf16 [num_adapters,N,r]; scale
+ * fp32 [num_adapters] or NULL (1).  x, y bf16 with row strides ldx >= K,
+ * ldy >= N (elements, multiples of 8).  hidden receives v, each fp32 value as
+ * two bf16 parts (16 bits), for the backward; its layout is the library's own,
+ * moe_adapter_hidden_size(T, r) bytes.  y may not overlap x.
+ *
+ * moe_adapter_linear_bwd, W frozen:
+ *   u[t]  = scale[a] B[a]^T dy[t]  (two bf16 parts)
+ *   dx[t] = W^T dy[t] + A[a]^T u[t]                                      -> bf16 [T,K]
+ *   dA[a] = sum over a's rows of u[t] x[t]^T     fp32 [num_adapters,r,K]
+ *   dB[a] = sum over a's rows of dy[t] v[t]^T    fp32 [num_adapters,N,r]
+ * dA and dB are overwritten (zero for an adapter without rows), or added to
+ * when accumulate != 0.  dx may not overlap dy or x.
+ * Limits: K, N multiples of 64; r a multiple of 8, at most 128; num_adapters
+ * and num_seg at most 1024.  Sums are fp32; results are deterministic. */
+size_t moe_adapter_hidden_size(int T, int r);
+int moe_adapter_linear(const void* x, long long ldx, const void* W, const void* A, const void* B, const float* scale,
+                       int num_seg, const int32_t* seg_offsets, const int32_t* seg_adapter, int T, int K, int N, int r,
+                       int num_adapters, void* hidden, size_t hidden_bytes, void* y, long long ldy, void* stream);
+size_t moe_adapter_linear_bwd_workspace_size(int T, int K, int N, int r, int num_seg);
+int moe_adapter_linear_bwd(const void* dy, long long lddy, const void* x, long long ldx, const void* W, const void* A,
+                           const void* B, const float* scale, const void* hidden, size_t hidden_bytes, int num_seg,
+                           const int32_t* seg_offsets, const int32_t* seg_adapter, int T, int K, int N, int r,
+                           int num_adapters, void* dx, long long lddx, float* dA, float* dB, int accumulate, void* ws,
+                           size_t ws_bytes, void* stream);
+
 /* Persistent-grid limit of the grouped GEMMs (no counterpart on the pages).
  * Every grouped GEMM kernel (the forward, backward and router-backward
  * GEMMs of the calls above) runs one CTA per SM over its tiles.  After

@@ -33,6 +33,8 @@ __all__ = ["lib", "MoEError", "LIB_PATH", "ENTRY_POINTS",
            "moe_route_topk_logits", "moe_route_topk_logits_bwd",
            "moe_balance_loss_workspace_size", "moe_balance_loss", "moe_balance_loss_bwd",
            "moe_dropout", "moe_combine_dropout", "moe_combine_dropout_bwd",
+           "moe_adapter_hidden_size", "moe_adapter_linear", "moe_adapter_linear_bwd_workspace_size",
+           "moe_adapter_linear_bwd",
            "moe_read_device_status", "moe_abi_version", "moe_probe_fma", "moe_set_gemm_sm_limit", "sm_count"]
 
 LIB_PATH: Path = _build_mod.LIB
@@ -87,6 +89,11 @@ ENTRY_POINTS = {
     "moe_dropout": ([_P, _P, _L, _I, _D, _P, _P, _P], _I),
     "moe_combine_dropout": ([_P, _P, _P, _P, _I, _I, _I, _D, _P, _P, _P], _I),
     "moe_combine_dropout_bwd": ([_P, _P, _P, _P, _I, _I, _I, _D, _P, _P, _P, _P], _I),
+    "moe_adapter_hidden_size": ([_I, _I], _Z),
+    "moe_adapter_linear": ([_P, _L, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _P, _Z, _P, _L, _P], _I),
+    "moe_adapter_linear_bwd_workspace_size": ([_I, _I, _I, _I, _I], _Z),
+    "moe_adapter_linear_bwd": ([_P, _L, _P, _L, _P, _P, _P, _P, _P, _Z, _I, _P, _P, _I, _I, _I, _I, _I, _P, _L, _P, _P,
+                                _I, _P, _Z, _P], _I),
     "moe_probe_fma": ([_I, _I, _I, _P, ctypes.POINTER(ctypes.c_longlong), _P], _I),
     "moe_set_gemm_sm_limit": ([_I, ctypes.POINTER(ctypes.c_int)], _I),
 }
@@ -390,6 +397,42 @@ def moe_combine_dropout(y_perm, topk_w, row_of_slot, residual, T, H, k, p, rng, 
 def moe_combine_dropout_bwd(dy, y_perm, topk_w, row_of_slot, T, H, k, p, rng, dy_perm, d_w, stream=None):
     _call("moe_combine_dropout_bwd", _ptr(dy), _ptr(y_perm), _ptr(topk_w), _ptr(row_of_slot), T, H, k, p,
           _ptr(rng), _ptr(dy_perm), _ptr(d_w), _stream(stream))
+
+
+def _rows(t):
+    """Pointer and row stride of a 2-D tensor whose rows may lie apart."""
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must live on the GPU")
+    if t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError("row tensors must be 2-D with contiguous rows")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def moe_adapter_hidden_size(T, r) -> int:
+    return lib().moe_adapter_hidden_size(T, r)
+
+
+def moe_adapter_linear_bwd_workspace_size(T, K, N, r, num_seg) -> int:
+    return lib().moe_adapter_linear_bwd_workspace_size(T, K, N, r, num_seg)
+
+
+def moe_adapter_linear(x, W, A, B, scale, num_seg, seg_offsets, seg_adapter, T, K, N, r, num_adapters, hidden, y,
+                       stream=None):
+    """y = x W^T plus each request's adapter; x and y may be row slices of wider tensors."""
+    px, ldx = _rows(x)
+    py, ldy = _rows(y)
+    _call("moe_adapter_linear", px, ldx, _ptr(W), _ptr(A), _ptr(B), _ptr(scale), num_seg, _ptr(seg_offsets),
+          _ptr(seg_adapter), T, K, N, r, num_adapters, _ptr(hidden), _nbytes(hidden), py, ldy, _stream(stream))
+
+
+def moe_adapter_linear_bwd(dy, x, W, A, B, scale, hidden, num_seg, seg_offsets, seg_adapter, T, K, N, r, num_adapters,
+                           dx, dA, dB, accumulate=0, ws=None, stream=None):
+    pd, lddy = _rows(dy)
+    px, ldx = _rows(x)
+    po, lddx = _rows(dx)
+    _call("moe_adapter_linear_bwd", pd, lddy, px, ldx, _ptr(W), _ptr(A), _ptr(B), _ptr(scale), _ptr(hidden),
+          _nbytes(hidden), num_seg, _ptr(seg_offsets), _ptr(seg_adapter), T, K, N, r, num_adapters, po, lddx, _ptr(dA),
+          _ptr(dB), int(accumulate), _ptr(ws), _nbytes(ws), _stream(stream))
 
 
 def moe_set_gemm_sm_limit(max_sms: int) -> int:

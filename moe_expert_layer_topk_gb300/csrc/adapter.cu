@@ -1,0 +1,1190 @@
+// A projection shared by all requests plus a low-rank adapter for each
+// request, forward and backward.
+//
+// Row t of a request with adapter a:
+//   y_t  = W x_t + B_a v_t,        v_t = s_a A_a x_t
+//   dx_t = W^T dy_t + A_a^T u_t,   u_t = s_a B_a^T dy_t
+//   dA_a = sum_t u_t x_t^T,        dB_a = sum_t dy_t v_t^T
+// Rows of requests without an adapter leave the second terms out.
+//
+// Two products per direction.  The narrow one (v or u, r <= 128 columns,
+// bound by reading x or dy) writes its fp32 result as kPlanes bf16 parts whose
+// sum has 16 bits, so the wide products that take it stay on the tensor cores
+// without losing what the first one computed.  The wide one appends the
+// adapter to the shared projection's reduction: after the W blocks, the same
+// accumulator tile takes v_t's parts times B_a for every run of rows with one
+// adapter, with the tile's other rows switched off by the MMA's lane mask
+// (tcgen05.mma disable-output-lane).  A tile may so hold any mix of requests,
+// no row is computed for another request's adapter, and a non-finite value in
+// one request's row or adapter reaches no other row.
+#include <cuda.h>
+
+#include "tc_common.cuh"
+
+namespace moe {
+namespace tc {
+namespace {
+
+constexpr int kPlanes = 2;        // bf16 parts of v, u
+constexpr int kMaxRank = 128;
+constexpr int kMaxAdapters = 1024;
+
+__host__ __device__ constexpr int round_up(int v, int to) { return (v + to - 1) / to * to; }
+// Columns of one part in the hidden tensor: whole 16-wide MMA steps when all
+// parts fit one 64-column block, else whole 64-column blocks.
+__host__ __device__ constexpr int plane_cols(int r) {
+  return kPlanes * round_up(r, 16) <= 64 ? round_up(r, 16) : round_up(r, 64);
+}
+__host__ __device__ constexpr int hidden_cols(int r) { return kPlanes * plane_cols(r); }
+
+// ------------------------------------------------------------ request table
+
+struct Reqs {
+  int T, num_seg, num_adapters;
+  const int32_t* offsets;  // [num_seg + 1]
+  const int32_t* adapter;  // [num_seg], negative: none
+};
+
+// Shared-memory copy: offsets made monotone and clamped to [0, T], adapter ids
+// out of range replaced by -1 (both reported).  off[num_seg + 1], ad[num_seg].
+__device__ __forceinline__ void load_requests(const Reqs& q, int* off, int* ad, int* status) {
+  if (q.num_seg == 0) {  // there may be no table at all
+    if (threadIdx.x == 0) off[0] = 0;
+    __syncthreads();
+    return;
+  }
+  bool bad = false;
+  for (int s = threadIdx.x; s <= q.num_seg; s += blockDim.x) {
+    int v = __ldg(q.offsets + s);
+    if (v < 0 || v > q.T) {
+      bad = true;
+      v = v < 0 ? 0 : q.T;
+    }
+    off[s] = v;
+    if (s < q.num_seg) {
+      int a = __ldg(q.adapter + s);
+      if (a >= q.num_adapters || a < -1) {
+        bad = true;
+        a = -1;
+      }
+      ad[s] = a;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int carry = 0;
+    for (int b = 0; b <= q.num_seg; b += 32) {
+      const int s = b + lane, v = s <= q.num_seg ? off[s] : 0;
+      int m = v;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, m, d);
+        if (lane >= d) m = max(m, o);
+      }
+      m = max(m, carry);
+      if (s <= q.num_seg) {
+        bad |= m != v;
+        off[s] = m;
+      }
+      carry = __shfl_sync(0xffffffffu, m, 31);
+    }
+  }
+  if (bad) set_status(status, MOE_STATUS_BAD_SEGMENTS);
+  __syncthreads();
+}
+
+// First request that ends after row t.
+__device__ __forceinline__ int first_request(const int* off, int num_seg, int t) {
+  int lo = 0, hi = num_seg;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid + 1] > t) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
+// f(lo, hi, adapter) -> bool (go on) for every run of rows of [m0, m1) with one
+// adapter, in row order; neighbouring requests with the same adapter are one run.
+template <class F>
+__device__ __forceinline__ void for_each_run(const int* off, const int* ad, int num_seg, int m0, int m1, F&& f) {
+  int lo = -1, hi = 0, a = -1;
+  for (int s = first_request(off, num_seg, m0); s < num_seg && off[s] < m1; ++s) {
+    const int b = max(off[s], m0), e = min(off[s + 1], m1);
+    if (b >= e || ad[s] < 0) continue;
+    if (lo >= 0 && ad[s] == a && b == hi) {
+      hi = e;
+      continue;
+    }
+    if (lo >= 0 && !f(lo, hi, a)) return;
+    lo = b;
+    hi = e;
+    a = ad[s];
+  }
+  if (lo >= 0) f(lo, hi, a);
+}
+
+// Word w of the MMA's lane mask (1 = lane off) that leaves rows [lo, hi) on.
+__device__ __forceinline__ uint32_t lanes_off(int lo, int hi, int w) {
+  const int a = max(lo - 32 * w, 0), b = min(hi - 32 * w, 32);
+  if (a >= b) return 0xffffffffu;
+  const uint32_t below_b = b == 32 ? 0xffffffffu : (1u << b) - 1u;
+  return ~(below_b & ~((1u << a) - 1u));
+}
+
+struct LaneMask {
+  uint32_t w[4];
+};
+__device__ __forceinline__ LaneMask lane_mask(int lo, int hi) {
+  return {{lanes_off(lo, hi, 0), lanes_off(lo, hi, 1), lanes_off(lo, hi, 2), lanes_off(lo, hi, 3)}};
+}
+
+// mma_bf16 that leaves the accumulator rows of masked lanes as they are.
+__device__ __forceinline__ void mma_bf16_lanes(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                               const LaneMask& m) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(m.w[0]), "r"(m.w[1]), "r"(m.w[2]), "r"(m.w[3])
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ uint32_t align1k(uint32_t a) { return (a + 1023u) & ~1023u; }
+
+// v split into kPlanes bf16 parts, largest first, 8 columns: one 16-byte vector a part
+__device__ __forceinline__ void split8(const float (&v)[8], uint4 (&out)[kPlanes]) {
+  float rest[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) rest[i] = v[i];
+#pragma unroll
+  for (int p = 0; p < kPlanes; ++p) {
+    float h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      h[i] = __bfloat162float(__float2bfloat16_rn(rest[i]));
+      // of an infinity or a NaN, whose difference would be NaN, only the first part is kept
+      rest[i] = isfinite(rest[i]) ? rest[i] - h[i] : 0.f;
+    }
+    out[p] = pack8(h);
+  }
+}
+
+// ------------------------------------------------- narrow product, tensor cores
+//
+// hidden[t] = parts of s_a F_a . in[t] for 128 rows a cluster; the cluster's
+// CTAs share the reduction (a K slice each) and add their fp32 accumulators
+// through distributed shared memory.  F_a is A_a [r, K] (K-major operand) or
+// B_a^T, read from B_a [N, r] as it lies (MN-major operand).  One row tile's
+// runs follow one another for every block of the reduction, each with the
+// lanes of the other runs off, so x is read once whatever the mix of requests.
+struct ShrinkParams {
+  Reqs q;
+  int red;              // reduction length
+  int r, rN;            // rank, MMA columns (rank up to a multiple of 16)
+  int f_bytes;          // shared-memory bytes of one F block
+  int f_rows;           // rows of F's 2-D view per adapter
+  const float* scale;   // [num_adapters] or null
+  __nv_bfloat16* hidden;
+  uint32_t idesc;
+  uint32_t tmem_cols;
+  int* status;
+};
+constexpr int kShrinkX = 4, kShrinkF = 4;  // blocks of x and of F in flight
+
+struct ShrinkCtl {
+  unsigned long long xfull[kShrinkX], xempty[kShrinkX], ffull[kShrinkF], fempty[kShrinkF], done;
+  uint32_t tmem_base;
+  int abort_flag;
+  int row_ad[BM];
+};
+
+template <bool kMN>
+__global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_constant__ CUtensorMap tmX,
+                                                             const __grid_constant__ CUtensorMap tmF,
+                                                             const ShrinkParams p) {
+  pdl_wait();
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ ShrinkCtl ctl;
+  const uint32_t base = align1k(smem_u32(smem_raw));
+  uint8_t* bytes = smem_raw + (base - smem_u32(smem_raw));
+  const uint32_t sX = base, sF = base + kShrinkX * (BM * BK * 2);
+  float* acc = reinterpret_cast<float*>(bytes);  // [rN][BM], over the x blocks once they are consumed
+  int* off = reinterpret_cast<int*>(bytes + kShrinkX * (BM * BK * 2) + kShrinkF * p.f_bytes);
+  int* ad = off + p.q.num_seg + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nrank = gridDim.x, rank = blockIdx.x;
+  const int m0 = blockIdx.y * BM, m1 = min(p.q.T, m0 + BM);
+  load_requests(p.q, off, ad, p.status);
+  if (threadIdx.x < BM) {
+    const int t = m0 + threadIdx.x;
+    const int s = first_request(off, p.q.num_seg, t);
+    ctl.row_ad[threadIdx.x] = t < m1 && s < p.q.num_seg && off[s] <= t ? ad[s] : -1;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kShrinkX; ++i) {
+      mbar_init(smem_u32(&ctl.xfull[i]), 1);
+      mbar_init(smem_u32(&ctl.xempty[i]), 1);
+    }
+    for (int i = 0; i < kShrinkF; ++i) {
+      mbar_init(smem_u32(&ctl.ffull[i]), 1);
+      mbar_init(smem_u32(&ctl.fempty[i]), 1);
+    }
+    mbar_init(smem_u32(&ctl.done), 1);
+    ctl.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_tmap(&tmX);
+    prefetch_tmap(&tmF);
+  }
+  if (warp == 1) tmem_alloc_n<1>(smem_u32(&ctl.tmem_base), p.tmem_cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // only now may the next kernel of the stream start beside this one: it must
+  // not take the tensor memory that this one still has to allocate
+  pdl_trigger();
+  const uint32_t tmem = ctl.tmem_base;
+  const int nkb = p.red / BK;
+  const int kb0 = (int)((long long)nkb * rank / nrank), kb1 = (int)((long long)nkb * (rank + 1) / nrank);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int xs = 0, fs = 0;
+      uint32_t xp = 0, fp = 0;
+      bool ok = true, any = false;
+      for_each_run(off, ad, p.q.num_seg, m0, m1, [&](int, int, int) { any = true; return false; });
+      for (int kb = kb0; ok && any && kb < kb1; ++kb) {
+        if (!wait_bar(smem_u32(&ctl.xempty[xs]), xp ^ 1u, &ctl.abort_flag, p.status)) break;
+        const uint32_t xb = smem_u32(&ctl.xfull[xs]);
+        mbar_arrive_expect_tx(xb, BM * BK * 2);
+        tma_load_2d(sX + xs * (BM * BK * 2), &tmX, xb, kb * BK, m0);
+        if (++xs == kShrinkX) { xs = 0; xp ^= 1u; }
+        for_each_run(off, ad, p.q.num_seg, m0, m1, [&](int, int, int a) {
+          if (!wait_bar(smem_u32(&ctl.fempty[fs]), fp ^ 1u, &ctl.abort_flag, p.status)) return ok = false;
+          const uint32_t fb = smem_u32(&ctl.ffull[fs]), dst = sF + fs * p.f_bytes;
+          mbar_arrive_expect_tx(fb, p.f_bytes);
+          if (kMN) {
+            for (int c = 0; c < p.r; c += 64) tma_load_2d(dst + c * 128, &tmF, fb, c, a * p.f_rows + kb * BK);
+          } else {
+            tma_load_2d(dst, &tmF, fb, kb * BK, a * p.f_rows);
+          }
+          if (++fs == kShrinkF) { fs = 0; fp ^= 1u; }
+          return true;
+        });
+      }
+    }
+  } else if (warp == 1) {
+    int xs = 0, fs = 0;
+    uint32_t xp = 0, fp = 0;
+    bool ok = true, any = false;
+    for_each_run(off, ad, p.q.num_seg, m0, m1, [&](int, int, int) { any = true; return false; });
+    for (int kb = kb0; ok && any && kb < kb1; ++kb) {
+      ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.xfull[xs]), xp, &ctl.abort_flag, p.status));
+      if (!ok) break;
+      const uint32_t a0 = sX + xs * (BM * BK * 2);
+      for_each_run(off, ad, p.q.num_seg, m0, m1, [&](int lo, int hi, int) {
+        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.ffull[fs]), fp, &ctl.abort_flag, p.status));
+        if (!ok) return false;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t b0 = sF + fs * p.f_bytes;
+          const LaneMask m = lane_mask(lo - m0, hi - m0);
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk)
+            mma_bf16_lanes(tmem, sdesc(a0 + kk * 32, 16, 1024),
+                           kMN ? sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024) : sdesc(b0 + kk * 32, 16, 1024), p.idesc,
+                           kb > kb0 || kk > 0, m);
+          mma_commit(smem_u32(&ctl.fempty[fs]));
+        }
+        __syncwarp();
+        if (++fs == kShrinkF) { fs = 0; fp ^= 1u; }
+        return true;
+      });
+      if (lane == 0) mma_commit(smem_u32(&ctl.xempty[xs]));
+      __syncwarp();
+      if (++xs == kShrinkX) { xs = 0; xp ^= 1u; }
+    }
+    if (lane == 0) mma_commit(smem_u32(&ctl.done));
+    __syncwarp();
+  }
+  __syncwarp();  // the producer's other lanes do not spin beside it
+  // every MMA of this CTA has ended (on an abort: those issued), the x blocks are free
+  const bool fine = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.done), 0, &ctl.abort_flag, p.status));
+  tc_fence_after();
+  if (warp >= 2 && fine) {
+    const int row = (warp & 3) * 32 + lane;
+    for (int c = 0; c < p.rN; c += 16) {
+      uint32_t v[16];
+      asm volatile(
+          "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+          "%15}, [%16];"
+          : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+            "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+          : "r"(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)c));
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[(c + i) * BM + row] = f32(v[i]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_n<1>(tmem, p.tmem_cols);
+  cluster_sync();
+  // this CTA's share of the rows: the slices' sums in order, scaled and split
+  {
+    const int per = BM / nrank, rp = plane_cols(p.r), hc = hidden_cols(p.r);
+    const uint32_t local = smem_u32(acc);
+    for (int i = threadIdx.x; i < per * (rp / 8); i += blockDim.x) {
+      const int row = rank * per + i % per, c = i / per * 8;
+      if (m0 + row >= p.q.T) continue;
+      const int a = ctl.row_ad[row];
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (a >= 0 && c < p.r) {
+        for (int k = 0; k < nrank; ++k) {
+          const uint32_t peer = map_to_rank(local + (uint32_t)(c * BM + row) * 4, k);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] += ld_cluster(peer + j * BM * 4);
+        }
+        const float s = p.scale ? __ldg(p.scale + a) : 1.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= s;
+      }
+      uint4 o[kPlanes];
+      split8(v, o);
+#pragma unroll
+      for (int k = 0; k < kPlanes; ++k)
+        *reinterpret_cast<uint4*>(p.hidden + (size_t)(m0 + row) * hc + k * rp + c) = o[k];
+    }
+  }
+  cluster_sync();  // a peer may still read this CTA's accumulator
+}
+
+// --------------------------------------------------- wide product, whole tiles
+//
+// out[128 rows x BN] = in W^T (kMN: in W) + hidden F, one CTA per SM over the
+// tiles: a TMA warp, an MMA warp, four epilogue warps; two accumulators, so
+// that a tile's epilogue runs beside the next one's MMAs.
+struct WideParams {
+  Reqs q;
+  int red, out_cols, r, rN;
+  int f_rows;          // K-major F: rows of its 2-D view per adapter
+  int n_tiles, tiles;
+  int has_hidden;      // a narrow kernel of the same call wrote hidden
+  uint32_t idesc;
+  int* status;
+};
+
+template <int BN>
+struct WideCfg {
+  static constexpr int STAGES = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
+  static constexpr int B_BYTES = BN * BK * 2;
+  static constexpr int STAGE_BYTES = BM * BK * 2 + B_BYTES;
+  static constexpr int EP_BYTES = 4 * EP_SLOTS * EP_BOX_BYTES;
+  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + EP_BYTES + (2 * kMaxSegments + 4) * 4;
+  static_assert(SMEM <= kSmemMax - 1024, "shared memory budget exceeded");
+};
+
+struct WideCtl {
+  unsigned long long full[8], empty[8], tfull[2], tempty[2], drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+template <int BN, bool kMN>
+__global__ void __launch_bounds__(192, 1) adapter_wide_kernel(const __grid_constant__ CUtensorMap tmX,
+                                                              const __grid_constant__ CUtensorMap tmW,
+                                                              const __grid_constant__ CUtensorMap tmH,
+                                                              const __grid_constant__ CUtensorMap tmF,
+                                                              const __grid_constant__ CUtensorMap tmO,
+                                                              const WideParams p) {
+  using C = WideCfg<BN>;
+  // The narrow kernel of this call waited for everything before it and lets
+  // this one start early; x, W and the request table are older than it, so only
+  // hidden has to be waited for.
+  if (!p.has_hidden) pdl_wait();
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ WideCtl ctl;
+  const uint32_t base = align1k(smem_u32(smem_raw));
+  uint8_t* bytes = smem_raw + (base - smem_u32(smem_raw));
+  int* off = reinterpret_cast<int*>(bytes + (size_t)C::STAGES * C::STAGE_BYTES + C::EP_BYTES);
+  int* ad = off + p.q.num_seg + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  load_requests(p.q, off, ad, p.status);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(smem_u32(&ctl.full[i]), 1);
+      mbar_init(smem_u32(&ctl.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ctl.tfull[i]), 1);
+      mbar_init(smem_u32(&ctl.tempty[i]), 4);
+    }
+    mbar_init(smem_u32(&ctl.drain), 1);
+    ctl.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_tmap(&tmX);
+    prefetch_tmap(&tmW);
+    prefetch_tmap(&tmH);
+    prefetch_tmap(&tmF);
+    prefetch_tmap(&tmO);
+  }
+  if (warp == 1) tmem_alloc_n<1>(smem_u32(&ctl.tmem_base), 2 * BN);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();
+  const uint32_t tmem = ctl.tmem_base;
+  const int nkb = p.red / BK;
+  // blocks of one run: the parts of hidden times F, 64 hidden columns a block.
+  // With all parts in one block (r <= 32) the block's MMA steps walk the parts.
+  const int rp = plane_cols(p.r);
+  const bool one_block = hidden_cols(p.r) <= 64;
+  const int fblk = (p.r + 63) / 64;                       // 64-column blocks of F
+  const int run_blocks = one_block ? 1 : kPlanes * fblk;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int st = 0;
+      uint32_t ph = 0;
+      bool ok = true, waited = !p.has_hidden;
+      auto next = [&]() { if (++st == C::STAGES) { st = 0; ph ^= 1u; } };
+      for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
+        const int m0 = tile / p.n_tiles * BM, n0 = tile % p.n_tiles * BN;
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!(ok = wait_bar(smem_u32(&ctl.empty[st]), ph ^ 1u, &ctl.abort_flag, p.status))) break;
+          const uint32_t fb = smem_u32(&ctl.full[st]), sA = base + st * C::STAGE_BYTES, sB = sA + BM * BK * 2;
+          mbar_arrive_expect_tx(fb, C::STAGE_BYTES);
+          tma_load_2d(sA, &tmX, fb, kb * BK, m0);
+          if (kMN)
+            tma_load_3d(sB, &tmW, fb, 0, kb * BK, n0 / 64);
+          else
+            tma_load_2d(sB, &tmW, fb, kb * BK, n0);
+          next();
+        }
+        if (!ok) break;
+        for_each_run(off, ad, p.q.num_seg, m0, min(p.q.T, m0 + BM), [&](int, int, int a) {
+          if (!waited) {
+            pdl_wait();
+            waited = true;
+          }
+          for (int b = 0; b < run_blocks; ++b) {
+            if (!(ok = wait_bar(smem_u32(&ctl.empty[st]), ph ^ 1u, &ctl.abort_flag, p.status))) return false;
+            const uint32_t fb = smem_u32(&ctl.full[st]), sA = base + st * C::STAGE_BYTES, sB = sA + BM * BK * 2;
+            const int c = b % fblk * 64;  // F columns (ranks) of this block
+            mbar_arrive_expect_tx(fb, C::STAGE_BYTES);
+            tma_load_2d(sA, &tmH, fb, b / fblk * rp + c, m0);
+            if (kMN)
+              tma_load_4d(sB, &tmF, fb, 0, c, n0 / 64, a);
+            else
+              tma_load_2d(sB, &tmF, fb, c, a * p.f_rows + n0);
+            next();
+          }
+          return true;
+        });
+      }
+      if (!waited) pdl_wait();  // the grid may not end before the narrow kernel does
+    }
+  } else if (warp == 1) {
+    int st = 0, local = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    auto next = [&]() { if (++st == C::STAGES) { st = 0; ph ^= 1u; } };
+    for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x, ++local) {
+      const int m0 = tile / p.n_tiles * BM;
+      const int buf = local & 1;
+      ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.tempty[buf]), ((local >> 1) & 1) ^ 1, &ctl.abort_flag, p.status));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + buf * BN;
+      for (int kb = 0; kb < nkb; ++kb) {
+        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.full[st]), ph, &ctl.abort_flag, p.status));
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t a0 = base + st * C::STAGE_BYTES, b0 = a0 + BM * BK * 2;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk)
+            mma_bf16(d, sdesc(a0 + kk * 32, 16, 1024),
+                     kMN ? sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024) : sdesc(b0 + kk * 32, 16, 1024), p.idesc,
+                     kb > 0 || kk > 0);
+          mma_commit(smem_u32(&ctl.empty[st]));
+        }
+        __syncwarp();
+        next();
+      }
+      if (!ok) break;
+      for_each_run(off, ad, p.q.num_seg, m0, min(p.q.T, m0 + BM), [&](int lo, int hi, int) {
+        const LaneMask m = lane_mask(lo - m0, hi - m0);
+        for (int b = 0; b < run_blocks; ++b) {
+          ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.full[st]), ph, &ctl.abort_flag, p.status));
+          if (!ok) return false;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t a0 = base + st * C::STAGE_BYTES, b0 = a0 + BM * BK * 2;
+            const int steps = min(4, (p.r - b % fblk * 64 + 15) / 16);  // 16-wide steps of this block of F
+            for (int pl = 0; pl < (one_block ? kPlanes : 1); ++pl)
+              for (int kk = 0; kk < steps; ++kk)
+                mma_bf16_lanes(d, sdesc(a0 + (pl * rp / 16 + kk) * 32, 16, 1024),
+                               kMN ? sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024) : sdesc(b0 + kk * 32, 16, 1024),
+                               p.idesc, 1u, m);
+            mma_commit(smem_u32(&ctl.empty[st]));
+          }
+          __syncwarp();
+          next();
+        }
+        return true;
+      });
+      if (!ok) break;
+      if (lane == 0) mma_commit(smem_u32(&ctl.tfull[buf]));
+      __syncwarp();
+    }
+    if (!ok) {  // drain MMAs still in flight before TMEM is released
+      if (lane == 0) mma_commit(smem_u32(&ctl.drain));
+      __syncwarp();
+      const unsigned long long t0 = globaltimer();
+      while (!mbar_try_wait(smem_u32(&ctl.drain), 0) && globaltimer() - t0 < TIMEOUT_NS) {
+      }
+    }
+  } else {
+    const int q = warp & 3;
+    EpRing<EP_SLOTS> ring{bytes + (size_t)C::STAGES * C::STAGE_BYTES + (size_t)(warp - 2) * EP_SLOTS * EP_BOX_BYTES, 0, lane};
+    int local = 0;
+    for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, ++local) {
+      const int rb = tile / p.n_tiles * BM + q * 32, n0 = tile % p.n_tiles * BN;
+      const int buf = local & 1;
+      if (!__all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.tfull[buf]), (local >> 1) & 1, &ctl.abort_flag, p.status))) break;
+      tc_fence_after();
+      if (rb < p.q.T) {
+        for (int c = 0; c < BN; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN + c), v);
+          tmem_wait_ld();
+          uint8_t* box = ring.acquire();
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            ring.put(box, i, make_uint4(pack_bf16x2(f32(v[8 * i]), f32(v[8 * i + 1])), pack_bf16x2(f32(v[8 * i + 2]), f32(v[8 * i + 3])),
+                                        pack_bf16x2(f32(v[8 * i + 4]), f32(v[8 * i + 5])), pack_bf16x2(f32(v[8 * i + 6]), f32(v[8 * i + 7]))));
+          ring.issue(box, &tmO, n0 + c, rb);  // rows past the last token are clipped by the map
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl.tempty[buf]));
+    }
+    ring.drain();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_n<1>(tmem, 2 * BN);
+}
+
+// ------------------------------------------------------- adapters' gradients
+//
+// dA_a^T [K, r] = sum over a's rows of x^T u, dB_a [N, r] = sum of dy^T v: a
+// tile is 128 rows of the output (columns of x or dy) times the hidden columns
+// of all parts, over at most part_rows of the adapter's rows; the parts'
+// products are added in the epilogue.  An adapter's rows are those of all its
+// requests in order.  A run's last block may reach into the next request's
+// rows: those are overwritten with zeros in shared memory.
+struct GradParams {
+  Reqs q;
+  int K, N, r;
+  int part_rows;
+  int tiles_a, tiles_b;   // 128-row tiles of dA^T and of dB
+  float* dA;              // [num_adapters, r, K]
+  float* dB;              // [num_adapters, N, r]
+  float* part;            // [parts][r K + N r]
+  int accumulate;
+  uint32_t idesc;
+  int stages;
+  int* status;
+};
+
+constexpr int kGradStagesMax = 6;
+struct GradCtl {
+  unsigned long long full[kGradStagesMax], empty[kGradStagesMax], tfull[2], tempty[2], drain;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// Shared-memory table: rows of each adapter -> first part of each adapter
+// (first[num_adapters] = all parts).
+__device__ __forceinline__ void load_parts(const Reqs& q, const int* off, const int* ad, int part_rows, int* rows, int* first) {
+  for (int a = threadIdx.x; a < q.num_adapters; a += blockDim.x) rows[a] = 0;
+  __syncthreads();
+  for (int s = threadIdx.x; s < q.num_seg; s += blockDim.x)
+    if (ad[s] >= 0 && off[s + 1] > off[s]) atomicAdd(&rows[ad[s]], off[s + 1] - off[s]);
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int carry = 0;
+    for (int b = 0; b < q.num_adapters; b += 32) {
+      const int a = b + lane, n = a < q.num_adapters ? (rows[a] + part_rows - 1) / part_rows : 0;
+      int m = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, m, d);
+        if (lane >= d) m += o;
+      }
+      if (a < q.num_adapters) first[a] = carry + m - n;
+      carry += __shfl_sync(0xffffffffu, m, 31);
+    }
+    if (lane == 0) first[q.num_adapters] = carry;
+  }
+  __syncthreads();
+}
+
+// f(first row, valid rows <= 64) -> bool for the blocks of part `part` of adapter a.
+template <class F>
+__device__ __forceinline__ void for_each_block(const Reqs& q, const int* off, const int* ad, int a, int part, int part_rows, F&& f) {
+  const long long lo = (long long)part * part_rows, hi = lo + part_rows;
+  long long at = 0;  // adapter rows before request s
+  for (int s = 0; s < q.num_seg && at < hi; ++s) {
+    if (ad[s] != a) continue;
+    const int n = off[s + 1] - off[s];
+    if (n <= 0) continue;
+    const int b = (int)max(lo - at, 0ll), e = (int)min(hi - at, (long long)n);
+    for (int t = b; t < e; t += BK)
+      if (!f(off[s] + t, min(BK, e - t))) return;
+    at += n;
+  }
+}
+
+__device__ __forceinline__ int adapter_of_part(const int* first, int num_adapters, int part) {
+  int lo = 0, hi = num_adapters - 1;  // last a with first[a] <= part
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= part) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(192) adapter_grad_kernel(const __grid_constant__ CUtensorMap tmX,
+                                                           const __grid_constant__ CUtensorMap tmU,
+                                                           const __grid_constant__ CUtensorMap tmDy,
+                                                           const __grid_constant__ CUtensorMap tmV,
+                                                           const GradParams p) {
+  pdl_wait();
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ GradCtl ctl;
+  const uint32_t base = align1k(smem_u32(smem_raw));
+  uint8_t* bytes = smem_raw + (base - smem_u32(smem_raw));
+  const int hc = hidden_cols(p.r), rp = plane_cols(p.r);
+  const int nck = (hc + 63) / 64;                    // 64-column chunks of hidden
+  const int stage_bytes = BM * BK * 2 + nck * CHUNK_BYTES;
+  int* off = reinterpret_cast<int*>(bytes + (size_t)p.stages * stage_bytes);
+  int* ad = off + p.q.num_seg + 1;
+  int* rows = ad + p.q.num_seg;
+  int* first = rows + p.q.num_adapters;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int bufs = hc <= 128 ? 2 : 1;
+  const uint32_t cols = hc <= 32 ? 64 : (hc <= 64 ? 128 : 256);
+  load_requests(p.q, off, ad, p.status);
+  load_parts(p.q, off, ad, p.part_rows, rows, first);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(smem_u32(&ctl.full[i]), 1);
+      mbar_init(smem_u32(&ctl.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ctl.tfull[i]), 1);
+      mbar_init(smem_u32(&ctl.tempty[i]), 4);
+    }
+    mbar_init(smem_u32(&ctl.drain), 1);
+    ctl.abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_tmap(&tmX);
+    prefetch_tmap(&tmU);
+    prefetch_tmap(&tmDy);
+    prefetch_tmap(&tmV);
+  }
+  if (warp == 1) tmem_alloc_n<1>(smem_u32(&ctl.tmem_base), cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();
+  const uint32_t tmem = ctl.tmem_base;
+  const int per = p.tiles_a + p.tiles_b;
+  const long long items = (long long)first[p.q.num_adapters] * per;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int st = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (long long it = blockIdx.x; ok && it < items; it += gridDim.x) {
+        const int part = (int)(it / per), mt = (int)(it % per);
+        const int a = adapter_of_part(first, p.q.num_adapters, part);
+        const bool is_a = mt < p.tiles_a;
+        const CUtensorMap* ml = is_a ? &tmX : &tmDy;
+        const CUtensorMap* mr = is_a ? &tmU : &tmV;
+        const int ck = (is_a ? mt : mt - p.tiles_a) * 2;
+        for_each_block(p.q, off, ad, a, part - first[a], p.part_rows, [&](int row, int) {
+          if (!(ok = wait_bar(smem_u32(&ctl.empty[st]), ph ^ 1u, &ctl.abort_flag, p.status))) return false;
+          const uint32_t fb = smem_u32(&ctl.full[st]), sA = base + st * stage_bytes;
+          mbar_arrive_expect_tx(fb, stage_bytes);
+          tma_load_3d(sA, ml, fb, 0, row, ck);
+          tma_load_3d(sA + BM * BK * 2, mr, fb, 0, row, 0);
+          if (++st == p.stages) { st = 0; ph ^= 1u; }
+          return true;
+        });
+      }
+    }
+  } else if (warp == 1) {
+    int st = 0, local = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (long long it = blockIdx.x; ok && it < items; it += gridDim.x, ++local) {
+      const int part = (int)(it / per);
+      const int a = adapter_of_part(first, p.q.num_adapters, part);
+      const int buf = local % bufs, use = local / bufs;
+      ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.tempty[buf]), (use & 1) ^ 1, &ctl.abort_flag, p.status));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + buf * (cols / bufs);
+      uint32_t started = 0;
+      for_each_block(p.q, off, ad, a, part - first[a], p.part_rows, [&](int, int valid) {
+        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.full[st]), ph, &ctl.abort_flag, p.status));
+        if (!ok) return false;
+        const int steps = (valid + 15) / 16;
+        const uint32_t a0 = base + st * stage_bytes, b0 = a0 + BM * BK * 2;
+        if (valid & 15) {  // rows of the last step past the run: zeros in both operands
+          uint8_t* blk = bytes + (size_t)st * stage_bytes;
+          const int nz = (steps * 16 - valid) * 8;
+          for (int c = 0; c < 2 + nck; ++c)
+            for (int i = lane; i < nz; i += 32)
+              *reinterpret_cast<uint4*>(blk + c * CHUNK_BYTES + valid * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+        tc_fence_after();
+        if (lane == 0) {
+          for (int kk = 0; kk < steps; ++kk) {
+            mma_bf16(d, sdesc(a0 + kk * 2048, CHUNK_BYTES, 1024), sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024), p.idesc, started);
+            started = 1;
+          }
+          mma_commit(smem_u32(&ctl.empty[st]));
+        }
+        __syncwarp();
+        if (++st == p.stages) { st = 0; ph ^= 1u; }
+        return true;
+      });
+      if (!ok) break;
+      if (lane == 0) mma_commit(smem_u32(&ctl.tfull[buf]));
+      __syncwarp();
+    }
+    if (!ok) {
+      if (lane == 0) mma_commit(smem_u32(&ctl.drain));
+      __syncwarp();
+      const unsigned long long t0 = globaltimer();
+      while (!mbar_try_wait(smem_u32(&ctl.drain), 0) && globaltimer() - t0 < TIMEOUT_NS) {
+      }
+    }
+  } else {
+    const int q = warp & 3;
+    int local = 0;
+    const size_t part_sz = (size_t)p.r * (p.K + p.N);
+    for (long long it = blockIdx.x; it < items; it += gridDim.x, ++local) {
+      const int part = (int)(it / per), mt = (int)(it % per);
+      const int a = adapter_of_part(first, p.q.num_adapters, part);
+      const bool is_a = mt < p.tiles_a;
+      const int m = (is_a ? mt : mt - p.tiles_a) * BM + q * 32 + lane;
+      const bool direct = first[a + 1] - first[a] == 1 && !p.accumulate;
+      const int buf = local % bufs, use = local / bufs;
+      if (!__all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.tfull[buf]), use & 1, &ctl.abort_flag, p.status))) break;
+      tc_fence_after();
+      const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * (cols / bufs));
+      float* dst;
+      if (is_a)
+        dst = (direct ? p.dA + (size_t)a * p.r * p.K : p.part + (size_t)part * part_sz) + m;
+      else
+        dst = (direct ? p.dB + (size_t)a * p.N * p.r : p.part + (size_t)part * part_sz + (size_t)p.r * p.K) + (size_t)m * p.r;
+      for (int c = 0; c < p.r; c += 8) {
+        float s[8];
+#pragma unroll
+        for (int pl = 0; pl < kPlanes; ++pl) {
+          uint32_t v[8];
+          asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                       : "r"(d + (uint32_t)(pl * rp + c)));
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[i] = pl == 0 ? f32(v[i]) : s[i] + f32(v[i]);
+        }
+        if (is_a) {
+          if (m < p.K) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[(size_t)(c + i) * p.K] = s[i];
+          }
+        } else if (m < p.N) {
+          *reinterpret_cast<float4*>(dst + c) = make_float4(s[0], s[1], s[2], s[3]);
+          *reinterpret_cast<float4*>(dst + c + 4) = make_float4(s[4], s[5], s[6], s[7]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl.tempty[buf]));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_n<1>(tmem, cols);
+}
+
+// dA, dB of the adapters whose rows were not one part: the parts' sums in
+// order, zero for an adapter without rows, added to the old values when
+// accumulating.
+__global__ void __launch_bounds__(256) adapter_grad_sum_kernel(const GradParams p) {
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ int tab[];
+  int* off = tab;
+  int* ad = off + p.q.num_seg + 1;
+  int* rows = ad + p.q.num_seg;
+  int* first = rows + p.q.num_adapters;
+  load_requests(p.q, off, ad, p.status);
+  load_parts(p.q, off, ad, p.part_rows, rows, first);
+  const int a = blockIdx.y;
+  const int n = first[a + 1] - first[a];
+  if (n == 1 && !p.accumulate) return;
+  const size_t na = (size_t)p.r * p.K, sz = na + (size_t)p.r * p.N;
+  const float4* src = reinterpret_cast<const float4*>(p.part + (size_t)first[a] * sz);
+  for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < sz / 4; i += (size_t)gridDim.x * blockDim.x) {
+    float4* dst = reinterpret_cast<float4*>(4 * i < na ? p.dA + (size_t)a * na + 4 * i : p.dB + (size_t)a * (sz - na) + (4 * i - na));
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float4 w = __ldcg(src + (size_t)k * (sz / 4) + i);
+      v = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+    }
+    if (p.accumulate) {
+      const float4 o = *dst;
+      v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+    }
+    *dst = v;
+  }
+}
+
+// --------------------------------------------------------------- host side
+
+// bf16 map of rank <= 4: dims and box innermost first, pitches (elements) of dims 1..
+int make_map(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims, const uint64_t* pitch, const uint32_t* box,
+             CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t d[4], s[3];
+  cuuint32_t b[4], es[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i] > 0 ? dims[i] : 1;
+    b[i] = box[i];
+    if (i > 0) s[i - 1] = pitch[i - 1] * 2;
+  }
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), d, s, b, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for an adapter operand of %llu columns", (int)r, (unsigned long long)dims[0]);
+  return MOE_OK;
+}
+int map2(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint64_t pitch, uint32_t bi, uint32_t bo,
+         CUtensorMapSwizzle swz = CU_TENSOR_MAP_SWIZZLE_128B) {
+  const uint64_t d[2] = {inner, outer}, s[1] = {pitch};
+  const uint32_t b[2] = {bi, bo};
+  return make_map(m, ptr, 2, d, s, b, swz);
+}
+// MN-major operand: [rows, cols] as {64 columns, rows, chunks of 64 columns}
+int map_mn(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t pitch, uint32_t chunks) {
+  const uint64_t d[3] = {cols < 64 ? cols : 64, rows, (cols + 63) / 64}, s[2] = {pitch, 64};
+  const uint32_t b[3] = {64, 64, chunks};
+  return make_map(m, ptr, 3, d, s, b);
+}
+
+int set_smem(const void* kern, bool* done, const char* fn) {
+  const int dev = current_device();
+  if (dev < 0) return fail(MOE_ERR_CUDA, "%s: no current CUDA device", fn);
+  if (done[dev]) return MOE_OK;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax - 2048);
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+  done[dev] = true;
+  return MOE_OK;
+}
+
+template <typename... KArgs, typename... Args>
+int launch_adapter(const char* fn, void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, int cluster_x,
+                   cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = threads;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster_x;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster_x > 0 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+  return check_launch(fn);
+}
+
+// hidden = parts of scale F . in.  kMN false: F = A [nA, r, red]; true: F = B^T, B [nA, red, r].
+template <bool kMN>
+int run_shrink(const char* fn, const Reqs& q, const void* in, long long ld, const void* F, const float* scale, int red, int r,
+               void* hidden, cudaStream_t s) {
+  static bool attr[64] = {};
+  auto kern = adapter_shrink_kernel<kMN>;
+  if (int rc = set_smem(reinterpret_cast<const void*>(kern), attr, fn)) return rc;
+  const int tiles = (q.T + BM - 1) / BM, nkb = red / BK;
+  int cs = 1;
+  while (cs < 8 && cs * 2 <= nkb && tiles * cs * 2 <= 304) cs *= 2;
+  CUtensorMap tx, tf;
+  if (int rc = map2(&tx, in, red, q.T, ld, BK, BM)) return rc;
+  if (kMN) {
+    if (int rc = map2(&tf, F, r, (uint64_t)q.num_adapters * red, r, 64, 64)) return rc;
+  } else {
+    if (int rc = map2(&tf, F, red, (uint64_t)q.num_adapters * r, red, BK, r)) return rc;
+  }
+  ShrinkParams p{};
+  p.q = q;
+  p.red = red;
+  p.r = r;
+  p.rN = round_up(r, 16);
+  p.f_bytes = kMN ? (r + 63) / 64 * CHUNK_BYTES : r * 128;
+  p.f_rows = kMN ? red : r;
+  p.scale = scale;
+  p.hidden = static_cast<__nv_bfloat16*>(hidden);
+  p.idesc = make_idesc(p.rN, BM, false, kMN);
+  p.tmem_cols = p.rN <= 32 ? 32 : (p.rN <= 64 ? 64 : 128);
+  p.status = status_word();
+  // one 16-row block of slack: an F block of r rows is read as rN
+  const size_t smem = 1024 + kShrinkX * (BM * BK * 2) + (size_t)kShrinkF * p.f_bytes + 2048 + (2 * q.num_seg + 2) * 4;
+  return launch_adapter(fn, kern, dim3(cs, tiles), 192, smem, cs, s, tx, tf, p);
+}
+
+template <int BN, bool kMN>
+int run_wide_bn(const char* fn, const Reqs& q, const void* in, long long ld, const void* W, const void* hidden, const void* F,
+                int red, int out_cols, int r, void* out, long long ldo, bool has_hidden, cudaStream_t s) {
+  using C = WideCfg<BN>;
+  static bool attr[64] = {};
+  auto kern = adapter_wide_kernel<BN, kMN>;
+  if (int rc = set_smem(reinterpret_cast<const void*>(kern), attr, fn)) return rc;
+  const int sms = sm_count();
+  if (sms <= 0) return fail(MOE_ERR_CUDA, "%s: cannot query the SM count", fn);
+  CUtensorMap tx, tw, th, tf, to;
+  if (int rc = map2(&tx, in, red, q.T, ld, BK, BM)) return rc;
+  const int hc = hidden_cols(r);
+  if (has_hidden) {
+    if (int rc = map2(&th, hidden, hc, q.T, hc, 64, BM)) return rc;
+  } else {
+    th = tx;
+  }
+  if (kMN) {
+    if (int rc = map_mn(&tw, W, out_cols, red, out_cols, BN / 64)) return rc;
+    const uint64_t d[4] = {64, (uint64_t)r, (uint64_t)out_cols / 64, (uint64_t)q.num_adapters};
+    const uint64_t pt[3] = {(uint64_t)out_cols, 64, (uint64_t)r * out_cols};
+    const uint32_t b[4] = {64, 64, BN / 64, 1};
+    if (has_hidden) {
+      if (int rc = make_map(&tf, F, 4, d, pt, b)) return rc;
+    } else {
+      tf = tw;
+    }
+  } else {
+    if (int rc = map2(&tw, W, red, out_cols, red, BK, BN)) return rc;
+    if (has_hidden) {
+      if (int rc = map2(&tf, F, r, (uint64_t)q.num_adapters * out_cols, r, 64, BN)) return rc;
+    } else {
+      tf = tw;
+    }
+  }
+  if (int rc = map2(&to, out, out_cols, q.T, ldo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) return rc;
+  WideParams p{};
+  p.q = q;
+  p.red = red;
+  p.out_cols = out_cols;
+  p.r = r;
+  p.rN = round_up(r, 16);
+  p.f_rows = out_cols;
+  p.n_tiles = out_cols / BN;
+  p.tiles = (q.T + BM - 1) / BM * p.n_tiles;
+  p.has_hidden = has_hidden;
+  p.idesc = make_idesc(BN, BM, false, kMN);
+  p.status = status_word();
+  return launch_adapter(fn, kern, dim3(p.tiles < sms ? p.tiles : sms), 192, C::SMEM, 0, s, tx, tw, th, tf, to, p);
+}
+
+template <bool kMN>
+int run_wide(const char* fn, const Reqs& q, const void* in, long long ld, const void* W, const void* hidden, const void* F,
+             int red, int out_cols, int r, void* out, long long ldo, bool has_hidden, cudaStream_t s) {
+  // the widest tile that divides the columns and still gives every SM one
+  const int sms = sm_count() > 0 ? sm_count() : 148, rows = (q.T + BM - 1) / BM;
+  if (out_cols % 256 == 0 && rows * (out_cols / 256) >= sms)
+    return run_wide_bn<256, kMN>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, s);
+  if (out_cols % 128 == 0 && rows * (out_cols / 128) >= sms)
+    return run_wide_bn<128, kMN>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, s);
+  return run_wide_bn<64, kMN>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, s);
+}
+
+int check_adapter(const char* fn, const Reqs& q, int K, int N, int r, long long ldx, long long ldy) {
+  if (q.T < 0 || K <= 0 || N <= 0 || r <= 0 || q.num_adapters <= 0 || q.num_seg < 0)
+    return fail(MOE_ERR_INVALID_ARG, "%s: need T>=0, K>0, N>0, r>0, num_adapters>0, num_seg>=0", fn);
+  if (K % 64 || N % 64 || r % 8 || r > kMaxRank || q.num_adapters > kMaxAdapters || q.num_seg > kMaxSegments ||
+      (long long)q.num_adapters * (N > r ? N : r) >= (1ll << 31))
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE,
+                "%s: need K%%64==0, N%%64==0, r%%8==0, r<=%d, num_adapters<=%d, num_seg<=%d (K=%d N=%d r=%d)", fn, kMaxRank,
+                kMaxAdapters, kMaxSegments, K, N, r);
+  if (ldx < K || ldy < N || ldx % 8 || ldy % 8 || ldx >= (1ll << 31) || ldy >= (1ll << 31))
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: row strides must be multiples of 8 and at least the row length", fn);
+  if (q.num_seg > 0 && (!q.offsets || !q.adapter)) return fail(MOE_ERR_INVALID_ARG, "%s: NULL request table", fn);
+  return MOE_OK;
+}
+
+size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
+
+// Rows of one part of an adapter's gradient sum.
+constexpr int kPartRows = 512;
+
+struct BwdLayout {
+  size_t u, part, total;
+};
+BwdLayout bwd_layout(int T, int K, int N, int r, int num_seg) {
+  BwdLayout L;
+  // an adapter's last part may be short: at most one a request more than whole parts
+  const size_t parts = (size_t)T / kPartRows + (size_t)num_seg;
+  size_t at = 0;
+  L.u = at; at += align256((size_t)T * hidden_cols(r) * 2);
+  L.part = at; at += align256(parts * r * (size_t)(K + N) * sizeof(float));
+  L.total = at > 256 ? at : 256;
+  return L;
+}
+
+}  // namespace
+}  // namespace tc
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::tc;
+
+extern "C" {
+
+size_t moe_adapter_hidden_size(int T, int r) {
+  if (T < 0 || r <= 0 || r > kMaxRank) return 0;
+  const size_t n = align256((size_t)T * hidden_cols(r) * 2);
+  return n > 0 ? n : 256;
+}
+
+size_t moe_adapter_linear_bwd_workspace_size(int T, int K, int N, int r, int num_seg) {
+  if (T < 0 || K <= 0 || N <= 0 || r <= 0 || r > kMaxRank || num_seg < 0) return 0;
+  return bwd_layout(T, K, N, r, num_seg).total;
+}
+
+int moe_adapter_linear(const void* x, long long ldx, const void* W, const void* A, const void* B, const float* scale,
+                       int num_seg, const int32_t* seg_offsets, const int32_t* seg_adapter, int T, int K, int N, int r,
+                       int num_adapters, void* hidden, size_t hidden_bytes, void* y, long long ldy, void* stream) {
+  clear_error();
+  const char* fn = "moe_adapter_linear";
+  const Reqs q{T, num_seg, num_adapters, seg_offsets, seg_adapter};
+  if (int rc = check_adapter(fn, q, K, N, r, ldx, ldy)) return rc;
+  if (T == 0) return MOE_OK;
+  if (!x || !W || !A || !B || !hidden || !y) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer argument", fn);
+  if (!aligned16(x) || !aligned16(W) || !aligned16(A) || !aligned16(B) || !aligned16(hidden) || !aligned16(y))
+    return fail(MOE_ERR_ALIGNMENT, "%s: tensors must be 16-byte aligned", fn);
+  if (hidden_bytes < moe_adapter_hidden_size(T, r))
+    return fail(MOE_ERR_WORKSPACE, "%s: hidden %zu < %zu bytes", fn, hidden_bytes, moe_adapter_hidden_size(T, r));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (num_seg > 0)
+    if (int rc = run_shrink<false>(fn, q, x, ldx, A, scale, K, r, hidden, s)) return rc;
+  return run_wide<false>(fn, q, x, ldx, W, hidden, B, K, N, r, y, ldy, num_seg > 0, s);
+}
+
+int moe_adapter_linear_bwd(const void* dy, long long lddy, const void* x, long long ldx, const void* W, const void* A,
+                           const void* B, const float* scale, const void* hidden, size_t hidden_bytes, int num_seg,
+                           const int32_t* seg_offsets, const int32_t* seg_adapter, int T, int K, int N, int r,
+                           int num_adapters, void* dx, long long lddx, float* dA, float* dB, int accumulate, void* ws,
+                           size_t ws_bytes, void* stream) {
+  clear_error();
+  const char* fn = "moe_adapter_linear_bwd";
+  const Reqs q{T, num_seg, num_adapters, seg_offsets, seg_adapter};
+  if (int rc = check_adapter(fn, q, K, N, r, ldx, lddy)) return rc;
+  if (lddx < K || lddx % 8 || lddx >= (1ll << 31))
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: row strides must be multiples of 8 and at least the row length", fn);
+  if (!dA || !dB || !ws || (T > 0 && (!dy || !x || !W || !A || !B || !hidden || !dx)))
+    return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer argument", fn);
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(W) || !aligned16(A) || !aligned16(B) || !aligned16(hidden) ||
+      !aligned16(dx) || !aligned16(dA) || !aligned16(dB) || !aligned16(ws))
+    return fail(MOE_ERR_ALIGNMENT, "%s: tensors must be 16-byte aligned", fn);
+  if (T > 0 && hidden_bytes < moe_adapter_hidden_size(T, r))
+    return fail(MOE_ERR_WORKSPACE, "%s: hidden %zu < %zu bytes", fn, hidden_bytes, moe_adapter_hidden_size(T, r));
+  const BwdLayout L = bwd_layout(T, K, N, r, num_seg);
+  if (ws_bytes < L.total) return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, L.total);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0 || num_seg == 0) {
+    if (!accumulate) {
+      cudaError_t e = cudaMemsetAsync(dA, 0, sizeof(float) * (size_t)num_adapters * r * K, s);
+      if (e == cudaSuccess) e = cudaMemsetAsync(dB, 0, sizeof(float) * (size_t)num_adapters * r * N, s);
+      if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    }
+    if (T == 0) return MOE_OK;
+    return run_wide<true>(fn, q, dy, lddy, W, nullptr, A, N, K, r, dx, lddx, false, s);
+  }
+  char* base = static_cast<char*>(ws);
+  void* u = base + L.u;
+  if (int rc = run_shrink<true>(fn, q, dy, lddy, B, scale, N, r, u, s)) return rc;
+  if (int rc = run_wide<true>(fn, q, dy, lddy, W, u, A, N, K, r, dx, lddx, true, s)) return rc;
+
+  GradParams p{};
+  p.q = q;
+  p.K = K;
+  p.N = N;
+  p.r = r;
+  p.part_rows = kPartRows;
+  p.tiles_a = (K + BM - 1) / BM;
+  p.tiles_b = (N + BM - 1) / BM;
+  p.dA = dA;
+  p.dB = dB;
+  p.part = reinterpret_cast<float*>(base + L.part);
+  p.accumulate = accumulate;
+  const int hc = hidden_cols(r), nck = (hc + 63) / 64;
+  p.idesc = make_idesc(hc, BM, true, true);
+  p.stages = nck == 1 ? 4 : (nck == 2 ? 3 : 4);
+  p.status = status_word();
+  static bool attr[64] = {};
+  if (int rc = set_smem(reinterpret_cast<const void*>(adapter_grad_kernel), attr, fn)) return rc;
+  CUtensorMap tx, tu, td, tv;
+  if (int rc = map_mn(&tx, x, K, T, ldx, 2)) return rc;
+  if (int rc = map_mn(&tu, u, hc, T, hc, nck)) return rc;
+  if (int rc = map_mn(&td, dy, N, T, lddy, 2)) return rc;
+  if (int rc = map_mn(&tv, hidden, hc, T, hc, nck)) return rc;
+  const size_t table = sizeof(int) * (size_t)(2 * num_seg + 2 + 2 * num_adapters + 2);
+  const size_t smem = 1024 + (size_t)p.stages * (BM * BK * 2 + nck * CHUNK_BYTES) + table;
+  const int per_sm = nck <= 2 ? 2 : 1;
+  const long long most = ((long long)T / kPartRows + num_seg) * (p.tiles_a + p.tiles_b);
+  const int sms = sm_count() > 0 ? sm_count() : 148;
+  const int grid = (int)(most < (long long)sms * per_sm ? most : (long long)sms * per_sm);
+  if (int rc = launch_adapter(fn, adapter_grad_kernel, dim3(grid), 192, smem, 0, s, tx, tu, td, tv, p)) return rc;
+  const size_t vec = (size_t)r * (K + N) / 4;
+  const int gx = (int)((vec + 255) / 256 < 64 ? (vec + 255) / 256 : 64);
+  return launch_adapter(fn, adapter_grad_sum_kernel, dim3(gx, num_adapters), 256, table, 0, s, p);
+}
+
+}  // extern "C"

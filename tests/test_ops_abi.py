@@ -69,3 +69,39 @@ def test_dropout(L):
     assert L.moe_combine_dropout_bwd(P, P, P, None, 4, 64, 2, 0.1, P, P, P, None) == INVALID
     assert L.moe_combine_dropout_bwd(P, P, P, P, 4, 64, 2, 0.1, P, P + 4, P, None) == ALIGN
     assert L.moe_combine_dropout_bwd(P, P, P, P, 0, 64, 2, 0.1, P, P, P, None) == OK
+
+
+def fwd(L, T=16, K=64, N=64, r=8, nA=2, S=1, off=P, wh=P, ldx=64, ldy=64, x=P, W=P, A=P, B=P, hid=P, hb=1 << 20, y=P):
+    return L.moe_adapter_linear(x, ldx, W, A, B, None, S, off, wh, T, K, N, r, nA, hid, hb, y, ldy, None)
+
+
+def bwd(L, T=16, K=64, N=64, r=8, nA=2, S=1, off=P, wh=P, lddy=64, ldx=64, lddx=64, dy=P, x=P, W=P, A=P, B=P, hid=P,
+        hb=1 << 20, dx=P, dA=P, dB=P, ws=P, wsb=1 << 24):
+    return L.moe_adapter_linear_bwd(dy, lddy, x, ldx, W, A, B, None, hid, hb, S, off, wh, T, K, N, r, nA, dx, lddx, dA, dB,
+                                    0, ws, wsb, None)
+
+
+@pytest.mark.parametrize("call", [fwd, bwd])
+def test_adapter(L, call):
+    for kw in (dict(T=-1), dict(K=0), dict(N=-64), dict(r=0), dict(nA=0), dict(S=-1), dict(off=None), dict(wh=None)):
+        assert call(L, **kw) == INVALID, kw
+    for kw in (dict(K=96, ldx=96), dict(N=100, ldy=104) if call is fwd else dict(N=100, lddy=104), dict(r=12), dict(r=136),
+               dict(nA=1025), dict(S=1025), dict(ldx=56), dict(ldx=68), dict(ldx=1 << 32)):
+        assert call(L, **kw) == SHAPE, kw
+    for name in ("x", "W", "A", "B", "hid") + (("y",) if call is fwd else ("dy", "dx", "dA", "dB", "ws")):
+        assert call(L, **{name: None}) == INVALID, name
+        assert call(L, **{name: P + 8}) == ALIGN, name
+    assert call(L, hb=64) == WS and "hidden" in L.moe_last_error_string().decode()
+    if call is fwd:
+        assert fwd(L, ldy=32) == SHAPE and fwd(L, ldy=65) == SHAPE
+        assert fwd(L, T=0) == OK
+    else:
+        assert bwd(L, lddx=56) == SHAPE and bwd(L, lddx=68) == SHAPE and bwd(L, lddy=8) == SHAPE
+        assert bwd(L, wsb=128) == WS and "workspace" in L.moe_last_error_string().decode()
+
+
+def test_adapter_sizes(L):
+    assert m.moe_adapter_hidden_size(8192, 16) >= 8192 * 2 * 16 * 2
+    assert m.moe_adapter_hidden_size(0, 16) > 0 and m.moe_adapter_hidden_size(4, 256) == 0
+    assert m.moe_adapter_linear_bwd_workspace_size(8192, 2048, 2048, 16, 8) > 0
+    assert m.moe_adapter_linear_bwd_workspace_size(-1, 2048, 2048, 16, 8) == 0
