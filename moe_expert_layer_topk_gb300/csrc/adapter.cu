@@ -8,9 +8,11 @@
 // Rows of requests without an adapter leave the second terms out.
 //
 // Two products per direction.  The narrow one (v or u, r <= 128 columns,
-// bound by reading x or dy) writes its fp32 result as kPlanes bf16 parts whose
-// sum has 16 bits, so the wide products that take it stay on the tensor cores
-// without losing what the first one computed.  The wide one appends the
+// bound by reading x or dy) writes its fp32 result as three bf16 parts whose
+// sum is that value (8 bits each), so the products that take it stay on the
+// tensor cores without losing what the first one computed: the gradients of
+// A and B, kept in fp32, take all three, the wide product, rounded to bf16 at
+// its end, the first two (16 bits).  The wide one appends the
 // adapter to the shared projection's reduction: after the W blocks, the same
 // accumulator tile takes v_t's parts times B_a for every run of rows with one
 // adapter, with the tile's other rows switched off by the MMA's lane mask
@@ -25,17 +27,21 @@ namespace moe {
 namespace tc {
 namespace {
 
-constexpr int kPlanes = 2;        // bf16 parts of v, u
+constexpr int kPlanes = 3;        // bf16 parts of v, u
+constexpr int kWidePlanes = 2;    // of them in the wide product
 constexpr int kMaxRank = 128;
 constexpr int kMaxAdapters = 1024;
 
 __host__ __device__ constexpr int round_up(int v, int to) { return (v + to - 1) / to * to; }
-// Columns of one part in the hidden tensor: whole 16-wide MMA steps when all
-// parts fit one 64-column block, else whole 64-column blocks.
+// Columns of one part in the hidden tensor: whole 16-wide MMA steps when the
+// wide product's parts fit one 64-column block, else whole 64-column blocks.
 __host__ __device__ constexpr int plane_cols(int r) {
-  return kPlanes * round_up(r, 16) <= 64 ? round_up(r, 16) : round_up(r, 64);
+  return kWidePlanes * round_up(r, 16) <= 64 ? round_up(r, 16) : round_up(r, 64);
 }
+// Columns of all parts, and of a row of the hidden tensor (whole 64-column
+// blocks; what pads a row is never used).
 __host__ __device__ constexpr int hidden_cols(int r) { return kPlanes * plane_cols(r); }
+__host__ __device__ constexpr int hidden_pitch(int r) { return round_up(hidden_cols(r), 64); }
 
 // ------------------------------------------------------------ request table
 
@@ -348,7 +354,7 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
   cluster_sync();
   // this CTA's share of the rows: the slices' sums in order, scaled and split
   {
-    const int per = BM / nrank, rp = plane_cols(p.r), hc = hidden_cols(p.r);
+    const int per = BM / nrank, rp = plane_cols(p.r), hp = hidden_pitch(p.r);
     const uint32_t local = smem_u32(acc);
     for (int i = threadIdx.x; i < per * (rp / 8); i += blockDim.x) {
       const int row = rank * per + i % per, c = i / per * 8;
@@ -369,7 +375,7 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
       split8(v, o);
 #pragma unroll
       for (int k = 0; k < kPlanes; ++k)
-        *reinterpret_cast<uint4*>(p.hidden + (size_t)(m0 + row) * hc + k * rp + c) = o[k];
+        *reinterpret_cast<uint4*>(p.hidden + (size_t)(m0 + row) * hp + k * rp + c) = o[k];
     }
   }
   cluster_sync();  // a peer may still read this CTA's accumulator
@@ -451,12 +457,12 @@ __global__ void __launch_bounds__(192, 1) adapter_wide_kernel(const __grid_const
   pdl_trigger();
   const uint32_t tmem = ctl.tmem_base;
   const int nkb = p.red / BK;
-  // blocks of one run: the parts of hidden times F, 64 hidden columns a block.
-  // With all parts in one block (r <= 32) the block's MMA steps walk the parts.
+  // blocks of one run: two parts of hidden times F, 64 hidden columns a block.
+  // With both in one block (r <= 32) the block's MMA steps walk the parts.
   const int rp = plane_cols(p.r);
-  const bool one_block = hidden_cols(p.r) <= 64;
+  const bool one_block = kWidePlanes * rp <= 64;
   const int fblk = (p.r + 63) / 64;                       // 64-column blocks of F
-  const int run_blocks = one_block ? 1 : kPlanes * fblk;
+  const int run_blocks = one_block ? 1 : kWidePlanes * fblk;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -538,7 +544,7 @@ __global__ void __launch_bounds__(192, 1) adapter_wide_kernel(const __grid_const
           if (lane == 0) {
             const uint32_t a0 = base + st * C::STAGE_BYTES, b0 = a0 + BM * BK * 2;
             const int steps = min(4, (p.r - b % fblk * 64 + 15) / 16);  // 16-wide steps of this block of F
-            for (int pl = 0; pl < (one_block ? kPlanes : 1); ++pl)
+            for (int pl = 0; pl < (one_block ? kWidePlanes : 1); ++pl)
               for (int kk = 0; kk < steps; ++kk)
                 mma_bf16_lanes(d, sdesc(a0 + (pl * rp / 16 + kk) * 32, 16, 1024),
                                kMN ? sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024) : sdesc(b0 + kk * 32, 16, 1024),
@@ -618,6 +624,11 @@ struct GradParams {
 };
 
 constexpr int kGradStagesMax = 6;
+// two accumulators up to 96 hidden columns, one beyond
+__host__ __device__ constexpr uint32_t grad_tmem_cols(int r) {
+  const int hc = hidden_cols(r);
+  return hc <= 64 ? 128 : (hc <= 192 ? 256 : 512);
+}
 struct GradCtl {
   unsigned long long full[kGradStagesMax], empty[kGradStagesMax], tfull[2], tempty[2], drain;
   uint32_t tmem_base;
@@ -687,15 +698,16 @@ __global__ void __launch_bounds__(192) adapter_grad_kernel(const __grid_constant
   const uint32_t base = align1k(smem_u32(smem_raw));
   uint8_t* bytes = smem_raw + (base - smem_u32(smem_raw));
   const int hc = hidden_cols(p.r), rp = plane_cols(p.r);
-  const int nck = (hc + 63) / 64;                    // 64-column chunks of hidden
+  const int nck = hidden_pitch(p.r) / 64;            // 64-column chunks of hidden
+  const int nmma = hc > 256 ? 2 : 1;                 // MMAs (column halves) of a step
   const int stage_bytes = BM * BK * 2 + nck * CHUNK_BYTES;
   int* off = reinterpret_cast<int*>(bytes + (size_t)p.stages * stage_bytes);
   int* ad = off + p.q.num_seg + 1;
   int* rows = ad + p.q.num_seg;
   int* first = rows + p.q.num_adapters;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bufs = hc <= 128 ? 2 : 1;
-  const uint32_t cols = hc <= 32 ? 64 : (hc <= 64 ? 128 : 256);
+  const int bufs = hc <= 96 ? 2 : 1;
+  const uint32_t cols = grad_tmem_cols(p.r);
   load_requests(p.q, off, ad, p.status);
   load_parts(p.q, off, ad, p.part_rows, rows, first);
   if (threadIdx.x == 0) {
@@ -777,7 +789,9 @@ __global__ void __launch_bounds__(192) adapter_grad_kernel(const __grid_constant
         tc_fence_after();
         if (lane == 0) {
           for (int kk = 0; kk < steps; ++kk) {
-            mma_bf16(d, sdesc(a0 + kk * 2048, CHUNK_BYTES, 1024), sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024), p.idesc, started);
+            for (int h = 0; h < nmma; ++h)
+              mma_bf16(d + h * (hc / 2), sdesc(a0 + kk * 2048, CHUNK_BYTES, 1024),
+                       sdesc(b0 + h * (nck / 2 * CHUNK_BYTES) + kk * 2048, CHUNK_BYTES, 1024), p.idesc, started);
             started = 1;
           }
           mma_commit(smem_u32(&ctl.empty[st]));
@@ -993,9 +1007,9 @@ int run_wide_bn(const char* fn, const Reqs& q, const void* in, long long ld, con
   if (sms <= 0) return fail(MOE_ERR_CUDA, "%s: cannot query the SM count", fn);
   CUtensorMap tx, tw, th, tf, to;
   if (int rc = map2(&tx, in, red, q.T, ld, BK, BM)) return rc;
-  const int hc = hidden_cols(r);
+  const int hp = hidden_pitch(r);
   if (has_hidden) {
-    if (int rc = map2(&th, hidden, hc, q.T, hc, 64, BM)) return rc;
+    if (int rc = map2(&th, hidden, hp, q.T, hp, 64, BM)) return rc;
   } else {
     th = tx;
   }
@@ -1072,7 +1086,7 @@ BwdLayout bwd_layout(int T, int K, int N, int r, int num_seg) {
   // an adapter's last part may be short: at most one a request more than whole parts
   const size_t parts = (size_t)T / kPartRows + (size_t)num_seg;
   size_t at = 0;
-  L.u = at; at += align256((size_t)T * hidden_cols(r) * 2);
+  L.u = at; at += align256((size_t)T * hidden_pitch(r) * 2);
   L.part = at; at += align256(parts * r * (size_t)(K + N) * sizeof(float));
   L.total = at > 256 ? at : 256;
   return L;
@@ -1089,7 +1103,7 @@ extern "C" {
 
 size_t moe_adapter_hidden_size(int T, int r) {
   if (T < 0 || r <= 0 || r > kMaxRank) return 0;
-  const size_t n = align256((size_t)T * hidden_cols(r) * 2);
+  const size_t n = align256((size_t)T * hidden_pitch(r) * 2);
   return n > 0 ? n : 256;
 }
 
@@ -1164,17 +1178,17 @@ int moe_adapter_linear_bwd(const void* dy, long long lddy, const void* x, long l
   p.dB = dB;
   p.part = reinterpret_cast<float*>(base + L.part);
   p.accumulate = accumulate;
-  const int hc = hidden_cols(r), nck = (hc + 63) / 64;
-  p.idesc = make_idesc(hc, BM, true, true);
-  p.stages = nck == 1 ? 4 : (nck == 2 ? 3 : 4);
+  const int hp = hidden_pitch(r), hc = hidden_cols(r), nck = hp / 64;
+  p.idesc = make_idesc(hc > 256 ? hc / 2 : hc, BM, true, true);
+  p.stages = nck == 1 ? 4 : (nck == 2 ? 3 : (nck == 3 ? 5 : 3));
   p.status = status_word();
   static bool attr[64] = {};
   if (int rc = set_smem(reinterpret_cast<const void*>(adapter_grad_kernel), attr, fn)) return rc;
   CUtensorMap tx, tu, td, tv;
   if (int rc = map_mn(&tx, x, K, T, ldx, 2)) return rc;
-  if (int rc = map_mn(&tu, u, hc, T, hc, nck)) return rc;
+  if (int rc = map_mn(&tu, u, hp, T, hp, nck)) return rc;
   if (int rc = map_mn(&td, dy, N, T, lddy, 2)) return rc;
-  if (int rc = map_mn(&tv, hidden, hc, T, hc, nck)) return rc;
+  if (int rc = map_mn(&tv, hidden, hp, T, hp, nck)) return rc;
   const size_t table = sizeof(int) * (size_t)(2 * num_seg + 2 + 2 * num_adapters + 2);
   const size_t smem = 1024 + (size_t)p.stages * (BM * BK * 2 + nck * CHUNK_BYTES) + table;
   const int per_sm = nck <= 2 ? 2 : 1;
