@@ -205,13 +205,14 @@ struct ShrinkParams {
   int r, rN;            // rank, MMA columns (rank up to a multiple of 16)
   int f_bytes;          // shared-memory bytes of one F block
   int f_rows;           // rows of F's 2-D view per adapter
+  int f_stages;         // blocks of F in flight
   const float* scale;   // [num_adapters] or null
   __nv_bfloat16* hidden;
   uint32_t idesc;
   uint32_t tmem_cols;
   int* status;
 };
-constexpr int kShrinkX = 4, kShrinkF = 4;  // blocks of x and of F in flight
+constexpr int kShrinkX = 4, kShrinkF = 16;  // blocks of x in flight, of F at most
 
 struct ShrinkCtl {
   unsigned long long xfull[kShrinkX], xempty[kShrinkX], ffull[kShrinkF], fempty[kShrinkF], done;
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
   uint8_t* bytes = smem_raw + (base - smem_u32(smem_raw));
   const uint32_t sX = base, sF = base + kShrinkX * (BM * BK * 2);
   float* acc = reinterpret_cast<float*>(bytes);  // [rN][BM], over the x blocks once they are consumed
-  int* off = reinterpret_cast<int*>(bytes + kShrinkX * (BM * BK * 2) + kShrinkF * p.f_bytes);
+  int* off = reinterpret_cast<int*>(bytes + kShrinkX * (BM * BK * 2) + p.f_stages * p.f_bytes);
   int* ad = off + p.q.num_seg + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nrank = gridDim.x, rank = blockIdx.x;
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
       mbar_init(smem_u32(&ctl.xfull[i]), 1);
       mbar_init(smem_u32(&ctl.xempty[i]), 1);
     }
-    for (int i = 0; i < kShrinkF; ++i) {
+    for (int i = 0; i < p.f_stages; ++i) {
       mbar_init(smem_u32(&ctl.ffull[i]), 1);
       mbar_init(smem_u32(&ctl.fempty[i]), 1);
     }
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
           } else {
             tma_load_2d(dst, &tmF, fb, kb * BK, a * p.f_rows);
           }
-          if (++fs == kShrinkF) { fs = 0; fp ^= 1u; }
+          if (++fs == p.f_stages) { fs = 0; fp ^= 1u; }
           return true;
         });
       }
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
           mma_commit(smem_u32(&ctl.fempty[fs]));
         }
         __syncwarp();
-        if (++fs == kShrinkF) { fs = 0; fp ^= 1u; }
+        if (++fs == p.f_stages) { fs = 0; fp ^= 1u; }
         return true;
       });
       if (lane == 0) mma_commit(smem_u32(&ctl.xempty[xs]));
@@ -381,45 +382,159 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
   cluster_sync();  // a peer may still read this CTA's accumulator
 }
 
-// --------------------------------------------------- wide product, whole tiles
+// ------------------------------------------------- narrow product, few rows
 //
-// out[128 rows x BN] = in W^T (kMN: in W) + hidden F, one CTA per SM over the
-// tiles: a TMA warp, an MMA warp, four epilogue warps; two accumulators, so
-// that a tile's epilogue runs beside the next one's MMAs.
-struct WideParams {
+// v_t for requests of a row or a few: one warp a (row, kGemvRanks ranks), the
+// lanes along the reduction, fp32 throughout.  Bound by reading each row's own
+// A_a once, which spreads over all SMs here; on the tensor cores one 128-row
+// tile would walk its adapters one after the other.
+constexpr int kGemvRanks = 2, kGemvWarps = 4;
+
+struct GemvParams {
   Reqs q;
-  int red, out_cols, r, rN;
-  int f_rows;          // K-major F: rows of its 2-D view per adapter
-  int n_tiles, tiles;
-  int has_hidden;      // a narrow kernel of the same call wrote hidden
-  uint32_t idesc;
+  const __nv_bfloat16* x;
+  long long ldx;
+  const __nv_bfloat16* A;
+  const float* scale;
+  int K, r;
+  __nv_bfloat16* hidden;
   int* status;
 };
 
-template <int BN>
-struct WideCfg {
-  static constexpr int STAGES = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
-  static constexpr int B_BYTES = BN * BK * 2;
-  static constexpr int STAGE_BYTES = BM * BK * 2 + B_BYTES;
-  static constexpr int EP_BYTES = 4 * EP_SLOTS * EP_BOX_BYTES;
-  static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE_BYTES + EP_BYTES + (2 * kMaxSegments + 4) * 4;
-  static_assert(SMEM <= kSmemMax - 1024, "shared memory budget exceeded");
+__global__ void __launch_bounds__(kGemvWarps * 32) adapter_gemv_kernel(const GemvParams p) {
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ int tab[];
+  int* off = tab;
+  int* ad = off + p.q.num_seg + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = blockIdx.x;
+  const int j0 = (blockIdx.y * kGemvWarps + warp) * kGemvRanks;
+  const uint4* x = reinterpret_cast<const uint4*>(p.x + (size_t)t * p.ldx);
+  const int nv = p.K / 8;
+  uint4 xv[4];  // the row's first values, on their way while the table is read
+#pragma unroll
+  for (int u = 0; u < 4; ++u) xv[u] = u * 32 + lane < nv ? __ldg(x + u * 32 + lane) : make_uint4(0, 0, 0, 0);
+  load_requests(p.q, off, ad, p.status);
+  const int s = first_request(off, p.q.num_seg, t);
+  const int a = s < p.q.num_seg && off[s] <= t ? ad[s] : -1;
+  const int rp = plane_cols(p.r), hp = hidden_pitch(p.r);
+  if (j0 >= rp) return;
+  float sum[kGemvRanks] = {0.f, 0.f};
+  if (a >= 0 && j0 < p.r) {
+    const uint4* f = reinterpret_cast<const uint4*>(p.A + ((size_t)a * p.r + j0) * p.K);
+    for (int v0 = 0; v0 < nv; v0 += 128) {
+      uint4 fv[kGemvRanks][4];
+#pragma unroll
+      for (int j = 0; j < kGemvRanks; ++j)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int v = v0 + u * 32 + lane;
+          fv[j][u] = v < nv ? __ldg(f + (size_t)j * nv + v) : make_uint4(0, 0, 0, 0);
+        }
+      if (v0 > 0) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int v = v0 + u * 32 + lane;
+          xv[u] = v < nv ? __ldg(x + v) : make_uint4(0, 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float xf[8];
+        unpack8(xv[u], xf);
+#pragma unroll
+        for (int j = 0; j < kGemvRanks; ++j) {
+          float ff[8];
+          unpack8(fv[j][u], ff);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[j] = fmaf(xf[i], ff[i], sum[j]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kGemvRanks; ++j) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
+  }
+  if (lane < kGemvRanks) {  // ranks are even in number, columns past them are zero
+    float v[8] = {(lane == 0 ? sum[0] : sum[1]) * (a >= 0 && p.scale ? __ldg(p.scale + a) : 1.f), 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    uint4 o[kPlanes];
+    split8(v, o);
+#pragma unroll
+    for (int k = 0; k < kPlanes; ++k)
+      p.hidden[(size_t)t * hp + k * rp + j0 + lane] = __ushort_as_bfloat16((unsigned short)(o[k].x & 0xFFFFu));
+  }
+}
+
+// ------------------------------------------------------------- wide product
+//
+// out[128 rows x BN] = in W^T (kMN: in W) + hidden F.  A TMA warp streams the
+// blocks of in and W and then, run by run, those of F; one warp loads hidden's
+// blocks of the tile (once, whatever the number of runs); one warp issues the
+// MMAs; four warps write the tile out.
+//
+// Whole tiles (kSplit false): one CTA per SM over the tiles, two accumulators,
+// so that a tile's epilogue runs beside the next one's MMAs.  256-column tiles
+// whose last wave would fill less than half of the SMs give that wave as
+// 128-column halves.
+//
+// kSplit: for so few rows that the tiles do not fill the SMs.  A cluster shares
+// one tile: each CTA takes a slice of the reduction and every nrank-th run, and
+// the fp32 accumulators are added through distributed shared memory, each CTA
+// writing a share of the columns.  Blocks of in hold only the rows there are.
+struct WideParams {
+  Reqs q;
+  int red, r;
+  int f_rows;          // K-major F: rows of its 2-D view per adapter
+  int n_tiles;         // tiles along the columns
+  int units;           // whole tiles and halves (kSplit: unused)
+  int full;            // units that are whole tiles
+  int a_rows;          // rows of a block of in and hidden
+  int stages;
+  int has_hidden;      // a narrow kernel of the same call wrote hidden
+  uint32_t idesc, idesc_half;
+  __nv_bfloat16* out;  // kSplit
+  long long ldo;
+  int* status;
 };
 
+constexpr int kWideStagesMax = 12;
+constexpr int kWideThreads = 224;
+
+template <int BN, bool kSplit>
+struct WideCfg {
+  static constexpr int WB = BN < 128 ? BN : 128;  // W rows (columns) of one TMA box
+  static constexpr int B_BYTES = BN * BK * 2;
+  static constexpr int VBUF = BN == 256 ? 1 : 2;  // hidden blocks held at a time
+  static constexpr int EP = BN == 256 ? 1 : EP_SLOTS;
+  static constexpr int EP_BYTES = kSplit ? 0 : 4 * EP * EP_BOX_BYTES;
+  static constexpr int STAGES = BN == 256 ? 4 : (BN == 128 ? 5 : 6);
+  static constexpr size_t smem(int a_rows, int stages) {
+    // the MMA reads 128 rows from a hidden block's start, however few it holds
+    return 1024 + (size_t)stages * (a_rows * BK * 2 + B_BYTES) + (size_t)((VBUF - 1) * a_rows + BM) * BK * 2 + EP_BYTES +
+           (2 * kMaxSegments + 4) * 4;
+  }
+};
+static_assert(WideCfg<256, false>::smem(BM, 4) <= kSmemMax - 1024 && WideCfg<128, false>::smem(BM, 5) <= kSmemMax - 1024 &&
+                  WideCfg<64, false>::smem(BM, 6) <= kSmemMax - 1024,
+              "shared memory budget exceeded");
+
 struct WideCtl {
-  unsigned long long full[8], empty[8], tfull[2], tempty[2], drain;
+  unsigned long long full[kWideStagesMax], empty[kWideStagesMax], tfull[2], tempty[2], vfull, vempty, drain;
   uint32_t tmem_base;
   int abort_flag;
 };
 
-template <int BN, bool kMN>
-__global__ void __launch_bounds__(192, 1) adapter_wide_kernel(const __grid_constant__ CUtensorMap tmX,
-                                                              const __grid_constant__ CUtensorMap tmW,
-                                                              const __grid_constant__ CUtensorMap tmH,
-                                                              const __grid_constant__ CUtensorMap tmF,
-                                                              const __grid_constant__ CUtensorMap tmO,
-                                                              const WideParams p) {
-  using C = WideCfg<BN>;
+template <int BN, bool kMN, bool kSplit>
+__global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __grid_constant__ CUtensorMap tmX,
+                                                                       const __grid_constant__ CUtensorMap tmW,
+                                                                       const __grid_constant__ CUtensorMap tmH,
+                                                                       const __grid_constant__ CUtensorMap tmF,
+                                                                       const __grid_constant__ CUtensorMap tmO,
+                                                                       const WideParams p) {
+  using C = WideCfg<BN, kSplit>;
   // The narrow kernel of this call waited for everything before it and lets
   // this one start early; x, W and the request table are older than it, so only
   // hidden has to be waited for.
@@ -428,12 +543,17 @@ __global__ void __launch_bounds__(192, 1) adapter_wide_kernel(const __grid_const
   __shared__ WideCtl ctl;
   const uint32_t base = align1k(smem_u32(smem_raw));
   uint8_t* bytes = smem_raw + (base - smem_u32(smem_raw));
-  int* off = reinterpret_cast<int*>(bytes + (size_t)C::STAGES * C::STAGE_BYTES + C::EP_BYTES);
+  const int a_bytes = kSplit ? p.a_rows * (BK * 2) : BM * BK * 2;
+  const int nst = kSplit ? p.stages : C::STAGES;
+  const int stage_bytes = a_bytes + C::B_BYTES;
+  const uint32_t sV = base + nst * stage_bytes;
+  uint8_t* ep = bytes + (size_t)nst * stage_bytes + (C::VBUF - 1) * a_bytes + BM * BK * 2;
+  int* off = reinterpret_cast<int*>(ep + C::EP_BYTES);
   int* ad = off + p.q.num_seg + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   load_requests(p.q, off, ad, p.status);
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::STAGES; ++i) {
+    for (int i = 0; i < nst; ++i) {
       mbar_init(smem_u32(&ctl.full[i]), 1);
       mbar_init(smem_u32(&ctl.empty[i]), 1);
     }
@@ -441,6 +561,8 @@ __global__ void __launch_bounds__(192, 1) adapter_wide_kernel(const __grid_const
       mbar_init(smem_u32(&ctl.tfull[i]), 1);
       mbar_init(smem_u32(&ctl.tempty[i]), 4);
     }
+    mbar_init(smem_u32(&ctl.vfull), 1);
+    mbar_init(smem_u32(&ctl.vempty), 1);
     mbar_init(smem_u32(&ctl.drain), 1);
     ctl.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -448,114 +570,171 @@ __global__ void __launch_bounds__(192, 1) adapter_wide_kernel(const __grid_const
     prefetch_tmap(&tmW);
     prefetch_tmap(&tmH);
     prefetch_tmap(&tmF);
-    prefetch_tmap(&tmO);
+    if (!kSplit) prefetch_tmap(&tmO);
   }
-  if (warp == 1) tmem_alloc_n<1>(smem_u32(&ctl.tmem_base), 2 * BN);
+  constexpr int kTmem = kSplit ? BN : 2 * BN;
+  if (warp == 1) tmem_alloc_n<1>(smem_u32(&ctl.tmem_base), kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   pdl_trigger();
   const uint32_t tmem = ctl.tmem_base;
+  const int nrank = kSplit ? (int)gridDim.x : 1, rank = kSplit ? (int)blockIdx.x : 0;
   const int nkb = p.red / BK;
-  // blocks of one run: two parts of hidden times F, 64 hidden columns a block.
-  // With both in one block (r <= 32) the block's MMA steps walk the parts.
+  const int kb0 = kSplit ? (int)((long long)nkb * rank / nrank) : 0;
+  const int kb1 = kSplit ? (int)((long long)nkb * (rank + 1) / nrank) : nkb;
+  // Blocks of a run: 64 ranks of F at a time, times two parts of hidden.  Both
+  // parts share one 64-column block of hidden up to r = 32; beyond, they are two
+  // blocks, held together where there is room, else one after the other (and F's
+  // block comes twice).
   const int rp = plane_cols(p.r);
   const bool one_block = kWidePlanes * rp <= 64;
-  const int fblk = (p.r + 63) / 64;                       // 64-column blocks of F
-  const int run_blocks = one_block ? 1 : kWidePlanes * fblk;
+  const int fblk = (p.r + 63) / 64;
+  const int vset = one_block ? 1 : C::VBUF;                     // hidden blocks held at a time
+  const int passes = fblk * (one_block ? 1 : kWidePlanes / C::VBUF);
+  const int psplit = passes / fblk;                             // passes per block of F
+
+  struct Unit {
+    int m0, n0, bn;
+  };
+  auto unit_at = [&](int u) -> Unit {
+    if (kSplit) return {(int)blockIdx.z * BM, (int)blockIdx.y * BN, BN};
+    if (BN < 256 || u < p.full) return {u / p.n_tiles * BM, u % p.n_tiles * BN, BN};
+    const int t = p.full + (u - p.full) / 2;
+    return {t / p.n_tiles * BM, t % p.n_tiles * BN + ((u - p.full) & 1) * (BN / 2), BN / 2};
+  };
+  const int u0 = kSplit ? 0 : blockIdx.x, u1 = kSplit ? 1 : p.units, du = kSplit ? 1 : gridDim.x;
+  // this CTA's runs of a tile
+  auto my_runs = [&](int m0, auto&& f) {
+    int i = 0;
+    for_each_run(off, ad, p.q.num_seg, m0, min(p.q.T, m0 + BM), [&](int lo, int hi, int a) {
+      if (kSplit && i++ % nrank != rank) return true;
+      return f(lo, hi, a);
+    });
+  };
+  auto any_run = [&](int m0) {
+    bool any = false;
+    my_runs(m0, [&](int, int, int) { any = true; return false; });
+    return any;
+  };
 
   if (warp == 0) {
     if (lane == 0) {
       int st = 0;
       uint32_t ph = 0;
-      bool ok = true, waited = !p.has_hidden;
-      auto next = [&]() { if (++st == C::STAGES) { st = 0; ph ^= 1u; } };
-      for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
-        const int m0 = tile / p.n_tiles * BM, n0 = tile % p.n_tiles * BN;
-        for (int kb = 0; kb < nkb; ++kb) {
+      bool ok = true;
+      auto next = [&]() { if (++st == nst) { st = 0; ph ^= 1u; } };
+      for (int u = u0; ok && u < u1; u += du) {
+        const Unit t = unit_at(u);
+        const uint32_t b_bytes = (uint32_t)t.bn * BK * 2;
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!(ok = wait_bar(smem_u32(&ctl.empty[st]), ph ^ 1u, &ctl.abort_flag, p.status))) break;
-          const uint32_t fb = smem_u32(&ctl.full[st]), sA = base + st * C::STAGE_BYTES, sB = sA + BM * BK * 2;
-          mbar_arrive_expect_tx(fb, C::STAGE_BYTES);
-          tma_load_2d(sA, &tmX, fb, kb * BK, m0);
-          if (kMN)
-            tma_load_3d(sB, &tmW, fb, 0, kb * BK, n0 / 64);
-          else
-            tma_load_2d(sB, &tmW, fb, kb * BK, n0);
+          const uint32_t fb = smem_u32(&ctl.full[st]), sA = base + st * stage_bytes, sB = sA + a_bytes;
+          mbar_arrive_expect_tx(fb, a_bytes + b_bytes);
+          tma_load_2d(sA, &tmX, fb, kb * BK, t.m0);
+          for (int h = 0; h < t.bn / C::WB; ++h) {
+            if (kMN)
+              tma_load_3d(sB + h * (C::WB * BK * 2), &tmW, fb, 0, kb * BK, t.n0 / 64 + h * (C::WB / 64));
+            else
+              tma_load_2d(sB + h * (C::WB * BK * 2), &tmW, fb, kb * BK, t.n0 + h * C::WB);
+          }
           next();
         }
-        if (!ok) break;
-        for_each_run(off, ad, p.q.num_seg, m0, min(p.q.T, m0 + BM), [&](int, int, int a) {
-          if (!waited) {
-            pdl_wait();
-            waited = true;
-          }
-          for (int b = 0; b < run_blocks; ++b) {
+        for (int ps = 0; ok && ps < passes; ++ps) {
+          const int c = ps / psplit * 64;  // F's columns (ranks) of this pass
+          my_runs(t.m0, [&](int, int, int a) {
             if (!(ok = wait_bar(smem_u32(&ctl.empty[st]), ph ^ 1u, &ctl.abort_flag, p.status))) return false;
-            const uint32_t fb = smem_u32(&ctl.full[st]), sA = base + st * C::STAGE_BYTES, sB = sA + BM * BK * 2;
-            const int c = b % fblk * 64;  // F columns (ranks) of this block
-            mbar_arrive_expect_tx(fb, C::STAGE_BYTES);
-            tma_load_2d(sA, &tmH, fb, b / fblk * rp + c, m0);
-            if (kMN)
-              tma_load_4d(sB, &tmF, fb, 0, c, n0 / 64, a);
-            else
-              tma_load_2d(sB, &tmF, fb, c, a * p.f_rows + n0);
+            const uint32_t fb = smem_u32(&ctl.full[st]), sB = base + st * stage_bytes + a_bytes;
+            mbar_arrive_expect_tx(fb, b_bytes);
+            for (int h = 0; h < t.bn / C::WB; ++h) {
+              if (kMN)
+                tma_load_4d(sB + h * (C::WB * BK * 2), &tmF, fb, 0, c, t.n0 / 64 + h * (C::WB / 64), a);
+              else
+                tma_load_2d(sB + h * (C::WB * BK * 2), &tmF, fb, c, a * p.f_rows + t.n0 + h * C::WB);
+            }
             next();
-          }
-          return true;
-        });
+            return true;
+          });
+        }
       }
-      if (!waited) pdl_wait();  // the grid may not end before the narrow kernel does
+    }
+  } else if (warp == 6) {
+    if (lane == 0) {
+      if (p.has_hidden) pdl_wait();  // also: the grid may not end before the narrow kernel does
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int u = u0; ok && u < u1; u += du) {
+        const Unit t = unit_at(u);
+        if (!any_run(t.m0)) continue;
+        for (int ps = 0; ok && ps < passes; ++ps, ph ^= 1u) {
+          ok = wait_bar(smem_u32(&ctl.vempty), ph ^ 1u, &ctl.abort_flag, p.status);
+          if (!ok) break;
+          const uint32_t fb = smem_u32(&ctl.vfull);
+          mbar_arrive_expect_tx(fb, vset * a_bytes);
+          for (int v = 0; v < vset; ++v)
+            tma_load_2d(sV + v * a_bytes, &tmH, fb, (ps % psplit + v) * rp + ps / psplit * 64, t.m0);
+        }
+      }
     }
   } else if (warp == 1) {
     int st = 0, local = 0;
-    uint32_t ph = 0;
+    uint32_t ph = 0, vph = 0;
     bool ok = true;
-    auto next = [&]() { if (++st == C::STAGES) { st = 0; ph ^= 1u; } };
-    for (int tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x, ++local) {
-      const int m0 = tile / p.n_tiles * BM;
+    auto next = [&]() { if (++st == nst) { st = 0; ph ^= 1u; } };
+    for (int u = u0; ok && u < u1; u += du, ++local) {
+      const Unit t = unit_at(u);
+      const uint32_t idesc = t.bn == BN ? p.idesc : p.idesc_half;
       const int buf = local & 1;
       ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.tempty[buf]), ((local >> 1) & 1) ^ 1, &ctl.abort_flag, p.status));
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + buf * BN;
-      for (int kb = 0; kb < nkb; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.full[st]), ph, &ctl.abort_flag, p.status));
         if (!ok) break;
         tc_fence_after();
         if (lane == 0) {
-          const uint32_t a0 = base + st * C::STAGE_BYTES, b0 = a0 + BM * BK * 2;
+          const uint32_t a0 = base + st * stage_bytes, b0 = a0 + a_bytes;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
             mma_bf16(d, sdesc(a0 + kk * 32, 16, 1024),
-                     kMN ? sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024) : sdesc(b0 + kk * 32, 16, 1024), p.idesc,
-                     kb > 0 || kk > 0);
+                     kMN ? sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024) : sdesc(b0 + kk * 32, 16, 1024), idesc,
+                     kb > kb0 || kk > 0);
           mma_commit(smem_u32(&ctl.empty[st]));
         }
         __syncwarp();
         next();
       }
       if (!ok) break;
-      for_each_run(off, ad, p.q.num_seg, m0, min(p.q.T, m0 + BM), [&](int lo, int hi, int) {
-        const LaneMask m = lane_mask(lo - m0, hi - m0);
-        for (int b = 0; b < run_blocks; ++b) {
-          ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.full[st]), ph, &ctl.abort_flag, p.status));
-          if (!ok) return false;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t a0 = base + st * C::STAGE_BYTES, b0 = a0 + BM * BK * 2;
-            const int steps = min(4, (p.r - b % fblk * 64 + 15) / 16);  // 16-wide steps of this block of F
-            for (int pl = 0; pl < (one_block ? kWidePlanes : 1); ++pl)
-              for (int kk = 0; kk < steps; ++kk)
-                mma_bf16_lanes(d, sdesc(a0 + (pl * rp / 16 + kk) * 32, 16, 1024),
-                               kMN ? sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024) : sdesc(b0 + kk * 32, 16, 1024),
-                               p.idesc, 1u, m);
-            mma_commit(smem_u32(&ctl.empty[st]));
-          }
+      if (any_run(t.m0)) {
+        for (int ps = 0; ok && ps < passes; ++ps, vph ^= 1u) {
+          ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.vfull), vph, &ctl.abort_flag, p.status));
+          if (!ok) break;
+          const int steps = min(4, (p.r - ps / psplit * 64 + 15) / 16);  // 16-wide steps of this block of F
+          const int parts = one_block ? kWidePlanes : C::VBUF;           // of hidden, in this pass
+          const int pstep = one_block ? rp * 2 : a_bytes;                // bytes from one to the next
+          my_runs(t.m0, [&](int lo, int hi, int) {
+            ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.full[st]), ph, &ctl.abort_flag, p.status));
+            if (!ok) return false;
+            tc_fence_after();
+            if (lane == 0) {
+              const LaneMask m = lane_mask(lo - t.m0, hi - t.m0);
+              const uint32_t b0 = base + st * stage_bytes + a_bytes;
+              for (int pl = 0; pl < parts; ++pl)
+                for (int kk = 0; kk < steps; ++kk)
+                  mma_bf16_lanes(d, sdesc(sV + pl * pstep + kk * 32, 16, 1024),
+                                 kMN ? sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024) : sdesc(b0 + kk * 32, 16, 1024), idesc,
+                                 1u, m);
+              mma_commit(smem_u32(&ctl.empty[st]));
+            }
+            __syncwarp();
+            next();
+            return true;
+          });
+          if (ok && lane == 0) mma_commit(smem_u32(&ctl.vempty));
           __syncwarp();
-          next();
         }
-        return true;
-      });
+      }
       if (!ok) break;
       if (lane == 0) mma_commit(smem_u32(&ctl.tfull[buf]));
       __syncwarp();
@@ -567,17 +746,32 @@ __global__ void __launch_bounds__(192, 1) adapter_wide_kernel(const __grid_const
       while (!mbar_try_wait(smem_u32(&ctl.drain), 0) && globaltimer() - t0 < TIMEOUT_NS) {
       }
     }
+  } else if constexpr (kSplit) {
+    // the slice's accumulator, column by column, over the ring (all of it consumed)
+    const int q = warp & 3;
+    float* acc = reinterpret_cast<float*>(bytes);  // [BN][BM]
+    if (__all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.tfull[0]), 0, &ctl.abort_flag, p.status)) && q * 32 < p.a_rows) {
+      tc_fence_after();
+      for (int c = 0; c < BN; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[(c + i) * BM + q * 32 + lane] = f32(v[i]);
+      }
+    }
   } else {
     const int q = warp & 3;
-    EpRing<EP_SLOTS> ring{bytes + (size_t)C::STAGES * C::STAGE_BYTES + (size_t)(warp - 2) * EP_SLOTS * EP_BOX_BYTES, 0, lane};
+    EpRing<C::EP> ring{ep + (size_t)(warp - 2) * C::EP * EP_BOX_BYTES, 0, lane};
     int local = 0;
-    for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, ++local) {
-      const int rb = tile / p.n_tiles * BM + q * 32, n0 = tile % p.n_tiles * BN;
+    for (int u = u0; u < u1; u += du, ++local) {
+      const Unit t = unit_at(u);
+      const int rb = t.m0 + q * 32;
       const int buf = local & 1;
       if (!__all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.tfull[buf]), (local >> 1) & 1, &ctl.abort_flag, p.status))) break;
       tc_fence_after();
       if (rb < p.q.T) {
-        for (int c = 0; c < BN; c += 32) {
+        for (int c = 0; c < t.bn; c += 32) {
           uint32_t v[32];
           tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN + c), v);
           tmem_wait_ld();
@@ -586,7 +780,7 @@ __global__ void __launch_bounds__(192, 1) adapter_wide_kernel(const __grid_const
           for (int i = 0; i < 4; ++i)
             ring.put(box, i, make_uint4(pack_bf16x2(f32(v[8 * i]), f32(v[8 * i + 1])), pack_bf16x2(f32(v[8 * i + 2]), f32(v[8 * i + 3])),
                                         pack_bf16x2(f32(v[8 * i + 4]), f32(v[8 * i + 5])), pack_bf16x2(f32(v[8 * i + 6]), f32(v[8 * i + 7]))));
-          ring.issue(box, &tmO, n0 + c, rb);  // rows past the last token are clipped by the map
+          ring.issue(box, &tmO, t.n0 + c, rb);  // rows past the last token are clipped by the map
         }
       }
       tc_fence_before();
@@ -598,7 +792,25 @@ __global__ void __launch_bounds__(192, 1) adapter_wide_kernel(const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_n<1>(tmem, 2 * BN);
+  if (warp == 1) tmem_dealloc_n<1>(tmem, kTmem);
+  if constexpr (kSplit) {
+    cluster_sync();
+    // this CTA's share of the columns: the slices' sums in order
+    const int m0 = blockIdx.z * BM, per = BN / nrank;
+    const int rows = min(p.a_rows, p.q.T - m0);
+    const uint32_t local = base;
+    for (int i = threadIdx.x; i < rows * (per / 8); i += kWideThreads) {
+      const int row = i % rows, c = rank * per + i / rows * 8;
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < nrank; ++k) {
+        const uint32_t peer = map_to_rank(local + (uint32_t)(c * BM + row) * 4, k);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += ld_cluster(peer + j * BM * 4);
+      }
+      *reinterpret_cast<uint4*>(p.out + (size_t)(m0 + row) * p.ldo + (int)blockIdx.y * BN + c) = pack8(v);
+    }
+    cluster_sync();  // a peer may still read this CTA's accumulator
+  }
 }
 
 // ------------------------------------------------------- adapters' gradients
@@ -934,7 +1146,7 @@ int set_smem(const void* kern, bool* done, const char* fn) {
   const int dev = current_device();
   if (dev < 0) return fail(MOE_ERR_CUDA, "%s: no current CUDA device", fn);
   if (done[dev]) return MOE_OK;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax - 2048);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax - 1024);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
   done[dev] = true;
   return MOE_OK;
@@ -986,77 +1198,103 @@ int run_shrink(const char* fn, const Reqs& q, const void* in, long long ld, cons
   p.rN = round_up(r, 16);
   p.f_bytes = kMN ? (r + 63) / 64 * CHUNK_BYTES : r * 128;
   p.f_rows = kMN ? red : r;
+  p.f_stages = 32768 / p.f_bytes < 4 ? 4 : (32768 / p.f_bytes > kShrinkF ? kShrinkF : 32768 / p.f_bytes);
   p.scale = scale;
   p.hidden = static_cast<__nv_bfloat16*>(hidden);
   p.idesc = make_idesc(p.rN, BM, false, kMN);
   p.tmem_cols = p.rN <= 32 ? 32 : (p.rN <= 64 ? 64 : 128);
   p.status = status_word();
   // one 16-row block of slack: an F block of r rows is read as rN
-  const size_t smem = 1024 + kShrinkX * (BM * BK * 2) + (size_t)kShrinkF * p.f_bytes + 2048 + (2 * q.num_seg + 2) * 4;
+  const size_t smem = 1024 + kShrinkX * (BM * BK * 2) + (size_t)p.f_stages * p.f_bytes + 2048 + (2 * q.num_seg + 2) * 4;
   return launch_adapter(fn, kern, dim3(cs, tiles), 192, smem, cs, s, tx, tf, p);
 }
 
-template <int BN, bool kMN>
+template <int BN, bool kMN, bool kSplit>
 int run_wide_bn(const char* fn, const Reqs& q, const void* in, long long ld, const void* W, const void* hidden, const void* F,
-                int red, int out_cols, int r, void* out, long long ldo, bool has_hidden, cudaStream_t s) {
-  using C = WideCfg<BN>;
+                int red, int out_cols, int r, void* out, long long ldo, bool has_hidden, int nrank, cudaStream_t s) {
+  using C = WideCfg<BN, kSplit>;
   static bool attr[64] = {};
-  auto kern = adapter_wide_kernel<BN, kMN>;
+  auto kern = adapter_wide_kernel<BN, kMN, kSplit>;
   if (int rc = set_smem(reinterpret_cast<const void*>(kern), attr, fn)) return rc;
   const int sms = sm_count();
   if (sms <= 0) return fail(MOE_ERR_CUDA, "%s: cannot query the SM count", fn);
+  WideParams p{};
+  p.a_rows = kSplit && q.T < BM ? round_up(q.T, 8) : BM;
   CUtensorMap tx, tw, th, tf, to;
-  if (int rc = map2(&tx, in, red, q.T, ld, BK, BM)) return rc;
+  if (int rc = map2(&tx, in, red, q.T, ld, BK, p.a_rows)) return rc;
   const int hp = hidden_pitch(r);
-  if (has_hidden) {
-    if (int rc = map2(&th, hidden, hp, q.T, hp, 64, BM)) return rc;
-  } else {
-    th = tx;
-  }
   if (kMN) {
-    if (int rc = map_mn(&tw, W, out_cols, red, out_cols, BN / 64)) return rc;
-    const uint64_t d[4] = {64, (uint64_t)r, (uint64_t)out_cols / 64, (uint64_t)q.num_adapters};
-    const uint64_t pt[3] = {(uint64_t)out_cols, 64, (uint64_t)r * out_cols};
-    const uint32_t b[4] = {64, 64, BN / 64, 1};
-    if (has_hidden) {
+    if (int rc = map_mn(&tw, W, out_cols, red, out_cols, C::WB / 64)) return rc;
+  } else {
+    if (int rc = map2(&tw, W, red, out_cols, red, BK, C::WB)) return rc;
+  }
+  th = tx;
+  tf = tw;
+  if (has_hidden) {
+    if (int rc = map2(&th, hidden, hp, q.T, hp, 64, p.a_rows)) return rc;
+    if (kMN) {
+      const uint64_t d[4] = {64, (uint64_t)r, (uint64_t)out_cols / 64, (uint64_t)q.num_adapters};
+      const uint64_t pt[3] = {(uint64_t)out_cols, 64, (uint64_t)r * out_cols};
+      const uint32_t b[4] = {64, 64, C::WB / 64, 1};
       if (int rc = make_map(&tf, F, 4, d, pt, b)) return rc;
     } else {
-      tf = tw;
-    }
-  } else {
-    if (int rc = map2(&tw, W, red, out_cols, red, BK, BN)) return rc;
-    if (has_hidden) {
-      if (int rc = map2(&tf, F, r, (uint64_t)q.num_adapters * out_cols, r, 64, BN)) return rc;
-    } else {
-      tf = tw;
+      if (int rc = map2(&tf, F, r, (uint64_t)q.num_adapters * out_cols, r, 64, C::WB)) return rc;
     }
   }
-  if (int rc = map2(&to, out, out_cols, q.T, ldo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) return rc;
-  WideParams p{};
+  to = tx;
+  if (!kSplit)
+    if (int rc = map2(&to, out, out_cols, q.T, ldo, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) return rc;
   p.q = q;
   p.red = red;
-  p.out_cols = out_cols;
   p.r = r;
-  p.rN = round_up(r, 16);
   p.f_rows = out_cols;
   p.n_tiles = out_cols / BN;
-  p.tiles = (q.T + BM - 1) / BM * p.n_tiles;
+  const int rows = (q.T + BM - 1) / BM, tiles = rows * p.n_tiles;
+  const int rest = BN == 256 ? tiles % sms : 0;
+  p.full = rest > 0 && 2 * rest <= sms ? tiles - rest : tiles;
+  p.units = p.full + 2 * (tiles - p.full);
   p.has_hidden = has_hidden;
   p.idesc = make_idesc(BN, BM, false, kMN);
+  p.idesc_half = make_idesc(BN / 2, BM, false, kMN);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.ldo = ldo;
   p.status = status_word();
-  return launch_adapter(fn, kern, dim3(p.tiles < sms ? p.tiles : sms), 192, C::SMEM, 0, s, tx, tw, th, tf, to, p);
+  p.stages = C::STAGES;
+  if (kSplit) {
+    // a slice's blocks all in flight where they fit; four hold the accumulator afterwards
+    while (p.stages < kWideStagesMax && C::smem(p.a_rows, p.stages + 1) <= kSmemMax - 1024) ++p.stages;
+    return launch_adapter(fn, kern, dim3(nrank, p.n_tiles, rows), kWideThreads, C::smem(p.a_rows, p.stages), nrank, s, tx, tw,
+                          th, tf, to, p);
+  }
+  return launch_adapter(fn, kern, dim3(p.units < sms ? p.units : sms), kWideThreads, C::smem(BM, p.stages), 0, s, tx, tw, th, tf,
+                        to, p);
 }
 
 template <bool kMN>
 int run_wide(const char* fn, const Reqs& q, const void* in, long long ld, const void* W, const void* hidden, const void* F,
              int red, int out_cols, int r, void* out, long long ldo, bool has_hidden, cudaStream_t s) {
-  // the widest tile that divides the columns and still gives every SM one
+  // the widest tile that divides the columns and still gives every SM one;
+  // where even the narrowest leave half of them idle, clusters along the reduction
   const int sms = sm_count() > 0 ? sm_count() : 148, rows = (q.T + BM - 1) / BM;
   if (out_cols % 256 == 0 && rows * (out_cols / 256) >= sms)
-    return run_wide_bn<256, kMN>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, s);
+    return run_wide_bn<256, kMN, false>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, 1, s);
   if (out_cols % 128 == 0 && rows * (out_cols / 128) >= sms)
-    return run_wide_bn<128, kMN>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, s);
-  return run_wide_bn<64, kMN>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, s);
+    return run_wide_bn<128, kMN, false>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, 1, s);
+  const int tiles = rows * (out_cols / 64);
+  int nrank = 1;
+  while (nrank < 8 && nrank * 2 <= red / BK && tiles * nrank * 2 <= sms) nrank *= 2;
+  if (nrank > 1)
+    return run_wide_bn<64, kMN, true>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, nrank, s);
+  return run_wide_bn<64, kMN, false>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, 1, s);
+}
+
+// v of requests of a row or a few.
+int run_gemv(const char* fn, const Reqs& q, const void* x, long long ldx, const void* A, const float* scale, int K, int r,
+             void* hidden, cudaStream_t s) {
+  const GemvParams p{q, static_cast<const __nv_bfloat16*>(x), ldx, static_cast<const __nv_bfloat16*>(A), scale, K, r,
+                     static_cast<__nv_bfloat16*>(hidden), status_word()};
+  const dim3 grid(q.T, (plane_cols(r) + kGemvWarps * kGemvRanks - 1) / (kGemvWarps * kGemvRanks));
+  return launch_adapter(fn, adapter_gemv_kernel, grid, kGemvWarps * 32, sizeof(int) * (size_t)(2 * q.num_seg + 2), 0, s, p);
 }
 
 int check_adapter(const char* fn, const Reqs& q, int K, int N, int r, long long ldx, long long ldy) {
@@ -1126,8 +1364,12 @@ int moe_adapter_linear(const void* x, long long ldx, const void* W, const void* 
   if (hidden_bytes < moe_adapter_hidden_size(T, r))
     return fail(MOE_ERR_WORKSPACE, "%s: hidden %zu < %zu bytes", fn, hidden_bytes, moe_adapter_hidden_size(T, r));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (num_seg > 0)
-    if (int rc = run_shrink<false>(fn, q, x, ldx, A, scale, K, r, hidden, s)) return rc;
+  if (num_seg > 0) {
+    const bool few = T <= 4 * num_seg || T <= 16;
+    if (int rc = few ? run_gemv(fn, q, x, ldx, A, scale, K, r, hidden, s)
+                     : run_shrink<false>(fn, q, x, ldx, A, scale, K, r, hidden, s))
+      return rc;
+  }
   return run_wide<false>(fn, q, x, ldx, W, hidden, B, K, N, r, y, ldy, num_seg > 0, s);
 }
 
