@@ -51,9 +51,11 @@ struct Reqs {
   const int32_t* adapter;  // [num_seg], negative: none
 };
 
+__host__ __device__ constexpr size_t table_bytes(int num_seg) { return (size_t)(num_seg + 2) * 4 + (size_t)(num_seg + 2) * 2; }
+
 // Shared-memory copy: offsets made monotone and clamped to [0, T], adapter ids
 // out of range replaced by -1 (both reported).  off[num_seg + 1], ad[num_seg].
-__device__ __forceinline__ void load_requests(const Reqs& q, int* off, int* ad, int* status) {
+__device__ __forceinline__ void load_requests(const Reqs& q, int* off, int16_t* ad, int* status) {
   if (q.num_seg == 0) {  // there may be no table at all
     if (threadIdx.x == 0) off[0] = 0;
     __syncthreads();
@@ -73,7 +75,7 @@ __device__ __forceinline__ void load_requests(const Reqs& q, int* off, int* ad, 
         bad = true;
         a = -1;
       }
-      ad[s] = a;
+      ad[s] = (int16_t)a;
     }
   }
   __syncthreads();
@@ -110,24 +112,60 @@ __device__ __forceinline__ int first_request(const int* off, int num_seg, int t)
   return lo;
 }
 
-// f(lo, hi, adapter) -> bool (go on) for every run of rows of [m0, m1) with one
-// adapter, in row order; neighbouring requests with the same adapter are one run.
-template <class F>
-__device__ __forceinline__ void for_each_run(const int* off, const int* ad, int num_seg, int m0, int m1, F&& f) {
-  int lo = -1, hi = 0, a = -1;
-  for (int s = first_request(off, num_seg, m0); s < num_seg && off[s] < m1; ++s) {
-    const int b = max(off[s], m0), e = min(off[s + 1], m1);
-    if (b >= e || ad[s] < 0) continue;
-    if (lo >= 0 && ad[s] == a && b == hi) {
-      hi = e;
-      continue;
-    }
-    if (lo >= 0 && !f(lo, hi, a)) return;
-    lo = b;
-    hi = e;
-    a = ad[s];
+// A run: rows lo <= row - m0 < hi of a 128-row tile with one adapter;
+// neighbouring requests with the same adapter are one run.
+struct Run {
+  int lo, hi, a;
+};
+__device__ __forceinline__ Run unpack_run(uint32_t v) {
+  return {(int)(v & 0xFFu), (int)((v >> 8) & 0xFFu) + 1, (int)(v >> 16)};
+}
+
+// Adapter of row t, -1: none.
+__device__ __forceinline__ int adapter_of_row(const int* off, const int16_t* ad, int num_seg, int t) {
+  const int s = first_request(off, num_seg, t);
+  return s < num_seg && off[s] <= t ? ad[s] : -1;
+}
+
+// The runs of tile [m0, m1) in row order into list (BM entries); returns how
+// many.  A warp's common work: each lane looks four rows up, run starts are
+// found and numbered by ballots (walking the table request by request took
+// 0.07 us a request, more than the run's products).
+__device__ __forceinline__ int build_runs(const int* off, const int16_t* ad, int num_seg, int m0, int m1, uint32_t* list) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();  // the list's last reader is done
+  int a[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int t = m0 + 32 * w + lane;
+    a[w] = t < m1 ? adapter_of_row(off, ad, num_seg, t) : -1;
   }
-  if (lo >= 0) f(lo, hi, a);
+  uint32_t start[4], brk[4];
+  int before = -1;  // adapter of the row before this word
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int up = __shfl_up_sync(0xffffffffu, a[w], 1);
+    const int prev = lane == 0 ? before : up;
+    start[w] = __ballot_sync(0xffffffffu, a[w] >= 0 && a[w] != prev);
+    brk[w] = start[w] | __ballot_sync(0xffffffffu, a[w] < 0);
+    before = __shfl_sync(0xffffffffu, a[w], 31);
+  }
+  int n = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    if ((start[w] >> lane) & 1u) {
+      const uint32_t later = lane == 31 ? 0u : brk[w] & (0xffffffffu << (lane + 1));
+      int hi = later ? 32 * w + __ffs(later) - 1 : -1;
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (v > w && hi < 0 && brk[v]) hi = 32 * v + __ffs(brk[v]) - 1;
+      if (hi < 0) hi = BM;
+      list[n + __popc(start[w] & ((1u << lane) - 1u))] = (uint32_t)(32 * w + lane) | (uint32_t)(hi - 1) << 8 | (uint32_t)a[w] << 16;
+    }
+    n += __popc(start[w]);
+  }
+  __syncwarp();
+  return n;
 }
 
 // Word w of the MMA's lane mask (1 = lane off) that leaves rows [lo, hi) on.
@@ -219,6 +257,7 @@ struct ShrinkCtl {
   uint32_t tmem_base;
   int abort_flag;
   int row_ad[BM];
+  uint32_t runs[2][BM];  // the loading warp's and the MMA warp's
 };
 
 template <bool kMN>
@@ -233,15 +272,14 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
   const uint32_t sX = base, sF = base + kShrinkX * (BM * BK * 2);
   float* acc = reinterpret_cast<float*>(bytes);  // [rN][BM], over the x blocks once they are consumed
   int* off = reinterpret_cast<int*>(bytes + kShrinkX * (BM * BK * 2) + p.f_stages * p.f_bytes);
-  int* ad = off + p.q.num_seg + 1;
+  int16_t* ad = reinterpret_cast<int16_t*>(off + p.q.num_seg + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nrank = gridDim.x, rank = blockIdx.x;
   const int m0 = blockIdx.y * BM, m1 = min(p.q.T, m0 + BM);
   load_requests(p.q, off, ad, p.status);
   if (threadIdx.x < BM) {
     const int t = m0 + threadIdx.x;
-    const int s = first_request(off, p.q.num_seg, t);
-    ctl.row_ad[threadIdx.x] = t < m1 && s < p.q.num_seg && off[s] <= t ? ad[s] : -1;
+    ctl.row_ad[threadIdx.x] = t < m1 ? adapter_of_row(off, ad, p.q.num_seg, t) : -1;
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kShrinkX; ++i) {
@@ -270,19 +308,20 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
   const int kb0 = (int)((long long)nkb * rank / nrank), kb1 = (int)((long long)nkb * (rank + 1) / nrank);
 
   if (warp == 0) {
-    if (lane == 0) {
+    const int n = build_runs(off, ad, p.q.num_seg, m0, m1, ctl.runs[0]);
+    if (lane == 0 && n > 0) {
       int xs = 0, fs = 0;
       uint32_t xp = 0, fp = 0;
-      bool ok = true, any = false;
-      for_each_run(off, ad, p.q.num_seg, m0, m1, [&](int, int, int) { any = true; return false; });
-      for (int kb = kb0; ok && any && kb < kb1; ++kb) {
+      bool ok = true;
+      for (int kb = kb0; ok && kb < kb1; ++kb) {
         if (!wait_bar(smem_u32(&ctl.xempty[xs]), xp ^ 1u, &ctl.abort_flag, p.status)) break;
         const uint32_t xb = smem_u32(&ctl.xfull[xs]);
         mbar_arrive_expect_tx(xb, BM * BK * 2);
         tma_load_2d(sX + xs * (BM * BK * 2), &tmX, xb, kb * BK, m0);
         if (++xs == kShrinkX) { xs = 0; xp ^= 1u; }
-        for_each_run(off, ad, p.q.num_seg, m0, m1, [&](int, int, int a) {
-          if (!wait_bar(smem_u32(&ctl.fempty[fs]), fp ^ 1u, &ctl.abort_flag, p.status)) return ok = false;
+        for (int i = 0; i < n; ++i) {
+          const int a = unpack_run(ctl.runs[0][i]).a;
+          if (!(ok = wait_bar(smem_u32(&ctl.fempty[fs]), fp ^ 1u, &ctl.abort_flag, p.status))) break;
           const uint32_t fb = smem_u32(&ctl.ffull[fs]), dst = sF + fs * p.f_bytes;
           mbar_arrive_expect_tx(fb, p.f_bytes);
           if (kMN) {
@@ -291,26 +330,26 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
             tma_load_2d(dst, &tmF, fb, kb * BK, a * p.f_rows);
           }
           if (++fs == p.f_stages) { fs = 0; fp ^= 1u; }
-          return true;
-        });
+        }
       }
     }
   } else if (warp == 1) {
+    const int n = build_runs(off, ad, p.q.num_seg, m0, m1, ctl.runs[1]);
     int xs = 0, fs = 0;
     uint32_t xp = 0, fp = 0;
-    bool ok = true, any = false;
-    for_each_run(off, ad, p.q.num_seg, m0, m1, [&](int, int, int) { any = true; return false; });
-    for (int kb = kb0; ok && any && kb < kb1; ++kb) {
+    bool ok = true;
+    for (int kb = kb0; ok && n > 0 && kb < kb1; ++kb) {
       ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.xfull[xs]), xp, &ctl.abort_flag, p.status));
       if (!ok) break;
       const uint32_t a0 = sX + xs * (BM * BK * 2);
-      for_each_run(off, ad, p.q.num_seg, m0, m1, [&](int lo, int hi, int) {
+      for (int i = 0; i < n; ++i) {
         ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.ffull[fs]), fp, &ctl.abort_flag, p.status));
-        if (!ok) return false;
+        if (!ok) break;
         tc_fence_after();
         if (lane == 0) {
+          const Run run = unpack_run(ctl.runs[1][i]);
           const uint32_t b0 = sF + fs * p.f_bytes;
-          const LaneMask m = lane_mask(lo - m0, hi - m0);
+          const LaneMask m = lane_mask(run.lo, run.hi);
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
             mma_bf16_lanes(tmem, sdesc(a0 + kk * 32, 16, 1024),
@@ -320,8 +359,7 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
         }
         __syncwarp();
         if (++fs == p.f_stages) { fs = 0; fp ^= 1u; }
-        return true;
-      });
+      }
       if (lane == 0) mma_commit(smem_u32(&ctl.xempty[xs]));
       __syncwarp();
       if (++xs == kShrinkX) { xs = 0; xp ^= 1u; }
@@ -406,7 +444,7 @@ __global__ void __launch_bounds__(kGemvWarps * 32) adapter_gemv_kernel(const Gem
   pdl_trigger();
   extern __shared__ int tab[];
   int* off = tab;
-  int* ad = off + p.q.num_seg + 1;
+  int16_t* ad = reinterpret_cast<int16_t*>(off + p.q.num_seg + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x;
   const int j0 = (blockIdx.y * kGemvWarps + warp) * kGemvRanks;
@@ -416,8 +454,7 @@ __global__ void __launch_bounds__(kGemvWarps * 32) adapter_gemv_kernel(const Gem
 #pragma unroll
   for (int u = 0; u < 4; ++u) xv[u] = u * 32 + lane < nv ? __ldg(x + u * 32 + lane) : make_uint4(0, 0, 0, 0);
   load_requests(p.q, off, ad, p.status);
-  const int s = first_request(off, p.q.num_seg, t);
-  const int a = s < p.q.num_seg && off[s] <= t ? ad[s] : -1;
+  const int a = adapter_of_row(off, ad, p.q.num_seg, t);
   const int rp = plane_cols(p.r), hp = hidden_pitch(p.r);
   if (j0 >= rp) return;
   float sum[kGemvRanks] = {0.f, 0.f};
@@ -514,17 +551,18 @@ struct WideCfg {
   static constexpr size_t smem(int a_rows, int stages) {
     // the MMA reads 128 rows from a hidden block's start, however few it holds
     return 1024 + (size_t)stages * (a_rows * BK * 2 + B_BYTES) + (size_t)((VBUF - 1) * a_rows + BM) * BK * 2 + EP_BYTES +
-           (2 * kMaxSegments + 4) * 4;
+           table_bytes(kMaxSegments);
   }
 };
-static_assert(WideCfg<256, false>::smem(BM, 4) <= kSmemMax - 1024 && WideCfg<128, false>::smem(BM, 5) <= kSmemMax - 1024 &&
-                  WideCfg<64, false>::smem(BM, 6) <= kSmemMax - 1024,
+static_assert(WideCfg<256, false>::smem(BM, 4) <= kSmemMax - 2048 && WideCfg<128, false>::smem(BM, 5) <= kSmemMax - 2048 &&
+                  WideCfg<64, false>::smem(BM, 6) <= kSmemMax - 2048,
               "shared memory budget exceeded");
 
 struct WideCtl {
   unsigned long long full[kWideStagesMax], empty[kWideStagesMax], tfull[2], tempty[2], vfull, vempty, drain;
   uint32_t tmem_base;
   int abort_flag;
+  uint32_t runs[3][BM];  // of the tile that each of the three feeding warps is at
 };
 
 template <int BN, bool kMN, bool kSplit>
@@ -549,7 +587,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
   const uint32_t sV = base + nst * stage_bytes;
   uint8_t* ep = bytes + (size_t)nst * stage_bytes + (C::VBUF - 1) * a_bytes + BM * BK * 2;
   int* off = reinterpret_cast<int*>(ep + C::EP_BYTES);
-  int* ad = off + p.q.num_seg + 1;
+  int16_t* ad = reinterpret_cast<int16_t*>(off + p.q.num_seg + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   load_requests(p.q, off, ad, p.status);
   if (threadIdx.x == 0) {
@@ -604,28 +642,21 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
     return {t / p.n_tiles * BM, t % p.n_tiles * BN + ((u - p.full) & 1) * (BN / 2), BN / 2};
   };
   const int u0 = kSplit ? 0 : blockIdx.x, u1 = kSplit ? 1 : p.units, du = kSplit ? 1 : gridDim.x;
-  // this CTA's runs of a tile
-  auto my_runs = [&](int m0, auto&& f) {
-    int i = 0;
-    for_each_run(off, ad, p.q.num_seg, m0, min(p.q.T, m0 + BM), [&](int lo, int hi, int a) {
-      if (kSplit && i++ % nrank != rank) return true;
-      return f(lo, hi, a);
-    });
-  };
-  auto any_run = [&](int m0) {
-    bool any = false;
-    my_runs(m0, [&](int, int, int) { any = true; return false; });
-    return any;
+  // this CTA's runs of a tile: every nrank-th
+  const int r0 = rank, dr = nrank;
+  auto runs_of = [&](int m0, int who) {
+    return p.q.num_seg == 0 ? 0 : build_runs(off, ad, p.q.num_seg, m0, min(p.q.T, m0 + BM), ctl.runs[who]);
   };
 
   if (warp == 0) {
-    if (lane == 0) {
-      int st = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      auto next = [&]() { if (++st == nst) { st = 0; ph ^= 1u; } };
-      for (int u = u0; ok && u < u1; u += du) {
-        const Unit t = unit_at(u);
+    int st = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    auto next = [&]() { if (++st == nst) { st = 0; ph ^= 1u; } };
+    for (int u = u0; ok && u < u1; u += du) {
+      const Unit t = unit_at(u);
+      const int n = runs_of(t.m0, 0);
+      if (lane == 0) {
         const uint32_t b_bytes = (uint32_t)t.bn * BK * 2;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!(ok = wait_bar(smem_u32(&ctl.empty[st]), ph ^ 1u, &ctl.abort_flag, p.status))) break;
@@ -642,8 +673,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
         }
         for (int ps = 0; ok && ps < passes; ++ps) {
           const int c = ps / psplit * 64;  // F's columns (ranks) of this pass
-          my_runs(t.m0, [&](int, int, int a) {
-            if (!(ok = wait_bar(smem_u32(&ctl.empty[st]), ph ^ 1u, &ctl.abort_flag, p.status))) return false;
+          for (int i = r0; i < n; i += dr) {
+            const int a = unpack_run(ctl.runs[0][i]).a;
+            if (!(ok = wait_bar(smem_u32(&ctl.empty[st]), ph ^ 1u, &ctl.abort_flag, p.status))) break;
             const uint32_t fb = smem_u32(&ctl.full[st]), sB = base + st * stage_bytes + a_bytes;
             mbar_arrive_expect_tx(fb, b_bytes);
             for (int h = 0; h < t.bn / C::WB; ++h) {
@@ -653,28 +685,28 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
                 tma_load_2d(sB + h * (C::WB * BK * 2), &tmF, fb, c, a * p.f_rows + t.n0 + h * C::WB);
             }
             next();
-            return true;
-          });
+          }
         }
       }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
   } else if (warp == 6) {
-    if (lane == 0) {
-      if (p.has_hidden) pdl_wait();  // also: the grid may not end before the narrow kernel does
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int u = u0; ok && u < u1; u += du) {
-        const Unit t = unit_at(u);
-        if (!any_run(t.m0)) continue;
-        for (int ps = 0; ok && ps < passes; ++ps, ph ^= 1u) {
-          ok = wait_bar(smem_u32(&ctl.vempty), ph ^ 1u, &ctl.abort_flag, p.status);
-          if (!ok) break;
+    if (p.has_hidden) pdl_wait();  // also: the grid may not end before the narrow kernel does
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int u = u0; ok && u < u1; u += du) {
+      const Unit t = unit_at(u);
+      if (runs_of(t.m0, 2) <= r0) continue;
+      if (lane == 0) {
+        for (int ps = 0; ps < passes; ++ps, ph ^= 1u) {
+          if (!(ok = wait_bar(smem_u32(&ctl.vempty), ph ^ 1u, &ctl.abort_flag, p.status))) break;
           const uint32_t fb = smem_u32(&ctl.vfull);
           mbar_arrive_expect_tx(fb, vset * a_bytes);
           for (int v = 0; v < vset; ++v)
             tma_load_2d(sV + v * a_bytes, &tmH, fb, (ps % psplit + v) * rp + ps / psplit * 64, t.m0);
         }
       }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
   } else if (warp == 1) {
     int st = 0, local = 0;
@@ -685,6 +717,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
       const Unit t = unit_at(u);
       const uint32_t idesc = t.bn == BN ? p.idesc : p.idesc_half;
       const int buf = local & 1;
+      const int n = runs_of(t.m0, 1);
       ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.tempty[buf]), ((local >> 1) & 1) ^ 1, &ctl.abort_flag, p.status));
       if (!ok) break;
       tc_fence_after();
@@ -706,19 +739,20 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
         next();
       }
       if (!ok) break;
-      if (any_run(t.m0)) {
+      if (n > r0) {
         for (int ps = 0; ok && ps < passes; ++ps, vph ^= 1u) {
           ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.vfull), vph, &ctl.abort_flag, p.status));
           if (!ok) break;
           const int steps = min(4, (p.r - ps / psplit * 64 + 15) / 16);  // 16-wide steps of this block of F
           const int parts = one_block ? kWidePlanes : C::VBUF;           // of hidden, in this pass
           const int pstep = one_block ? rp * 2 : a_bytes;                // bytes from one to the next
-          my_runs(t.m0, [&](int lo, int hi, int) {
+          for (int i = r0; i < n; i += dr) {
             ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.full[st]), ph, &ctl.abort_flag, p.status));
-            if (!ok) return false;
+            if (!ok) break;
             tc_fence_after();
             if (lane == 0) {
-              const LaneMask m = lane_mask(lo - t.m0, hi - t.m0);
+              const Run run = unpack_run(ctl.runs[1][i]);
+              const LaneMask m = lane_mask(run.lo, run.hi);
               const uint32_t b0 = base + st * stage_bytes + a_bytes;
               for (int pl = 0; pl < parts; ++pl)
                 for (int kk = 0; kk < steps; ++kk)
@@ -729,8 +763,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
             }
             __syncwarp();
             next();
-            return true;
-          });
+          }
           if (ok && lane == 0) mma_commit(smem_u32(&ctl.vempty));
           __syncwarp();
         }
@@ -849,7 +882,7 @@ struct GradCtl {
 
 // Shared-memory table: rows of each adapter -> first part of each adapter
 // (first[num_adapters] = all parts).
-__device__ __forceinline__ void load_parts(const Reqs& q, const int* off, const int* ad, int part_rows, int* rows, int* first) {
+__device__ __forceinline__ void load_parts(const Reqs& q, const int* off, const int16_t* ad, int part_rows, int* rows, int* first) {
   for (int a = threadIdx.x; a < q.num_adapters; a += blockDim.x) rows[a] = 0;
   __syncthreads();
   for (int s = threadIdx.x; s < q.num_seg; s += blockDim.x)
@@ -876,7 +909,7 @@ __device__ __forceinline__ void load_parts(const Reqs& q, const int* off, const 
 
 // f(first row, valid rows <= 64) -> bool for the blocks of part `part` of adapter a.
 template <class F>
-__device__ __forceinline__ void for_each_block(const Reqs& q, const int* off, const int* ad, int a, int part, int part_rows, F&& f) {
+__device__ __forceinline__ void for_each_block(const Reqs& q, const int* off, const int16_t* ad, int a, int part, int part_rows, F&& f) {
   const long long lo = (long long)part * part_rows, hi = lo + part_rows;
   long long at = 0;  // adapter rows before request s
   for (int s = 0; s < q.num_seg && at < hi; ++s) {
@@ -914,8 +947,8 @@ __global__ void __launch_bounds__(192) adapter_grad_kernel(const __grid_constant
   const int nmma = hc > 256 ? 2 : 1;                 // MMAs (column halves) of a step
   const int stage_bytes = BM * BK * 2 + nck * CHUNK_BYTES;
   int* off = reinterpret_cast<int*>(bytes + (size_t)p.stages * stage_bytes);
-  int* ad = off + p.q.num_seg + 1;
-  int* rows = ad + p.q.num_seg;
+  int16_t* ad = reinterpret_cast<int16_t*>(off + p.q.num_seg + 1);
+  int* rows = reinterpret_cast<int*>(ad + (p.q.num_seg + 1) / 2 * 2);
   int* first = rows + p.q.num_adapters;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bufs = hc <= 96 ? 2 : 1;
@@ -1083,8 +1116,8 @@ __global__ void __launch_bounds__(256) adapter_grad_sum_kernel(const GradParams 
   pdl_trigger();
   extern __shared__ int tab[];
   int* off = tab;
-  int* ad = off + p.q.num_seg + 1;
-  int* rows = ad + p.q.num_seg;
+  int16_t* ad = reinterpret_cast<int16_t*>(off + p.q.num_seg + 1);
+  int* rows = reinterpret_cast<int*>(ad + (p.q.num_seg + 1) / 2 * 2);
   int* first = rows + p.q.num_adapters;
   load_requests(p.q, off, ad, p.status);
   load_parts(p.q, off, ad, p.part_rows, rows, first);
@@ -1146,7 +1179,7 @@ int set_smem(const void* kern, bool* done, const char* fn) {
   const int dev = current_device();
   if (dev < 0) return fail(MOE_ERR_CUDA, "%s: no current CUDA device", fn);
   if (done[dev]) return MOE_OK;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax - 1024);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax - 2048);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
   done[dev] = true;
   return MOE_OK;
@@ -1205,7 +1238,7 @@ int run_shrink(const char* fn, const Reqs& q, const void* in, long long ld, cons
   p.tmem_cols = p.rN <= 32 ? 32 : (p.rN <= 64 ? 64 : 128);
   p.status = status_word();
   // one 16-row block of slack: an F block of r rows is read as rN
-  const size_t smem = 1024 + kShrinkX * (BM * BK * 2) + (size_t)p.f_stages * p.f_bytes + 2048 + (2 * q.num_seg + 2) * 4;
+  const size_t smem = 1024 + kShrinkX * (BM * BK * 2) + (size_t)p.f_stages * p.f_bytes + 2048 + table_bytes(q.num_seg);
   return launch_adapter(fn, kern, dim3(cs, tiles), 192, smem, cs, s, tx, tf, p);
 }
 
@@ -1262,7 +1295,7 @@ int run_wide_bn(const char* fn, const Reqs& q, const void* in, long long ld, con
   p.stages = C::STAGES;
   if (kSplit) {
     // a slice's blocks all in flight where they fit; four hold the accumulator afterwards
-    while (p.stages < kWideStagesMax && C::smem(p.a_rows, p.stages + 1) <= kSmemMax - 1024) ++p.stages;
+    while (p.stages < kWideStagesMax && C::smem(p.a_rows, p.stages + 1) <= kSmemMax - 2048) ++p.stages;
     return launch_adapter(fn, kern, dim3(nrank, p.n_tiles, rows), kWideThreads, C::smem(p.a_rows, p.stages), nrank, s, tx, tw,
                           th, tf, to, p);
   }
@@ -1294,7 +1327,7 @@ int run_gemv(const char* fn, const Reqs& q, const void* x, long long ldx, const 
   const GemvParams p{q, static_cast<const __nv_bfloat16*>(x), ldx, static_cast<const __nv_bfloat16*>(A), scale, K, r,
                      static_cast<__nv_bfloat16*>(hidden), status_word()};
   const dim3 grid(q.T, (plane_cols(r) + kGemvWarps * kGemvRanks - 1) / (kGemvWarps * kGemvRanks));
-  return launch_adapter(fn, adapter_gemv_kernel, grid, kGemvWarps * 32, sizeof(int) * (size_t)(2 * q.num_seg + 2), 0, s, p);
+  return launch_adapter(fn, adapter_gemv_kernel, grid, kGemvWarps * 32, table_bytes(q.num_seg), 0, s, p);
 }
 
 int check_adapter(const char* fn, const Reqs& q, int K, int N, int r, long long ldx, long long ldy) {
@@ -1431,7 +1464,7 @@ int moe_adapter_linear_bwd(const void* dy, long long lddy, const void* x, long l
   if (int rc = map_mn(&tu, u, hp, T, hp, nck)) return rc;
   if (int rc = map_mn(&td, dy, N, T, lddy, 2)) return rc;
   if (int rc = map_mn(&tv, hidden, hp, T, hp, nck)) return rc;
-  const size_t table = sizeof(int) * (size_t)(2 * num_seg + 2 + 2 * num_adapters + 2);
+  const size_t table = table_bytes(num_seg) + sizeof(int) * (size_t)(2 * num_adapters + 2);
   const size_t smem = 1024 + (size_t)p.stages * (BM * BK * 2 + nck * CHUNK_BYTES) + table;
   const int per_sm = nck <= 2 ? 2 : 1;
   const long long most = ((long long)T / kPartRows + num_seg) * (p.tiles_a + p.tiles_b);
