@@ -112,7 +112,7 @@ __device__ __forceinline__ int first_request(const int* off, int num_seg, int t)
   return lo;
 }
 
-// A run: rows lo <= row - m0 < hi of a 128-row tile with one adapter;
+// A run: rows lo <= row - m0 < hi of a tile with one adapter;
 // neighbouring requests with the same adapter are one run.
 struct Run {
   int lo, hi, a;
@@ -127,23 +127,25 @@ __device__ __forceinline__ int adapter_of_row(const int* off, const int16_t* ad,
   return s < num_seg && off[s] <= t ? ad[s] : -1;
 }
 
-// The runs of tile [m0, m1) in row order into list (BM entries); returns how
-// many.  A warp's common work: each lane looks four rows up, run starts are
-// found and numbered by ballots (walking the table request by request took
-// 0.07 us a request, more than the run's products).
+// The runs of a tile of 32 NW rows from m0, those below m1, in row order into
+// list (32 NW entries); returns how many.  A warp's common work: each lane
+// looks NW rows up, run starts are found and numbered by ballots (walking the
+// table request by request took 0.07 us a request, more than the run's
+// products).
+template <int NW>
 __device__ __forceinline__ int build_runs(const int* off, const int16_t* ad, int num_seg, int m0, int m1, uint32_t* list) {
   const int lane = threadIdx.x & 31;
   __syncwarp();  // the list's last reader is done
-  int a[4];
+  int a[NW];
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < NW; ++w) {
     const int t = m0 + 32 * w + lane;
     a[w] = t < m1 ? adapter_of_row(off, ad, num_seg, t) : -1;
   }
-  uint32_t start[4], brk[4];
+  uint32_t start[NW], brk[NW];
   int before = -1;  // adapter of the row before this word
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < NW; ++w) {
     const int up = __shfl_up_sync(0xffffffffu, a[w], 1);
     const int prev = lane == 0 ? before : up;
     start[w] = __ballot_sync(0xffffffffu, a[w] >= 0 && a[w] != prev);
@@ -152,14 +154,14 @@ __device__ __forceinline__ int build_runs(const int* off, const int16_t* ad, int
   }
   int n = 0;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < NW; ++w) {
     if ((start[w] >> lane) & 1u) {
       const uint32_t later = lane == 31 ? 0u : brk[w] & (0xffffffffu << (lane + 1));
       int hi = later ? 32 * w + __ffs(later) - 1 : -1;
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
+      for (int v = 0; v < NW; ++v)
         if (v > w && hi < 0 && brk[v]) hi = 32 * v + __ffs(brk[v]) - 1;
-      if (hi < 0) hi = BM;
+      if (hi < 0) hi = 32 * NW;
       list[n + __popc(start[w] & ((1u << lane) - 1u))] = (uint32_t)(32 * w + lane) | (uint32_t)(hi - 1) << 8 | (uint32_t)a[w] << 16;
     }
     n += __popc(start[w]);
@@ -176,16 +178,23 @@ __device__ __forceinline__ uint32_t lanes_off(int lo, int hi, int w) {
   return ~(below_b & ~((1u << a) - 1u));
 }
 
+// Lane mask of a tile of 128 rows (one CTA) or 256 (a pair: the second CTA's
+// 128 lanes in words 4..7).
+template <int CTAS>
 struct LaneMask {
-  uint32_t w[4];
+  uint32_t w[4 * CTAS];
 };
-__device__ __forceinline__ LaneMask lane_mask(int lo, int hi) {
-  return {{lanes_off(lo, hi, 0), lanes_off(lo, hi, 1), lanes_off(lo, hi, 2), lanes_off(lo, hi, 3)}};
+template <int CTAS>
+__device__ __forceinline__ LaneMask<CTAS> lane_mask(int lo, int hi) {
+  LaneMask<CTAS> m;
+#pragma unroll
+  for (int i = 0; i < 4 * CTAS; ++i) m.w[i] = lanes_off(lo, hi, i);
+  return m;
 }
 
-// mma_bf16 that leaves the accumulator rows of masked lanes as they are.
-__device__ __forceinline__ void mma_bf16_lanes(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
-                                               const LaneMask& m) {
+// D (+)= A B that leaves the accumulator rows of masked lanes as they are.
+__device__ __forceinline__ void mma_lanes(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                          const LaneMask<1>& m) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
@@ -193,14 +202,32 @@ __device__ __forceinline__ void mma_bf16_lanes(uint32_t d, uint64_t a, uint64_t 
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(m.w[0]), "r"(m.w[1]), "r"(m.w[2]), "r"(m.w[3])
       : "memory");
 }
+__device__ __forceinline__ void mma_lanes(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                          const LaneMask<2>& m) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8, %9, %10, %11, %12}, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(m.w[0]), "r"(m.w[1]), "r"(m.w[2]), "r"(m.w[3]), "r"(m.w[4]),
+      "r"(m.w[5]), "r"(m.w[6]), "r"(m.w[7])
+      : "memory");
+}
 
+template <int CTAS>
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
                                             int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-      : "memory");
+  if constexpr (CTAS == 1)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
 }
 
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
@@ -308,7 +335,7 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
   const int kb0 = (int)((long long)nkb * rank / nrank), kb1 = (int)((long long)nkb * (rank + 1) / nrank);
 
   if (warp == 0) {
-    const int n = build_runs(off, ad, p.q.num_seg, m0, m1, ctl.runs[0]);
+    const int n = build_runs<4>(off, ad, p.q.num_seg, m0, m1, ctl.runs[0]);
     if (lane == 0 && n > 0) {
       int xs = 0, fs = 0;
       uint32_t xp = 0, fp = 0;
@@ -334,7 +361,7 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
       }
     }
   } else if (warp == 1) {
-    const int n = build_runs(off, ad, p.q.num_seg, m0, m1, ctl.runs[1]);
+    const int n = build_runs<4>(off, ad, p.q.num_seg, m0, m1, ctl.runs[1]);
     int xs = 0, fs = 0;
     uint32_t xp = 0, fp = 0;
     bool ok = true;
@@ -349,10 +376,10 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
         if (lane == 0) {
           const Run run = unpack_run(ctl.runs[1][i]);
           const uint32_t b0 = sF + fs * p.f_bytes;
-          const LaneMask m = lane_mask(run.lo, run.hi);
+          const LaneMask<1> m = lane_mask<1>(run.lo, run.hi);
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
-            mma_bf16_lanes(tmem, sdesc(a0 + kk * 32, 16, 1024),
+            mma_lanes(tmem, sdesc(a0 + kk * 32, 16, 1024),
                            kMN ? sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024) : sdesc(b0 + kk * 32, 16, 1024), p.idesc,
                            kb > kb0 || kk > 0, m);
           mma_commit(smem_u32(&ctl.fempty[fs]));
@@ -508,14 +535,18 @@ __global__ void __launch_bounds__(kGemvWarps * 32) adapter_gemv_kernel(const Gem
 // ------------------------------------------------------------- wide product
 //
 // out[128 rows x BN] = in W^T (kMN: in W) + hidden F.  A TMA warp streams the
-// blocks of in and W and then, run by run, those of F; one warp loads hidden's
-// blocks of the tile (once, whatever the number of runs); one warp issues the
-// MMAs; four warps write the tile out.
+// blocks of in and W and then, run by run, those of F; one warp lists the next
+// tile's runs (a search that cost 2.4 us a tile where the TMA and MMA warps did
+// it themselves) and loads hidden's blocks of the tile, once, whatever the
+// number of runs; one warp issues the MMAs; four warps write the tile out.
 //
-// Whole tiles (kSplit false): one CTA per SM over the tiles, two accumulators,
-// so that a tile's epilogue runs beside the next one's MMAs.  256-column tiles
-// whose last wave would fill less than half of the SMs give that wave as
-// 128-column halves.
+// Whole tiles (kSplit false): persistent over the tiles, two accumulators, so
+// that a tile's epilogue runs beside the next one's MMAs.  256-column tiles run
+// as CTA pairs on 256 rows (tcgen05 cta_group::2: each CTA holds its 128 rows
+// of in and half of W's columns, the leader issues the MMAs): one CTA per
+// 128 x 256 tile was bound by the 48 KB it loads per block, 18 TB/s over all
+// SMs, where a pair's CTA loads 32.  When their last wave would fill less than
+// half of the SMs it is given out as 128-column halves.
 //
 // kSplit: for so few rows that the tiles do not fill the SMs.  A cluster shares
 // one tile: each CTA takes a slice of the reduction and every nrank-th run, and
@@ -542,27 +573,29 @@ constexpr int kWideThreads = 224;
 
 template <int BN, bool kSplit>
 struct WideCfg {
-  static constexpr int WB = BN < 128 ? BN : 128;  // W rows (columns) of one TMA box
-  static constexpr int B_BYTES = BN * BK * 2;
-  static constexpr int VBUF = BN == 256 ? 1 : 2;  // hidden blocks held at a time
-  static constexpr int EP = BN == 256 ? 1 : EP_SLOTS;
-  static constexpr int EP_BYTES = kSplit ? 0 : 4 * EP * EP_BOX_BYTES;
-  static constexpr int STAGES = BN == 256 ? 4 : (BN == 128 ? 5 : 6);
+  static constexpr int CTAS = BN == 256 ? 2 : 1;
+  static constexpr int B_BYTES = BN / CTAS * BK * 2;       // a CTA's share of a block of W
+  static constexpr int WB = BN / CTAS > 64 && CTAS == 1 ? BN : 64;  // W rows (columns) of one TMA box
+  static constexpr int VBUF = 2;                  // hidden blocks held at a time
+  static constexpr int EP_BYTES = kSplit ? 0 : 4 * EP_SLOTS * EP_BOX_BYTES;
+  static constexpr int STAGES = BN == 64 ? 6 : 5;
   static constexpr size_t smem(int a_rows, int stages) {
     // the MMA reads 128 rows from a hidden block's start, however few it holds
     return 1024 + (size_t)stages * (a_rows * BK * 2 + B_BYTES) + (size_t)((VBUF - 1) * a_rows + BM) * BK * 2 + EP_BYTES +
            table_bytes(kMaxSegments);
   }
 };
-static_assert(WideCfg<256, false>::smem(BM, 4) <= kSmemMax - 2048 && WideCfg<128, false>::smem(BM, 5) <= kSmemMax - 2048 &&
-                  WideCfg<64, false>::smem(BM, 6) <= kSmemMax - 2048,
+constexpr size_t kAdapterSmem = kSmemMax - 4096;  // dynamic; the rest is for static tables
+static_assert(WideCfg<256, false>::smem(BM, 5) <= kAdapterSmem && WideCfg<128, false>::smem(BM, 5) <= kAdapterSmem &&
+                  WideCfg<64, false>::smem(BM, 6) <= kAdapterSmem,
               "shared memory budget exceeded");
 
 struct WideCtl {
-  unsigned long long full[kWideStagesMax], empty[kWideStagesMax], tfull[2], tempty[2], vfull, vempty, drain;
+  unsigned long long full[kWideStagesMax], empty[kWideStagesMax], tfull[2], tempty[2], lfull[2], lempty[2], vfull, vempty, drain;
   uint32_t tmem_base;
   int abort_flag;
-  uint32_t runs[3][BM];  // of the tile that each of the three feeding warps is at
+  int num_runs[2];
+  uint32_t runs[2][2 * BM];  // of this tile and the next
 };
 
 template <int BN, bool kMN, bool kSplit>
@@ -573,6 +606,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
                                                                        const __grid_constant__ CUtensorMap tmO,
                                                                        const WideParams p) {
   using C = WideCfg<BN, kSplit>;
+  constexpr int CTAS = C::CTAS;
   // The narrow kernel of this call waited for everything before it and lets
   // this one start early; x, W and the request table are older than it, so only
   // hidden has to be waited for.
@@ -589,6 +623,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
   int* off = reinterpret_cast<int*>(ep + C::EP_BYTES);
   int16_t* ad = reinterpret_cast<int16_t*>(off + p.q.num_seg + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pair_rank = CTAS == 2 ? (int)cluster_rank() : 0;
+  const bool leader = pair_rank == 0;
   load_requests(p.q, off, ad, p.status);
   if (threadIdx.x == 0) {
     for (int i = 0; i < nst; ++i) {
@@ -597,7 +633,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ctl.tfull[i]), 1);
-      mbar_init(smem_u32(&ctl.tempty[i]), 4);
+      mbar_init(smem_u32(&ctl.tempty[i]), 4 * CTAS);
+      mbar_init(smem_u32(&ctl.lfull[i]), 1);
+      mbar_init(smem_u32(&ctl.lempty[i]), leader ? 2 : 1);  // a pair's second CTA issues no MMAs
     }
     mbar_init(smem_u32(&ctl.vfull), 1);
     mbar_init(smem_u32(&ctl.vempty), 1);
@@ -611,9 +649,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
     if (!kSplit) prefetch_tmap(&tmO);
   }
   constexpr int kTmem = kSplit ? BN : 2 * BN;
-  if (warp == 1) tmem_alloc_n<1>(smem_u32(&ctl.tmem_base), kTmem);
+  if (warp == 1) tmem_alloc_n<CTAS>(smem_u32(&ctl.tmem_base), kTmem);
   tc_fence_before();
   __syncthreads();
+  if constexpr (CTAS == 2) cluster_sync();  // peer barriers initialised before any remote signal
   tc_fence_after();
   pdl_trigger();
   const uint32_t tmem = ctl.tmem_base;
@@ -621,103 +660,118 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
   const int nkb = p.red / BK;
   const int kb0 = kSplit ? (int)((long long)nkb * rank / nrank) : 0;
   const int kb1 = kSplit ? (int)((long long)nkb * (rank + 1) / nrank) : nkb;
-  // Blocks of a run: 64 ranks of F at a time, times two parts of hidden.  Both
-  // parts share one 64-column block of hidden up to r = 32; beyond, they are two
-  // blocks, held together where there is room, else one after the other (and F's
-  // block comes twice).
+  // Passes: 64 ranks of F at a time, times two parts of hidden, which share one
+  // 64-column block up to r = 32 and are two blocks beyond.
   const int rp = plane_cols(p.r);
   const bool one_block = kWidePlanes * rp <= 64;
-  const int fblk = (p.r + 63) / 64;
-  const int vset = one_block ? 1 : C::VBUF;                     // hidden blocks held at a time
-  const int passes = fblk * (one_block ? 1 : kWidePlanes / C::VBUF);
-  const int psplit = passes / fblk;                             // passes per block of F
+  const int vset = one_block ? 1 : kWidePlanes;
+  const int passes = (p.r + 63) / 64;
+  static_assert(C::VBUF == kWidePlanes, "room for both parts of hidden");
 
   struct Unit {
-    int m0, n0, bn;
+    int m0, n0, bn;  // the tile's first row (of the pair's 256) and column, its columns
   };
+  constexpr int TM = BM * CTAS;
   auto unit_at = [&](int u) -> Unit {
     if (kSplit) return {(int)blockIdx.z * BM, (int)blockIdx.y * BN, BN};
-    if (BN < 256 || u < p.full) return {u / p.n_tiles * BM, u % p.n_tiles * BN, BN};
+    if (BN < 256 || u < p.full) return {u / p.n_tiles * TM, u % p.n_tiles * BN, BN};
     const int t = p.full + (u - p.full) / 2;
-    return {t / p.n_tiles * BM, t % p.n_tiles * BN + ((u - p.full) & 1) * (BN / 2), BN / 2};
+    return {t / p.n_tiles * TM, t % p.n_tiles * BN + ((u - p.full) & 1) * (BN / 2), BN / 2};
   };
-  const int u0 = kSplit ? 0 : blockIdx.x, u1 = kSplit ? 1 : p.units, du = kSplit ? 1 : gridDim.x;
-  // this CTA's runs of a tile: every nrank-th
+  const int u0 = kSplit ? 0 : (int)blockIdx.x / CTAS, u1 = kSplit ? 1 : p.units, du = kSplit ? 1 : (int)gridDim.x / CTAS;
+  // this CTA's (pair's) runs of a tile: every nrank-th
   const int r0 = rank, dr = nrank;
-  auto runs_of = [&](int m0, int who) {
-    return p.q.num_seg == 0 ? 0 : build_runs(off, ad, p.q.num_seg, m0, min(p.q.T, m0 + BM), ctl.runs[who]);
-  };
+  const bool listed = p.q.num_seg > 0;
+  auto at_leader = [&](uint32_t bar) { return CTAS == 2 ? map_to_rank(bar, 0) : bar; };
 
   if (warp == 0) {
-    int st = 0;
-    uint32_t ph = 0;
-    bool ok = true;
-    auto next = [&]() { if (++st == nst) { st = 0; ph ^= 1u; } };
-    for (int u = u0; ok && u < u1; u += du) {
-      const Unit t = unit_at(u);
-      const int n = runs_of(t.m0, 0);
-      if (lane == 0) {
-        const uint32_t b_bytes = (uint32_t)t.bn * BK * 2;
+    if (lane == 0) {
+      int st = 0, local = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      auto next = [&]() { if (++st == nst) { st = 0; ph ^= 1u; } };
+      for (int u = u0; ok && u < u1; u += du, ++local) {
+        const Unit t = unit_at(u);
+        const int lb = local & 1;
+        const uint32_t b_bytes = (uint32_t)t.bn / CTAS * BK * 2;
+        const int row = t.m0 + pair_rank * BM, col = t.n0 + pair_rank * (t.bn / CTAS), nbox = t.bn / CTAS / C::WB;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!(ok = wait_bar(smem_u32(&ctl.empty[st]), ph ^ 1u, &ctl.abort_flag, p.status))) break;
-          const uint32_t fb = smem_u32(&ctl.full[st]), sA = base + st * stage_bytes, sB = sA + a_bytes;
-          mbar_arrive_expect_tx(fb, a_bytes + b_bytes);
-          tma_load_2d(sA, &tmX, fb, kb * BK, t.m0);
-          for (int h = 0; h < t.bn / C::WB; ++h) {
+          const uint32_t fb = at_leader(smem_u32(&ctl.full[st])), sA = base + st * stage_bytes, sB = sA + a_bytes;
+          if (leader) mbar_arrive_expect_tx(smem_u32(&ctl.full[st]), CTAS * (a_bytes + b_bytes));
+          tma_load<CTAS>(sA, &tmX, fb, kb * BK, row);
+          for (int h = 0; h < nbox; ++h) {
             if (kMN)
-              tma_load_3d(sB + h * (C::WB * BK * 2), &tmW, fb, 0, kb * BK, t.n0 / 64 + h * (C::WB / 64));
+              tma_load_mn<CTAS>(sB + h * (C::WB * BK * 2), &tmW, fb, kb * BK, col / 64 + h * (C::WB / 64));
             else
-              tma_load_2d(sB + h * (C::WB * BK * 2), &tmW, fb, kb * BK, t.n0 + h * C::WB);
+              tma_load<CTAS>(sB + h * (C::WB * BK * 2), &tmW, fb, kb * BK, col + h * C::WB);
           }
           next();
         }
+        if (!ok || !listed) continue;
+        if (!(ok = wait_bar(smem_u32(&ctl.lfull[lb]), (local >> 1) & 1, &ctl.abort_flag, p.status))) break;
+        const int n = ctl.num_runs[lb];
         for (int ps = 0; ok && ps < passes; ++ps) {
-          const int c = ps / psplit * 64;  // F's columns (ranks) of this pass
+          const int c = ps * 64;  // F's columns (ranks) of this pass
           for (int i = r0; i < n; i += dr) {
-            const int a = unpack_run(ctl.runs[0][i]).a;
+            const int a = unpack_run(ctl.runs[lb][i]).a;
             if (!(ok = wait_bar(smem_u32(&ctl.empty[st]), ph ^ 1u, &ctl.abort_flag, p.status))) break;
-            const uint32_t fb = smem_u32(&ctl.full[st]), sB = base + st * stage_bytes + a_bytes;
-            mbar_arrive_expect_tx(fb, b_bytes);
-            for (int h = 0; h < t.bn / C::WB; ++h) {
+            const uint32_t fb = at_leader(smem_u32(&ctl.full[st])), sB = base + st * stage_bytes + a_bytes;
+            if (leader) mbar_arrive_expect_tx(smem_u32(&ctl.full[st]), CTAS * b_bytes);
+            for (int h = 0; h < nbox; ++h) {
               if (kMN)
-                tma_load_4d(sB + h * (C::WB * BK * 2), &tmF, fb, 0, c, t.n0 / 64 + h * (C::WB / 64), a);
+                tma_load_4d<CTAS>(sB + h * (C::WB * BK * 2), &tmF, fb, 0, c, col / 64 + h * (C::WB / 64), a);
               else
-                tma_load_2d(sB + h * (C::WB * BK * 2), &tmF, fb, c, a * p.f_rows + t.n0 + h * C::WB);
+                tma_load<CTAS>(sB + h * (C::WB * BK * 2), &tmF, fb, c, a * p.f_rows + col + h * C::WB);
             }
             next();
           }
         }
+        mbar_arrive(smem_u32(&ctl.lempty[lb]));
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
   } else if (warp == 6) {
-    if (p.has_hidden) pdl_wait();  // also: the grid may not end before the narrow kernel does
-    uint32_t ph = 0;
-    bool ok = true;
-    for (int u = u0; ok && u < u1; u += du) {
-      const Unit t = unit_at(u);
-      if (runs_of(t.m0, 2) <= r0) continue;
-      if (lane == 0) {
-        for (int ps = 0; ps < passes; ++ps, ph ^= 1u) {
-          if (!(ok = wait_bar(smem_u32(&ctl.vempty), ph ^ 1u, &ctl.abort_flag, p.status))) break;
-          const uint32_t fb = smem_u32(&ctl.vfull);
-          mbar_arrive_expect_tx(fb, vset * a_bytes);
-          for (int v = 0; v < vset; ++v)
-            tma_load_2d(sV + v * a_bytes, &tmH, fb, (ps % psplit + v) * rp + ps / psplit * 64, t.m0);
+    if (p.has_hidden) {
+      uint32_t ph = 0;
+      int local = 0;
+      bool ok = true, waited = false;
+      for (int u = u0; ok && u < u1; u += du, ++local) {
+        const Unit t = unit_at(u);
+        const int lb = local & 1;
+        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.lempty[lb]), ((local >> 1) & 1) ^ 1, &ctl.abort_flag, p.status));
+        if (!ok) break;
+        const int n = build_runs<4 * CTAS>(off, ad, p.q.num_seg, t.m0, min(p.q.T, t.m0 + TM), ctl.runs[lb]);
+        if (lane == 0) {
+          ctl.num_runs[lb] = n;
+          mbar_arrive(smem_u32(&ctl.lfull[lb]));
         }
+        if (!waited) {
+          pdl_wait();
+          waited = true;
+        }
+        if (lane == 0 && n > r0) {
+          for (int ps = 0; ps < passes; ++ps, ph ^= 1u) {
+            if (!(ok = wait_bar(smem_u32(&ctl.vempty), ph ^ 1u, &ctl.abort_flag, p.status))) break;
+            const uint32_t fb = at_leader(smem_u32(&ctl.vfull));
+            if (leader) mbar_arrive_expect_tx(smem_u32(&ctl.vfull), CTAS * vset * a_bytes);
+            for (int v = 0; v < vset; ++v)
+              tma_load<CTAS>(sV + v * a_bytes, &tmH, fb, v * rp + ps * 64, t.m0 + pair_rank * BM);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!waited) pdl_wait();  // the grid may not end before the narrow kernel does
     }
   } else if (warp == 1) {
     int st = 0, local = 0;
     uint32_t ph = 0, vph = 0;
     bool ok = true;
     auto next = [&]() { if (++st == nst) { st = 0; ph ^= 1u; } };
-    for (int u = u0; ok && u < u1; u += du, ++local) {
+    // a pair's second CTA only keeps its tensor memory
+    for (int u = u0; leader && ok && u < u1; u += du, ++local) {
       const Unit t = unit_at(u);
       const uint32_t idesc = t.bn == BN ? p.idesc : p.idesc_half;
       const int buf = local & 1;
-      const int n = runs_of(t.m0, 1);
       ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.tempty[buf]), ((local >> 1) & 1) ^ 1, &ctl.abort_flag, p.status));
       if (!ok) break;
       tc_fence_after();
@@ -730,50 +784,58 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
           const uint32_t a0 = base + st * stage_bytes, b0 = a0 + a_bytes;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
-            mma_bf16(d, sdesc(a0 + kk * 32, 16, 1024),
-                     kMN ? sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024) : sdesc(b0 + kk * 32, 16, 1024), idesc,
-                     kb > kb0 || kk > 0);
-          mma_commit(smem_u32(&ctl.empty[st]));
+            mma_issue<CTAS>(d, sdesc(a0 + kk * 32, 16, 1024),
+                            kMN ? sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024) : sdesc(b0 + kk * 32, 16, 1024), idesc,
+                            kb > kb0 || kk > 0);
+          mma_commit_to<CTAS>(smem_u32(&ctl.empty[st]));
         }
         __syncwarp();
         next();
       }
       if (!ok) break;
+      const int lb = local & 1;
+      if (listed) {
+        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.lfull[lb]), (local >> 1) & 1, &ctl.abort_flag, p.status));
+        if (!ok) break;
+      }
+      const int n = listed ? ctl.num_runs[lb] : 0;
       if (n > r0) {
         for (int ps = 0; ok && ps < passes; ++ps, vph ^= 1u) {
           ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.vfull), vph, &ctl.abort_flag, p.status));
           if (!ok) break;
-          const int steps = min(4, (p.r - ps / psplit * 64 + 15) / 16);  // 16-wide steps of this block of F
-          const int parts = one_block ? kWidePlanes : C::VBUF;           // of hidden, in this pass
-          const int pstep = one_block ? rp * 2 : a_bytes;                // bytes from one to the next
+          const int steps = min(4, (p.r - ps * 64 + 15) / 16);  // 16-wide steps of this block of F
+          const int pstep = one_block ? rp * 2 : a_bytes;        // bytes from one part of hidden to the next
           for (int i = r0; i < n; i += dr) {
             ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.full[st]), ph, &ctl.abort_flag, p.status));
             if (!ok) break;
             tc_fence_after();
             if (lane == 0) {
-              const Run run = unpack_run(ctl.runs[1][i]);
-              const LaneMask m = lane_mask(run.lo, run.hi);
+              const Run run = unpack_run(ctl.runs[lb][i]);
+              const LaneMask<CTAS> m = lane_mask<CTAS>(run.lo, run.hi);
               const uint32_t b0 = base + st * stage_bytes + a_bytes;
-              for (int pl = 0; pl < parts; ++pl)
+              for (int pl = 0; pl < kWidePlanes; ++pl)
                 for (int kk = 0; kk < steps; ++kk)
-                  mma_bf16_lanes(d, sdesc(sV + pl * pstep + kk * 32, 16, 1024),
-                                 kMN ? sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024) : sdesc(b0 + kk * 32, 16, 1024), idesc,
-                                 1u, m);
-              mma_commit(smem_u32(&ctl.empty[st]));
+                  mma_lanes(d, sdesc(sV + pl * pstep + kk * 32, 16, 1024),
+                            kMN ? sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024) : sdesc(b0 + kk * 32, 16, 1024), idesc, 1u, m);
+              mma_commit_to<CTAS>(smem_u32(&ctl.empty[st]));
             }
             __syncwarp();
             next();
           }
-          if (ok && lane == 0) mma_commit(smem_u32(&ctl.vempty));
+          if (ok && lane == 0) mma_commit_to<CTAS>(smem_u32(&ctl.vempty));
           __syncwarp();
         }
       }
       if (!ok) break;
-      if (lane == 0) mma_commit(smem_u32(&ctl.tfull[buf]));
+      __syncwarp();
+      if (lane == 0) {
+        if (listed) mbar_arrive(smem_u32(&ctl.lempty[lb]));
+        mma_commit_to<CTAS>(smem_u32(&ctl.tfull[buf]));
+      }
       __syncwarp();
     }
     if (!ok) {  // drain MMAs still in flight before TMEM is released
-      if (lane == 0) mma_commit(smem_u32(&ctl.drain));
+      if (lane == 0) mma_commit_to<CTAS>(smem_u32(&ctl.drain));
       __syncwarp();
       const unsigned long long t0 = globaltimer();
       while (!mbar_try_wait(smem_u32(&ctl.drain), 0) && globaltimer() - t0 < TIMEOUT_NS) {
@@ -795,11 +857,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
     }
   } else {
     const int q = warp & 3;
-    EpRing<C::EP> ring{ep + (size_t)(warp - 2) * C::EP * EP_BOX_BYTES, 0, lane};
+    EpRing<EP_SLOTS> ring{ep + (size_t)(warp - 2) * EP_SLOTS * EP_BOX_BYTES, 0, lane};
+    const uint32_t tempty[2] = {at_leader(smem_u32(&ctl.tempty[0])), at_leader(smem_u32(&ctl.tempty[1]))};
     int local = 0;
     for (int u = u0; u < u1; u += du, ++local) {
       const Unit t = unit_at(u);
-      const int rb = t.m0 + q * 32;
+      const int rb = t.m0 + pair_rank * BM + q * 32;
       const int buf = local & 1;
       if (!__all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.tfull[buf]), (local >> 1) & 1, &ctl.abort_flag, p.status))) break;
       tc_fence_after();
@@ -818,14 +881,20 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&ctl.tempty[buf]));
+      if (lane == 0) {
+        if (CTAS == 1)
+          mbar_arrive(tempty[buf]);
+        else
+          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(tempty[buf]) : "memory");
+      }
     }
     ring.drain();
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (CTAS == 2) cluster_sync();  // neither CTA frees tensor memory while the pair still uses it
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_n<1>(tmem, kTmem);
+  if (warp == 1) tmem_dealloc_n<CTAS>(tmem, kTmem);
   if constexpr (kSplit) {
     cluster_sync();
     // this CTA's share of the columns: the slices' sums in order
@@ -1179,7 +1248,7 @@ int set_smem(const void* kern, bool* done, const char* fn) {
   const int dev = current_device();
   if (dev < 0) return fail(MOE_ERR_CUDA, "%s: no current CUDA device", fn);
   if (done[dev]) return MOE_OK;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax - 2048);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAdapterSmem);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
   done[dev] = true;
   return MOE_OK;
@@ -1282,24 +1351,25 @@ int run_wide_bn(const char* fn, const Reqs& q, const void* in, long long ld, con
   p.r = r;
   p.f_rows = out_cols;
   p.n_tiles = out_cols / BN;
-  const int rows = (q.T + BM - 1) / BM, tiles = rows * p.n_tiles;
-  const int rest = BN == 256 ? tiles % sms : 0;
-  p.full = rest > 0 && 2 * rest <= sms ? tiles - rest : tiles;
+  const int tm = BM * C::CTAS, rows = (q.T + tm - 1) / tm, tiles = rows * p.n_tiles, places = sms / C::CTAS;
+  const int rest = BN == 256 ? tiles % places : 0;
+  p.full = rest > 0 && 2 * rest <= places ? tiles - rest : tiles;
   p.units = p.full + 2 * (tiles - p.full);
   p.has_hidden = has_hidden;
-  p.idesc = make_idesc(BN, BM, false, kMN);
-  p.idesc_half = make_idesc(BN / 2, BM, false, kMN);
+  p.idesc = make_idesc(BN, tm, false, kMN);
+  p.idesc_half = make_idesc(BN / 2, tm, false, kMN);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.ldo = ldo;
   p.status = status_word();
   p.stages = C::STAGES;
   if (kSplit) {
     // a slice's blocks all in flight where they fit; four hold the accumulator afterwards
-    while (p.stages < kWideStagesMax && C::smem(p.a_rows, p.stages + 1) <= kSmemMax - 2048) ++p.stages;
+    while (p.stages < kWideStagesMax && C::smem(p.a_rows, p.stages + 1) <= kAdapterSmem) ++p.stages;
     return launch_adapter(fn, kern, dim3(nrank, p.n_tiles, rows), kWideThreads, C::smem(p.a_rows, p.stages), nrank, s, tx, tw,
                           th, tf, to, p);
   }
-  return launch_adapter(fn, kern, dim3(p.units < sms ? p.units : sms), kWideThreads, C::smem(BM, p.stages), 0, s, tx, tw, th, tf,
+  return launch_adapter(fn, kern, dim3((p.units < places ? p.units : places) * C::CTAS), kWideThreads, C::smem(BM, p.stages),
+                        C::CTAS == 2 ? 2 : 0, s, tx, tw, th, tf,
                         to, p);
 }
 
@@ -1309,7 +1379,7 @@ int run_wide(const char* fn, const Reqs& q, const void* in, long long ld, const 
   // the widest tile that divides the columns and still gives every SM one;
   // where even the narrowest leave half of them idle, clusters along the reduction
   const int sms = sm_count() > 0 ? sm_count() : 148, rows = (q.T + BM - 1) / BM;
-  if (out_cols % 256 == 0 && rows * (out_cols / 256) >= sms)
+  if (out_cols % 256 == 0 && (q.T + 2 * BM - 1) / (2 * BM) * (out_cols / 256) >= sms / 2)
     return run_wide_bn<256, kMN, false>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, 1, s);
   if (out_cols % 128 == 0 && rows * (out_cols / 128) >= sms)
     return run_wide_bn<128, kMN, false>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, 1, s);
