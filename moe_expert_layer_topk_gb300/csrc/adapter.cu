@@ -127,21 +127,14 @@ __device__ __forceinline__ int adapter_of_row(const int* off, const int16_t* ad,
   return s < num_seg && off[s] <= t ? ad[s] : -1;
 }
 
-// The runs of a tile of 32 NW rows from m0, those below m1, in row order into
-// list (32 NW entries); returns how many.  A warp's common work: each lane
-// looks NW rows up, run starts are found and numbered by ballots (walking the
-// table request by request took 0.07 us a request, more than the run's
-// products).
+// The runs of a tile of 32 NW rows into list (32 NW entries), in row order, from
+// the adapters of rows 32 w + lane (-1: none); returns how many.  A warp's
+// common work: run starts are found and numbered by ballots (walking the table
+// request by request took 0.07 us a request, more than the run's products).
 template <int NW>
-__device__ __forceinline__ int build_runs(const int* off, const int16_t* ad, int num_seg, int m0, int m1, uint32_t* list) {
+__device__ __forceinline__ int list_runs(const int (&a)[NW], uint32_t* list) {
   const int lane = threadIdx.x & 31;
   __syncwarp();  // the list's last reader is done
-  int a[NW];
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    const int t = m0 + 32 * w + lane;
-    a[w] = t < m1 ? adapter_of_row(off, ad, num_seg, t) : -1;
-  }
   uint32_t start[NW], brk[NW];
   int before = -1;  // adapter of the row before this word
 #pragma unroll
@@ -168,6 +161,18 @@ __device__ __forceinline__ int build_runs(const int* off, const int16_t* ad, int
   }
   __syncwarp();
   return n;
+}
+
+// The same from the request table, for the rows of [m0, m1).
+template <int NW>
+__device__ __forceinline__ int build_runs(const int* off, const int16_t* ad, int num_seg, int m0, int m1, uint32_t* list) {
+  int a[NW];
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const int t = m0 + 32 * w + (threadIdx.x & 31);
+    a[w] = t < m1 ? adapter_of_row(off, ad, num_seg, t) : -1;
+  }
+  return list_runs<NW>(a, list);
 }
 
 // Word w of the MMA's lane mask (1 = lane off) that leaves rows [lo, hi) on.
@@ -230,6 +235,9 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
@@ -297,17 +305,20 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
   const uint32_t base = align1k(smem_u32(smem_raw));
   uint8_t* bytes = smem_raw + (base - smem_u32(smem_raw));
   const uint32_t sX = base, sF = base + kShrinkX * (BM * BK * 2);
-  float* acc = reinterpret_cast<float*>(bytes);  // [rN][BM], over the x blocks once they are consumed
-  int* off = reinterpret_cast<int*>(bytes + kShrinkX * (BM * BK * 2) + p.f_stages * p.f_bytes);
+  // the slices' sums of this CTA's share of the rows: [slice][rN][rows]
+  float* sums = reinterpret_cast<float*>(bytes + kShrinkX * (BM * BK * 2) + p.f_stages * p.f_bytes);
+  int* off = reinterpret_cast<int*>(sums + p.rN * BM);
   int16_t* ad = reinterpret_cast<int16_t*>(off + p.q.num_seg + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nrank = gridDim.x, rank = blockIdx.x;
   const int m0 = blockIdx.y * BM, m1 = min(p.q.T, m0 + BM);
-  load_requests(p.q, off, ad, p.status);
-  if (threadIdx.x < BM) {
-    const int t = m0 + threadIdx.x;
-    ctl.row_ad[threadIdx.x] = t < m1 ? adapter_of_row(off, ad, p.q.num_seg, t) : -1;
-  }
+  const int nkb = p.red / BK;
+  const int kb0 = (int)((long long)nkb * rank / nrank), kb1 = (int)((long long)nkb * (rank + 1) / nrank);
+  auto load_x = [&](int kb, int xs) {
+    const uint32_t xb = smem_u32(&ctl.xfull[xs]);
+    mbar_arrive_expect_tx(xb, BM * BK * 2);
+    tma_load_2d(sX + xs * (BM * BK * 2), &tmX, xb, kb * BK, m0);
+  };
   if (threadIdx.x == 0) {
     for (int i = 0; i < kShrinkX; ++i) {
       mbar_init(smem_u32(&ctl.xfull[i]), 1);
@@ -320,8 +331,14 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
     mbar_init(smem_u32(&ctl.done), 1);
     ctl.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    prefetch_tmap(&tmX);
+    // the first blocks are on their way while the table is read
+    for (int i = 0; i < kShrinkX && kb0 + i < kb1; ++i) load_x(kb0 + i, i);
     prefetch_tmap(&tmF);
+  }
+  load_requests(p.q, off, ad, p.status);
+  if (threadIdx.x < BM) {
+    const int t = m0 + threadIdx.x;
+    ctl.row_ad[threadIdx.x] = t < m1 ? adapter_of_row(off, ad, p.q.num_seg, t) : -1;
   }
   if (warp == 1) tmem_alloc_n<1>(smem_u32(&ctl.tmem_base), p.tmem_cols);
   tc_fence_before();
@@ -330,21 +347,25 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
   // only now may the next kernel of the stream start beside this one: it must
   // not take the tensor memory that this one still has to allocate
   pdl_trigger();
+  // (waited for before the first access to a peer's shared memory: it has to run by then)
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   const uint32_t tmem = ctl.tmem_base;
-  const int nkb = p.red / BK;
-  const int kb0 = (int)((long long)nkb * rank / nrank), kb1 = (int)((long long)nkb * (rank + 1) / nrank);
+  auto runs_to = [&](uint32_t* list) {
+    const int a[4] = {ctl.row_ad[lane], ctl.row_ad[32 + lane], ctl.row_ad[64 + lane], ctl.row_ad[96 + lane]};
+    return list_runs<4>(a, list);
+  };
 
   if (warp == 0) {
-    const int n = build_runs<4>(off, ad, p.q.num_seg, m0, m1, ctl.runs[0]);
-    if (lane == 0 && n > 0) {
+    const int n = runs_to(ctl.runs[0]);
+    if (lane == 0) {
       int xs = 0, fs = 0;
       uint32_t xp = 0, fp = 0;
       bool ok = true;
       for (int kb = kb0; ok && kb < kb1; ++kb) {
-        if (!wait_bar(smem_u32(&ctl.xempty[xs]), xp ^ 1u, &ctl.abort_flag, p.status)) break;
-        const uint32_t xb = smem_u32(&ctl.xfull[xs]);
-        mbar_arrive_expect_tx(xb, BM * BK * 2);
-        tma_load_2d(sX + xs * (BM * BK * 2), &tmX, xb, kb * BK, m0);
+        if (kb >= kb0 + kShrinkX) {
+          if (!wait_bar(smem_u32(&ctl.xempty[xs]), xp ^ 1u, &ctl.abort_flag, p.status)) break;
+          load_x(kb, xs);
+        }
         if (++xs == kShrinkX) { xs = 0; xp ^= 1u; }
         for (int i = 0; i < n; ++i) {
           const int a = unpack_run(ctl.runs[0][i]).a;
@@ -361,11 +382,11 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
       }
     }
   } else if (warp == 1) {
-    const int n = build_runs<4>(off, ad, p.q.num_seg, m0, m1, ctl.runs[1]);
+    const int n = runs_to(ctl.runs[1]);
     int xs = 0, fs = 0;
     uint32_t xp = 0, fp = 0;
     bool ok = true;
-    for (int kb = kb0; ok && n > 0 && kb < kb1; ++kb) {
+    for (int kb = kb0; ok && kb < kb1; ++kb) {
       ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.xfull[xs]), xp, &ctl.abort_flag, p.status));
       if (!ok) break;
       const uint32_t a0 = sX + xs * (BM * BK * 2);
@@ -380,8 +401,8 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
             mma_lanes(tmem, sdesc(a0 + kk * 32, 16, 1024),
-                           kMN ? sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024) : sdesc(b0 + kk * 32, 16, 1024), p.idesc,
-                           kb > kb0 || kk > 0, m);
+                      kMN ? sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024) : sdesc(b0 + kk * 32, 16, 1024), p.idesc,
+                      kb > kb0 || kk > 0, m);
           mma_commit(smem_u32(&ctl.fempty[fs]));
         }
         __syncwarp();
@@ -398,8 +419,12 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
   // every MMA of this CTA has ended (on an abort: those issued), the x blocks are free
   const bool fine = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.done), 0, &ctl.abort_flag, p.status));
   tc_fence_after();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  const int per = BM / nrank;  // rows of a CTA's share
   if (warp >= 2 && fine) {
+    // each row's sums go straight to the CTA that finishes the row
     const int row = (warp & 3) * 32 + lane;
+    const uint32_t dst = map_to_rank(smem_u32(sums + (size_t)rank * p.rN * per + row % per), row / per);
     for (int c = 0; c < p.rN; c += 16) {
       uint32_t v[16];
       asm volatile(
@@ -410,41 +435,36 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
           : "r"(tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)c));
       tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[(c + i) * BM + row] = f32(v[i]);
+      for (int i = 0; i < 16; ++i) st_cluster(dst + (uint32_t)((c + i) * per) * 4, f32(v[i]));
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_n<1>(tmem, p.tmem_cols);
-  cluster_sync();
-  // this CTA's share of the rows: the slices' sums in order, scaled and split
-  {
-    const int per = BM / nrank, rp = plane_cols(p.r), hp = hidden_pitch(p.r);
-    const uint32_t local = smem_u32(acc);
-    for (int i = threadIdx.x; i < per * (rp / 8); i += blockDim.x) {
-      const int row = rank * per + i % per, c = i / per * 8;
-      if (m0 + row >= p.q.T) continue;
-      const int a = ctl.row_ad[row];
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (a >= 0 && c < p.r) {
-        for (int k = 0; k < nrank; ++k) {
-          const uint32_t peer = map_to_rank(local + (uint32_t)(c * BM + row) * 4, k);
+  cluster_sync();  // all slices' sums have arrived; nothing remote follows
+  // the slices' sums in order, scaled and split
+  const int rp = plane_cols(p.r), hp = hidden_pitch(p.r);
+  for (int i = threadIdx.x; i < per * (rp / 8); i += blockDim.x) {
+    const int row = rank * per + i % per, c = i / per * 8;
+    if (m0 + row >= p.q.T) continue;
+    const int a = ctl.row_ad[row];
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (a >= 0 && c < p.r) {
+      for (int k = 0; k < nrank; ++k) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] += ld_cluster(peer + j * BM * 4);
-        }
-        const float s = p.scale ? __ldg(p.scale + a) : 1.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= s;
+        for (int j = 0; j < 8; ++j) v[j] += sums[((size_t)k * p.rN + c + j) * per + i % per];
       }
-      uint4 o[kPlanes];
-      split8(v, o);
+      const float s = p.scale ? __ldg(p.scale + a) : 1.f;
 #pragma unroll
-      for (int k = 0; k < kPlanes; ++k)
-        *reinterpret_cast<uint4*>(p.hidden + (size_t)(m0 + row) * hp + k * rp + c) = o[k];
+      for (int j = 0; j < 8; ++j) v[j] *= s;
     }
+    uint4 o[kPlanes];
+    split8(v, o);
+#pragma unroll
+    for (int k = 0; k < kPlanes; ++k)
+      *reinterpret_cast<uint4*>(p.hidden + (size_t)(m0 + row) * hp + k * rp + c) = o[k];
   }
-  cluster_sync();  // a peer may still read this CTA's accumulator
 }
 
 // ------------------------------------------------- narrow product, few rows
@@ -1300,14 +1320,16 @@ int run_shrink(const char* fn, const Reqs& q, const void* in, long long ld, cons
   p.rN = round_up(r, 16);
   p.f_bytes = kMN ? (r + 63) / 64 * CHUNK_BYTES : r * 128;
   p.f_rows = kMN ? red : r;
-  p.f_stages = 32768 / p.f_bytes < 4 ? 4 : (32768 / p.f_bytes > kShrinkF ? kShrinkF : 32768 / p.f_bytes);
+  // tiles of many runs want many blocks of F in flight: more of them where a CTA has its SM alone
+  const int f_room = tiles * cs <= (sm_count() > 0 ? sm_count() : 148) ? 65536 : 16384;
+  p.f_stages = f_room / p.f_bytes < 4 ? 4 : (f_room / p.f_bytes > kShrinkF ? kShrinkF : f_room / p.f_bytes);
   p.scale = scale;
   p.hidden = static_cast<__nv_bfloat16*>(hidden);
   p.idesc = make_idesc(p.rN, BM, false, kMN);
   p.tmem_cols = p.rN <= 32 ? 32 : (p.rN <= 64 ? 64 : 128);
   p.status = status_word();
-  // one 16-row block of slack: an F block of r rows is read as rN
-  const size_t smem = 1024 + kShrinkX * (BM * BK * 2) + (size_t)p.f_stages * p.f_bytes + 2048 + table_bytes(q.num_seg);
+  // (an F block of r rows is read as rN: the last one reads into the sums, whose columns past r are not used)
+  const size_t smem = 1024 + kShrinkX * (BM * BK * 2) + (size_t)p.f_stages * p.f_bytes + (size_t)p.rN * BM * 4 + table_bytes(q.num_seg);
   return launch_adapter(fn, kern, dim3(cs, tiles), 192, smem, cs, s, tx, tf, p);
 }
 
@@ -1376,18 +1398,30 @@ int run_wide_bn(const char* fn, const Reqs& q, const void* in, long long ld, con
 template <bool kMN>
 int run_wide(const char* fn, const Reqs& q, const void* in, long long ld, const void* W, const void* hidden, const void* F,
              int red, int out_cols, int r, void* out, long long ldo, bool has_hidden, cudaStream_t s) {
-  // the widest tile that divides the columns and still gives every SM one;
-  // where even the narrowest leave half of them idle, clusters along the reduction
   const int sms = sm_count() > 0 ? sm_count() : 148, rows = (q.T + BM - 1) / BM;
-  if (out_cols % 256 == 0 && (q.T + 2 * BM - 1) / (2 * BM) * (out_cols / 256) >= sms / 2)
-    return run_wide_bn<256, kMN, false>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, 1, s);
-  if (out_cols % 128 == 0 && rows * (out_cols / 128) >= sms)
-    return run_wide_bn<128, kMN, false>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, 1, s);
+  // where even the narrowest tiles leave half of the SMs idle: clusters along the reduction
   const int tiles = rows * (out_cols / 64);
   int nrank = 1;
   while (nrank < 8 && nrank * 2 <= red / BK && tiles * nrank * 2 <= sms) nrank *= 2;
   if (nrank > 1)
     return run_wide_bn<64, kMN, true>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, nrank, s);
+  // else the tile whose waves cost least: a block's time goes with the columns it multiplies plus the
+  // 128 rows it loads; a pair's last wave may be one of halves
+  const int w64 = (tiles + sms - 1) / sms * (64 + 64);
+  int best = w64, bn = 64;
+  if (out_cols % 128 == 0) {
+    const int w128 = (tiles / 2 + sms - 1) / sms * (128 + 64);
+    if (w128 <= best) best = w128, bn = 128;
+  }
+  if (out_cols % 256 == 0) {
+    const int places = sms / 2, t256 = (q.T + 2 * BM - 1) / (2 * BM) * (out_cols / 256), rest = t256 % places;
+    const int halves = t256 / places * 2 + (rest == 0 ? 0 : (2 * rest <= places ? 1 : 2));
+    if (halves * (256 + 64) / 2 <= best) bn = 256;
+  }
+  if (bn == 256)
+    return run_wide_bn<256, kMN, false>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, 1, s);
+  if (bn == 128)
+    return run_wide_bn<128, kMN, false>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, 1, s);
   return run_wide_bn<64, kMN, false>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, 1, s);
 }
 
