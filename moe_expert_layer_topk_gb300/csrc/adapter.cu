@@ -55,14 +55,15 @@ __host__ __device__ constexpr size_t table_bytes(int num_seg) { return (size_t)(
 
 // Shared-memory copy: offsets made monotone and clamped to [0, T], adapter ids
 // out of range replaced by -1 (both reported).  off[num_seg + 1], ad[num_seg].
-__device__ __forceinline__ void load_requests(const Reqs& q, int* off, int16_t* ad, int* status) {
+// Threads from `from` on (a multiple of 32) read it, that warp closes it.
+__device__ __forceinline__ void load_requests(const Reqs& q, int* off, int16_t* ad, int* status, int from = 0) {
   if (q.num_seg == 0) {  // there may be no table at all
     if (threadIdx.x == 0) off[0] = 0;
     __syncthreads();
     return;
   }
   bool bad = false;
-  for (int s = threadIdx.x; s <= q.num_seg; s += blockDim.x) {
+  for (int s = (int)threadIdx.x - from; s >= 0 && s <= q.num_seg; s += blockDim.x - from) {
     int v = __ldg(q.offsets + s);
     if (v < 0 || v > q.T) {
       bad = true;
@@ -79,8 +80,8 @@ __device__ __forceinline__ void load_requests(const Reqs& q, int* off, int16_t* 
     }
   }
   __syncthreads();
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
+  if ((int)threadIdx.x >= from && (int)threadIdx.x < from + 32) {
+    const int lane = threadIdx.x & 31;
     int carry = 0;
     for (int b = 0; b <= q.num_seg; b += 32) {
       const int s = b + lane, v = s <= q.num_seg ? off[s] : 0;
@@ -177,10 +178,10 @@ __device__ __forceinline__ int build_runs(const int* off, const int16_t* ad, int
 
 // Word w of the MMA's lane mask (1 = lane off) that leaves rows [lo, hi) on.
 __device__ __forceinline__ uint32_t lanes_off(int lo, int hi, int w) {
-  const int a = max(lo - 32 * w, 0), b = min(hi - 32 * w, 32);
-  if (a >= b) return 0xffffffffu;
-  const uint32_t below_b = b == 32 ? 0xffffffffu : (1u << b) - 1u;
-  return ~(below_b & ~((1u << a) - 1u));
+  const int a = max(lo - 32 * w, 0);
+  uint32_t on;
+  asm("bmsk.clamp.b32 %0, %1, %2;" : "=r"(on) : "r"(a), "r"(max(min(hi - 32 * w, 32) - a, 0)));
+  return ~on;
 }
 
 // Lane mask of a tile of 128 rows (one CTA) or 256 (a pair: the second CTA's
@@ -244,6 +245,15 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   return v;
 }
 
+// True in one lane of a converged warp.  The compiler knows such a branch for
+// one thread's and keeps its values in uniform registers: the MMA loop under
+// it issues a block's four MMAs in about 0.2 us less than under lane == 0.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ uint32_t align1k(uint32_t a) { return (a + 1023u) & ~1023u; }
 
 // v split into kPlanes bf16 parts, largest first, 8 columns: one 16-byte vector a part
@@ -278,14 +288,16 @@ struct ShrinkParams {
   int r, rN;            // rank, MMA columns (rank up to a multiple of 16)
   int f_bytes;          // shared-memory bytes of one F block
   int f_rows;           // rows of F's 2-D view per adapter
-  int f_stages;         // blocks of F in flight
+  int x_stages, f_stages;  // steps of x and of F in flight
   const float* scale;   // [num_adapters] or null
   __nv_bfloat16* hidden;
   uint32_t idesc;
   uint32_t tmem_cols;
   int* status;
 };
-constexpr int kShrinkX = 4, kShrinkF = 16;  // blocks of x in flight, of F at most
+constexpr int kShrinkK = 2;                  // 64-column blocks of the reduction a step
+constexpr int kShrinkX = 3, kShrinkF = 12;   // steps of x in flight, of F at most
+constexpr int kShrinkXBytes = kShrinkK * BM * BK * 2;
 
 struct ShrinkCtl {
   unsigned long long xfull[kShrinkX], xempty[kShrinkX], ffull[kShrinkF], fempty[kShrinkF], done;
@@ -304,9 +316,10 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
   __shared__ ShrinkCtl ctl;
   const uint32_t base = align1k(smem_u32(smem_raw));
   uint8_t* bytes = smem_raw + (base - smem_u32(smem_raw));
-  const uint32_t sX = base, sF = base + kShrinkX * (BM * BK * 2);
+  const int f_stage = kShrinkK * p.f_bytes;
+  const uint32_t sX = base, sF = base + p.x_stages * kShrinkXBytes;
   // the slices' sums of this CTA's share of the rows: [slice][rN][rows]
-  float* sums = reinterpret_cast<float*>(bytes + kShrinkX * (BM * BK * 2) + p.f_stages * p.f_bytes);
+  float* sums = reinterpret_cast<float*>(bytes + p.x_stages * kShrinkXBytes + p.f_stages * f_stage);
   int* off = reinterpret_cast<int*>(sums + p.rN * BM);
   int16_t* ad = reinterpret_cast<int16_t*>(off + p.q.num_seg + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -315,32 +328,40 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
   const int nkb = p.red / BK;
   const int kb0 = (int)((long long)nkb * rank / nrank), kb1 = (int)((long long)nkb * (rank + 1) / nrank);
   auto load_x = [&](int kb, int xs) {
+    const int nb = min(kShrinkK, kb1 - kb);
     const uint32_t xb = smem_u32(&ctl.xfull[xs]);
-    mbar_arrive_expect_tx(xb, BM * BK * 2);
-    tma_load_2d(sX + xs * (BM * BK * 2), &tmX, xb, kb * BK, m0);
+    mbar_arrive_expect_tx(xb, nb * (BM * BK * 2));
+    for (int i = 0; i < nb; ++i) tma_load_2d(sX + xs * kShrinkXBytes + i * (BM * BK * 2), &tmX, xb, (kb + i) * BK, m0);
   };
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kShrinkX; ++i) {
+  // one warp sets the barriers up and sends for the first blocks, one takes the
+  // tensor memory, the others read the request table
+  if (warp == 0) {
+    for (int i = lane; i < p.x_stages; i += 32) {
       mbar_init(smem_u32(&ctl.xfull[i]), 1);
       mbar_init(smem_u32(&ctl.xempty[i]), 1);
     }
-    for (int i = 0; i < p.f_stages; ++i) {
+    for (int i = lane; i < p.f_stages; i += 32) {
       mbar_init(smem_u32(&ctl.ffull[i]), 1);
       mbar_init(smem_u32(&ctl.fempty[i]), 1);
     }
-    mbar_init(smem_u32(&ctl.done), 1);
-    ctl.abort_flag = 0;
+    if (lane == 0) {
+      mbar_init(smem_u32(&ctl.done), 1);
+      ctl.abort_flag = 0;
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    // the first blocks are on their way while the table is read
-    for (int i = 0; i < kShrinkX && kb0 + i < kb1; ++i) load_x(kb0 + i, i);
-    prefetch_tmap(&tmF);
+    __syncwarp();
+    if (elect_one()) {
+      for (int i = 0; i < p.x_stages && kb0 + i * kShrinkK < kb1; ++i) load_x(kb0 + i * kShrinkK, i);
+      prefetch_tmap(&tmF);
+    }
+  } else if (warp == 1) {
+    tmem_alloc_n<1>(smem_u32(&ctl.tmem_base), p.tmem_cols);
   }
-  load_requests(p.q, off, ad, p.status);
+  load_requests(p.q, off, ad, p.status, 64);
   if (threadIdx.x < BM) {
     const int t = m0 + threadIdx.x;
     ctl.row_ad[threadIdx.x] = t < m1 ? adapter_of_row(off, ad, p.q.num_seg, t) : -1;
   }
-  if (warp == 1) tmem_alloc_n<1>(smem_u32(&ctl.tmem_base), p.tmem_cols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -357,25 +378,29 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
 
   if (warp == 0) {
     const int n = runs_to(ctl.runs[0]);
-    if (lane == 0) {
+    if (elect_one()) {
       int xs = 0, fs = 0;
       uint32_t xp = 0, fp = 0;
       bool ok = true;
-      for (int kb = kb0; ok && kb < kb1; ++kb) {
-        if (kb >= kb0 + kShrinkX) {
+      for (int kb = kb0; ok && kb < kb1; kb += kShrinkK) {
+        if (kb >= kb0 + p.x_stages * kShrinkK) {
           if (!wait_bar(smem_u32(&ctl.xempty[xs]), xp ^ 1u, &ctl.abort_flag, p.status)) break;
           load_x(kb, xs);
         }
-        if (++xs == kShrinkX) { xs = 0; xp ^= 1u; }
+        if (++xs == p.x_stages) { xs = 0; xp ^= 1u; }
+        const int nb = min(kShrinkK, kb1 - kb);
         for (int i = 0; i < n; ++i) {
           const int a = unpack_run(ctl.runs[0][i]).a;
           if (!(ok = wait_bar(smem_u32(&ctl.fempty[fs]), fp ^ 1u, &ctl.abort_flag, p.status))) break;
-          const uint32_t fb = smem_u32(&ctl.ffull[fs]), dst = sF + fs * p.f_bytes;
-          mbar_arrive_expect_tx(fb, p.f_bytes);
-          if (kMN) {
-            for (int c = 0; c < p.r; c += 64) tma_load_2d(dst + c * 128, &tmF, fb, c, a * p.f_rows + kb * BK);
-          } else {
-            tma_load_2d(dst, &tmF, fb, kb * BK, a * p.f_rows);
+          const uint32_t fb = smem_u32(&ctl.ffull[fs]);
+          mbar_arrive_expect_tx(fb, nb * p.f_bytes);
+          for (int j = 0; j < nb; ++j) {
+            const uint32_t dst = sF + fs * f_stage + j * p.f_bytes;
+            if (kMN) {
+              for (int c = 0; c < p.r; c += 64) tma_load_2d(dst + c * 128, &tmF, fb, c, a * p.f_rows + (kb + j) * BK);
+            } else {
+              tma_load_2d(dst, &tmF, fb, (kb + j) * BK, a * p.f_rows);
+            }
           }
           if (++fs == p.f_stages) { fs = 0; fp ^= 1u; }
         }
@@ -383,40 +408,39 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
     }
   } else if (warp == 1) {
     const int n = runs_to(ctl.runs[1]);
-    int xs = 0, fs = 0;
-    uint32_t xp = 0, fp = 0;
-    bool ok = true;
-    for (int kb = kb0; ok && kb < kb1; ++kb) {
-      ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.xfull[xs]), xp, &ctl.abort_flag, p.status));
-      if (!ok) break;
-      const uint32_t a0 = sX + xs * (BM * BK * 2);
-      for (int i = 0; i < n; ++i) {
-        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.ffull[fs]), fp, &ctl.abort_flag, p.status));
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
+    if (elect_one()) {
+      int xs = 0, fs = 0;
+      uint32_t xp = 0, fp = 0;
+      bool ok = true;
+      for (int kb = kb0; ok && kb < kb1; kb += kShrinkK) {
+        if (!(ok = wait_bar(smem_u32(&ctl.xfull[xs]), xp, &ctl.abort_flag, p.status))) break;
+        const uint32_t a0 = sX + xs * kShrinkXBytes;
+        const int nb = min(kShrinkK, kb1 - kb);
+        for (int i = 0; i < n; ++i) {
           const Run run = unpack_run(ctl.runs[1][i]);
-          const uint32_t b0 = sF + fs * p.f_bytes;
           const LaneMask<1> m = lane_mask<1>(run.lo, run.hi);
+          if (!(ok = wait_bar(smem_u32(&ctl.ffull[fs]), fp, &ctl.abort_flag, p.status))) break;
+          tc_fence_after();
+          const uint32_t b0 = sF + fs * f_stage;
+          for (int j = 0; j < nb; ++j) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
-            mma_lanes(tmem, sdesc(a0 + kk * 32, 16, 1024),
-                      kMN ? sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024) : sdesc(b0 + kk * 32, 16, 1024), p.idesc,
-                      kb > kb0 || kk > 0, m);
+            for (int kk = 0; kk < BK / 16; ++kk)
+              mma_lanes(tmem, sdesc(a0 + j * (BM * BK * 2) + kk * 32, 16, 1024),
+                        kMN ? sdesc(b0 + j * p.f_bytes + kk * 2048, CHUNK_BYTES, 1024)
+                            : sdesc(b0 + j * p.f_bytes + kk * 32, 16, 1024),
+                        p.idesc, kb > kb0 || j > 0 || kk > 0, m);
+          }
           mma_commit(smem_u32(&ctl.fempty[fs]));
+          if (++fs == p.f_stages) { fs = 0; fp ^= 1u; }
         }
-        __syncwarp();
-        if (++fs == p.f_stages) { fs = 0; fp ^= 1u; }
+        mma_commit(smem_u32(&ctl.xempty[xs]));
+        if (++xs == p.x_stages) { xs = 0; xp ^= 1u; }
       }
-      if (lane == 0) mma_commit(smem_u32(&ctl.xempty[xs]));
-      __syncwarp();
-      if (++xs == kShrinkX) { xs = 0; xp ^= 1u; }
+      mma_commit(smem_u32(&ctl.done));
     }
-    if (lane == 0) mma_commit(smem_u32(&ctl.done));
-    __syncwarp();
   }
-  __syncwarp();  // the producer's other lanes do not spin beside it
-  // every MMA of this CTA has ended (on an abort: those issued), the x blocks are free
+  __syncwarp();  // the two roles' other lanes do not spin beside them
+  // every MMA of this CTA has ended (on an abort: those issued)
   const bool fine = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.done), 0, &ctl.abort_flag, p.status));
   tc_fence_after();
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -645,31 +669,35 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pair_rank = CTAS == 2 ? (int)cluster_rank() : 0;
   const bool leader = pair_rank == 0;
-  load_requests(p.q, off, ad, p.status);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < nst; ++i) {
-      mbar_init(smem_u32(&ctl.full[i]), 1);
-      mbar_init(smem_u32(&ctl.empty[i]), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&ctl.tfull[i]), 1);
-      mbar_init(smem_u32(&ctl.tempty[i]), 4 * CTAS);
-      mbar_init(smem_u32(&ctl.lfull[i]), 1);
-      mbar_init(smem_u32(&ctl.lempty[i]), leader ? 2 : 1);  // a pair's second CTA issues no MMAs
-    }
-    mbar_init(smem_u32(&ctl.vfull), 1);
-    mbar_init(smem_u32(&ctl.vempty), 1);
-    mbar_init(smem_u32(&ctl.drain), 1);
-    ctl.abort_flag = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    prefetch_tmap(&tmX);
-    prefetch_tmap(&tmW);
-    prefetch_tmap(&tmH);
-    prefetch_tmap(&tmF);
-    if (!kSplit) prefetch_tmap(&tmO);
-  }
   constexpr int kTmem = kSplit ? BN : 2 * BN;
-  if (warp == 1) tmem_alloc_n<CTAS>(smem_u32(&ctl.tmem_base), kTmem);
+  // one warp sets the barriers up, one takes the tensor memory, the others read the request table
+  if (warp == 0) {
+    if (lane < nst) {
+      mbar_init(smem_u32(&ctl.full[lane]), 1);
+      mbar_init(smem_u32(&ctl.empty[lane]), 1);
+    }
+    if (lane < 2) {
+      mbar_init(smem_u32(&ctl.tfull[lane]), 1);
+      mbar_init(smem_u32(&ctl.tempty[lane]), 4 * CTAS);
+      mbar_init(smem_u32(&ctl.lfull[lane]), 1);
+      mbar_init(smem_u32(&ctl.lempty[lane]), leader ? 2 : 1);  // a pair's second CTA issues no MMAs
+    }
+    if (lane == 0) {
+      mbar_init(smem_u32(&ctl.vfull), 1);
+      mbar_init(smem_u32(&ctl.vempty), 1);
+      mbar_init(smem_u32(&ctl.drain), 1);
+      ctl.abort_flag = 0;
+      prefetch_tmap(&tmX);
+      prefetch_tmap(&tmW);
+      prefetch_tmap(&tmH);
+      prefetch_tmap(&tmF);
+      if (!kSplit) prefetch_tmap(&tmO);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  } else if (warp == 1) {
+    tmem_alloc_n<CTAS>(smem_u32(&ctl.tmem_base), kTmem);
+  }
+  load_requests(p.q, off, ad, p.status, 64);
   tc_fence_before();
   __syncthreads();
   if constexpr (CTAS == 2) cluster_sync();  // peer barriers initialised before any remote signal
@@ -705,7 +733,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
   auto at_leader = [&](uint32_t bar) { return CTAS == 2 ? map_to_rank(bar, 0) : bar; };
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       int st = 0, local = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -783,24 +811,22 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
       if (!waited) pdl_wait();  // the grid may not end before the narrow kernel does
     }
   } else if (warp == 1) {
-    int st = 0, local = 0;
-    uint32_t ph = 0, vph = 0;
-    bool ok = true;
-    auto next = [&]() { if (++st == nst) { st = 0; ph ^= 1u; } };
     // a pair's second CTA only keeps its tensor memory
-    for (int u = u0; leader && ok && u < u1; u += du, ++local) {
-      const Unit t = unit_at(u);
-      const uint32_t idesc = t.bn == BN ? p.idesc : p.idesc_half;
-      const int buf = local & 1;
-      ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.tempty[buf]), ((local >> 1) & 1) ^ 1, &ctl.abort_flag, p.status));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t d = tmem + buf * BN;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.full[st]), ph, &ctl.abort_flag, p.status));
-        if (!ok) break;
+    if (leader && elect_one()) {
+      int st = 0, local = 0;
+      uint32_t ph = 0, vph = 0;
+      bool ok = true;
+      auto next = [&]() { if (++st == nst) { st = 0; ph ^= 1u; } };
+      for (int u = u0; ok && u < u1; u += du, ++local) {
+        const Unit t = unit_at(u);
+        const uint32_t idesc = t.bn == BN ? p.idesc : p.idesc_half;
+        const int buf = local & 1;
+        if (!(ok = wait_bar(smem_u32(&ctl.tempty[buf]), ((local >> 1) & 1) ^ 1, &ctl.abort_flag, p.status))) break;
         tc_fence_after();
-        if (lane == 0) {
+        const uint32_t d = tmem + buf * BN;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!(ok = wait_bar(smem_u32(&ctl.full[st]), ph, &ctl.abort_flag, p.status))) break;
+          tc_fence_after();
           const uint32_t a0 = base + st * stage_bytes, b0 = a0 + a_bytes;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
@@ -808,57 +834,42 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
                             kMN ? sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024) : sdesc(b0 + kk * 32, 16, 1024), idesc,
                             kb > kb0 || kk > 0);
           mma_commit_to<CTAS>(smem_u32(&ctl.empty[st]));
+          next();
         }
-        __syncwarp();
-        next();
-      }
-      if (!ok) break;
-      const int lb = local & 1;
-      if (listed) {
-        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.lfull[lb]), (local >> 1) & 1, &ctl.abort_flag, p.status));
         if (!ok) break;
-      }
-      const int n = listed ? ctl.num_runs[lb] : 0;
-      if (n > r0) {
-        for (int ps = 0; ok && ps < passes; ++ps, vph ^= 1u) {
-          ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.vfull), vph, &ctl.abort_flag, p.status));
-          if (!ok) break;
-          const int steps = min(4, (p.r - ps * 64 + 15) / 16);  // 16-wide steps of this block of F
-          const int pstep = one_block ? rp * 2 : a_bytes;        // bytes from one part of hidden to the next
-          for (int i = r0; i < n; i += dr) {
-            ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.full[st]), ph, &ctl.abort_flag, p.status));
-            if (!ok) break;
-            tc_fence_after();
-            if (lane == 0) {
+        if (listed) {
+          const int lb = local & 1;
+          if (!(ok = wait_bar(smem_u32(&ctl.lfull[lb]), (local >> 1) & 1, &ctl.abort_flag, p.status))) break;
+          const int n = ctl.num_runs[lb];
+          for (int ps = 0; ok && n > r0 && ps < passes; ++ps, vph ^= 1u) {
+            if (!(ok = wait_bar(smem_u32(&ctl.vfull), vph, &ctl.abort_flag, p.status))) break;
+            const int steps = min(4, (p.r - ps * 64 + 15) / 16);  // 16-wide steps of this block of F
+            const int pstep = one_block ? rp * 2 : a_bytes;        // bytes from one part of hidden to the next
+            for (int i = r0; i < n; i += dr) {
               const Run run = unpack_run(ctl.runs[lb][i]);
               const LaneMask<CTAS> m = lane_mask<CTAS>(run.lo, run.hi);
+              if (!(ok = wait_bar(smem_u32(&ctl.full[st]), ph, &ctl.abort_flag, p.status))) break;
+              tc_fence_after();
               const uint32_t b0 = base + st * stage_bytes + a_bytes;
               for (int pl = 0; pl < kWidePlanes; ++pl)
                 for (int kk = 0; kk < steps; ++kk)
                   mma_lanes(d, sdesc(sV + pl * pstep + kk * 32, 16, 1024),
                             kMN ? sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024) : sdesc(b0 + kk * 32, 16, 1024), idesc, 1u, m);
               mma_commit_to<CTAS>(smem_u32(&ctl.empty[st]));
+              next();
             }
-            __syncwarp();
-            next();
+            if (ok) mma_commit_to<CTAS>(smem_u32(&ctl.vempty));
           }
-          if (ok && lane == 0) mma_commit_to<CTAS>(smem_u32(&ctl.vempty));
-          __syncwarp();
+          if (!ok) break;
+          mbar_arrive(smem_u32(&ctl.lempty[lb]));
         }
-      }
-      if (!ok) break;
-      __syncwarp();
-      if (lane == 0) {
-        if (listed) mbar_arrive(smem_u32(&ctl.lempty[lb]));
         mma_commit_to<CTAS>(smem_u32(&ctl.tfull[buf]));
       }
-      __syncwarp();
-    }
-    if (!ok) {  // drain MMAs still in flight before TMEM is released
-      if (lane == 0) mma_commit_to<CTAS>(smem_u32(&ctl.drain));
-      __syncwarp();
-      const unsigned long long t0 = globaltimer();
-      while (!mbar_try_wait(smem_u32(&ctl.drain), 0) && globaltimer() - t0 < TIMEOUT_NS) {
+      if (!ok) {  // drain MMAs still in flight before TMEM is released
+        mma_commit_to<CTAS>(smem_u32(&ctl.drain));
+        const unsigned long long t0 = globaltimer();
+        while (!mbar_try_wait(smem_u32(&ctl.drain), 0) && globaltimer() - t0 < TIMEOUT_NS) {
+        }
       }
     }
   } else if constexpr (kSplit) {
@@ -1121,21 +1132,22 @@ __global__ void __launch_bounds__(192) adapter_grad_kernel(const __grid_constant
           __syncwarp();
         }
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
           for (int kk = 0; kk < steps; ++kk) {
             for (int h = 0; h < nmma; ++h)
               mma_bf16(d + h * (hc / 2), sdesc(a0 + kk * 2048, CHUNK_BYTES, 1024),
-                       sdesc(b0 + h * (nck / 2 * CHUNK_BYTES) + kk * 2048, CHUNK_BYTES, 1024), p.idesc, started);
-            started = 1;
+                       sdesc(b0 + h * (nck / 2 * CHUNK_BYTES) + kk * 2048, CHUNK_BYTES, 1024), p.idesc,
+                       started || kk > 0);
           }
           mma_commit(smem_u32(&ctl.empty[st]));
         }
+        started = 1;
         __syncwarp();
         if (++st == p.stages) { st = 0; ph ^= 1u; }
         return true;
       });
       if (!ok) break;
-      if (lane == 0) mma_commit(smem_u32(&ctl.tfull[buf]));
+      if (elect_one()) mma_commit(smem_u32(&ctl.tfull[buf]));
       __syncwarp();
     }
     if (!ok) {
@@ -1321,15 +1333,16 @@ int run_shrink(const char* fn, const Reqs& q, const void* in, long long ld, cons
   p.f_bytes = kMN ? (r + 63) / 64 * CHUNK_BYTES : r * 128;
   p.f_rows = kMN ? red : r;
   // tiles of many runs want many blocks of F in flight: more of them where a CTA has its SM alone
-  const int f_room = tiles * cs <= (sm_count() > 0 ? sm_count() : 148) ? 65536 : 16384;
-  p.f_stages = f_room / p.f_bytes < 4 ? 4 : (f_room / p.f_bytes > kShrinkF ? kShrinkF : f_room / p.f_bytes);
+  const int f_room = tiles * cs <= (sm_count() > 0 ? sm_count() : 148) ? 65536 : 8192, f_stage = kShrinkK * p.f_bytes;
+  p.f_stages = f_room / f_stage < 2 ? 2 : (f_room / f_stage > kShrinkF ? kShrinkF : f_room / f_stage);
   p.scale = scale;
   p.hidden = static_cast<__nv_bfloat16*>(hidden);
   p.idesc = make_idesc(p.rN, BM, false, kMN);
   p.tmem_cols = p.rN <= 32 ? 32 : (p.rN <= 64 ? 64 : 128);
   p.status = status_word();
   // (an F block of r rows is read as rN: the last one reads into the sums, whose columns past r are not used)
-  const size_t smem = 1024 + kShrinkX * (BM * BK * 2) + (size_t)p.f_stages * p.f_bytes + (size_t)p.rN * BM * 4 + table_bytes(q.num_seg);
+  p.x_stages = r <= 64 ? kShrinkX : 2;
+  const size_t smem = 1024 + p.x_stages * kShrinkXBytes + (size_t)p.f_stages * f_stage + (size_t)p.rN * BM * 4 + table_bytes(q.num_seg);
   return launch_adapter(fn, kern, dim3(cs, tiles), 192, smem, cs, s, tx, tf, p);
 }
 
