@@ -1333,7 +1333,8 @@ int run_shrink(const char* fn, const Reqs& q, const void* in, long long ld, cons
   p.f_bytes = kMN ? (r + 63) / 64 * CHUNK_BYTES : r * 128;
   p.f_rows = kMN ? red : r;
   // tiles of many runs want many blocks of F in flight: more of them where a CTA has its SM alone
-  const int f_room = tiles * cs <= (sm_count() > 0 ? sm_count() : 148) ? 65536 : 8192, f_stage = kShrinkK * p.f_bytes;
+  const int sms = sm_count() > 0 ? sm_count() : 148;
+  const int f_room = tiles * cs <= sms ? 65536 : 8192, f_stage = kShrinkK * p.f_bytes;
   p.f_stages = f_room / f_stage < 2 ? 2 : (f_room / f_stage > kShrinkF ? kShrinkF : f_room / f_stage);
   p.scale = scale;
   p.hidden = static_cast<__nv_bfloat16*>(hidden);
@@ -1341,7 +1342,8 @@ int run_shrink(const char* fn, const Reqs& q, const void* in, long long ld, cons
   p.tmem_cols = p.rN <= 32 ? 32 : (p.rN <= 64 ? 64 : 128);
   p.status = status_word();
   // (an F block of r rows is read as rN: the last one reads into the sums, whose columns past r are not used)
-  p.x_stages = r <= 64 ? kShrinkX : 2;
+  // two such CTAs fit an SM with two steps of x in flight each (three: one CTA; 18 us instead of 13 for 8192 x 2048)
+  p.x_stages = r <= 64 && tiles * cs <= sms ? kShrinkX : 2;
   const size_t smem = 1024 + p.x_stages * kShrinkXBytes + (size_t)p.f_stages * f_stage + (size_t)p.rN * BM * 4 + table_bytes(q.num_seg);
   return launch_adapter(fn, kern, dim3(cs, tiles), 192, smem, cs, s, tx, tf, p);
 }

@@ -10,12 +10,18 @@
 // P: after a pass over topk_idx (the smallest tensor) one pass over the
 // logits gives the gradient and the sums P together.
 //
-// Deterministic: the token range is cut into one chunk per CTA, a chunk that
-// reaches into several sequences leaves one partial row per sequence, and the
-// rows of a sequence are added in chunk order.  (chunk c, sequence q) sits in
-// row c + q: along the token axis every new pair raises one of the two, so no
-// two pairs share a row.  Integer counts use atomics, whose order does not
-// matter.
+// Two kernels: the slots are counted per chunk of the token axis, then one CTA
+// per (finer) chunk adds up its sequences' counts, walks its tokens and leaves
+// its partial sums; the CTA that delivers a sequence's last partial adds them
+// and the sequence's losses up, and the one that delivers the last sequence
+// writes the totals.  A few tokens are done by a single CTA.
+//
+// Deterministic: a chunk that reaches into several sequences leaves one partial
+// row per sequence, and the rows of a sequence are added in chunk order by
+// whichever CTA comes last.  (chunk c, sequence q) sits in row c + q: along the
+// token axis every new pair raises one of the two, so no two pairs share a row.
+//
+// Bound by launch latency up to about 8192 tokens x 128 experts, by HBM above.
 #include <cfloat>
 
 #include "common.cuh"
@@ -24,31 +30,53 @@ namespace moe {
 namespace {
 
 constexpr int kMaxSeq = kMaxSegments;
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 
 struct Tokens {  // the packed token axis, cut into chunks
-  int T, E, k, num_seq, chunk;
+  int T, E, k, num_seq;
+  int chunk;        // tokens per chunk of the main kernel
+  int count_chunk;  // and of the counting kernel
+  int count_chunks;
   const int32_t* seq_offsets;  // null: one sequence of all tokens
   const uint8_t* mask;         // null: every token counts
+};
+
+struct Work {                  // in the caller's workspace
+  int32_t* cnt_part;           // [count chunk + sequence][E]
+  int32_t* tok_part;           // [count chunk + sequence]
+  int32_t* tok_chunk;          // [count chunk]
+  float* part;                 // [chunk + sequence][E]
+  float* zpart;                // [chunk + sequence]
+  float2* share;               // [sequence] its part of the two losses
+  unsigned* ticket;            // [num_seq + 1] partials delivered, sequences finished
+};
+
+struct Out {
+  int32_t* counts;
+  int32_t* tokens;
+  float* prob_sum;
+  float* loss;
 };
 
 // The sequence table in shared memory, made monotone and clamped to [0, T]
 // (a table that is not is reported): off[0..num_seq].
 __device__ __forceinline__ void load_table(const Tokens& k, int* off, int* status) {
-  if (threadIdx.x < 32) {
+  bool bad = false;
+  for (int s = threadIdx.x; s <= k.num_seq; s += kThreads) {
+    int v = k.seq_offsets ? __ldg(k.seq_offsets + s) : (s == 0 ? 0 : k.T);
+    if (v < 0 || v > k.T) {
+      bad = true;
+      v = v < 0 ? 0 : k.T;
+    }
+    off[s] = v;
+  }
+  __syncthreads();
+  if (k.num_seq > 1 && threadIdx.x < 32) {
     const int lane = threadIdx.x;
     int carry = 0;
     for (int b = 0; b <= k.num_seq; b += 32) {
-      const int s = b + lane;
-      int v = 0;
-      if (s <= k.num_seq) {
-        v = k.seq_offsets ? k.seq_offsets[s] : (s == 0 ? 0 : k.T);
-        if (v < 0 || v > k.T) {
-          set_status(status, MOE_STATUS_BAD_SEGMENTS);
-          v = v < 0 ? 0 : k.T;
-        }
-      }
+      const int s = b + lane, v = s <= k.num_seq ? off[s] : 0;
       int m = v;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -57,12 +85,16 @@ __device__ __forceinline__ void load_table(const Tokens& k, int* off, int* statu
       }
       m = max(m, carry);
       if (s <= k.num_seq) {
-        if (m != v) set_status(status, MOE_STATUS_BAD_SEGMENTS);
+        bad |= m != v;
         off[s] = m;
       }
       carry = __shfl_sync(0xffffffffu, m, 31);
     }
+  } else if (k.num_seq == 1 && threadIdx.x == 0 && off[1] < off[0]) {
+    bad = true;
+    off[1] = off[0];
   }
+  if (bad) set_status(status, MOE_STATUS_BAD_SEGMENTS);
   __syncthreads();
 }
 
@@ -92,11 +124,45 @@ __device__ __forceinline__ void for_each_piece(const int* off, int num_seq, int 
 }
 
 // ------------------------------------------------------------------ counts
-// counts[q][e], tokens[q] (zeroed before): shared-memory histogram of the
-// chunk, added to the sequence's row.
+// hist[e], *live: the slots and tokens of [a, b) that count (all threads).
+__device__ __forceinline__ void count_slots(const Tokens& tk, const int32_t* __restrict__ topk_idx, int a, int b, int* hist,
+                                            int* live, int* status) {
+  for (int e = threadIdx.x; e < tk.E; e += kThreads) hist[e] = 0;
+  if (threadIdx.x == 0) *live = 0;
+  __syncthreads();
+  int mine = 0;
+  if (tk.mask) {
+    for (int t = a + threadIdx.x; t < b; t += kThreads) mine += tk.mask[t] != 0;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
+    if ((threadIdx.x & 31) == 0 && mine) atomicAdd(live, mine);
+  } else if (threadIdx.x == 0) {
+    *live = b - a;
+  }
+  const long long q1 = (long long)b * tk.k;
+#pragma unroll 4
+  for (long long q = (long long)a * tk.k + threadIdx.x; q < q1; q += kThreads) {
+    const int e = __ldg(topk_idx + q);
+    if (tk.mask && !tk.mask[q / tk.k]) continue;
+    if (e >= 0 && e < tk.E)
+      atomicAdd(&hist[e], 1);
+    else
+      set_status(status, MOE_STATUS_BAD_INDEX);
+  }
+  __syncthreads();
+}
+
+// A sequence without tokens: everything about it is zero.
+__device__ __forceinline__ void zero_sequence(const Tokens& tk, const Out& o, int s) {
+  for (int e = threadIdx.x; e < tk.E; e += kThreads) {
+    o.counts[(size_t)s * tk.E + e] = 0;
+    o.prob_sum[(size_t)s * tk.E + e] = 0.f;
+  }
+  if (threadIdx.x == 0) o.tokens[s] = 0;
+}
+
 __global__ void __launch_bounds__(kThreads) balance_count_kernel(const Tokens tk, const int32_t* __restrict__ topk_idx,
-                                                                 int32_t* __restrict__ counts,
-                                                                 int32_t* __restrict__ tokens, int* status) {
+                                                                 const Work w, const Out o, int* status) {
   pdl_wait();
   pdl_trigger();
   extern __shared__ int sm[];
@@ -104,33 +170,25 @@ __global__ void __launch_bounds__(kThreads) balance_count_kernel(const Tokens tk
   int* hist = sm + tk.num_seq + 1;    // [E]
   __shared__ int live;
   load_table(tk, off, status);
-  const int t0 = blockIdx.x * tk.chunk, t1 = min(tk.T, t0 + tk.chunk);
+  const int c = blockIdx.x, t0 = c * tk.count_chunk, t1 = min(tk.T, t0 + tk.count_chunk);
+  int total = 0;
   for_each_piece(off, tk.num_seq, t0, t1, [&](int s, int a, int b) {
-    for (int e = threadIdx.x; e < tk.E; e += kThreads) hist[e] = 0;
-    if (threadIdx.x == 0) live = 0;
-    __syncthreads();
-    int mine = 0;
-    if (tk.mask) {
-      for (int t = a + threadIdx.x; t < b; t += kThreads) mine += tk.mask[t] != 0;
-    } else if (threadIdx.x == 0) {
-      mine = b - a;
-    }
-    if (mine) atomicAdd(&live, mine);
-    const long long q1 = (long long)b * tk.k;
-    for (long long q = (long long)a * tk.k + threadIdx.x; q < q1; q += kThreads) {
-      if (tk.mask && !tk.mask[q / tk.k]) continue;
-      const int e = topk_idx[q];
-      if (e >= 0 && e < tk.E)
-        atomicAdd(&hist[e], 1);
-      else
-        set_status(status, MOE_STATUS_BAD_INDEX);
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < tk.E; e += kThreads)
-      if (hist[e]) atomicAdd(counts + (size_t)s * tk.E + e, hist[e]);
-    if (threadIdx.x == 0 && live) atomicAdd(tokens + s, live);
+    count_slots(tk, topk_idx, a, b, hist, &live, status);
+    for (int e = threadIdx.x; e < tk.E; e += kThreads) w.cnt_part[(size_t)(c + s) * tk.E + e] = hist[e];
+    if (threadIdx.x == 0) w.tok_part[c + s] = live;
+    total += live;
     __syncthreads();
   });
+  if (threadIdx.x == 0) w.tok_chunk[c] = total;
+  for (int s = c; s < tk.num_seq; s += gridDim.x)
+    if (off[s + 1] == off[s]) {
+      zero_sequence(tk, o, s);
+      if (threadIdx.x == 0) w.share[s] = make_float2(0.f, 0.f);
+    }
+  if (c == 0) {  // for the main kernel, which starts after this one
+    for (int s = threadIdx.x; s <= tk.num_seq; s += kThreads) w.ticket[s] = 0;
+    if (threadIdx.x < 2) o.loss[threadIdx.x] = 0.f;
+  }
 }
 
 // ------------------------------------------------------------- main kernel
@@ -140,50 +198,50 @@ __global__ void __launch_bounds__(kThreads) balance_count_kernel(const Tokens tk
 // before the first is used.  The lane's share of P stays in registers over
 // the piece and is added over the warp's token groups and the warps at its
 // end.
+//
+// kInline: one CTA does everything, counting included.
 struct Grad {
   float a, b;            // coefficients of the two losses
   const float* dloss;    // their upstream gradients on the device, or null
   float* dlogits;
 };
 
-template <int LPT, int VEC, int NQ, bool kSum, bool kGrad>
-__global__ void __launch_bounds__(kThreads) balance_main_kernel(const Tokens tk, const float* __restrict__ logits,
-                                                                const int32_t* __restrict__ counts,
-                                                                const int32_t* __restrict__ tokens, const Grad gr,
-                                                                float* __restrict__ part, float* __restrict__ zpart,
-                                                                unsigned* __restrict__ ticket, int* status) {
+template <int LPT, int VEC, int NQ, bool kSum, bool kGrad, bool kInline>
+__global__ void __launch_bounds__(kThreads, NQ * VEC <= 8 ? 2 : 1) balance_main_kernel(const Tokens tk, const float* __restrict__ logits,
+                                                                const int32_t* __restrict__ topk_idx, const Work w,
+                                                                const Out o, const Grad gr, int* status) {
   constexpr int NV = NQ * VEC;       // values per lane
   constexpr int TPW = 32 / LPT;      // tokens per warp side by side
   constexpr int kU = NV <= 4 ? 4 : (NV <= 8 ? 2 : 1);
-  pdl_wait();
+  // After a counting kernel of the same call, which waited for everything before
+  // it, the logits and the table may be read at once; only the counts are waited for.
+  constexpr bool kCounted = kSum && !kInline;
+  if (!kCounted) pdl_wait();
   pdl_trigger();
   extern __shared__ int sm[];
-  int* off = sm;                                                       // [num_seq + 1]
-  float* red = reinterpret_cast<float*>(sm + ((tk.num_seq + 4) & ~3));  // kSum: [kWarps][E + 1]
-  __shared__ int s_n;
+  int* off = sm;                                                        // [num_seq + 1]
+  int* cnt = sm + ((tk.num_seq + 4) & ~3);                              // [E] the sequence's counts
+  float* red = reinterpret_cast<float*>(cnt + ((tk.E + 3) & ~3));       // kSum: [kWarps][E + 1]
+  __shared__ int s_n, s_tok, s_seqs;
+  __shared__ bool s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / LPT, el = lane % LPT;
   const int E = tk.E;
-  if (threadIdx.x == 0) {
-    s_n = 0;
-    if (kSum && blockIdx.x == 0) *ticket = 0;  // read by the finishing kernel only
-  }
   load_table(tk, off, status);
-  const int t0 = blockIdx.x * tk.chunk, t1 = min(tk.T, t0 + tk.chunk);
-  float ga = 0.f, gb = 0.f;
-  if constexpr (kGrad) {
-    int n = 0;
-    for (int s = threadIdx.x; s < tk.num_seq; s += kThreads) n += tokens[s];
-    if (n) atomicAdd(&s_n, n);
-    __syncthreads();
-    const float rn = 1.f / (float)max(s_n, 1);
-    ga = gr.a * (gr.dloss ? gr.dloss[0] : 1.f) * ((float)E / (float)tk.k) * rn;
-    gb = gr.b * (gr.dloss ? gr.dloss[1] : 1.f) * 2.f * rn;
-    // tokens outside every sequence get no gradient
+  const int chunk = blockIdx.x, t0 = chunk * tk.chunk, t1 = min(tk.T, t0 + tk.chunk);
+  if constexpr (kGrad) {  // tokens outside every sequence get no gradient
     const int lo = min(t1, max(t0, off[0])), hi = max(t0, min(t1, off[tk.num_seq]));
     for (size_t i = (size_t)t0 * E + threadIdx.x; i < (size_t)lo * E; i += kThreads) gr.dlogits[i] = 0.f;
     for (size_t i = (size_t)max(lo, hi) * E + threadIdx.x; i < (size_t)t1 * E; i += kThreads) gr.dlogits[i] = 0.f;
   }
+  if constexpr (kInline) {
+    for (int s = 0; s < tk.num_seq; ++s)
+      if (off[s + 1] == off[s]) zero_sequence(tk, o, s);
+    if (threadIdx.x < 2) o.loss[threadIdx.x] = 0.f;
+  }
+  float ga = 0.f, gb = 0.f, rn = 0.f;   // set with the first piece
+  float loss_b = 0.f, loss_z = 0.f;     // kInline: thread 0's running totals
+  bool ready = false;
   const unsigned gmask = LPT == 32 ? 0xffffffffu : (((1u << (LPT & 31)) - 1u) << (sub * LPT));
   auto gmax = [&](float v) {
 #pragma unroll
@@ -196,39 +254,96 @@ __global__ void __launch_bounds__(kThreads) balance_main_kernel(const Tokens tk,
     return v;
   };
   auto col = [&](int i) { return (i / VEC) * VEC * LPT + el * VEC + i % VEC; };
+  const int step = kWarps * TPW;
+
+  float l[kU][NV];
+  bool on[kU];
+  auto load = [&](int tb, int b) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int t = tb + u * step;
+      on[u] = t < b && (!tk.mask || tk.mask[t]);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        const int c0 = q * VEC * LPT + el * VEC;
+        if constexpr (VEC == 4) {
+          float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+          if (on[u] && c0 < E) v = __ldg(reinterpret_cast<const float4*>(logits + (size_t)t * E + c0));
+          l[u][4 * q] = v.x; l[u][4 * q + 1] = v.y; l[u][4 * q + 2] = v.z; l[u][4 * q + 3] = v.w;
+        } else {
+          l[u][q] = on[u] && c0 < E ? __ldg(logits + (size_t)t * E + c0) : -INFINITY;
+        }
+      }
+    }
+  };
 
   for_each_piece(off, tk.num_seq, t0, t1, [&](int s, int a, int b) {
-    float cf[kGrad ? NV : 1], acc[kSum ? NV : 1];
-    float ga_s = 0.f, z = 0.f;
+    float acc[kSum ? NV : 1];
+    float cf[kGrad ? NV : 1];
+    float z = 0.f;
+    int tb = a + warp * TPW + sub;
+    load(tb, b);  // under way while the counts are added up
+    if (!ready) {
+      if constexpr (kCounted) pdl_wait();
+      if (threadIdx.x == 0) s_n = s_seqs = 0;
+      __syncthreads();
+      int n = 0, seqs = 0;
+      if constexpr (kInline) {
+        if (tk.mask) {
+          for (int t = off[0] + threadIdx.x; t < off[tk.num_seq]; t += kThreads) n += tk.mask[t] != 0;
+        } else if (threadIdx.x == 0) {
+          n = off[tk.num_seq] - off[0];
+        }
+      } else if constexpr (kSum) {
+        for (int c = threadIdx.x; c < tk.count_chunks; c += kThreads) n += w.tok_chunk[c];
+        for (int q = threadIdx.x; q < tk.num_seq; q += kThreads) seqs += off[q + 1] > off[q];
+      } else {
+        for (int q = threadIdx.x; q < tk.num_seq; q += kThreads) n += o.tokens[q];
+      }
+      if (n) atomicAdd(&s_n, n);
+      if (seqs) atomicAdd(&s_seqs, seqs);
+      __syncthreads();
+      rn = 1.f / (float)max(s_n, 1);
+      if constexpr (kGrad) {
+        ga = gr.a * (gr.dloss ? gr.dloss[0] : 1.f) * ((float)E / (float)tk.k) * rn;
+        gb = gr.b * (gr.dloss ? gr.dloss[1] : 1.f) * 2.f * rn;
+      }
+      ready = true;
+    }
+    // the sequence's counts
+    if constexpr (kInline) {
+      count_slots(tk, topk_idx, a, b, cnt, &s_tok, status);
+    } else if constexpr (kSum) {
+      for (int e = threadIdx.x; e < E; e += kThreads) cnt[e] = 0;
+      if (threadIdx.x == 0) s_tok = 0;
+      __syncthreads();
+      const int c0 = off[s] / tk.count_chunk, c1 = (off[s + 1] - 1) / tk.count_chunk + 1;
+      // the rows side by side as far as the threads reach
+      const int groups = max(1, kThreads / E);
+      const int g = threadIdx.x / E, e0 = groups > 1 ? threadIdx.x % E : threadIdx.x;
+      if (g < groups || groups == 1) {
+        for (int e = e0; e < E; e += groups > 1 ? E : kThreads) {
+          int v = 0;
+#pragma unroll 8
+          for (int c = c0 + (groups > 1 ? g : 0); c < c1; c += groups) v += w.cnt_part[(size_t)(c + s) * E + e];
+          if (v) atomicAdd(&cnt[e], v);
+        }
+      }
+      for (int c = c0 + threadIdx.x; c < c1; c += kThreads) atomicAdd(&s_tok, w.tok_part[c + s]);
+      __syncthreads();
+    }
+    float ga_s = 0.f;
     if constexpr (kGrad) {
-      ga_s = ga / (float)max(tokens[s], 1);
+      ga_s = ga / (float)max(kSum ? s_tok : o.tokens[s], 1);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) cf[i] = col(i) < E ? (float)counts[(size_t)s * E + col(i)] : 0.f;
+      for (int i = 0; i < NV; ++i)
+        cf[i] = col(i) < E ? (float)(kSum ? cnt[col(i)] : o.counts[(size_t)s * E + col(i)]) : 0.f;
     }
     if constexpr (kSum) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) acc[i] = 0.f;
     }
-    const int step = kWarps * TPW;
-    for (int tb = a + warp * TPW + sub; tb < b; tb += kU * step) {
-      float l[kU][NV];
-      bool on[kU];
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int t = tb + u * step;
-        on[u] = t < b && (!tk.mask || tk.mask[t]);
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) {
-          const int c0 = q * VEC * LPT + el * VEC;
-          if constexpr (VEC == 4) {
-            float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-            if (on[u] && c0 < E) v = __ldg(reinterpret_cast<const float4*>(logits + (size_t)t * E + c0));
-            l[u][4 * q] = v.x; l[u][4 * q + 1] = v.y; l[u][4 * q + 2] = v.z; l[u][4 * q + 3] = v.w;
-          } else {
-            l[u][q] = on[u] && c0 < E ? __ldg(logits + (size_t)t * E + c0) : -INFINITY;
-          }
-        }
-      }
+    while (tb < b) {
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int t = tb + u * step;
@@ -257,9 +372,9 @@ __global__ void __launch_bounds__(kThreads) balance_main_kernel(const Tokens tk,
           }
           if constexpr (kGrad) {
             dot = gsum(dot) * r;
-            const float w = gb * lse - ga_s * dot;
+            const float c = gb * lse - ga_s * dot;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) dl[i] = l[u][i] * r * fmaf(ga_s, cf[i], w);
+            for (int i = 0; i < NV; ++i) dl[i] = l[u][i] * r * fmaf(ga_s, cf[i], c);
           }
         } else {
 #pragma unroll
@@ -270,15 +385,17 @@ __global__ void __launch_bounds__(kThreads) balance_main_kernel(const Tokens tk,
           for (int q = 0; q < NQ; ++q) {
             const int c0 = q * VEC * LPT + el * VEC;
             if (c0 < E) {
-              float* o = gr.dlogits + (size_t)t * E + c0;
+              float* d = gr.dlogits + (size_t)t * E + c0;
               if constexpr (VEC == 4)
-                *reinterpret_cast<float4*>(o) = make_float4(dl[4 * q], dl[4 * q + 1], dl[4 * q + 2], dl[4 * q + 3]);
+                *reinterpret_cast<float4*>(d) = make_float4(dl[4 * q], dl[4 * q + 1], dl[4 * q + 2], dl[4 * q + 3]);
               else
-                *o = dl[q];
+                *d = dl[q];
             }
           }
         }
       }
+      tb += kU * step;
+      if (tb < b) load(tb, b);
     }
     if constexpr (kSum) {
       __syncwarp();
@@ -296,171 +413,206 @@ __global__ void __launch_bounds__(kThreads) balance_main_kernel(const Tokens tk,
       }
       if (lane == 0) red[warp * (E + 1) + E] = z;
       __syncthreads();
-      const size_t row = (size_t)(blockIdx.x + s);
+      // rows of `red` added into row 0: the CTA's sums (kInline: the sequence's)
       for (int e = threadIdx.x; e <= E; e += kThreads) {
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += red[w * (E + 1) + e];
-        if (e < E)
-          part[row * E + e] = v;
-        else
-          zpart[row] = v;
+        for (int i = 0; i < kWarps; ++i) v += red[i * (E + 1) + e];
+        if constexpr (kInline) {
+          red[e] = v;
+        } else if (e < E) {
+          w.part[(size_t)(chunk + s) * E + e] = v;
+        } else {
+          w.zpart[chunk + s] = v;
+        }
+      }
+      bool finish = true;
+      if constexpr (!kInline) {
+        const int c0 = off[s] / tk.chunk, c1 = (off[s + 1] - 1) / tk.chunk + 1;
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) s_last = atomicAdd(w.ticket + s, 1u) == (unsigned)(c1 - c0 - 1);
+        __syncthreads();
+        finish = s_last;
+        if (finish) {  // this CTA delivered the sequence's last partial: add them all
+          __threadfence();
+          for (int v0 = 0; v0 <= E; v0 += 32) {
+            const int e = v0 + lane;
+            float v = 0.f;
+            if (e <= E) {
+#pragma unroll 8
+              for (int c = c0 + warp; c < c1; c += kWarps)
+                v += e < E ? __ldcg(w.part + (size_t)(c + s) * E + e) : __ldcg(w.zpart + c + s);
+              red[warp * (E + 1) + e] = v;
+            }
+          }
+          __syncthreads();
+          for (int e = threadIdx.x; e <= E; e += kThreads) {
+            float v = 0.f;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) v += red[i * (E + 1) + e];
+            red[e] = v;
+          }
+        }
+      }
+      if (finish) {
+        __syncthreads();
+        float dot = 0.f;
+        for (int e = threadIdx.x; e < E; e += kThreads) {
+          o.prob_sum[(size_t)s * E + e] = red[e];
+          o.counts[(size_t)s * E + e] = cnt[e];
+          dot = fmaf(red[e], (float)cnt[e], dot);
+        }
+        const float zz = red[E];
+        __syncthreads();
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+        if (lane == 0) red[warp] = dot;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          float t = 0.f;
+          for (int i = 0; i < kWarps; ++i) t += red[i];
+          o.tokens[s] = s_tok;
+          const float2 sh = make_float2(t * ((float)E / (float)tk.k) / (float)max(s_tok, 1) * rn, zz * rn);
+          if constexpr (kInline) {
+            loss_b += sh.x;
+            loss_z += sh.y;
+            o.loss[0] = loss_b;
+            o.loss[1] = loss_z;
+          } else {
+            __stcg(w.share + s, sh);
+            __threadfence();
+            s_last = atomicAdd(w.ticket + tk.num_seq, 1u) == (unsigned)(s_seqs - 1);
+          }
+        }
+        if constexpr (!kInline) {
+          __syncthreads();
+          if (s_last) {  // and the last sequence: the shares in order
+            __threadfence();
+            float lb = 0.f, lz = 0.f;
+            for (int i = threadIdx.x; i < tk.num_seq; i += kThreads) {
+              const float2 h = __ldcg(w.share + i);
+              lb += h.x;
+              lz += h.y;
+            }
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+              lb += __shfl_xor_sync(0xffffffffu, lb, d);
+              lz += __shfl_xor_sync(0xffffffffu, lz, d);
+            }
+            __syncthreads();
+            if (lane == 0) {
+              red[2 * warp] = lb;
+              red[2 * warp + 1] = lz;
+            }
+            __syncthreads();
+            if (threadIdx.x == 0) {
+              lb = lz = 0.f;
+              for (int i = 0; i < kWarps; ++i) {
+                lb += red[2 * i];
+                lz += red[2 * i + 1];
+              }
+              o.loss[0] = lb;
+              o.loss[1] = lz;
+            }
+          }
+        }
       }
       __syncthreads();
     }
   });
-}
-
-// -------------------------------------------------------------- finish kernel
-// CTA (sequence q, 32 experts): P_qe from the partial rows in order (32 row
-// groups side by side, added in order), and their share of the two losses;
-// the last CTA to finish adds the shares in order.
-__global__ void __launch_bounds__(1024) balance_finish_kernel(const Tokens tk, const float* __restrict__ part,
-                                                              const float* __restrict__ zpart,
-                                                              const int32_t* __restrict__ counts,
-                                                              const int32_t* __restrict__ tokens,
-                                                              float* __restrict__ prob_sum, float2* __restrict__ share,
-                                                              unsigned* __restrict__ ticket, float* __restrict__ loss,
-                                                              int* status) {
-  pdl_wait();
-  pdl_trigger();
-  extern __shared__ int sm[];
-  int* off = sm;
-  __shared__ float red[32][33];
-  __shared__ float zred[32];
-  __shared__ int s_n;
-  __shared__ bool last;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int q = blockIdx.x, e = blockIdx.y * 32 + lane;
-  if (threadIdx.x == 0) s_n = 0;
-  load_table(tk, off, status);
-  int n = 0;
-  for (int s = threadIdx.x; s < tk.num_seq; s += 1024) n += tokens[s];
-  if (n) atomicAdd(&s_n, n);
-  const int a = off[q], b = off[q + 1];
-  const int c0 = a / tk.chunk, c1 = b > a ? (b - 1) / tk.chunk + 1 : c0;
-  float v = 0.f;
-  if (e < tk.E) {
-#pragma unroll 4
-    for (int c = c0 + warp; c < c1; c += 32) v += part[(size_t)(c + q) * tk.E + e];
-  }
-  red[warp][lane] = v;
-  float z = 0.f;
-  if (blockIdx.y == 0) {
-    for (int c = c0 + threadIdx.x; c < c1; c += 1024) z += zpart[c + q];
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-    if (lane == 0) zred[warp] = z;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    float p = 0.f, zz = 0.f;
-    for (int w = 0; w < 32; ++w) p += red[w][lane];
-    if (e < tk.E) prob_sum[(size_t)q * tk.E + e] = p;
-    float t = e < tk.E ? p * (float)counts[(size_t)q * tk.E + e] : 0.f;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
-    if (blockIdx.y == 0)
-      for (int w = 0; w < 32; ++w) zz += zred[w];
-    if (lane == 0) {
-      const float rn = 1.f / (float)max(s_n, 1), nq = (float)max(tokens[q], 1);
-      share[(size_t)q * gridDim.y + blockIdx.y] =
-          make_float2(t * ((float)tk.E / (float)tk.k) / nq * rn, zz * rn);
-      __threadfence();
-      last = atomicAdd(ticket, 1u) == gridDim.x * gridDim.y - 1;
-    }
-  }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  const int total = gridDim.x * gridDim.y;
-  float lb = 0.f, lz = 0.f;
-  for (int i = threadIdx.x; i < total; i += 1024) {
-    const float2 h = __ldcg(share + i);
-    lb += h.x;
-    lz += h.y;
-  }
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    lb += __shfl_xor_sync(0xffffffffu, lb, d);
-    lz += __shfl_xor_sync(0xffffffffu, lz, d);
-  }
-  if (lane == 0) {
-    red[0][warp] = lb;
-    red[1][warp] = lz;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    lb = lz = 0.f;
-    for (int w = 0; w < 32; ++w) {
-      lb += red[0][w];
-      lz += red[1][w];
-    }
-    loss[0] = lb;
-    loss[1] = lz;
-  }
+  // a CTA without a piece still may not end before the counting kernel does
+  if constexpr (kCounted)
+    if (!ready) pdl_wait();
 }
 
 // --------------------------------------------------------------- host side
 
 size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 
-// Chunks: enough for four CTAs per SM, at least 16 tokens each.
-constexpr int kMaxChunks = 608;
-int chunk_tokens(int T) {
-  const int c = (T + kMaxChunks - 1) / kMaxChunks;
-  return c < 16 ? 16 : c;
+// Main chunks: two CTAs per SM, at least 16 tokens each; counting chunks fewer,
+// since every main CTA adds their rows up.
+constexpr int kMaxChunks = 304, kMaxCountChunks = 64;
+// One CTA does the whole of a problem of up to so many logits (and few sequences).
+constexpr int kInlineLogits = 16384, kInlineSeqs = 4;
+
+int chunk_tokens(int T, int most, int least) {
+  const int c = (T + most - 1) / most;
+  return c < least ? least : c;
 }
 
+bool is_inline(int T, int E, int num_seq) { return (long long)T * E <= kInlineLogits && num_seq <= kInlineSeqs; }
+
 struct Layout {
-  int chunk, nchunk;
-  size_t part, zpart, share, ticket, total;
+  int chunk, nchunk, count_chunk, ncount;
+  size_t cnt, tok, tokc, part, zpart, share, ticket, total;
 };
 Layout layout(int T, int E, int num_seq) {
   Layout L;
-  L.chunk = chunk_tokens(T);
+  L.chunk = chunk_tokens(T, kMaxChunks, 16);
   L.nchunk = (T + L.chunk - 1) / L.chunk;
-  const size_t rows = (size_t)L.nchunk + num_seq;
+  L.count_chunk = chunk_tokens(T, kMaxCountChunks, 64);
+  L.ncount = (T + L.count_chunk - 1) / L.count_chunk;
+  const size_t rows = (size_t)L.nchunk + num_seq, crows = (size_t)L.ncount + num_seq;
   size_t at = 0;
-  L.part = at; at += align256(rows * E * sizeof(float));
-  L.zpart = at; at += align256(rows * sizeof(float));
-  L.share = at; at += align256((size_t)num_seq * ((E + 31) / 32) * sizeof(float2));
-  L.ticket = at; at += 256;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
+  L.cnt = take(crows * E * sizeof(int32_t));
+  L.tok = take(crows * sizeof(int32_t));
+  L.tokc = take((size_t)L.ncount * sizeof(int32_t));
+  L.part = take(rows * E * sizeof(float));
+  L.zpart = take(rows * sizeof(float));
+  L.share = take((size_t)num_seq * sizeof(float2));
+  L.ticket = take((size_t)(num_seq + 1) * sizeof(unsigned));
   L.total = at;
   return L;
 }
 
-template <bool kSum, bool kGrad>
+template <bool kSum, bool kGrad, bool kInline>
 struct Main {
   template <int LPT, int VEC, int NQ>
-  static void go(const Layout& L, const Tokens& tk, const float* logits, const int32_t* counts, const int32_t* tokens,
-                 const Grad& gr, float* part, float* zpart, unsigned* ticket, cudaStream_t s) {
-    const size_t smem = sizeof(int) * ((tk.num_seq + 4) & ~3) + (kSum ? sizeof(float) * kWarps * (tk.E + 1) : 0);
-    launch_pdl(balance_main_kernel<LPT, VEC, NQ, kSum, kGrad>, L.nchunk, kThreads, smem, s, tk, logits, counts, tokens,
-               gr, part, zpart, ticket, status_word());
+  static int go(const char* fn, int grid, const Tokens& tk, const float* logits, const int32_t* idx, const Work& w, const Out& o,
+                const Grad& gr, cudaStream_t s) {
+    const size_t smem = sizeof(int) * (((tk.num_seq + 4) & ~3) + ((tk.E + 3) & ~3)) + (kSum ? sizeof(float) * kWarps * (tk.E + 1) : 0);
+    auto kern = balance_main_kernel<LPT, VEC, NQ, kSum, kGrad, kInline>;
+    if (smem > 48 * 1024) {
+      static bool set[64] = {};
+      const int dev = current_device();
+      if (dev < 0) return fail(MOE_ERR_CUDA, "%s: no current CUDA device", fn);
+      if (!set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+        if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+        set[dev] = true;
+      }
+    }
+    launch_pdl(kern, grid, kThreads, smem, s, tk, logits, idx, w, o, gr, status_word());
+    return check_launch(fn, "main kernel");
   }
   template <class... A>
-  static void pick(int E, A&&... a) {
+  static int pick(const char* fn, int grid, const Tokens& tk, A&&... a) {
+    const int E = tk.E;
     if (E % 4 == 0) {
-      if (E <= 4) go<1, 4, 1>(a...);
-      else if (E <= 8) go<2, 4, 1>(a...);
-      else if (E <= 16) go<4, 4, 1>(a...);
-      else if (E <= 32) go<8, 4, 1>(a...);
-      else if (E <= 64) go<16, 4, 1>(a...);
-      else if (E <= 128) go<32, 4, 1>(a...);
-      else if (E <= 256) go<32, 4, 2>(a...);
-      else if (E <= 512) go<32, 4, 4>(a...);
-      else go<32, 4, 8>(a...);
-    } else {
-      if (E <= 4) go<4, 1, 1>(a...);
-      else if (E <= 16) go<16, 1, 1>(a...);
-      else if (E <= 32) go<32, 1, 1>(a...);
-      else if (E <= 64) go<32, 1, 2>(a...);
-      else if (E <= 128) go<32, 1, 4>(a...);
-      else if (E <= 256) go<32, 1, 8>(a...);
-      else if (E <= 512) go<32, 1, 16>(a...);
-      else go<32, 1, 32>(a...);
+      if (E <= 4) return go<1, 4, 1>(fn, grid, tk, a...);
+      if (E <= 8) return go<2, 4, 1>(fn, grid, tk, a...);
+      if (E <= 16) return go<4, 4, 1>(fn, grid, tk, a...);
+      if (E <= 32) return go<8, 4, 1>(fn, grid, tk, a...);
+      if (E <= 64) return go<16, 4, 1>(fn, grid, tk, a...);
+      if (E <= 128) return go<32, 4, 1>(fn, grid, tk, a...);
+      if (E <= 256) return go<32, 4, 2>(fn, grid, tk, a...);
+      if (E <= 512) return go<32, 4, 4>(fn, grid, tk, a...);
+      return go<32, 4, 8>(fn, grid, tk, a...);
     }
+    if (E <= 4) return go<4, 1, 1>(fn, grid, tk, a...);
+    if (E <= 16) return go<16, 1, 1>(fn, grid, tk, a...);
+    if (E <= 32) return go<32, 1, 1>(fn, grid, tk, a...);
+    if (E <= 64) return go<32, 1, 2>(fn, grid, tk, a...);
+    if (E <= 128) return go<32, 1, 4>(fn, grid, tk, a...);
+    if (E <= 256) return go<32, 1, 8>(fn, grid, tk, a...);
+    if (E <= 512) return go<32, 1, 16>(fn, grid, tk, a...);
+    return go<32, 1, 32>(fn, grid, tk, a...);
   }
 };
 
@@ -502,31 +654,32 @@ int moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t
   const Layout L = layout(T, E, num_seg);
   if (ws_bytes < L.total) return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws_bytes, L.total);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaMemsetAsync(counts, 0, sizeof(int32_t) * (size_t)num_seg * E, s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(tokens, 0, sizeof(int32_t) * (size_t)num_seg, s);
-  if (e == cudaSuccess && T == 0) e = cudaMemsetAsync(prob_sum, 0, sizeof(float) * (size_t)num_seg * E, s);
-  if (e == cudaSuccess && T == 0) e = cudaMemsetAsync(loss, 0, 2 * sizeof(float), s);
-  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
-  if (T == 0) return MOE_OK;
-  const Tokens tk{T, E, k, num_seg, L.chunk, seg_offsets, mask};
+  if (T == 0) {
+    cudaError_t e = cudaMemsetAsync(counts, 0, sizeof(int32_t) * (size_t)num_seg * E, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(tokens, 0, sizeof(int32_t) * (size_t)num_seg, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(prob_sum, 0, sizeof(float) * (size_t)num_seg * E, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(loss, 0, 2 * sizeof(float), s);
+    if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    return MOE_OK;
+  }
+  Tokens tk{T, E, k, num_seg, L.chunk, L.count_chunk, L.ncount, seg_offsets, mask};
   char* base = static_cast<char*>(ws);
-  auto* part = reinterpret_cast<float*>(base + L.part);
-  auto* zpart = reinterpret_cast<float*>(base + L.zpart);
-  auto* share = reinterpret_cast<float2*>(base + L.share);
-  auto* ticket = reinterpret_cast<unsigned*>(base + L.ticket);
-  const size_t table = sizeof(int) * (size_t)(num_seg + 1);
-  launch_pdl(balance_count_kernel, L.nchunk, kThreads, table + sizeof(int) * (size_t)E, s, tk, topk_idx, counts, tokens,
+  const Work w{reinterpret_cast<int32_t*>(base + L.cnt),  reinterpret_cast<int32_t*>(base + L.tok),
+               reinterpret_cast<int32_t*>(base + L.tokc), reinterpret_cast<float*>(base + L.part),
+               reinterpret_cast<float*>(base + L.zpart),  reinterpret_cast<float2*>(base + L.share),
+               reinterpret_cast<unsigned*>(base + L.ticket)};
+  const Out o{counts, tokens, prob_sum, loss};
+  const Grad gr{balance_coef, z_coef, nullptr, dlogits};
+  if (is_inline(T, E, num_seg)) {
+    tk.chunk = T;
+    return dlogits ? Main<true, true, true>::pick(fn, 1, tk, logits, topk_idx, w, o, gr, s)
+                   : Main<true, false, true>::pick(fn, 1, tk, logits, topk_idx, w, o, gr, s);
+  }
+  launch_pdl(balance_count_kernel, L.ncount, kThreads, sizeof(int) * (size_t)(num_seg + 1 + E), s, tk, topk_idx, w, o,
              status_word());
   if (int rc = check_launch(fn, "count kernel")) return rc;
-  const Grad gr{balance_coef, z_coef, nullptr, dlogits};
-  if (dlogits)
-    Main<true, true>::pick(E, L, tk, logits, counts, tokens, gr, part, zpart, ticket, s);
-  else
-    Main<true, false>::pick(E, L, tk, logits, counts, tokens, gr, part, zpart, ticket, s);
-  if (int rc = check_launch(fn, "main kernel")) return rc;
-  launch_pdl(balance_finish_kernel, dim3(num_seg, (E + 31) / 32), 1024, table, s, tk, part, zpart, counts, tokens,
-             prob_sum, share, ticket, loss, status_word());
-  return check_launch(fn, "finish kernel");
+  return dlogits ? Main<true, true, false>::pick(fn, L.nchunk, tk, logits, topk_idx, w, o, gr, s)
+                 : Main<true, false, false>::pick(fn, L.nchunk, tk, logits, topk_idx, w, o, gr, s);
 }
 
 int moe_balance_loss_bwd(const float* logits, const uint8_t* mask, int T, int E, int k, int num_seg,
@@ -539,12 +692,11 @@ int moe_balance_loss_bwd(const float* logits, const uint8_t* mask, int T, int E,
   if (!counts || !tokens || !dlogits) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer argument", fn);
   if (!aligned16(dlogits)) return fail(MOE_ERR_ALIGNMENT, "%s: dlogits must be 16-byte aligned", fn);
   const Layout L = layout(T, E, num_seg);
-  const Tokens tk{T, E, k, num_seg, L.chunk, seg_offsets, mask};
+  const Tokens tk{T, E, k, num_seg, L.chunk, L.count_chunk, L.ncount, seg_offsets, mask};
+  const Out o{const_cast<int32_t*>(counts), const_cast<int32_t*>(tokens), nullptr, nullptr};  // read only
   const Grad gr{balance_coef, z_coef, dloss, dlogits};
-  Main<false, true>::pick(E, L, tk, logits, counts, tokens, gr, static_cast<float*>(nullptr),
-                          static_cast<float*>(nullptr), static_cast<unsigned*>(nullptr),
-                          static_cast<cudaStream_t>(stream));
-  return check_launch(fn);
+  return Main<false, true, false>::pick(fn, L.nchunk, tk, logits, static_cast<const int32_t*>(nullptr), Work{}, o, gr,
+                                        static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
