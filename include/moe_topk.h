@@ -443,7 +443,7 @@ int moe_route_topk_logits_bwd(const float* d_w, const float* topk_w, const int32
  * [seg_offsets[q], seg_offsets[q+1]); NULL with num_seg = 1 is one sequence
  * of all tokens.  Tokens before the first and after the last offset, and
  * tokens whose mask byte is 0 (mask uint8 [T], NULL: none), take no part:
- * their logits are not read and their dlogits are 0.  With m_t = 1 for the
+ * what their logits hold does not matter and their dlogits are 0.  With m_t = 1 for the
  * tokens that take part, p_t = softmax(logits[t]), n_q = sum m_t, n = sum n_q:
  *   counts[q,e]   = slots of q's tokens routed to e (topk_idx)   int32 [num_seg,E]
  *   tokens[q]     = n_q                                          int32 [num_seg]

@@ -132,22 +132,32 @@ __device__ __forceinline__ void count_slots(const Tokens& tk, const int32_t* __r
   __syncthreads();
   int mine = 0;
   if (tk.mask) {
-    for (int t = a + threadIdx.x; t < b; t += kThreads) mine += tk.mask[t] != 0;
+    for (int t = a + threadIdx.x; t < b; t += kThreads) mine += __ldg(tk.mask + t) != 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
     if ((threadIdx.x & 31) == 0 && mine) atomicAdd(live, mine);
   } else if (threadIdx.x == 0) {
     *live = b - a;
   }
-  const long long q1 = (long long)b * tk.k;
-#pragma unroll 4
-  for (long long q = (long long)a * tk.k + threadIdx.x; q < q1; q += kThreads) {
-    const int e = __ldg(topk_idx + q);
-    if (tk.mask && !tk.mask[q / tk.k]) continue;
-    if (e >= 0 && e < tk.E)
-      atomicAdd(&hist[e], 1);
-    else
-      set_status(status, MOE_STATUS_BAD_INDEX);
+  // four slots' loads under way before the first is counted
+  const unsigned q1 = (unsigned)b * tk.k;  // T k < 2^31
+  for (unsigned q0 = (unsigned)a * tk.k + threadIdx.x; q0 < q1; q0 += 4 * kThreads) {
+    int e[4];
+    bool on[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const unsigned q = q0 + u * kThreads;
+      e[u] = q < q1 ? __ldg(topk_idx + q) : 0;
+      on[u] = q < q1 && (!tk.mask || __ldg(tk.mask + q / (unsigned)tk.k));
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (!on[u]) continue;
+      if (e[u] >= 0 && e[u] < tk.E)
+        atomicAdd(&hist[e[u]], 1);
+      else
+        set_status(status, MOE_STATUS_BAD_INDEX);
+    }
   }
   __syncthreads();
 }
@@ -191,6 +201,22 @@ __global__ void __launch_bounds__(kThreads) balance_count_kernel(const Tokens tk
   }
 }
 
+// e^x, x <= 0, through the hardware's base-2 exponential: a product's rounding
+// more than expf (relative error below 2^-23 |x| + 2^-22) at a third of its
+// instructions, which bound the kernel.
+__device__ __forceinline__ float exp_of(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+
+// largest of a warp's values (all lanes converged)
+__device__ __forceinline__ float warp_max(float v) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+
 // ------------------------------------------------------------- main kernel
 //
 // LPT lanes hold one token's logits (VEC consecutive values NQ times, VEC LPT
@@ -212,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, NQ * VEC <= 8 ? 2 : 1) balance_main_
                                                                 const Out o, const Grad gr, int* status) {
   constexpr int NV = NQ * VEC;       // values per lane
   constexpr int TPW = 32 / LPT;      // tokens per warp side by side
-  constexpr int kU = NV <= 4 ? 4 : (NV <= 8 ? 2 : 1);
+  constexpr int kU = NV <= 8 ? 2 : 1;
   // After a counting kernel of the same call, which waited for everything before
   // it, the logits and the table may be read at once; only the counts are waited for.
   constexpr bool kCounted = kSum && !kInline;
@@ -243,35 +269,45 @@ __global__ void __launch_bounds__(kThreads, NQ * VEC <= 8 ? 2 : 1) balance_main_
   float loss_b = 0.f, loss_z = 0.f;     // kInline: thread 0's running totals
   bool ready = false;
   const unsigned gmask = LPT == 32 ? 0xffffffffu : (((1u << (LPT & 31)) - 1u) << (sub * LPT));
-  auto gmax = [&](float v) {
+  // over a token's lanes, kU tokens side by side
+  auto gmax = [&](float (&v)[kU]) {
+    if constexpr (LPT == 32) {
 #pragma unroll
-    for (int d = LPT / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(gmask, v, d));
-    return v;
+      for (int u = 0; u < kU; ++u) v[u] = warp_max(v[u]);
+    } else {
+#pragma unroll
+      for (int d = LPT / 2; d > 0; d >>= 1)
+#pragma unroll
+        for (int u = 0; u < kU; ++u) v[u] = fmaxf(v[u], __shfl_xor_sync(gmask, v[u], d));
+    }
   };
-  auto gsum = [&](float v) {
+  auto gsum = [&](float (&v)[kU]) {
 #pragma unroll
-    for (int d = LPT / 2; d > 0; d >>= 1) v += __shfl_xor_sync(gmask, v, d);
-    return v;
+    for (int d = LPT / 2; d > 0; d >>= 1)
+#pragma unroll
+      for (int u = 0; u < kU; ++u) v[u] += __shfl_xor_sync(gmask, v[u], d);
   };
   auto col = [&](int i) { return (i / VEC) * VEC * LPT + el * VEC + i % VEC; };
   const int step = kWarps * TPW;
 
-  float l[kU][NV];
-  bool on[kU];
+  // kU of this lane's tokens: the loads of the next are under way while these
+  // are worked on.  The rows of tokens that do not count are read and replaced.
+  float ln[kU][NV];
+  bool onn[kU];
   auto load = [&](int tb, int b) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int t = tb + u * step;
-      on[u] = t < b && (!tk.mask || tk.mask[t]);
+      onn[u] = t < b && (!tk.mask || __ldg(tk.mask + t));
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
         const int c0 = q * VEC * LPT + el * VEC;
         if constexpr (VEC == 4) {
-          float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-          if (on[u] && c0 < E) v = __ldg(reinterpret_cast<const float4*>(logits + (size_t)t * E + c0));
-          l[u][4 * q] = v.x; l[u][4 * q + 1] = v.y; l[u][4 * q + 2] = v.z; l[u][4 * q + 3] = v.w;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (t < b && c0 < E) v = __ldg(reinterpret_cast<const float4*>(logits + (size_t)t * E + c0));
+          ln[u][4 * q] = v.x; ln[u][4 * q + 1] = v.y; ln[u][4 * q + 2] = v.z; ln[u][4 * q + 3] = v.w;
         } else {
-          l[u][q] = on[u] && c0 < E ? __ldg(logits + (size_t)t * E + c0) : -INFINITY;
+          ln[u][q] = t < b && c0 < E ? __ldg(logits + (size_t)t * E + c0) : 0.f;
         }
       }
     }
@@ -283,54 +319,92 @@ __global__ void __launch_bounds__(kThreads, NQ * VEC <= 8 ? 2 : 1) balance_main_
     float z = 0.f;
     int tb = a + warp * TPW + sub;
     load(tb, b);  // under way while the counts are added up
-    if (!ready) {
-      if constexpr (kCounted) pdl_wait();
-      if (threadIdx.x == 0) s_n = s_seqs = 0;
+    if constexpr (kCounted)
+      if (!ready) pdl_wait();
+    // this sequence's counts and, with the first piece, the call's tokens and sequences
+    if (threadIdx.x == 0) s_tok = 0;
+    if (!ready && threadIdx.x == 0) s_n = s_seqs = 0;
+    if constexpr (kSum && !kInline) {
+      const int c0 = off[s] / tk.count_chunk, c1 = (off[s + 1] - 1) / tk.count_chunk + 1;
+      int iv[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) iv[i] = 0;
+      constexpr int kR = NV <= 4 ? 4 : 1;  // rows in flight
+      for (int r0 = c0 + warp * TPW + sub; r0 < c1; r0 += kR * step) {
+#pragma unroll
+        for (int u = 0; u < kR; ++u) {
+          const int c = r0 + u * step;
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            const int e0 = q * VEC * LPT + el * VEC;
+            const int32_t* src = w.cnt_part + (size_t)(c + s) * E + e0;
+            if (c < c1 && e0 < E) {
+              if constexpr (VEC == 4) {
+                const int4 f = *reinterpret_cast<const int4*>(src);
+                iv[4 * q] += f.x; iv[4 * q + 1] += f.y; iv[4 * q + 2] += f.z; iv[4 * q + 3] += f.w;
+              } else {
+                iv[q] += *src;
+              }
+            }
+          }
+        }
+      }
+      int tok = 0, n = 0, seqs = 0;
+      for (int c = c0 + threadIdx.x; c < c1; c += kThreads) tok += w.tok_part[c + s];
+      if (!ready) {
+        for (int c = threadIdx.x; c < tk.count_chunks; c += kThreads) n += w.tok_chunk[c];
+        for (int q = threadIdx.x; q < tk.num_seq; q += kThreads) seqs += off[q + 1] > off[q];
+      }
+      __syncwarp();
+#pragma unroll
+      for (int d = LPT; d < 32; d <<= 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) iv[i] += __shfl_xor_sync(0xffffffffu, iv[i], d);
+      }
+      int* rows = reinterpret_cast<int*>(red);
+      if (sub == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (col(i) < E) rows[warp * E + col(i)] = iv[i];
+      }
+      tok = __reduce_add_sync(0xffffffffu, tok);
+      n = __reduce_add_sync(0xffffffffu, n);
+      seqs = __reduce_add_sync(0xffffffffu, seqs);
       __syncthreads();
-      int n = 0, seqs = 0;
+      if (lane == 0 && tok) atomicAdd(&s_tok, tok);
+      if (lane == 0 && n) atomicAdd(&s_n, n);
+      if (lane == 0 && seqs) atomicAdd(&s_seqs, seqs);
+      for (int e = threadIdx.x; e < E; e += kThreads) {
+        int v = 0;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) v += rows[i * E + e];
+        cnt[e] = v;
+      }
+      __syncthreads();
+    } else if (!ready) {
+      __syncthreads();
+      int n = 0;
       if constexpr (kInline) {
         if (tk.mask) {
-          for (int t = off[0] + threadIdx.x; t < off[tk.num_seq]; t += kThreads) n += tk.mask[t] != 0;
+          for (int t = off[0] + threadIdx.x; t < off[tk.num_seq]; t += kThreads) n += __ldg(tk.mask + t) != 0;
         } else if (threadIdx.x == 0) {
           n = off[tk.num_seq] - off[0];
         }
-      } else if constexpr (kSum) {
-        for (int c = threadIdx.x; c < tk.count_chunks; c += kThreads) n += w.tok_chunk[c];
-        for (int q = threadIdx.x; q < tk.num_seq; q += kThreads) seqs += off[q + 1] > off[q];
       } else {
         for (int q = threadIdx.x; q < tk.num_seq; q += kThreads) n += o.tokens[q];
       }
-      if (n) atomicAdd(&s_n, n);
-      if (seqs) atomicAdd(&s_seqs, seqs);
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (lane == 0 && n) atomicAdd(&s_n, n);
       __syncthreads();
+    }
+    if constexpr (kInline) count_slots(tk, topk_idx, a, b, cnt, &s_tok, status);
+    if (!ready) {
       rn = 1.f / (float)max(s_n, 1);
       if constexpr (kGrad) {
         ga = gr.a * (gr.dloss ? gr.dloss[0] : 1.f) * ((float)E / (float)tk.k) * rn;
         gb = gr.b * (gr.dloss ? gr.dloss[1] : 1.f) * 2.f * rn;
       }
       ready = true;
-    }
-    // the sequence's counts
-    if constexpr (kInline) {
-      count_slots(tk, topk_idx, a, b, cnt, &s_tok, status);
-    } else if constexpr (kSum) {
-      for (int e = threadIdx.x; e < E; e += kThreads) cnt[e] = 0;
-      if (threadIdx.x == 0) s_tok = 0;
-      __syncthreads();
-      const int c0 = off[s] / tk.count_chunk, c1 = (off[s + 1] - 1) / tk.count_chunk + 1;
-      // the rows side by side as far as the threads reach
-      const int groups = max(1, kThreads / E);
-      const int g = threadIdx.x / E, e0 = groups > 1 ? threadIdx.x % E : threadIdx.x;
-      if (g < groups || groups == 1) {
-        for (int e = e0; e < E; e += groups > 1 ? E : kThreads) {
-          int v = 0;
-#pragma unroll 8
-          for (int c = c0 + (groups > 1 ? g : 0); c < c1; c += groups) v += w.cnt_part[(size_t)(c + s) * E + e];
-          if (v) atomicAdd(&cnt[e], v);
-        }
-      }
-      for (int c = c0 + threadIdx.x; c < c1; c += kThreads) atomicAdd(&s_tok, w.tok_part[c + s]);
-      __syncthreads();
     }
     float ga_s = 0.f;
     if constexpr (kGrad) {
@@ -344,115 +418,142 @@ __global__ void __launch_bounds__(kThreads, NQ * VEC <= 8 ? 2 : 1) balance_main_
       for (int i = 0; i < NV; ++i) acc[i] = 0.f;
     }
     while (tb < b) {
+      float l[kU][NV], m[kU], sum[kU], dot[kU];
+      bool on[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        on[u] = onn[u];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) l[u][i] = col(i) < E ? (on[u] ? ln[u][i] : 0.f) : -INFINITY;
+      }
+      const int tn = tb + kU * step;
+      if (tn < b) load(tn, b);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        m[u] = l[u][0];
+#pragma unroll
+        for (int i = 1; i < NV; ++i) m[u] = fmaxf(m[u], l[u][i]);
+      }
+      gmax(m);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        sum[u] = dot[u] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          // lanes past the last expert hold -inf; a real logit may be +inf or NaN, whose NaN has to show
+          l[u][i] = col(i) < E ? exp_of(l[u][i] - m[u]) : 0.f;
+          sum[u] += l[u][i];
+          if constexpr (kGrad) dot[u] = fmaf(cf[i], l[u][i], dot[u]);
+        }
+      }
+      gsum(sum);
+      if constexpr (kGrad) gsum(dot);
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int t = tb + u * step;
-        if (t >= b) break;
-        float dl[NV];
-        if (on[u]) {
-          float m = l[u][0];
+        const float r = on[u] ? 1.f / sum[u] : 0.f;
+        const float lse = m[u] + logf(sum[u]);
+        if constexpr (kSum) {
 #pragma unroll
-          for (int i = 1; i < NV; ++i) m = fmaxf(m, l[u][i]);
-          m = gmax(m);
-          float sum = 0.f, dot = 0.f;
-#pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            // lanes past the last expert hold -inf; a real logit may be +inf or NaN, whose NaN has to show
-            l[u][i] = col(i) < E ? expf(l[u][i] - m) : 0.f;
-            sum += l[u][i];
-            if constexpr (kGrad) dot = fmaf(cf[i], l[u][i], dot);
-          }
-          sum = gsum(sum);
-          const float r = 1.f / sum;
-          const float lse = m + logf(sum);
-          if constexpr (kSum) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) acc[i] = fmaf(l[u][i], r, acc[i]);
-            if (el == 0) z = fmaf(lse, lse, z);
-          }
-          if constexpr (kGrad) {
-            dot = gsum(dot) * r;
-            const float c = gb * lse - ga_s * dot;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) dl[i] = l[u][i] * r * fmaf(ga_s, cf[i], c);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < NV; ++i) dl[i] = 0.f;
+          for (int i = 0; i < NV; ++i) acc[i] = fmaf(l[u][i], r, acc[i]);
+          if (el == 0 && on[u]) z = fmaf(lse, lse, z);
         }
         if constexpr (kGrad) {
+          const float c = gb * lse - ga_s * dot[u] * r;
+          if (t < b) {
 #pragma unroll
-          for (int q = 0; q < NQ; ++q) {
-            const int c0 = q * VEC * LPT + el * VEC;
-            if (c0 < E) {
-              float* d = gr.dlogits + (size_t)t * E + c0;
-              if constexpr (VEC == 4)
-                *reinterpret_cast<float4*>(d) = make_float4(dl[4 * q], dl[4 * q + 1], dl[4 * q + 2], dl[4 * q + 3]);
-              else
-                *d = dl[q];
+            for (int q = 0; q < NQ; ++q) {
+              const int c0 = q * VEC * LPT + el * VEC;
+              if (c0 < E) {
+                float* d = gr.dlogits + (size_t)t * E + c0;
+                float dl[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) dl[i] = l[u][VEC * q + i] * r * fmaf(ga_s, cf[VEC * q + i], c);
+                if constexpr (VEC == 4)
+                  *reinterpret_cast<float4*>(d) = make_float4(dl[0], dl[1], dl[2], dl[3]);
+                else
+                  *d = dl[0];
+              }
             }
           }
         }
       }
-      tb += kU * step;
-      if (tb < b) load(tb, b);
+      tb = tn;
     }
     if constexpr (kSum) {
-      __syncwarp();
+      // acc and z over the warp's token groups and the warps: red[0..E)
+      auto gather = [&]() {
+        __syncwarp();
 #pragma unroll
-      for (int d = LPT; d < 32; d <<= 1) {
+        for (int d = LPT; d < 32; d <<= 1) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], d);
-      }
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-      if (sub == 0) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (col(i) < E) red[warp * (E + 1) + col(i)] = acc[i];
-      }
-      if (lane == 0) red[warp * (E + 1) + E] = z;
-      __syncthreads();
-      // rows of `red` added into row 0: the CTA's sums (kInline: the sequence's)
-      for (int e = threadIdx.x; e <= E; e += kThreads) {
-        float v = 0.f;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) v += red[i * (E + 1) + e];
-        if constexpr (kInline) {
-          red[e] = v;
-        } else if (e < E) {
-          w.part[(size_t)(chunk + s) * E + e] = v;
-        } else {
-          w.zpart[chunk + s] = v;
+          for (int i = 0; i < NV; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], d);
         }
-      }
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+        __syncthreads();  // red is free
+        if (sub == 0) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+            if (col(i) < E) red[warp * (E + 1) + col(i)] = acc[i];
+        }
+        if (lane == 0) red[warp * (E + 1) + E] = z;
+        __syncthreads();
+        for (int e = threadIdx.x; e <= E; e += kThreads) {
+          float v = 0.f;
+#pragma unroll
+          for (int i = 0; i < kWarps; ++i) v += red[i * (E + 1) + e];
+          red[e] = v;
+        }
+      };
+      gather();
       bool finish = true;
       if constexpr (!kInline) {
+        for (int e = threadIdx.x; e <= E; e += kThreads) {  // each thread its own sums
+          if (e < E)
+            w.part[(size_t)(chunk + s) * E + e] = red[e];
+          else
+            w.zpart[chunk + s] = red[e];
+        }
         const int c0 = off[s] / tk.chunk, c1 = (off[s + 1] - 1) / tk.chunk + 1;
         __threadfence();
         __syncthreads();
         if (threadIdx.x == 0) s_last = atomicAdd(w.ticket + s, 1u) == (unsigned)(c1 - c0 - 1);
         __syncthreads();
         finish = s_last;
-        if (finish) {  // this CTA delivered the sequence's last partial: add them all
+        if (finish && c1 - c0 > 1) {
+          // this CTA delivered the sequence's last partial: all of them, in chunk
+          // order, rows taken like tokens
           __threadfence();
-          for (int v0 = 0; v0 <= E; v0 += 32) {
-            const int e = v0 + lane;
-            float v = 0.f;
-            if (e <= E) {
-#pragma unroll 8
-              for (int c = c0 + warp; c < c1; c += kWarps)
-                v += e < E ? __ldcg(w.part + (size_t)(c + s) * E + e) : __ldcg(w.zpart + c + s);
-              red[warp * (E + 1) + e] = v;
-            }
-          }
-          __syncthreads();
-          for (int e = threadIdx.x; e <= E; e += kThreads) {
-            float v = 0.f;
+          z = 0.f;
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) v += red[i * (E + 1) + e];
-            red[e] = v;
+          for (int i = 0; i < NV; ++i) acc[i] = 0.f;
+          for (int c = c0 + threadIdx.x; c < c1; c += kThreads) z += __ldcg(w.zpart + c + s);
+          constexpr int kR = NV <= 4 ? 8 : (NV <= 8 ? 4 : 1);
+          for (int r0 = c0 + warp * TPW + sub; r0 < c1; r0 += kR * step) {
+            float v[kR][NV];
+#pragma unroll
+            for (int u = 0; u < kR; ++u) {
+              const int c = r0 + u * step;
+#pragma unroll
+              for (int q = 0; q < NQ; ++q) {
+                const int e0 = q * VEC * LPT + el * VEC;
+                const float* src = w.part + (size_t)(c + s) * E + e0;
+                if constexpr (VEC == 4) {
+                  float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                  if (c < c1 && e0 < E) f = __ldcg(reinterpret_cast<const float4*>(src));
+                  v[u][4 * q] = f.x; v[u][4 * q + 1] = f.y; v[u][4 * q + 2] = f.z; v[u][4 * q + 3] = f.w;
+                } else {
+                  v[u][q] = c < c1 && e0 < E ? __ldcg(src) : 0.f;
+                }
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < kR; ++u)
+#pragma unroll
+              for (int i = 0; i < NV; ++i) acc[i] += v[u][i];
           }
+          gather();
         }
       }
       if (finish) {
@@ -479,6 +580,10 @@ __global__ void __launch_bounds__(kThreads, NQ * VEC <= 8 ? 2 : 1) balance_main_
             loss_z += sh.y;
             o.loss[0] = loss_b;
             o.loss[1] = loss_z;
+          } else if (tk.num_seq == 1) {
+            o.loss[0] = sh.x;
+            o.loss[1] = sh.y;
+            s_last = false;
           } else {
             __stcg(w.share + s, sh);
             __threadfence();
@@ -530,11 +635,12 @@ __global__ void __launch_bounds__(kThreads, NQ * VEC <= 8 ? 2 : 1) balance_main_
 
 size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 
-// Main chunks: two CTAs per SM, at least 16 tokens each; counting chunks fewer,
-// since every main CTA adds their rows up.
-constexpr int kMaxChunks = 304, kMaxCountChunks = 64;
+// Main chunks: two CTAs per SM, at least 64 tokens each (what a CTA of 128
+// experts holds in flight); counting chunks fewer, since every main CTA adds
+// their rows up.
+constexpr int kMaxChunks = 304, kMaxCountChunks = 128;
 // One CTA does the whole of a problem of up to so many logits (and few sequences).
-constexpr int kInlineLogits = 16384, kInlineSeqs = 4;
+constexpr int kInlineLogits = 8192, kInlineSeqs = 4;
 
 int chunk_tokens(int T, int most, int least) {
   const int c = (T + most - 1) / most;
@@ -549,9 +655,9 @@ struct Layout {
 };
 Layout layout(int T, int E, int num_seq) {
   Layout L;
-  L.chunk = chunk_tokens(T, kMaxChunks, 16);
+  L.chunk = chunk_tokens(T, kMaxChunks, 64);
   L.nchunk = (T + L.chunk - 1) / L.chunk;
-  L.count_chunk = chunk_tokens(T, kMaxCountChunks, 64);
+  L.count_chunk = chunk_tokens(T, kMaxCountChunks, 128);
   L.ncount = (T + L.count_chunk - 1) / L.count_chunk;
   const size_t rows = (size_t)L.nchunk + num_seq, crows = (size_t)L.ncount + num_seq;
   size_t at = 0;
