@@ -220,10 +220,13 @@ __device__ __forceinline__ float warp_max(float v) {
 // ------------------------------------------------------------- main kernel
 //
 // LPT lanes hold one token's logits (VEC consecutive values NQ times, VEC LPT
-// apart), a warp 32/LPT tokens side by side; kU of a lane's tokens are loaded
-// before the first is used.  The lane's share of P stays in registers over
-// the piece and is added over the warp's token groups and the warps at its
-// end.
+// apart; 16 values a lane where the experts allow it), a warp 32/LPT tokens
+// side by side: with a token over all 32 lanes the three reductions' shuffles
+// and the per-token instructions bound the kernel (230 issued a token at 128
+// experts).  The next token's loads are under way while one is worked on.  The
+// lane's share of P stays in registers over the piece and is added over the
+// warp's token groups and the warps at its end.  kFull: the lanes' columns are
+// the experts exactly.
 //
 // kInline: one CTA does everything, counting included.
 struct Grad {
@@ -232,13 +235,12 @@ struct Grad {
   float* dlogits;
 };
 
-template <int LPT, int VEC, int NQ, bool kSum, bool kGrad, bool kInline>
-__global__ void __launch_bounds__(kThreads, NQ * VEC <= 8 ? 2 : 1) balance_main_kernel(const Tokens tk, const float* __restrict__ logits,
+template <int LPT, int VEC, int NQ, bool kFull, bool kSum, bool kGrad, bool kInline>
+__global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens tk, const float* __restrict__ logits,
                                                                 const int32_t* __restrict__ topk_idx, const Work w,
                                                                 const Out o, const Grad gr, int* status) {
   constexpr int NV = NQ * VEC;       // values per lane
   constexpr int TPW = 32 / LPT;      // tokens per warp side by side
-  constexpr int kU = NV <= 8 ? 2 : 1;
   // After a counting kernel of the same call, which waited for everything before
   // it, the logits and the table may be read at once; only the counts are waited for.
   constexpr bool kCounted = kSum && !kInline;
@@ -269,46 +271,40 @@ __global__ void __launch_bounds__(kThreads, NQ * VEC <= 8 ? 2 : 1) balance_main_
   float loss_b = 0.f, loss_z = 0.f;     // kInline: thread 0's running totals
   bool ready = false;
   const unsigned gmask = LPT == 32 ? 0xffffffffu : (((1u << (LPT & 31)) - 1u) << (sub * LPT));
-  // over a token's lanes, kU tokens side by side
-  auto gmax = [&](float (&v)[kU]) {
+  // over a token's lanes
+  auto gmax = [&](float v) {
     if constexpr (LPT == 32) {
-#pragma unroll
-      for (int u = 0; u < kU; ++u) v[u] = warp_max(v[u]);
+      return warp_max(v);
     } else {
 #pragma unroll
-      for (int d = LPT / 2; d > 0; d >>= 1)
-#pragma unroll
-        for (int u = 0; u < kU; ++u) v[u] = fmaxf(v[u], __shfl_xor_sync(gmask, v[u], d));
+      for (int d = LPT / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(gmask, v, d));
+      return v;
     }
   };
-  auto gsum = [&](float (&v)[kU]) {
+  auto gsum = [&](float v) {
 #pragma unroll
-    for (int d = LPT / 2; d > 0; d >>= 1)
-#pragma unroll
-      for (int u = 0; u < kU; ++u) v[u] += __shfl_xor_sync(gmask, v[u], d);
+    for (int d = LPT / 2; d > 0; d >>= 1) v += __shfl_xor_sync(gmask, v, d);
+    return v;
   };
   auto col = [&](int i) { return (i / VEC) * VEC * LPT + el * VEC + i % VEC; };
+  auto has = [&](int i) { return kFull || col(i) < E; };
   const int step = kWarps * TPW;
 
-  // kU of this lane's tokens: the loads of the next are under way while these
-  // are worked on.  The rows of tokens that do not count are read and replaced.
-  float ln[kU][NV];
-  bool onn[kU];
-  auto load = [&](int tb, int b) {
+  // The lane's share of the next token; the rows of tokens that do not count are
+  // read and replaced.
+  float ln[NV];
+  bool onn = false;
+  auto load = [&](int t) {
+    onn = !tk.mask || __ldg(tk.mask + t);
+    const float* src = logits + (size_t)t * E + el * VEC;
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int t = tb + u * step;
-      onn[u] = t < b && (!tk.mask || __ldg(tk.mask + t));
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        const int c0 = q * VEC * LPT + el * VEC;
-        if constexpr (VEC == 4) {
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (t < b && c0 < E) v = __ldg(reinterpret_cast<const float4*>(logits + (size_t)t * E + c0));
-          ln[u][4 * q] = v.x; ln[u][4 * q + 1] = v.y; ln[u][4 * q + 2] = v.z; ln[u][4 * q + 3] = v.w;
-        } else {
-          ln[u][q] = t < b && c0 < E ? __ldg(logits + (size_t)t * E + c0) : 0.f;
-        }
+    for (int q = 0; q < NQ; ++q) {
+      if constexpr (VEC == 4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (has(4 * q)) v = __ldg(reinterpret_cast<const float4*>(src + q * VEC * LPT));
+        ln[4 * q] = v.x; ln[4 * q + 1] = v.y; ln[4 * q + 2] = v.z; ln[4 * q + 3] = v.w;
+      } else {
+        ln[q] = has(q) ? __ldg(src + q * LPT) : 0.f;
       }
     }
   };
@@ -317,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, NQ * VEC <= 8 ? 2 : 1) balance_main_
     float acc[kSum ? NV : 1];
     float cf[kGrad ? NV : 1];
     float z = 0.f;
-    int tb = a + warp * TPW + sub;
-    load(tb, b);  // under way while the counts are added up
+    int t = a + warp * TPW + sub;
+    if (t < b) load(t);  // under way while the counts are added up
     if constexpr (kCounted)
       if (!ready) pdl_wait();
     // this sequence's counts and, with the first piece, the call's tokens and sequences
@@ -365,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, NQ * VEC <= 8 ? 2 : 1) balance_main_
       if (sub == 0) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-          if (col(i) < E) rows[warp * E + col(i)] = iv[i];
+          if (has(i)) rows[warp * E + col(i)] = iv[i];
       }
       tok = __reduce_add_sync(0xffffffffu, tok);
       n = __reduce_add_sync(0xffffffffu, n);
@@ -411,74 +407,60 @@ __global__ void __launch_bounds__(kThreads, NQ * VEC <= 8 ? 2 : 1) balance_main_
       ga_s = ga / (float)max(kSum ? s_tok : o.tokens[s], 1);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        cf[i] = col(i) < E ? (float)(kSum ? cnt[col(i)] : o.counts[(size_t)s * E + col(i)]) : 0.f;
+        cf[i] = has(i) ? (float)(kSum ? cnt[col(i)] : o.counts[(size_t)s * E + col(i)]) : 0.f;
     }
     if constexpr (kSum) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) acc[i] = 0.f;
     }
-    while (tb < b) {
-      float l[kU][NV], m[kU], sum[kU], dot[kU];
-      bool on[kU];
+    while (t < b) {
+      float l[NV];
+      const bool on = onn;
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        on[u] = onn[u];
+      for (int i = 0; i < NV; ++i) l[i] = has(i) ? ln[i] : -INFINITY;
+      if (!on) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) l[u][i] = col(i) < E ? (on[u] ? ln[u][i] : 0.f) : -INFINITY;
+        for (int i = 0; i < NV; ++i) l[i] = 0.f;
       }
-      const int tn = tb + kU * step;
-      if (tn < b) load(tn, b);
+      const int here = t;
+      t += step;
+      if (t < b) load(t);
+      float m = l[0], sum = 0.f, dot = 0.f;
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        m[u] = l[u][0];
+      for (int i = 1; i < NV; ++i) m = fmaxf(m, l[i]);
+      m = gmax(m);
 #pragma unroll
-        for (int i = 1; i < NV; ++i) m[u] = fmaxf(m[u], l[u][i]);
+      for (int i = 0; i < NV; ++i) {
+        // a real logit may be +inf or NaN, whose NaN has to show
+        l[i] = has(i) ? exp_of(l[i] - m) : 0.f;
+        sum += l[i];
+        if constexpr (kGrad) dot = fmaf(cf[i], l[i], dot);
       }
-      gmax(m);
+      sum = gsum(sum);
+      if constexpr (kGrad) dot = gsum(dot);
+      const float r = on ? 1.f / sum : 0.f;
+      const float lse = m + logf(sum);
+      if constexpr (kSum) {
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        sum[u] = dot[u] = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          // lanes past the last expert hold -inf; a real logit may be +inf or NaN, whose NaN has to show
-          l[u][i] = col(i) < E ? exp_of(l[u][i] - m[u]) : 0.f;
-          sum[u] += l[u][i];
-          if constexpr (kGrad) dot[u] = fmaf(cf[i], l[u][i], dot[u]);
-        }
+        for (int i = 0; i < NV; ++i) acc[i] = fmaf(l[i], r, acc[i]);
+        if (el == 0 && on) z = fmaf(lse, lse, z);
       }
-      gsum(sum);
-      if constexpr (kGrad) gsum(dot);
+      if constexpr (kGrad) {
+        const float ar = ga_s * r, c = (gb * lse - ga_s * dot * r) * r;
+        float* d = gr.dlogits + (size_t)here * E + el * VEC;
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int t = tb + u * step;
-        const float r = on[u] ? 1.f / sum[u] : 0.f;
-        const float lse = m[u] + logf(sum[u]);
-        if constexpr (kSum) {
+        for (int q = 0; q < NQ; ++q) {
+          if (has(VEC * q)) {
+            float dl[VEC];
 #pragma unroll
-          for (int i = 0; i < NV; ++i) acc[i] = fmaf(l[u][i], r, acc[i]);
-          if (el == 0 && on[u]) z = fmaf(lse, lse, z);
-        }
-        if constexpr (kGrad) {
-          const float c = gb * lse - ga_s * dot[u] * r;
-          if (t < b) {
-#pragma unroll
-            for (int q = 0; q < NQ; ++q) {
-              const int c0 = q * VEC * LPT + el * VEC;
-              if (c0 < E) {
-                float* d = gr.dlogits + (size_t)t * E + c0;
-                float dl[VEC];
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) dl[i] = l[u][VEC * q + i] * r * fmaf(ga_s, cf[VEC * q + i], c);
-                if constexpr (VEC == 4)
-                  *reinterpret_cast<float4*>(d) = make_float4(dl[0], dl[1], dl[2], dl[3]);
-                else
-                  *d = dl[0];
-              }
-            }
+            for (int i = 0; i < VEC; ++i) dl[i] = l[VEC * q + i] * fmaf(ar, cf[VEC * q + i], c);
+            if constexpr (VEC == 4)
+              *reinterpret_cast<float4*>(d + q * VEC * LPT) = make_float4(dl[0], dl[1], dl[2], dl[3]);
+            else
+              d[q * LPT] = dl[0];
           }
         }
       }
-      tb = tn;
     }
     if constexpr (kSum) {
       // acc and z over the warp's token groups and the warps: red[0..E)
@@ -495,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, NQ * VEC <= 8 ? 2 : 1) balance_main_
         if (sub == 0) {
 #pragma unroll
           for (int i = 0; i < NV; ++i)
-            if (col(i) < E) red[warp * (E + 1) + col(i)] = acc[i];
+            if (has(i)) red[warp * (E + 1) + col(i)] = acc[i];
         }
         if (lane == 0) red[warp * (E + 1) + E] = z;
         __syncthreads();
@@ -635,10 +617,10 @@ __global__ void __launch_bounds__(kThreads, NQ * VEC <= 8 ? 2 : 1) balance_main_
 
 size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 
-// Main chunks: two CTAs per SM, at least 64 tokens each (what a CTA of 128
-// experts holds in flight); counting chunks fewer, since every main CTA adds
+// Main chunks: one CTA per SM, at least 64 tokens each (what a CTA of 128
+// experts works on at a time); counting chunks fewer, since every main CTA adds
 // their rows up.
-constexpr int kMaxChunks = 304, kMaxCountChunks = 128;
+constexpr int kMaxChunks = 152, kMaxCountChunks = 128;
 // One CTA does the whole of a problem of up to so many logits (and few sequences).
 constexpr int kInlineLogits = 8192, kInlineSeqs = 4;
 
@@ -679,11 +661,11 @@ Layout layout(int T, int E, int num_seq) {
 
 template <bool kSum, bool kGrad, bool kInline>
 struct Main {
-  template <int LPT, int VEC, int NQ>
+  template <int LPT, int VEC, int NQ, bool kFull>
   static int go(const char* fn, int grid, const Tokens& tk, const float* logits, const int32_t* idx, const Work& w, const Out& o,
                 const Grad& gr, cudaStream_t s) {
     const size_t smem = sizeof(int) * (((tk.num_seq + 4) & ~3) + ((tk.E + 3) & ~3)) + (kSum ? sizeof(float) * kWarps * (tk.E + 1) : 0);
-    auto kern = balance_main_kernel<LPT, VEC, NQ, kSum, kGrad, kInline>;
+    auto kern = balance_main_kernel<LPT, VEC, NQ, kFull, kSum, kGrad, kInline>;
     if (smem > 48 * 1024) {
       static bool set[64] = {};
       const int dev = current_device();
@@ -697,28 +679,29 @@ struct Main {
     launch_pdl(kern, grid, kThreads, smem, s, tk, logits, idx, w, o, gr, status_word());
     return check_launch(fn, "main kernel");
   }
+  // experts in fours; full: they fill the lanes' columns (a single CTA is latency-bound either way)
+  template <int LPT, int NQ, class... A>
+  static int fours(const char* fn, int grid, const Tokens& tk, A&&... a) {
+    if constexpr (!kInline)
+      if (tk.E == 4 * LPT * NQ) return go<LPT, 4, NQ, true>(fn, grid, tk, a...);
+    return go<LPT, 4, NQ, false>(fn, grid, tk, a...);
+  }
   template <class... A>
   static int pick(const char* fn, int grid, const Tokens& tk, A&&... a) {
     const int E = tk.E;
     if (E % 4 == 0) {
-      if (E <= 4) return go<1, 4, 1>(fn, grid, tk, a...);
-      if (E <= 8) return go<2, 4, 1>(fn, grid, tk, a...);
-      if (E <= 16) return go<4, 4, 1>(fn, grid, tk, a...);
-      if (E <= 32) return go<8, 4, 1>(fn, grid, tk, a...);
-      if (E <= 64) return go<16, 4, 1>(fn, grid, tk, a...);
-      if (E <= 128) return go<32, 4, 1>(fn, grid, tk, a...);
-      if (E <= 256) return go<32, 4, 2>(fn, grid, tk, a...);
-      if (E <= 512) return go<32, 4, 4>(fn, grid, tk, a...);
-      return go<32, 4, 8>(fn, grid, tk, a...);
+      if (E <= 16) return fours<1, 4>(fn, grid, tk, a...);
+      if (E <= 32) return fours<2, 4>(fn, grid, tk, a...);
+      if (E <= 64) return fours<4, 4>(fn, grid, tk, a...);
+      if (E <= 128) return fours<8, 4>(fn, grid, tk, a...);
+      if (E <= 256) return fours<16, 4>(fn, grid, tk, a...);
+      if (E <= 512) return fours<32, 4>(fn, grid, tk, a...);
+      return fours<32, 8>(fn, grid, tk, a...);
     }
-    if (E <= 4) return go<4, 1, 1>(fn, grid, tk, a...);
-    if (E <= 16) return go<16, 1, 1>(fn, grid, tk, a...);
-    if (E <= 32) return go<32, 1, 1>(fn, grid, tk, a...);
-    if (E <= 64) return go<32, 1, 2>(fn, grid, tk, a...);
-    if (E <= 128) return go<32, 1, 4>(fn, grid, tk, a...);
-    if (E <= 256) return go<32, 1, 8>(fn, grid, tk, a...);
-    if (E <= 512) return go<32, 1, 16>(fn, grid, tk, a...);
-    return go<32, 1, 32>(fn, grid, tk, a...);
+    if (E <= 16) return go<4, 1, 4, false>(fn, grid, tk, a...);
+    if (E <= 64) return go<16, 1, 4, false>(fn, grid, tk, a...);
+    if (E <= 256) return go<32, 1, 8, false>(fn, grid, tk, a...);
+    return go<32, 1, 32, false>(fn, grid, tk, a...);
   }
 };
 
