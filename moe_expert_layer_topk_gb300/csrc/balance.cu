@@ -125,39 +125,44 @@ __device__ __forceinline__ void for_each_piece(const int* off, int num_seq, int 
 
 // ------------------------------------------------------------------ counts
 // hist[e], *live: the slots and tokens of [a, b) that count (all threads).
+// Four slots' loads are under way before the first is counted; a token is
+// counted with its first slot.
 __device__ __forceinline__ void count_slots(const Tokens& tk, const int32_t* __restrict__ topk_idx, int a, int b, int* hist,
                                             int* live, int* status) {
+  constexpr int kSlots = 4;
   for (int e = threadIdx.x; e < tk.E; e += kThreads) hist[e] = 0;
   if (threadIdx.x == 0) *live = 0;
   __syncthreads();
   int mine = 0;
-  if (tk.mask) {
-    for (int t = a + threadIdx.x; t < b; t += kThreads) mine += __ldg(tk.mask + t) != 0;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) mine += __shfl_xor_sync(0xffffffffu, mine, d);
-    if ((threadIdx.x & 31) == 0 && mine) atomicAdd(live, mine);
-  } else if (threadIdx.x == 0) {
-    *live = b - a;
-  }
-  // four slots' loads under way before the first is counted
   const unsigned q1 = (unsigned)b * tk.k;  // T k < 2^31
-  for (unsigned q0 = (unsigned)a * tk.k + threadIdx.x; q0 < q1; q0 += 4 * kThreads) {
-    int e[4];
-    bool on[4];
+  for (unsigned q0 = (unsigned)a * tk.k + threadIdx.x; q0 < q1; q0 += kSlots * kThreads) {
+    int e[kSlots];
+    bool on[kSlots];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kSlots; ++u) {
       const unsigned q = q0 + u * kThreads;
       e[u] = q < q1 ? __ldg(topk_idx + q) : 0;
-      on[u] = q < q1 && (!tk.mask || __ldg(tk.mask + q / (unsigned)tk.k));
+      on[u] = q < q1;
+      if (tk.mask && on[u]) {
+        const unsigned t = q / (unsigned)tk.k;
+        on[u] = __ldg(tk.mask + t) != 0;
+        mine += on[u] && q == t * (unsigned)tk.k;
+      }
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kSlots; ++u) {
       if (!on[u]) continue;
       if (e[u] >= 0 && e[u] < tk.E)
         atomicAdd(&hist[e[u]], 1);
       else
         set_status(status, MOE_STATUS_BAD_INDEX);
     }
+  }
+  if (tk.mask) {
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if ((threadIdx.x & 31) == 0 && mine) atomicAdd(live, mine);
+  } else if (threadIdx.x == 0) {
+    *live = b - a;
   }
   __syncthreads();
 }
@@ -270,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
   float ga = 0.f, gb = 0.f, rn = 0.f;   // set with the first piece
   float loss_b = 0.f, loss_z = 0.f;     // kInline: thread 0's running totals
   bool ready = false;
+  unsigned finished = 0;                // thread 0: sequences this CTA finished
   const unsigned gmask = LPT == 32 ? 0xffffffffu : (((1u << (LPT & 31)) - 1u) << (sub * LPT));
   // over a token's lanes
   auto gmax = [&](float v) {
@@ -322,10 +328,14 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
     if (!ready && threadIdx.x == 0) s_n = s_seqs = 0;
     if constexpr (kSum && !kInline) {
       const int c0 = off[s] / tk.count_chunk, c1 = (off[s + 1] - 1) / tk.count_chunk + 1;
+      int tok = 0, n = 0, seqs = 0;
+      for (int c = c0 + threadIdx.x; c < c1; c += kThreads) tok += __ldcg(w.tok_part + c + s);
+      if (!ready)
+        for (int c = threadIdx.x; c < tk.count_chunks; c += kThreads) n += __ldcg(w.tok_chunk + c);
       int iv[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) iv[i] = 0;
-      constexpr int kR = NV <= 4 ? 4 : 1;  // rows in flight
+      constexpr int kR = NV <= 16 ? 2 : 1;  // rows in flight
       for (int r0 = c0 + warp * TPW + sub; r0 < c1; r0 += kR * step) {
 #pragma unroll
         for (int u = 0; u < kR; ++u) {
@@ -336,21 +346,17 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
             const int32_t* src = w.cnt_part + (size_t)(c + s) * E + e0;
             if (c < c1 && e0 < E) {
               if constexpr (VEC == 4) {
-                const int4 f = *reinterpret_cast<const int4*>(src);
+                const int4 f = __ldcg(reinterpret_cast<const int4*>(src));
                 iv[4 * q] += f.x; iv[4 * q + 1] += f.y; iv[4 * q + 2] += f.z; iv[4 * q + 3] += f.w;
               } else {
-                iv[q] += *src;
+                iv[q] += __ldcg(src);
               }
             }
           }
         }
       }
-      int tok = 0, n = 0, seqs = 0;
-      for (int c = c0 + threadIdx.x; c < c1; c += kThreads) tok += w.tok_part[c + s];
-      if (!ready) {
-        for (int c = threadIdx.x; c < tk.count_chunks; c += kThreads) n += w.tok_chunk[c];
+      if (!ready)
         for (int q = threadIdx.x; q < tk.num_seq; q += kThreads) seqs += off[q + 1] > off[q];
-      }
       __syncwarp();
 #pragma unroll
       for (int d = LPT; d < 32; d <<= 1) {
@@ -490,20 +496,20 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
       };
       gather();
       bool finish = true;
-      if constexpr (!kInline) {
+      const int c0 = off[s] / tk.chunk, c1 = (off[s + 1] - 1) / tk.chunk + 1;
+      if (!kInline && c1 - c0 > 1) {  // a sequence wholly in this chunk needs no others' partials
         for (int e = threadIdx.x; e <= E; e += kThreads) {  // each thread its own sums
           if (e < E)
             w.part[(size_t)(chunk + s) * E + e] = red[e];
           else
             w.zpart[chunk + s] = red[e];
         }
-        const int c0 = off[s] / tk.chunk, c1 = (off[s + 1] - 1) / tk.chunk + 1;
         __threadfence();
         __syncthreads();
         if (threadIdx.x == 0) s_last = atomicAdd(w.ticket + s, 1u) == (unsigned)(c1 - c0 - 1);
         __syncthreads();
         finish = s_last;
-        if (finish && c1 - c0 > 1) {
+        if (finish) {
           // this CTA delivered the sequence's last partial: all of them, in chunk
           // order, rows taken like tokens
           __threadfence();
@@ -511,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
 #pragma unroll
           for (int i = 0; i < NV; ++i) acc[i] = 0.f;
           for (int c = c0 + threadIdx.x; c < c1; c += kThreads) z += __ldcg(w.zpart + c + s);
-          constexpr int kR = NV <= 4 ? 8 : (NV <= 8 ? 4 : 1);
+          constexpr int kR = NV <= 16 ? 2 : 1;
           for (int r0 = c0 + warp * TPW + sub; r0 < c1; r0 += kR * step) {
             float v[kR][NV];
 #pragma unroll
@@ -565,52 +571,56 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
           } else if (tk.num_seq == 1) {
             o.loss[0] = sh.x;
             o.loss[1] = sh.y;
-            s_last = false;
           } else {
             __stcg(w.share + s, sh);
-            __threadfence();
-            s_last = atomicAdd(w.ticket + tk.num_seq, 1u) == (unsigned)(s_seqs - 1);
-          }
-        }
-        if constexpr (!kInline) {
-          __syncthreads();
-          if (s_last) {  // and the last sequence: the shares in order
-            __threadfence();
-            float lb = 0.f, lz = 0.f;
-            for (int i = threadIdx.x; i < tk.num_seq; i += kThreads) {
-              const float2 h = __ldcg(w.share + i);
-              lb += h.x;
-              lz += h.y;
-            }
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-              lb += __shfl_xor_sync(0xffffffffu, lb, d);
-              lz += __shfl_xor_sync(0xffffffffu, lz, d);
-            }
-            __syncthreads();
-            if (lane == 0) {
-              red[2 * warp] = lb;
-              red[2 * warp + 1] = lz;
-            }
-            __syncthreads();
-            if (threadIdx.x == 0) {
-              lb = lz = 0.f;
-              for (int i = 0; i < kWarps; ++i) {
-                lb += red[2 * i];
-                lz += red[2 * i + 1];
-              }
-              o.loss[0] = lb;
-              o.loss[1] = lz;
-            }
+            ++finished;
           }
         }
       }
       __syncthreads();
     }
   });
-  // a CTA without a piece still may not end before the counting kernel does
-  if constexpr (kCounted)
+  if constexpr (kCounted) {
+    // a CTA without a piece still may not end before the counting kernel does
     if (!ready) pdl_wait();
+    if (tk.num_seq > 1) {  // the CTA that finishes the last sequence adds the shares up in order
+      if (threadIdx.x == 0) {
+        s_last = false;
+        if (finished > 0) {
+          __threadfence();
+          s_last = atomicAdd(w.ticket + tk.num_seq, finished) + finished == (unsigned)s_seqs;
+        }
+      }
+      __syncthreads();
+      if (!s_last) return;
+      __threadfence();
+      float lb = 0.f, lz = 0.f;
+      for (int i = threadIdx.x; i < tk.num_seq; i += kThreads) {
+        const float2 h = __ldcg(w.share + i);
+        lb += h.x;
+        lz += h.y;
+      }
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        lb += __shfl_xor_sync(0xffffffffu, lb, d);
+        lz += __shfl_xor_sync(0xffffffffu, lz, d);
+      }
+      if (lane == 0) {
+        red[2 * warp] = lb;
+        red[2 * warp + 1] = lz;
+      }
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        lb = lz = 0.f;
+        for (int i = 0; i < kWarps; ++i) {
+          lb += red[2 * i];
+          lz += red[2 * i + 1];
+        }
+        o.loss[0] = lb;
+        o.loss[1] = lz;
+      }
+    }
+  }
 }
 
 // --------------------------------------------------------------- host side
@@ -620,7 +630,7 @@ size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 // Main chunks: one CTA per SM, at least 64 tokens each (what a CTA of 128
 // experts works on at a time); counting chunks fewer, since every main CTA adds
 // their rows up.
-constexpr int kMaxChunks = 152, kMaxCountChunks = 128;
+constexpr int kMaxChunks = 152, kMaxCountChunks = 304;
 // One CTA does the whole of a problem of up to so many logits (and few sequences).
 constexpr int kInlineLogits = 8192, kInlineSeqs = 4;
 
@@ -639,7 +649,7 @@ Layout layout(int T, int E, int num_seq) {
   Layout L;
   L.chunk = chunk_tokens(T, kMaxChunks, 64);
   L.nchunk = (T + L.chunk - 1) / L.chunk;
-  L.count_chunk = chunk_tokens(T, kMaxCountChunks, 128);
+  L.count_chunk = chunk_tokens(T, kMaxCountChunks, 64);
   L.ncount = (T + L.count_chunk - 1) / L.count_chunk;
   const size_t rows = (size_t)L.nchunk + num_seq, crows = (size_t)L.ncount + num_seq;
   size_t at = 0;
