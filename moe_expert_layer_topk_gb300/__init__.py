@@ -448,9 +448,9 @@ def sm_count(device=None) -> int:
         .multi_processor_count
 
 
-from .layer import MoELayer  # noqa: E402  (buffers + call sequence over the entry points)
+from .layer import AdapterLinear, MoELayer  # noqa: E402  (buffers + call sequence over the entry points)
 
-__all__.append("MoELayer")
+__all__ += ["MoELayer", "AdapterLinear"]
 
 
 def moe_probe_fma(packed, per_sm, iters, out, stream=None) -> int:
