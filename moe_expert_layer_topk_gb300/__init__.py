@@ -401,11 +401,13 @@ def moe_combine_dropout_bwd(dy, y_perm, topk_w, row_of_slot, T, H, k, p, rng, dy
 
 def _rows(t):
     """Pointer and row stride of a 2-D tensor whose rows may lie apart."""
+    st = t.stride()
+    if len(st) != 2 or st[1] != 1:
+        raise ValueError("row tensors must be 2-D with contiguous rows")
     if not t.is_cuda:
         raise ValueError("tensor arguments must live on the GPU")
-    if t.dim() != 2 or t.stride(1) != 1:
-        raise ValueError("row tensors must be 2-D with contiguous rows")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    n, cols = t.shape
+    return t.data_ptr(), st[0] if n > 1 else cols
 
 
 def moe_adapter_hidden_size(T, r) -> int:

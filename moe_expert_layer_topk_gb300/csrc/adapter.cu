@@ -1332,9 +1332,16 @@ int run_shrink(const char* fn, const Reqs& q, const void* in, long long ld, cons
   p.rN = round_up(r, 16);
   p.f_bytes = kMN ? (r + 63) / 64 * CHUNK_BYTES : r * 128;
   p.f_rows = kMN ? red : r;
-  // tiles of many runs want many blocks of F in flight: more of them where a CTA has its SM alone
-  const int sms = sm_count() > 0 ? sm_count() : 148;
-  const int f_room = tiles * cs <= sms ? 65536 : 8192, f_stage = kShrinkK * p.f_bytes;
+  // Tiles of many runs want many blocks of F in flight: as many as fit where a CTA has its SM alone.
+  // Otherwise two CTAs share one, with two steps of x in flight each (three: one CTA an SM; 18 us instead
+  // of 13 for 8192 x 2048).
+  const int sms = sm_count() > 0 ? sm_count() : 148, f_stage = kShrinkK * p.f_bytes;
+  const bool alone = tiles * cs <= sms;
+  const int steps = ((nkb + cs - 1) / cs + kShrinkK - 1) / kShrinkK;
+  p.x_stages = r <= 64 && alone ? kShrinkX : 2;
+  if (steps < p.x_stages) p.x_stages = steps;
+  const int fixed = 1024 + p.x_stages * kShrinkXBytes + p.rN * BM * 4 + (int)table_bytes(q.num_seg);
+  const int f_room = alone ? (int)kAdapterSmem - fixed : 8192;
   p.f_stages = f_room / f_stage < 2 ? 2 : (f_room / f_stage > kShrinkF ? kShrinkF : f_room / f_stage);
   p.scale = scale;
   p.hidden = static_cast<__nv_bfloat16*>(hidden);
@@ -1342,9 +1349,7 @@ int run_shrink(const char* fn, const Reqs& q, const void* in, long long ld, cons
   p.tmem_cols = p.rN <= 32 ? 32 : (p.rN <= 64 ? 64 : 128);
   p.status = status_word();
   // (an F block of r rows is read as rN: the last one reads into the sums, whose columns past r are not used)
-  // two such CTAs fit an SM with two steps of x in flight each (three: one CTA; 18 us instead of 13 for 8192 x 2048)
-  p.x_stages = r <= 64 && tiles * cs <= sms ? kShrinkX : 2;
-  const size_t smem = 1024 + p.x_stages * kShrinkXBytes + (size_t)p.f_stages * f_stage + (size_t)p.rN * BM * 4 + table_bytes(q.num_seg);
+  const size_t smem = (size_t)fixed + (size_t)p.f_stages * f_stage;
   return launch_adapter(fn, kern, dim3(cs, tiles), 192, smem, cs, s, tx, tf, p);
 }
 
@@ -1420,18 +1425,19 @@ int run_wide(const char* fn, const Reqs& q, const void* in, long long ld, const 
   while (nrank < 8 && nrank * 2 <= red / BK && tiles * nrank * 2 <= sms) nrank *= 2;
   if (nrank > 1)
     return run_wide_bn<64, kMN, true>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, nrank, s);
-  // else the tile whose waves cost least: a block's time goes with the columns it multiplies plus the
-  // 128 rows it loads; a pair's last wave may be one of halves
-  const int w64 = (tiles + sms - 1) / sms * (64 + 64);
-  int best = w64, bn = 64;
+  // else the tile whose waves cost least: a block's time goes with the columns it multiplies plus half of
+  // the 128 rows it loads; a pair's last wave may be one of halves, which cost what a 128-column tile does
+  // (517 rows, 768 x 2048: 23.9 us on 128 columns, 26.6 on halves of 256, 23.5 on 64 with four times the
+  // loads; 8192 rows, 2048 x 2048: 40 us on 256 and a wave of halves)
+  int best = (tiles + sms - 1) / sms * (64 + 64), bn = 64;
   if (out_cols % 128 == 0) {
     const int w128 = (tiles / 2 + sms - 1) / sms * (128 + 64);
     if (w128 <= best) best = w128, bn = 128;
   }
   if (out_cols % 256 == 0) {
     const int places = sms / 2, t256 = (q.T + 2 * BM - 1) / (2 * BM) * (out_cols / 256), rest = t256 % places;
-    const int halves = t256 / places * 2 + (rest == 0 ? 0 : (2 * rest <= places ? 1 : 2));
-    if (halves * (256 + 64) / 2 <= best) bn = 256;
+    const int w256 = t256 / places * (256 + 64) + (rest == 0 ? 0 : (2 * rest <= places ? 128 + 64 : 256 + 64));
+    if (w256 < best) bn = 256;
   }
   if (bn == 256)
     return run_wide_bn<256, kMN, false>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, 1, s);
