@@ -132,11 +132,11 @@ def _ptr(t):
         return None
     if isinstance(t, int):
         return t
+    if t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError("tensor arguments must live on the GPU")
-    if not t.is_contiguous():
-        raise ValueError("tensor arguments must be contiguous")
-    return t.data_ptr()
+    raise ValueError("tensor arguments must be contiguous")
 
 
 # the raw handle of the current stream without building a Stream object
@@ -154,7 +154,7 @@ def _stream(stream):
 
 
 def _call(name, *args):
-    rc = getattr(lib(), name)(*args)
+    rc = getattr(_lib or lib(), name)(*args)
     if rc != 0:
         raise MoEError(name, rc, lib().moe_last_error_string().decode(errors="replace"))
 
