@@ -55,28 +55,24 @@ __device__ __forceinline__ uint4 philox8(const PhiloxKey& k, unsigned long long 
   return make_uint4(c0, c1, c2, c3);
 }
 
-// Bit i: element 8b + i stays.
-__device__ __forceinline__ uint32_t keep_bits(const PhiloxKey& k, unsigned long long b, uint32_t drop) {
-  const uint4 w = philox8(k, b);
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    m |= (uint32_t)((v[i] & 0xFFFFu) >= drop) << (2 * i);
-    m |= (uint32_t)((v[i] >> 16) >= drop) << (2 * i + 1);
-  }
-  return m;
+// Whether element i (0..7) of a generator block stays.
+__device__ __forceinline__ bool stays(const uint4& w, int i, uint32_t drop) {
+  const uint32_t v = i < 2 ? w.x : (i < 4 ? w.y : (i < 6 ? w.z : w.w));
+  return ((i & 1) ? v >> 16 : v & 0xFFFFu) >= drop;
 }
 
 // ------------------------------------------------------------- elementwise
-// out = residual + D(x), fp32 arithmetic, one rounding.  Thread = eight
-// elements (one generator block); the last, partial block element by element.
+// out = residual + D(x), fp32 arithmetic, one rounding.
+// Eight elements as they lie in memory.
 template <typename T>
 struct Vec8;
 template <>
 struct Vec8<__nv_bfloat16> {
-  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&f)[8]) {
-    unpack8(*reinterpret_cast<const uint4*>(p), f);
+  uint4 q;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t w = i < 2 ? q.x : (i < 4 ? q.y : (i < 6 ? q.z : q.w));
+    return (i & 1) ? bf16hi(w) : bf16lo(w);
   }
   static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
     *reinterpret_cast<uint4*>(p) = pack8(f);
@@ -86,10 +82,14 @@ struct Vec8<__nv_bfloat16> {
 };
 template <>
 struct Vec8<float> {
-  static __device__ __forceinline__ void load(const float* p, float (&f)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ float at(int i) const {
+    const float4& v = i < 4 ? a : b;
+    return (i & 3) == 0 ? v.x : ((i & 3) == 1 ? v.y : ((i & 3) == 2 ? v.z : v.w));
   }
   static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
     reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
@@ -100,30 +100,38 @@ struct Vec8<float> {
 };
 
 // x may be out (every element is read before it is written by its thread).
+// One generator block of eight elements a thread (16.8 M bf16 elements with a
+// residual: 16.8 us; two a thread 18.3, four 19.4: the registers they take cost
+// more warps than their loads are worth).
 template <typename T>
 __global__ void __launch_bounds__(256) dropout_kernel(const T* x, const T* residual, long long n, DropParams dp,
                                                       const unsigned long long* __restrict__ rng, T* out) {
   pdl_wait();
   pdl_trigger();
   const PhiloxKey key = load_key(rng);
-  const long long nb = (n + 7) / 8;
+  const long long nb = (n + 7) / 8, whole = n / 8;
   for (long long b = blockIdx.x * (long long)blockDim.x + threadIdx.x; b < nb; b += (long long)gridDim.x * blockDim.x) {
-    if (8 * b + 8 <= n) {
-      float v[8], r[8];
-      Vec8<T>::load(x + 8 * b, v);
-      if (residual) Vec8<T>::load(residual + 8 * b, r);
-      const uint32_t keep = keep_bits(key, b, dp.drop);
+    if (b < whole) {
+      Vec8<T> v, r;
+      v.load(x + 8 * b);
+      if (residual) r.load(residual + 8 * b);
+      const uint4 w = philox8(key, b);
+      float o[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float d = (keep >> i) & 1u ? v[i] * dp.scale : 0.f;
-        v[i] = residual ? r[i] + d : d;
+        const float d = stays(w, i, dp.drop) ? v.at(i) * dp.scale : 0.f;
+        o[i] = residual ? r.at(i) + d : d;
       }
-      Vec8<T>::store(out + 8 * b, v);
-    } else {
-      const uint32_t keep = keep_bits(key, b, dp.drop);
-      for (long long i = 8 * b; i < n; ++i) {
-        const float d = (keep >> (int)(i - 8 * b)) & 1u ? Vec8<T>::one(x + i) * dp.scale : 0.f;
-        out[i] = Vec8<T>::round(residual ? Vec8<T>::one(residual + i) + d : d);
+      Vec8<T>::store(out + 8 * b, o);
+    } else {  // the last, partial block
+      const uint4 w = philox8(key, b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const long long j = 8 * b + i;
+        if (j < n) {
+          const float d = stays(w, i, dp.drop) ? Vec8<T>::one(x + j) * dp.scale : 0.f;
+          out[j] = Vec8<T>::round(residual ? Vec8<T>::one(residual + j) + d : d);
+        }
       }
     }
   }
@@ -174,28 +182,28 @@ __global__ void __launch_bounds__(256) combine_dropout_kernel(
         }
       }
     }
-    const uint32_t keep = keep_bits(key, gid, dp.drop);
+    const uint4 bits = philox8(key, gid);
     float res[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (residual) unpack8(*(reinterpret_cast<const uint4*>(residual) + gid), res);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = res[i] + ((keep >> i) & 1u ? acc[i] * dp.scale : 0.f);
+    for (int i = 0; i < 8; ++i) acc[i] = res[i] + (stays(bits, i, dp.drop) ? acc[i] * dp.scale : 0.f);
     reinterpret_cast<uint4*>(y)[gid] = pack8(acc);
   }
 }
 
 // bf16 element pairs of a vector with the dropped ones replaced by zero
-__device__ __forceinline__ uint4 select8(uint4 v, uint32_t keep) {
+__device__ __forceinline__ uint4 select8(uint4 v, const uint4& bits, uint32_t drop) {
   uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    w[i] &= ((keep >> (2 * i)) & 1u ? 0xFFFFu : 0u) | ((keep >> (2 * i + 1)) & 1u ? 0xFFFF0000u : 0u);
+    w[i] &= (stays(bits, 2 * i, drop) ? 0xFFFFu : 0u) | (stays(bits, 2 * i + 1, drop) ? 0xFFFF0000u : 0u);
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Warp per token: the token's dy row with its dropped elements zeroed sits in
 // registers; for every slot the warp writes dy_perm[row] = (w scale) dy[t] and
 // reduces dy[t] . y_perm[row]; the scale is applied to the sum once.
-__global__ void __launch_bounds__(256) combine_dropout_bwd_kernel(
+__global__ void __launch_bounds__(64) combine_dropout_bwd_kernel(
     const __nv_bfloat16* __restrict__ dy, const __nv_bfloat16* __restrict__ y_perm,
     const float* __restrict__ topk_w, const int32_t* __restrict__ row_of_slot, int T, int H, int k, int R,
     DropParams dp, const unsigned long long* __restrict__ rng, __nv_bfloat16* __restrict__ dy_perm,
@@ -224,7 +232,7 @@ __global__ void __launch_bounds__(256) combine_dropout_bwd_kernel(
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int v = v0 + u * 32 + lane;
-        if (v < nvec) gp[u] = select8(gp[u], keep_bits(key, (unsigned long long)t * nvec + v, dp.drop));
+        if (v < nvec) gp[u] = select8(gp[u], philox8(key, (unsigned long long)t * nvec + v), dp.drop);
       }
       for (int j = 0; j < k; ++j) {
         const int row = __shfl_sync(0xffffffffu, my_row, j);
@@ -346,7 +354,7 @@ int moe_combine_dropout_bwd(const void* dy, const void* y_perm, const float* top
     return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer argument", fn);
   if (!aligned16(dy) || !aligned16(y_perm) || !aligned16(dy_perm))
     return fail(MOE_ERR_ALIGNMENT, "%s: dy, y_perm and dy_perm must be 16-byte aligned", fn);
-  launch_pdl(combine_dropout_bwd_kernel, grid_for((size_t)T * 32, 256, 16), 256, 0, static_cast<cudaStream_t>(stream),
+  launch_pdl(combine_dropout_bwd_kernel, grid_for((size_t)T * 32, 64, 32), 64, 0, static_cast<cudaStream_t>(stream),
              static_cast<const __nv_bfloat16*>(dy), static_cast<const __nv_bfloat16*>(y_perm), topk_w, row_of_slot, T,
              H, k, T * k, dp, reinterpret_cast<const unsigned long long*>(rng),
              static_cast<__nv_bfloat16*>(dy_perm), d_w, status_word());
