@@ -304,6 +304,7 @@ struct ShrinkCtl {
   uint32_t tmem_base;
   int abort_flag;
   int row_ad[BM];
+  float row_scale[BM];
   uint32_t runs[2][BM];  // the loading warp's and the MMA warp's
 };
 
@@ -311,7 +312,6 @@ template <bool kMN>
 __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_constant__ CUtensorMap tmX,
                                                              const __grid_constant__ CUtensorMap tmF,
                                                              const ShrinkParams p) {
-  pdl_wait();
   extern __shared__ uint8_t smem_raw[];
   __shared__ ShrinkCtl ctl;
   const uint32_t base = align1k(smem_u32(smem_raw));
@@ -351,16 +351,24 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncwarp();
     if (elect_one()) {
-      for (int i = 0; i < p.x_stages && kb0 + i * kShrinkK < kb1; ++i) load_x(kb0 + i * kShrinkK, i);
+      prefetch_tmap(&tmX);
       prefetch_tmap(&tmF);
     }
-  } else if (warp == 1) {
-    tmem_alloc_n<1>(smem_u32(&ctl.tmem_base), p.tmem_cols);
+    pdl_wait();  // (so far nothing that an earlier kernel writes or needs)
+    __syncwarp();
+    if (elect_one()) {
+      for (int i = 0; i < p.x_stages && kb0 + i * kShrinkK < kb1; ++i) load_x(kb0 + i * kShrinkK, i);
+    }
+  } else {
+    pdl_wait();
+    if (warp == 1) tmem_alloc_n<1>(smem_u32(&ctl.tmem_base), p.tmem_cols);
   }
   load_requests(p.q, off, ad, p.status, 64);
   if (threadIdx.x < BM) {
     const int t = m0 + threadIdx.x;
-    ctl.row_ad[threadIdx.x] = t < m1 ? adapter_of_row(off, ad, p.q.num_seg, t) : -1;
+    const int a = t < m1 ? adapter_of_row(off, ad, p.q.num_seg, t) : -1;
+    ctl.row_ad[threadIdx.x] = a;
+    ctl.row_scale[threadIdx.x] = a >= 0 && p.scale ? __ldg(p.scale + a) : 1.f;
   }
   tc_fence_before();
   __syncthreads();
@@ -479,9 +487,8 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] += sums[((size_t)k * p.rN + c + j) * per + i % per];
       }
-      const float s = p.scale ? __ldg(p.scale + a) : 1.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= s;
+      for (int j = 0; j < 8; ++j) v[j] *= ctl.row_scale[row];
     }
     uint4 o[kPlanes];
     split8(v, o);

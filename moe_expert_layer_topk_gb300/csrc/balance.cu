@@ -255,6 +255,11 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
   int* off = sm;                                                        // [num_seq + 1]
   int* cnt = sm + ((tk.num_seq + 4) & ~3);                              // [E] the sequence's counts
   float* red = reinterpret_cast<float*>(cnt + ((tk.E + 3) & ~3));       // kSum: [kWarps][E + 1]
+  // kSum: every kFold tokens a lane's running sums are moved to sums of sums, so
+  // that no fp32 sum takes more than about the square root of a long piece's
+  // tokens (16.8 M equal rows in one run: 8e-5 off without)
+  float* fold = red + kWarps * (tk.E + 1) + threadIdx.x;                // [NV] kThreads apart
+  constexpr int kFold = 64;
   __shared__ int s_n, s_tok, s_seqs;
   __shared__ bool s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -318,7 +323,9 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
   for_each_piece(off, tk.num_seq, t0, t1, [&](int s, int a, int b) {
     float acc[kSum ? NV : 1];
     float cf[kGrad ? NV : 1];
-    float z = 0.f;
+    float z = 0.f, z_fold = 0.f;
+    int since = 0;
+    bool folded = false;
     int t = a + warp * TPW + sub;
     if (t < b) load(t);  // under way while the counts are added up
     if constexpr (kCounted)
@@ -450,6 +457,17 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
 #pragma unroll
         for (int i = 0; i < NV; ++i) acc[i] = fmaf(l[i], r, acc[i]);
         if (el == 0 && on) z = fmaf(lse, lse, z);
+        if (++since == kFold) {
+          since = 0;
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            fold[i * kThreads] = folded ? fold[i * kThreads] + acc[i] : acc[i];
+            acc[i] = 0.f;
+          }
+          z_fold += z;
+          z = 0.f;
+          folded = true;
+        }
       }
       if constexpr (kGrad) {
         const float ar = ga_s * r, c = (gb * lse - ga_s * dot * r) * r;
@@ -469,6 +487,11 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
       }
     }
     if constexpr (kSum) {
+      if (folded) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) acc[i] += fold[i * kThreads];
+        z += z_fold;
+      }
       // acc and z over the warp's token groups and the warps: red[0..E)
       auto gather = [&]() {
         __syncwarp();
@@ -674,14 +697,14 @@ struct Main {
   template <int LPT, int VEC, int NQ, bool kFull>
   static int go(const char* fn, int grid, const Tokens& tk, const float* logits, const int32_t* idx, const Work& w, const Out& o,
                 const Grad& gr, cudaStream_t s) {
-    const size_t smem = sizeof(int) * (((tk.num_seq + 4) & ~3) + ((tk.E + 3) & ~3)) + (kSum ? sizeof(float) * kWarps * (tk.E + 1) : 0);
+    const size_t smem = sizeof(int) * (((tk.num_seq + 4) & ~3) + ((tk.E + 3) & ~3)) + (kSum ? sizeof(float) * (kWarps * (tk.E + 1) + VEC * NQ * kThreads) : 0);
     auto kern = balance_main_kernel<LPT, VEC, NQ, kFull, kSum, kGrad, kInline>;
     if (smem > 48 * 1024) {
       static bool set[64] = {};
       const int dev = current_device();
       if (dev < 0) return fail(MOE_ERR_CUDA, "%s: no current CUDA device", fn);
       if (!set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 * 1024);
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
         if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
         set[dev] = true;
       }

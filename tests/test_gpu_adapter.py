@@ -181,6 +181,24 @@ def test_one_request_does_not_reach_another(T):
         assert torch.equal(g[[0, 2, 3]], w[[0, 2, 3]]) and not torch.isfinite(g[1]).all()
 
 
+def test_more_than_2_31_outputs():
+    """Rows beyond element 2^31 of y and of dy: a few rows checked in float64."""
+    T, K, N, r, nA = 1_100_003, 64, 2048, 8, 2
+    d, c = make(1, K, N, r, nA, seed=3)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    c["x"] = torch.randn(T, K, generator=g, device="cuda").bfloat16()
+    offsets, which = [5, 600_000, T - 1], [1, 0]
+    y, hid = forward(c, offsets, which, T, K, N, r, nA)
+    c["dy"] = y
+    dx, _, _ = backward(c, hid, offsets, which, T, K, N, r, nA)
+    at = [0, 4, 5, 599_999, 600_000, T - 2, T - 1]
+    f = lambda v: v.double().cpu().numpy()  # noqa: E731
+    ref = ops_ref.adapter(f(c["x"][at]), *(d[k].double().numpy() for k in ("W", "A", "B", "scale")), [2, 4, 6], [1, 0], f(c["dy"][at]))
+    near(y[at], ref, "y", True)
+    near(dx[at], ref, "dx", True)
+    assert m.moe_read_device_status(reset=True) == 0
+
+
 def test_gradient_against_differences():
     """y is linear in x, in A and in B (each alone): a difference of the float64
     loss sum(y dy) over a step is its derivative up to rounding."""

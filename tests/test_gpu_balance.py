@@ -185,6 +185,33 @@ def test_bad_tables_and_ids_are_reported():
     assert m.moe_read_device_status(reset=True) == 2
 
 
+def test_more_than_2_31_logits():
+    """Two kinds of rows, so that every row's gradient is known from float64 of
+    two: element offsets pass 2^31 in the logits and in their gradient."""
+    T, E, k = (1 << 24) + 77, 130, 2
+    kinds = torch.randn(2, E, generator=torch.Generator().manual_seed(2))
+    kind = torch.arange(T, device="cuda") % 3 == 0
+    l = torch.where(kind[:, None], kinds[0].cuda(), kinds[1].cuda())
+    idx = torch.topk(kinds, k, dim=1).indices.to(torch.int32).cuda()[(~kind).long()]
+    o = call(l, idx, None, None, k)
+    n = [int(kind.sum()), T - int(kind.sum())]
+    p = torch.softmax(kinds.double(), 1).numpy()
+    lse = torch.logsumexp(kinds.double(), 1).numpy()
+    counts = np.zeros(E)
+    for q in range(2):
+        counts[torch.topk(kinds, k, dim=1).indices[q].numpy()] += n[q]
+    assert np.array_equal(o["counts"].cpu().numpy()[0], counts)
+    np.testing.assert_allclose(o["prob_sum"].cpu().numpy()[0], n[0] * p[0] + n[1] * p[1], rtol=8e-6)
+    a, b = COEF
+    for q in range(2):
+        mean = (p[q] * counts).sum()
+        want = p[q] * (a * E / (k * T * T) * (counts - mean) + 2 * b / T * lse[q])
+        mag = p[q] * (a * E / (k * T * T) * (counts + mean) + 2 * b / T * abs(lse[q]))
+        for t in (q, T // 2 // 3 * 3 + q, (T - 3) // 3 * 3 + q):  # first rows, the middle, the last
+            assert bool(kind[t]) == (q == 0)
+            assert np.all(np.abs(o["dlogits"][t].cpu().numpy() - want) <= 1.6e-5 * mag)
+
+
 def test_other_stream():
     T, E, k = 500, 128, 8
     l, idx, _ = inputs(T, E, k, seed=2)

@@ -93,6 +93,23 @@ def test_more_than_2_32_elements():
         assert np.array_equal(out[first:first + cnt].float().cpu().numpy() != 0, want), first
 
 
+def test_combine_of_more_than_2_31_elements():
+    T, H, k, p, seed = (1 << 20) + 9, 2048, 1, 0.5, 11
+    rows = torch.arange(T, dtype=torch.int32, device="cuda").flip(0).view(T, 1)
+    y_perm = torch.ones(T, H, dtype=torch.bfloat16, device="cuda")
+    w = torch.full((T, 1), 1.5, device="cuda")
+    y = torch.empty_like(y_perm)
+    m.moe_combine_dropout(y_perm, w, rows.contiguous(), None, T, H, k, p, rng(seed), y)
+    dyp, dw = torch.empty_like(y_perm), torch.empty(T, 1, device="cuda")
+    m.moe_combine_dropout_bwd(y_perm, y_perm, w, rows.contiguous(), T, H, k, p, rng(seed), dyp, dw)
+    for t in (0, T // 2, T - 1):
+        keep = ops_ref.keep(seed, 0, t * H, H, p)
+        assert np.array_equal(y[t].float().cpu().numpy(), np.where(keep, 3.0, 0.0))
+        assert np.array_equal(dyp[T - 1 - t].float().cpu().numpy(), np.where(keep, 3.0, 0.0))
+        assert float(dw[t, 0]) == 2.0 * keep.sum()
+    assert m.moe_read_device_status(reset=True) == 0
+
+
 def combine_inputs(T, H, k, seed):
     g = torch.Generator().manual_seed(seed)
     rows = torch.randperm(T * k, generator=g).to(torch.int32).view(T, k)
