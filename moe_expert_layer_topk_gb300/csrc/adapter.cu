@@ -289,6 +289,7 @@ struct ShrinkParams {
   int f_bytes;          // shared-memory bytes of one F block
   int f_rows;           // rows of F's 2-D view per adapter
   int x_stages, f_stages;  // steps of x and of F in flight
+  int f_runs;              // runs a step of F holds
   const float* scale;   // [num_adapters] or null
   __nv_bfloat16* hidden;
   uint32_t idesc;
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
   __shared__ ShrinkCtl ctl;
   const uint32_t base = align1k(smem_u32(smem_raw));
   uint8_t* bytes = smem_raw + (base - smem_u32(smem_raw));
-  const int f_stage = kShrinkK * p.f_bytes;
+  const int f_run = kShrinkK * p.f_bytes, f_stage = p.f_runs * f_run;
   const uint32_t sX = base, sF = base + p.x_stages * kShrinkXBytes;
   // the slices' sums of this CTA's share of the rows: [slice][rN][rows]
   float* sums = reinterpret_cast<float*>(bytes + p.x_stages * kShrinkXBytes + p.f_stages * f_stage);
@@ -397,17 +398,20 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
         }
         if (++xs == p.x_stages) { xs = 0; xp ^= 1u; }
         const int nb = min(kShrinkK, kb1 - kb);
-        for (int i = 0; i < n; ++i) {
-          const int a = unpack_run(ctl.runs[0][i]).a;
+        for (int i = 0; i < n; i += p.f_runs) {
           if (!(ok = wait_bar(smem_u32(&ctl.fempty[fs]), fp ^ 1u, &ctl.abort_flag, p.status))) break;
+          const int here = min(p.f_runs, n - i);
           const uint32_t fb = smem_u32(&ctl.ffull[fs]);
-          mbar_arrive_expect_tx(fb, nb * p.f_bytes);
-          for (int j = 0; j < nb; ++j) {
-            const uint32_t dst = sF + fs * f_stage + j * p.f_bytes;
-            if (kMN) {
-              for (int c = 0; c < p.r; c += 64) tma_load_2d(dst + c * 128, &tmF, fb, c, a * p.f_rows + (kb + j) * BK);
-            } else {
-              tma_load_2d(dst, &tmF, fb, (kb + j) * BK, a * p.f_rows);
+          mbar_arrive_expect_tx(fb, here * nb * p.f_bytes);
+          for (int g = 0; g < here; ++g) {
+            const int a = unpack_run(ctl.runs[0][i + g]).a;
+            for (int j = 0; j < nb; ++j) {
+              const uint32_t dst = sF + fs * f_stage + g * f_run + j * p.f_bytes;
+              if (kMN) {
+                for (int c = 0; c < p.r; c += 64) tma_load_2d(dst + c * 128, &tmF, fb, c, a * p.f_rows + (kb + j) * BK);
+              } else {
+                tma_load_2d(dst, &tmF, fb, (kb + j) * BK, a * p.f_rows);
+              }
             }
           }
           if (++fs == p.f_stages) { fs = 0; fp ^= 1u; }
@@ -424,19 +428,22 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
         if (!(ok = wait_bar(smem_u32(&ctl.xfull[xs]), xp, &ctl.abort_flag, p.status))) break;
         const uint32_t a0 = sX + xs * kShrinkXBytes;
         const int nb = min(kShrinkK, kb1 - kb);
-        for (int i = 0; i < n; ++i) {
-          const Run run = unpack_run(ctl.runs[1][i]);
-          const LaneMask<1> m = lane_mask<1>(run.lo, run.hi);
+        for (int i = 0; i < n; i += p.f_runs) {
           if (!(ok = wait_bar(smem_u32(&ctl.ffull[fs]), fp, &ctl.abort_flag, p.status))) break;
           tc_fence_after();
-          const uint32_t b0 = sF + fs * f_stage;
-          for (int j = 0; j < nb; ++j) {
+          const int here = min(p.f_runs, n - i);
+          for (int g = 0; g < here; ++g) {
+            const Run run = unpack_run(ctl.runs[1][i + g]);
+            const LaneMask<1> m = lane_mask<1>(run.lo, run.hi);
+            const uint32_t b0 = sF + fs * f_stage + g * f_run;
+            for (int j = 0; j < nb; ++j) {
 #pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk)
-              mma_lanes(tmem, sdesc(a0 + j * (BM * BK * 2) + kk * 32, 16, 1024),
-                        kMN ? sdesc(b0 + j * p.f_bytes + kk * 2048, CHUNK_BYTES, 1024)
-                            : sdesc(b0 + j * p.f_bytes + kk * 32, 16, 1024),
-                        p.idesc, kb > kb0 || j > 0 || kk > 0, m);
+              for (int kk = 0; kk < BK / 16; ++kk)
+                mma_lanes(tmem, sdesc(a0 + j * (BM * BK * 2) + kk * 32, 16, 1024),
+                          kMN ? sdesc(b0 + j * p.f_bytes + kk * 2048, CHUNK_BYTES, 1024)
+                              : sdesc(b0 + j * p.f_bytes + kk * 32, 16, 1024),
+                          p.idesc, kb > kb0 || j > 0 || kk > 0, m);
+            }
           }
           mma_commit(smem_u32(&ctl.fempty[fs]));
           if (++fs == p.f_stages) { fs = 0; fp ^= 1u; }
@@ -722,6 +729,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
   const int vset = one_block ? 1 : kWidePlanes;
   const int passes = (p.r + 63) / 64;
   static_assert(C::VBUF == kWidePlanes, "room for both parts of hidden");
+  // A stage holds F's blocks of several runs: one in W's place, the others in in's
+  // (a barrier wait and a commit a run cost about what its MMAs do).
+  const int per_stage = 1 + a_bytes / C::B_BYTES;
+  auto run_slot = [&](int j) { return j == 0 ? a_bytes : (j - 1) * C::B_BYTES; };
 
   struct Unit {
     int m0, n0, bn;  // the tile's first row (of the pair's 256) and column, its columns
@@ -768,16 +779,20 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
         const int n = ctl.num_runs[lb];
         for (int ps = 0; ok && ps < passes; ++ps) {
           const int c = ps * 64;  // F's columns (ranks) of this pass
-          for (int i = r0; i < n; i += dr) {
-            const int a = unpack_run(ctl.runs[lb][i]).a;
+          for (int i = r0; i < n; i += dr * per_stage) {
             if (!(ok = wait_bar(smem_u32(&ctl.empty[st]), ph ^ 1u, &ctl.abort_flag, p.status))) break;
-            const uint32_t fb = at_leader(smem_u32(&ctl.full[st])), sB = base + st * stage_bytes + a_bytes;
-            if (leader) mbar_arrive_expect_tx(smem_u32(&ctl.full[st]), CTAS * b_bytes);
-            for (int h = 0; h < nbox; ++h) {
-              if (kMN)
-                tma_load_4d<CTAS>(sB + h * (C::WB * BK * 2), &tmF, fb, 0, c, col / 64 + h * (C::WB / 64), a);
-              else
-                tma_load<CTAS>(sB + h * (C::WB * BK * 2), &tmF, fb, c, a * p.f_rows + col + h * C::WB);
+            const int here = min(per_stage, (n - i + dr - 1) / dr);
+            const uint32_t fb = at_leader(smem_u32(&ctl.full[st])), sA = base + st * stage_bytes;
+            if (leader) mbar_arrive_expect_tx(smem_u32(&ctl.full[st]), CTAS * here * b_bytes);
+            for (int j = 0; j < here; ++j) {
+              const int a = unpack_run(ctl.runs[lb][i + j * dr]).a;
+              const uint32_t sB = sA + run_slot(j);
+              for (int h = 0; h < nbox; ++h) {
+                if (kMN)
+                  tma_load_4d<CTAS>(sB + h * (C::WB * BK * 2), &tmF, fb, 0, c, col / 64 + h * (C::WB / 64), a);
+                else
+                  tma_load<CTAS>(sB + h * (C::WB * BK * 2), &tmF, fb, c, a * p.f_rows + col + h * C::WB);
+              }
             }
             next();
           }
@@ -852,16 +867,25 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
             if (!(ok = wait_bar(smem_u32(&ctl.vfull), vph, &ctl.abort_flag, p.status))) break;
             const int steps = min(4, (p.r - ps * 64 + 15) / 16);  // 16-wide steps of this block of F
             const int pstep = one_block ? rp * 2 : a_bytes;        // bytes from one part of hidden to the next
-            for (int i = r0; i < n; i += dr) {
-              const Run run = unpack_run(ctl.runs[lb][i]);
-              const LaneMask<CTAS> m = lane_mask<CTAS>(run.lo, run.hi);
+            const uint64_t vd = sdesc(sV, 16, 1024);
+            for (int i = r0; i < n; i += dr * per_stage) {
               if (!(ok = wait_bar(smem_u32(&ctl.full[st]), ph, &ctl.abort_flag, p.status))) break;
               tc_fence_after();
-              const uint32_t b0 = base + st * stage_bytes + a_bytes;
-              for (int pl = 0; pl < kWidePlanes; ++pl)
-                for (int kk = 0; kk < steps; ++kk)
-                  mma_lanes(d, sdesc(sV + pl * pstep + kk * 32, 16, 1024),
-                            kMN ? sdesc(b0 + kk * 2048, CHUNK_BYTES, 1024) : sdesc(b0 + kk * 32, 16, 1024), idesc, 1u, m);
+              const int here = min(per_stage, (n - i + dr - 1) / dr);
+              for (int j = 0; j < here; ++j) {
+                const Run run = unpack_run(ctl.runs[lb][i + j * dr]);
+                const LaneMask<CTAS> m = lane_mask<CTAS>(run.lo, run.hi);
+                const uint32_t b0 = base + st * stage_bytes + run_slot(j);
+                // (descriptors count 16-byte units: a step adds to their low word)
+                const uint64_t bd = kMN ? sdesc(b0, CHUNK_BYTES, 1024) : sdesc(b0, 16, 1024);
+#pragma unroll
+                for (int kk = 0; kk < BK / 16; ++kk) {
+                  if (kk >= steps) break;
+#pragma unroll
+                  for (int pl = 0; pl < kWidePlanes; ++pl)
+                    mma_lanes(d, vd + (uint64_t)(pl * (pstep >> 4) + kk * 2), bd + (uint64_t)(kk * (kMN ? 128 : 2)), idesc, 1u, m);
+                }
+              }
               mma_commit_to<CTAS>(smem_u32(&ctl.empty[st]));
               next();
             }
@@ -1342,8 +1366,11 @@ int run_shrink(const char* fn, const Reqs& q, const void* in, long long ld, cons
   // Tiles of many runs want many blocks of F in flight: as many as fit where a CTA has its SM alone.
   // Otherwise two CTAs share one, with two steps of x in flight each (three: one CTA an SM; 18 us instead
   // of 13 for 8192 x 2048).
-  const int sms = sm_count() > 0 ? sm_count() : 148, f_stage = kShrinkK * p.f_bytes;
+  const int sms = sm_count() > 0 ? sm_count() : 148;
   const bool alone = tiles * cs <= sms;
+  // more runs than rows of tiles: several share a step of F, its barrier wait and its commit
+  p.f_runs = q.num_seg <= 2 * tiles ? 1 : (kShrinkK * p.f_bytes <= 8192 ? 4 : (kShrinkK * p.f_bytes <= 16384 ? 2 : 1));
+  const int f_stage = p.f_runs * kShrinkK * p.f_bytes;
   const int steps = ((nkb + cs - 1) / cs + kShrinkK - 1) / kShrinkK;
   p.x_stages = r <= 64 && alone ? kShrinkX : 2;
   if (steps < p.x_stages) p.x_stages = steps;
