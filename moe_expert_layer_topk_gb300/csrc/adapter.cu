@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
       bool ok = true;
       for (int kb = kb0; ok && kb < kb1; kb += kShrinkK) {
         if (!(ok = wait_bar(smem_u32(&ctl.xfull[xs]), xp, &ctl.abort_flag, p.status))) break;
-        const uint32_t a0 = sX + xs * kShrinkXBytes;
+        const uint64_t xd = sdesc(sX + xs * kShrinkXBytes, 16, 1024);
         const int nb = min(kShrinkK, kb1 - kb);
         for (int i = 0; i < n; i += p.f_runs) {
           if (!(ok = wait_bar(smem_u32(&ctl.ffull[fs]), fp, &ctl.abort_flag, p.status))) break;
@@ -435,14 +435,17 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
           for (int g = 0; g < here; ++g) {
             const Run run = unpack_run(ctl.runs[1][i + g]);
             const LaneMask<1> m = lane_mask<1>(run.lo, run.hi);
+            // (descriptors count 16-byte units: blocks and steps add to their low word)
             const uint32_t b0 = sF + fs * f_stage + g * f_run;
-            for (int j = 0; j < nb; ++j) {
+            const uint64_t bd = kMN ? sdesc(b0, CHUNK_BYTES, 1024) : sdesc(b0, 16, 1024);
+#pragma unroll
+            for (int j = 0; j < kShrinkK; ++j) {
+              if (j >= nb) break;
+              const uint64_t bj = bd + (uint64_t)(j * (p.f_bytes >> 4));
 #pragma unroll
               for (int kk = 0; kk < BK / 16; ++kk)
-                mma_lanes(tmem, sdesc(a0 + j * (BM * BK * 2) + kk * 32, 16, 1024),
-                          kMN ? sdesc(b0 + j * p.f_bytes + kk * 2048, CHUNK_BYTES, 1024)
-                              : sdesc(b0 + j * p.f_bytes + kk * 32, 16, 1024),
-                          p.idesc, kb > kb0 || j > 0 || kk > 0, m);
+                mma_lanes(tmem, xd + (uint64_t)(j * (BM * BK * 2 / 16) + kk * 2), bj + (uint64_t)(kk * (kMN ? 128 : 2)), p.idesc,
+                          kb > kb0 || j > 0 || kk > 0, m);
             }
           }
           mma_commit(smem_u32(&ctl.fempty[fs]));
