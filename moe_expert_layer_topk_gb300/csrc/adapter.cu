@@ -719,7 +719,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
   __syncthreads();
   if constexpr (CTAS == 2) cluster_sync();  // peer barriers initialised before any remote signal
   tc_fence_after();
-  pdl_trigger();
+  // With a narrow kernel before it the next kernel may start only once that one
+  // has ended (below): what follows may then take hidden without waiting for this one.
+  if (!p.has_hidden) pdl_trigger();
   const uint32_t tmem = ctl.tmem_base;
   const int nrank = kSplit ? (int)gridDim.x : 1, rank = kSplit ? (int)blockIdx.x : 0;
   const int nkb = p.red / BK;
@@ -820,6 +822,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
         }
         if (!waited) {
           pdl_wait();
+          pdl_trigger();
           waited = true;
         }
         if (lane == 0 && n > r0) {
@@ -833,7 +836,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
       }
-      if (!waited) pdl_wait();  // the grid may not end before the narrow kernel does
+      if (!waited) {  // the grid may not end before the narrow kernel does
+        pdl_wait();
+        pdl_trigger();
+      }
     }
   } else if (warp == 1) {
     // a pair's second CTA only keeps its tensor memory
@@ -1071,7 +1077,8 @@ __global__ void __launch_bounds__(192) adapter_grad_kernel(const __grid_constant
                                                            const __grid_constant__ CUtensorMap tmDy,
                                                            const __grid_constant__ CUtensorMap tmV,
                                                            const GradParams p) {
-  pdl_wait();
+  // The wide kernel before this one lets it start once u is there, and neither
+  // needs the other: this one fills the SMs that the other's last tiles leave.
   extern __shared__ uint8_t smem_raw[];
   __shared__ GradCtl ctl;
   const uint32_t base = align1k(smem_u32(smem_raw));
@@ -1241,6 +1248,7 @@ __global__ void __launch_bounds__(192) adapter_grad_kernel(const __grid_constant
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_n<1>(tmem, cols);
+  pdl_wait();  // this grid may not end before the wide kernel does
 }
 
 // dA, dB of the adapters whose rows were not one part: the parts' sums in
