@@ -21,7 +21,10 @@
 // whichever CTA comes last.  (chunk c, sequence q) sits in row c + q: along the
 // token axis every new pair raises one of the two, so no two pairs share a row.
 //
-// Bound by launch latency up to about 8192 tokens x 128 experts, by HBM above.
+// Up to about 65536 tokens x 128 experts a chain of latencies bounds the call
+// (two launches, the counts' rows, a piece's sums, its ticket, the last rows:
+// 12 us at 8192 x 128, 21.6 at 65519 x 128 in one sequence, of which the tokens
+// are 7), above it HBM (300000 x 128: 74 us, 4.1 TB/s).
 #include <cfloat>
 
 #include "common.cuh"
@@ -35,9 +38,7 @@ constexpr int kWarps = kThreads / 32;
 
 struct Tokens {  // the packed token axis, cut into chunks
   int T, E, k, num_seq;
-  int chunk;        // tokens per chunk of the main kernel
-  int count_chunk;  // and of the counting kernel
-  int count_chunks;
+  int count_chunks; // chunks of the counting kernel
   const int32_t* seq_offsets;  // null: one sequence of all tokens
   const uint8_t* mask;         // null: every token counts
 };
@@ -60,8 +61,9 @@ struct Out {
 };
 
 // The sequence table in shared memory, made monotone and clamped to [0, T]
-// (a table that is not is reported): off[0..num_seq].
-__device__ __forceinline__ void load_table(const Tokens& k, int* off, int* status) {
+// (a table that is not is reported): off[0..num_seq], and the number of
+// sequences with tokens before each, nb[0..num_seq].
+__device__ __forceinline__ void load_table(const Tokens& k, int* off, int* nb, int* status) {
   bool bad = false;
   for (int s = threadIdx.x; s <= k.num_seq; s += kThreads) {
     int v = k.seq_offsets ? __ldg(k.seq_offsets + s) : (s == 0 ? 0 : k.T);
@@ -74,7 +76,7 @@ __device__ __forceinline__ void load_table(const Tokens& k, int* off, int* statu
   __syncthreads();
   if (k.num_seq > 1 && threadIdx.x < 32) {
     const int lane = threadIdx.x;
-    int carry = 0;
+    int carry = 0, full = 0;
     for (int b = 0; b <= k.num_seq; b += 32) {
       const int s = b + lane, v = s <= k.num_seq ? off[s] : 0;
       int m = v;
@@ -84,44 +86,65 @@ __device__ __forceinline__ void load_table(const Tokens& k, int* off, int* statu
         if (lane >= d) m = max(m, o);
       }
       m = max(m, carry);
+      int before = __shfl_up_sync(0xffffffffu, m, 1);
+      if (lane == 0) before = carry;
+      const unsigned more = __ballot_sync(0xffffffffu, s > 0 && s <= k.num_seq && m > before);
       if (s <= k.num_seq) {
         bad |= m != v;
         off[s] = m;
+        nb[s] = full + __popc(more & (0xffffffffu >> (31 - lane)));
       }
+      full += __popc(more);
       carry = __shfl_sync(0xffffffffu, m, 31);
     }
-  } else if (k.num_seq == 1 && threadIdx.x == 0 && off[1] < off[0]) {
-    bad = true;
-    off[1] = off[0];
+  } else if (k.num_seq == 1 && threadIdx.x == 0) {
+    if (off[1] < off[0]) {
+      bad = true;
+      off[1] = off[0];
+    }
+    nb[0] = 0;
+    nb[1] = off[1] > off[0];
   }
   if (bad) set_status(status, MOE_STATUS_BAD_SEGMENTS);
   __syncthreads();
 }
 
-// The sequence that token t lies in, given off[0] <= t < off[num_seq].
-__device__ __forceinline__ int seq_of(const int* off, int num_seq, int t) {
-  int lo = 0, hi = num_seq - 1;  // last s with off[s] <= t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (off[mid] <= t) lo = mid; else hi = mid - 1;
+// The sequences' tokens cut into equal chunks, where a sequence counts for `pad`
+// tokens more than it has: a chunk pays for each piece it holds (its counts, its
+// sums, its ticket), and with chunks of equal tokens the one with the most pieces
+// sets the time (65519 x 128: 37 sequences 28.9 us, 150 38.8; with the pad 24.1
+// and 28.9; 8192 x 128 in 64 sequences 34.6 and 16.8).  Sequence s takes places [start(s), start(s + 1)), the first pad
+// of them without a token.
+struct Cut {
+  const int *off, *nb;
+  int num_seq;
+  unsigned pad, chunk;
+  __device__ __forceinline__ Cut(const int* off, const int* nb, int num_seq, int chunks, int pad)
+      : off(off), nb(nb), num_seq(num_seq), pad(nb[num_seq] > 1 ? pad : 0) {
+    chunk = max(1u, (start(num_seq) + chunks - 1) / chunks);
   }
-  return lo;
-}
-
-// f(seq, first token, end) for every non-empty piece of [t0, t1) inside a sequence.
-template <class F>
-__device__ __forceinline__ void for_each_piece(const int* off, int num_seq, int t0, int t1, F&& f) {
-  int a = max(t0, off[0]);
-  const int end = min(t1, off[num_seq]);
-  if (a >= end) return;
-  int s = seq_of(off, num_seq, a);
-  while (a < end) {
-    const int b = min(end, off[s + 1]);
-    if (b > a) f(s, a, b);
-    a = max(a, b);
-    ++s;
+  __device__ __forceinline__ unsigned start(int s) const { return (unsigned)(off[s] - off[0]) + pad * nb[s]; }
+  // the chunks that hold tokens of s (which has some)
+  __device__ __forceinline__ int first(int s) const { return (start(s) + pad) / chunk; }
+  __device__ __forceinline__ int last(int s) const { return (start(s + 1) - 1) / chunk; }
+  // f(seq, first token, end) for every piece of chunk c
+  template <class F>
+  __device__ __forceinline__ void pieces(int c, F&& f) const {
+    const unsigned all = start(num_seq), v0 = c * chunk, v1 = min(all, v0 + chunk);
+    if (v0 >= all) return;
+    int lo = 0, hi = num_seq - 1;  // last s with start(s) <= v0
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (start(mid) <= v0) lo = mid; else hi = mid - 1;
+    }
+    for (int s = lo; s < num_seq && start(s) < v1; ++s) {
+      const unsigned v = start(s) + pad;  // its first token's place
+      const int a = off[s] + (v0 > v ? (int)(v0 - v) : 0);
+      const int b = min(off[s + 1], off[s] + (v1 > v ? (int)(v1 - v) : 0));
+      if (a < b) f(s, a, b);
+    }
   }
-}
+};
 
 // ------------------------------------------------------------------ counts
 // hist[e], *live: the slots and tokens of [a, b) that count (all threads).
@@ -176,18 +199,23 @@ __device__ __forceinline__ void zero_sequence(const Tokens& tk, const Out& o, in
   if (threadIdx.x == 0) o.tokens[s] = 0;
 }
 
+// A piece costs about as much as so many tokens of the count (none: 24.4 us at
+// 65519 x 128 in 37 sequences, 128: 24.1).
+constexpr int kCountPad = 128;
+
 __global__ void __launch_bounds__(kThreads) balance_count_kernel(const Tokens tk, const int32_t* __restrict__ topk_idx,
                                                                  const Work w, const Out o, int* status) {
   pdl_wait();
   pdl_trigger();
   extern __shared__ int sm[];
   int* off = sm;                      // [num_seq + 1]
-  int* hist = sm + tk.num_seq + 1;    // [E]
+  int* nb = off + tk.num_seq + 1;     // [num_seq + 1]
+  int* hist = nb + tk.num_seq + 1;    // [E]
   __shared__ int live;
-  load_table(tk, off, status);
-  const int c = blockIdx.x, t0 = c * tk.count_chunk, t1 = min(tk.T, t0 + tk.count_chunk);
+  load_table(tk, off, nb, status);
+  const int c = blockIdx.x;
   int total = 0;
-  for_each_piece(off, tk.num_seq, t0, t1, [&](int s, int a, int b) {
+  Cut(off, nb, tk.num_seq, gridDim.x, kCountPad).pieces(c, [&](int s, int a, int b) {
     count_slots(tk, topk_idx, a, b, hist, &live, status);
     for (int e = threadIdx.x; e < tk.E; e += kThreads) w.cnt_part[(size_t)(c + s) * tk.E + e] = hist[e];
     if (threadIdx.x == 0) w.tok_part[c + s] = live;
@@ -240,6 +268,11 @@ struct Grad {
   float* dlogits;
 };
 
+// A piece's counts, sums and ticket cost about as much as so many steps of its
+// warps over tokens (2: 25.5 us at 65519 x 128 in 37 sequences, 4: 24.1, 6: 24.6);
+// without sums, one.
+constexpr int kPieceSteps = 4;
+
 template <int LPT, int VEC, int NQ, bool kFull, bool kSum, bool kGrad, bool kInline>
 __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens tk, const float* __restrict__ logits,
                                                                 const int32_t* __restrict__ topk_idx, const Work w,
@@ -253,24 +286,29 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
   pdl_trigger();
   extern __shared__ int sm[];
   int* off = sm;                                                        // [num_seq + 1]
-  int* cnt = sm + ((tk.num_seq + 4) & ~3);                              // [E] the sequence's counts
+  int* nb = sm + tk.num_seq + 1;                                        // [num_seq + 1]
+  int* cnt = sm + ((2 * tk.num_seq + 5) & ~3);                          // [E] the sequence's counts
   float* red = reinterpret_cast<float*>(cnt + ((tk.E + 3) & ~3));       // kSum: [kWarps][E + 1]
   // kSum: every kFold tokens a lane's running sums are moved to sums of sums, so
   // that no fp32 sum takes more than about the square root of a long piece's
   // tokens (16.8 M equal rows in one run: 8e-5 off without)
   float* fold = red + kWarps * (tk.E + 1) + threadIdx.x;                // [NV] kThreads apart
   constexpr int kFold = 64;
-  __shared__ int s_n, s_tok, s_seqs;
+  __shared__ int s_n, s_tok;
   __shared__ bool s_last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / LPT, el = lane % LPT;
   const int E = tk.E;
-  load_table(tk, off, status);
-  const int chunk = blockIdx.x, t0 = chunk * tk.chunk, t1 = min(tk.T, t0 + tk.chunk);
+  load_table(tk, off, nb, status);
+  const int chunk = blockIdx.x;
+  const int step = kWarps * TPW;
+  const Cut cut(off, nb, tk.num_seq, gridDim.x, (kSum ? kPieceSteps : 1) * step);
+  const Cut counted(off, nb, tk.num_seq, kCounted ? tk.count_chunks : 1, kCountPad);
   if constexpr (kGrad) {  // tokens outside every sequence get no gradient
-    const int lo = min(t1, max(t0, off[0])), hi = max(t0, min(t1, off[tk.num_seq]));
-    for (size_t i = (size_t)t0 * E + threadIdx.x; i < (size_t)lo * E; i += kThreads) gr.dlogits[i] = 0.f;
-    for (size_t i = (size_t)max(lo, hi) * E + threadIdx.x; i < (size_t)t1 * E; i += kThreads) gr.dlogits[i] = 0.f;
+    const size_t lo = (size_t)off[0] * E, hi = (size_t)off[tk.num_seq] * E, n = (size_t)tk.T * E;
+    const size_t i0 = (size_t)chunk * kThreads + threadIdx.x, di = (size_t)gridDim.x * kThreads;
+    for (size_t i = i0; i < lo; i += di) gr.dlogits[i] = 0.f;
+    for (size_t i = hi + i0; i < n; i += di) gr.dlogits[i] = 0.f;
   }
   if constexpr (kInline) {
     for (int s = 0; s < tk.num_seq; ++s)
@@ -299,7 +337,6 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
   };
   auto col = [&](int i) { return (i / VEC) * VEC * LPT + el * VEC + i % VEC; };
   auto has = [&](int i) { return kFull || col(i) < E; };
-  const int step = kWarps * TPW;
 
   // The lane's share of the next token; the rows of tokens that do not count are
   // read and replaced.
@@ -320,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
     }
   };
 
-  for_each_piece(off, tk.num_seq, t0, t1, [&](int s, int a, int b) {
+  cut.pieces(chunk, [&](int s, int a, int b) {
     float acc[kSum ? NV : 1];
     float cf[kGrad ? NV : 1];
     float z = 0.f, z_fold = 0.f;
@@ -332,10 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
       if (!ready) pdl_wait();
     // this sequence's counts and, with the first piece, the call's tokens and sequences
     if (threadIdx.x == 0) s_tok = 0;
-    if (!ready && threadIdx.x == 0) s_n = s_seqs = 0;
+    if (!ready && threadIdx.x == 0) s_n = 0;
     if constexpr (kSum && !kInline) {
-      const int c0 = off[s] / tk.count_chunk, c1 = (off[s + 1] - 1) / tk.count_chunk + 1;
-      int tok = 0, n = 0, seqs = 0;
+      const int c0 = counted.first(s), c1 = counted.last(s) + 1;
+      int tok = 0, n = 0;
       for (int c = c0 + threadIdx.x; c < c1; c += kThreads) tok += __ldcg(w.tok_part + c + s);
       if (!ready)
         for (int c = threadIdx.x; c < tk.count_chunks; c += kThreads) n += __ldcg(w.tok_chunk + c);
@@ -362,8 +399,6 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
           }
         }
       }
-      if (!ready)
-        for (int q = threadIdx.x; q < tk.num_seq; q += kThreads) seqs += off[q + 1] > off[q];
       __syncwarp();
 #pragma unroll
       for (int d = LPT; d < 32; d <<= 1) {
@@ -378,11 +413,9 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
       }
       tok = __reduce_add_sync(0xffffffffu, tok);
       n = __reduce_add_sync(0xffffffffu, n);
-      seqs = __reduce_add_sync(0xffffffffu, seqs);
       __syncthreads();
       if (lane == 0 && tok) atomicAdd(&s_tok, tok);
       if (lane == 0 && n) atomicAdd(&s_n, n);
-      if (lane == 0 && seqs) atomicAdd(&s_seqs, seqs);
       for (int e = threadIdx.x; e < E; e += kThreads) {
         int v = 0;
 #pragma unroll
@@ -519,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
       };
       gather();
       bool finish = true;
-      const int c0 = off[s] / tk.chunk, c1 = (off[s + 1] - 1) / tk.chunk + 1;
+      const int c0 = cut.first(s), c1 = cut.last(s) + 1;
       if (!kInline && c1 - c0 > 1) {  // a sequence wholly in this chunk needs no others' partials
         for (int e = threadIdx.x; e <= E; e += kThreads) {  // each thread its own sums
           if (e < E)
@@ -611,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
         s_last = false;
         if (finished > 0) {
           __threadfence();
-          s_last = atomicAdd(w.ticket + tk.num_seq, finished) + finished == (unsigned)s_seqs;
+          s_last = atomicAdd(w.ticket + tk.num_seq, finished) + finished == (unsigned)nb[tk.num_seq];
         }
       }
       __syncthreads();
@@ -650,30 +683,28 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
 
 size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 
-// Main chunks: one CTA per SM, at least 64 tokens each (what a CTA of 128
+// Main chunks: one CTA per SM, about 64 tokens each at least (what a CTA of 128
 // experts works on at a time); counting chunks fewer, since every main CTA adds
 // their rows up.
 constexpr int kMaxChunks = 152, kMaxCountChunks = 304;
 // One CTA does the whole of a problem of up to so many logits (and few sequences).
 constexpr int kInlineLogits = 8192, kInlineSeqs = 4;
 
-int chunk_tokens(int T, int most, int least) {
-  const int c = (T + most - 1) / most;
-  return c < least ? least : c;
+int chunks(int T, int num_seq, int most) {
+  const int c = T / 64 + (T % 64 != 0) + num_seq - 1;
+  return c < most ? c : most;
 }
 
 bool is_inline(int T, int E, int num_seq) { return (long long)T * E <= kInlineLogits && num_seq <= kInlineSeqs; }
 
 struct Layout {
-  int chunk, nchunk, count_chunk, ncount;
+  int nchunk, ncount;
   size_t cnt, tok, tokc, part, zpart, share, ticket, total;
 };
 Layout layout(int T, int E, int num_seq) {
   Layout L;
-  L.chunk = chunk_tokens(T, kMaxChunks, 64);
-  L.nchunk = (T + L.chunk - 1) / L.chunk;
-  L.count_chunk = chunk_tokens(T, kMaxCountChunks, 64);
-  L.ncount = (T + L.count_chunk - 1) / L.count_chunk;
+  L.nchunk = chunks(T, num_seq, kMaxChunks);
+  L.ncount = chunks(T, num_seq, kMaxCountChunks);
   const size_t rows = (size_t)L.nchunk + num_seq, crows = (size_t)L.ncount + num_seq;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -697,7 +728,7 @@ struct Main {
   template <int LPT, int VEC, int NQ, bool kFull>
   static int go(const char* fn, int grid, const Tokens& tk, const float* logits, const int32_t* idx, const Work& w, const Out& o,
                 const Grad& gr, cudaStream_t s) {
-    const size_t smem = sizeof(int) * (((tk.num_seq + 4) & ~3) + ((tk.E + 3) & ~3)) + (kSum ? sizeof(float) * (kWarps * (tk.E + 1) + VEC * NQ * kThreads) : 0);
+    const size_t smem = sizeof(int) * (((2 * tk.num_seq + 5) & ~3) + ((tk.E + 3) & ~3)) + (kSum ? sizeof(float) * (kWarps * (tk.E + 1) + VEC * NQ * kThreads) : 0);
     auto kern = balance_main_kernel<LPT, VEC, NQ, kFull, kSum, kGrad, kInline>;
     if (smem > 48 * 1024) {
       static bool set[64] = {};
@@ -784,7 +815,7 @@ int moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t
     if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
     return MOE_OK;
   }
-  Tokens tk{T, E, k, num_seg, L.chunk, L.count_chunk, L.ncount, seg_offsets, mask};
+  const Tokens tk{T, E, k, num_seg, L.ncount, seg_offsets, mask};
   char* base = static_cast<char*>(ws);
   const Work w{reinterpret_cast<int32_t*>(base + L.cnt),  reinterpret_cast<int32_t*>(base + L.tok),
                reinterpret_cast<int32_t*>(base + L.tokc), reinterpret_cast<float*>(base + L.part),
@@ -792,12 +823,10 @@ int moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t
                reinterpret_cast<unsigned*>(base + L.ticket)};
   const Out o{counts, tokens, prob_sum, loss};
   const Grad gr{balance_coef, z_coef, nullptr, dlogits};
-  if (is_inline(T, E, num_seg)) {
-    tk.chunk = T;
+  if (is_inline(T, E, num_seg))
     return dlogits ? Main<true, true, true>::pick(fn, 1, tk, logits, topk_idx, w, o, gr, s)
                    : Main<true, false, true>::pick(fn, 1, tk, logits, topk_idx, w, o, gr, s);
-  }
-  launch_pdl(balance_count_kernel, L.ncount, kThreads, sizeof(int) * (size_t)(num_seg + 1 + E), s, tk, topk_idx, w, o,
+  launch_pdl(balance_count_kernel, L.ncount, kThreads, sizeof(int) * (size_t)(2 * num_seg + 2 + E), s, tk, topk_idx, w, o,
              status_word());
   if (int rc = check_launch(fn, "count kernel")) return rc;
   return dlogits ? Main<true, true, false>::pick(fn, L.nchunk, tk, logits, topk_idx, w, o, gr, s)
@@ -814,7 +843,7 @@ int moe_balance_loss_bwd(const float* logits, const uint8_t* mask, int T, int E,
   if (!counts || !tokens || !dlogits) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer argument", fn);
   if (!aligned16(dlogits)) return fail(MOE_ERR_ALIGNMENT, "%s: dlogits must be 16-byte aligned", fn);
   const Layout L = layout(T, E, num_seg);
-  const Tokens tk{T, E, k, num_seg, L.chunk, L.count_chunk, L.ncount, seg_offsets, mask};
+  const Tokens tk{T, E, k, num_seg, L.ncount, seg_offsets, mask};
   const Out o{const_cast<int32_t*>(counts), const_cast<int32_t*>(tokens), nullptr, nullptr};  // read only
   const Grad gr{balance_coef, z_coef, dloss, dlogits};
   return Main<false, true, false>::pick(fn, L.nchunk, tk, logits, static_cast<const int32_t*>(nullptr), Work{}, o, gr,
