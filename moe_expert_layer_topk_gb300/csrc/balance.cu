@@ -365,22 +365,22 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
     bool folded = false;
     int t = a + warp * TPW + sub;
     if (t < b) load(t);  // under way while the counts are added up
+    const int cc0 = kCounted ? counted.first(s) : 0, cc1 = kCounted ? counted.last(s) + 1 : 0;
     if constexpr (kCounted)
       if (!ready) pdl_wait();
     // this sequence's counts and, with the first piece, the call's tokens and sequences
     if (threadIdx.x == 0) s_tok = 0;
     if (!ready && threadIdx.x == 0) s_n = 0;
     if constexpr (kSum && !kInline) {
-      const int c0 = counted.first(s), c1 = counted.last(s) + 1;
       int tok = 0, n = 0;
-      for (int c = c0 + threadIdx.x; c < c1; c += kThreads) tok += __ldcg(w.tok_part + c + s);
+      for (int c = cc0 + threadIdx.x; c < cc1; c += kThreads) tok += __ldcg(w.tok_part + c + s);
       if (!ready)
         for (int c = threadIdx.x; c < tk.count_chunks; c += kThreads) n += __ldcg(w.tok_chunk + c);
       int iv[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) iv[i] = 0;
       constexpr int kR = NV <= 16 ? 2 : 1;  // rows in flight
-      for (int r0 = c0 + warp * TPW + sub; r0 < c1; r0 += kR * step) {
+      for (int r0 = cc0 + warp * TPW + sub; r0 < cc1; r0 += kR * step) {
 #pragma unroll
         for (int u = 0; u < kR; ++u) {
           const int c = r0 + u * step;
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
           for (int q = 0; q < NQ; ++q) {
             const int e0 = q * VEC * LPT + el * VEC;
             const int32_t* src = w.cnt_part + (size_t)(c + s) * E + e0;
-            if (c < c1 && e0 < E) {
+            if (c < cc1 && e0 < E) {
               if constexpr (VEC == 4) {
                 const int4 f = __ldcg(reinterpret_cast<const int4*>(src));
                 iv[4 * q] += f.x; iv[4 * q + 1] += f.y; iv[4 * q + 2] += f.z; iv[4 * q + 3] += f.w;
