@@ -19,6 +19,15 @@
 // (tcgen05.mma disable-output-lane).  A tile may so hold any mix of requests,
 // no row is computed for another request's adapter, and a non-finite value in
 // one request's row or adapter reaches no other row.
+//
+// Measured (r = 16 unless said; graph replays, cold L2 not forced):
+//   1 row, 2048 x 2048, one request                6.7 us   launches and latency
+//   64 rows of 64 requests, 48 adapters            11.1     masked MMAs, one run a row
+//   517 rows, mixed, r = 64, 768 x 2048            22.9     the same
+//   16384 rows, 2048 x 4096                        164-180  tensor cores: 1.5 PFLOP/s of
+//                                                  the wide product's 0.28 TFLOP in 146
+//   8192 rows, 2048 x 2048, backward               122.5 with the forward: narrow 13 and
+//                                                  wide 44 each way, gradients 17 + 6
 #include <cuda.h>
 
 #include "tc_common.cuh"
@@ -282,9 +291,12 @@ __device__ __forceinline__ void split8(const float (&v)[8], uint4 (&out)[kPlanes
 // B_a^T, read from B_a [N, r] as it lies (MN-major operand).  One row tile's
 // runs follow one another for every block of the reduction, each with the
 // lanes of the other runs off, so x is read once whatever the mix of requests.
+// With few runs it is bound by reading x (8192 x 2048: 13 us, 2.6 TB/s with the
+// start and the sums across the cluster), with many by issuing their MMAs.
 struct ShrinkParams {
   Reqs q;
   int red;              // reduction length
+  int nrank;            // CTAs of a cluster
   int r, rN;            // rank, MMA columns (rank up to a multiple of 16)
   int f_bytes;          // shared-memory bytes of one F block
   int f_rows;           // rows of F's 2-D view per adapter
@@ -324,8 +336,8 @@ __global__ void __launch_bounds__(192) adapter_shrink_kernel(const __grid_consta
   int* off = reinterpret_cast<int*>(sums + p.rN * BM);
   int16_t* ad = reinterpret_cast<int16_t*>(off + p.q.num_seg + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int nrank = gridDim.x, rank = blockIdx.x;
-  const int m0 = blockIdx.y * BM, m1 = min(p.q.T, m0 + BM);
+  const int nrank = p.nrank, rank = (int)cluster_rank();
+  const int m0 = (int)(blockIdx.x / nrank) * BM, m1 = min(p.q.T, m0 + BM);
   const int nkb = p.red / BK;
   const int kb0 = (int)((long long)nkb * rank / nrank), kb1 = (int)((long long)nkb * (rank + 1) / nrank);
   auto load_x = [&](int kb, int xs) {
@@ -994,6 +1006,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
 // products are added in the epilogue.  An adapter's rows are those of all its
 // requests in order.  A run's last block may reach into the next request's
 // rows: those are overwritten with zeros in shared memory.
+//
+// Bound by reading x and dy once, 67 MB at 8192 x (2048 + 2048): 17 us, 3.9 TB/s
+// (tensor cores 9% busy; a CTA's ring waits for its loads).  Parts of 512 rows:
+// fewer leave more sums to add up, more leave SMs idle (128, 256 and 384 rows
+// were slower).  All three parts of u and v are taken: with two the gradients
+// were further from the exact ones than with products of fp32 tensors.
 struct GradParams {
   Reqs q;
   int K, N, r;
@@ -1370,6 +1388,7 @@ int run_shrink(const char* fn, const Reqs& q, const void* in, long long ld, cons
   ShrinkParams p{};
   p.q = q;
   p.red = red;
+  p.nrank = cs;
   p.r = r;
   p.rN = round_up(r, 16);
   p.f_bytes = kMN ? (r + 63) / 64 * CHUNK_BYTES : r * 128;
@@ -1395,7 +1414,7 @@ int run_shrink(const char* fn, const Reqs& q, const void* in, long long ld, cons
   p.status = status_word();
   // (an F block of r rows is read as rN: the last one reads into the sums, whose columns past r are not used)
   const size_t smem = (size_t)fixed + (size_t)p.f_stages * f_stage;
-  return launch_adapter(fn, kern, dim3(cs, tiles), 192, smem, cs, s, tx, tf, p);
+  return launch_adapter(fn, kern, dim3(cs * tiles), 192, smem, cs, s, tx, tf, p);
 }
 
 template <int BN, bool kMN, bool kSplit>
@@ -1516,7 +1535,7 @@ int check_adapter(const char* fn, const Reqs& q, int K, int N, int r, long long 
 
 size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 
-// Rows of one part of an adapter's gradient sum.
+// Rows of one part of an adapter's gradient sum (see adapter_grad_kernel).
 constexpr int kPartRows = 512;
 
 struct BwdLayout {

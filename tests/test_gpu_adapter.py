@@ -199,6 +199,24 @@ def test_more_than_2_31_outputs():
     assert m.moe_read_device_status(reset=True) == 0
 
 
+def test_more_row_tiles_than_a_grid_dimension():
+    """More than 65535 tiles of 128 rows: a few rows checked in float64."""
+    T, K, N, r, nA = 65535 * 128 + 11_521, 64, 64, 8, 2
+    d, c = make(1, K, N, r, nA, seed=7)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    c["x"] = torch.empty(T, K, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    offsets, which = [5, 6_000_000, T - 1], [1, 0]
+    y, hid = forward(c, offsets, which, T, K, N, r, nA)
+    c["dy"] = y
+    dx, _, _ = backward(c, hid, offsets, which, T, K, N, r, nA)
+    at = [0, 4, 5, 5_999_999, 6_000_000, 65535 * 128, T - 2, T - 1]
+    f = lambda v: v.double().cpu().numpy()  # noqa: E731
+    ref = ops_ref.adapter(f(c["x"][at]), *(d[k].double().numpy() for k in ("W", "A", "B", "scale")), [2, 4, 7], [1, 0], f(c["dy"][at]))
+    near(y[at], ref, "y", True)
+    near(dx[at], ref, "dx", True)
+    assert m.moe_read_device_status(reset=True) == 0
+
+
 def test_gradient_against_differences():
     """y is linear in x, in A and in B (each alone): a difference of the float64
     loss sum(y dy) over a step is its derivative up to rounding."""
