@@ -1375,9 +1375,15 @@ int run_shrink(const char* fn, const Reqs& q, const void* in, long long ld, cons
   static bool attr[64] = {};
   auto kern = adapter_shrink_kernel<kMN>;
   if (int rc = set_smem(reinterpret_cast<const void*>(kern), attr, fn)) return rc;
-  const int tiles = (q.T + BM - 1) / BM, nkb = red / BK;
+  const int tiles = (q.T + BM - 1) / BM, nkb = red / BK, sms = sm_count() > 0 ? sm_count() : 148;
+  const int rN = round_up(r, 16), f_bytes = kMN ? (r + 63) / 64 * CHUNK_BYTES : r * 128;
+  // as many slices as run at a time: two CTAs an SM where both fit (r = 64, of which one fits, with slices
+  // for two: 155 us instead of 144 for 8192 x 2048 x 2048 in both directions; 33.1 instead of 34.6 for the
+  // narrow product of 16384 x 2048 alone, whose 128 tiles leave SMs idle)
+  const int least = 1024 + 2 * kShrinkXBytes + rN * BM * 4 + (int)table_bytes(q.num_seg) + 2 * kShrinkK * f_bytes;
+  const bool two = least <= 110 * 1024;
   int cs = 1;
-  while (cs < 8 && cs * 2 <= nkb && tiles * cs * 2 <= 304) cs *= 2;
+  while (cs < 8 && cs * 2 <= nkb && tiles * cs * 2 <= (two ? 2 : 1) * sms) cs *= 2;
   CUtensorMap tx, tf;
   if (int rc = map2(&tx, in, red, q.T, ld, BK, BM)) return rc;
   if (kMN) {
@@ -1390,14 +1396,13 @@ int run_shrink(const char* fn, const Reqs& q, const void* in, long long ld, cons
   p.red = red;
   p.nrank = cs;
   p.r = r;
-  p.rN = round_up(r, 16);
-  p.f_bytes = kMN ? (r + 63) / 64 * CHUNK_BYTES : r * 128;
+  p.rN = rN;
+  p.f_bytes = f_bytes;
   p.f_rows = kMN ? red : r;
   // Tiles of many runs want many blocks of F in flight: as many as fit where a CTA has its SM alone.
   // Otherwise two CTAs share one, with two steps of x in flight each (three: one CTA an SM; 18 us instead
   // of 13 for 8192 x 2048).
-  const int sms = sm_count() > 0 ? sm_count() : 148;
-  const bool alone = tiles * cs <= sms;
+  const bool alone = !two || tiles * cs <= sms;
   // more runs than rows of tiles: several share a step of F, its barrier wait and its commit
   p.f_runs = q.num_seg <= 2 * tiles ? 1 : (kShrinkK * p.f_bytes <= 8192 ? 4 : (kShrinkK * p.f_bytes <= 16384 ? 2 : 1));
   const int f_stage = p.f_runs * kShrinkK * p.f_bytes;
