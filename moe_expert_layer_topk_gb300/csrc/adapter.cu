@@ -1273,8 +1273,6 @@ __global__ void __launch_bounds__(192) adapter_grad_kernel(const __grid_constant
 // order, zero for an adapter without rows, added to the old values when
 // accumulating.
 __global__ void __launch_bounds__(256) adapter_grad_sum_kernel(const GradParams p) {
-  pdl_wait();
-  pdl_trigger();
   extern __shared__ int tab[];
   int* off = tab;
   int16_t* ad = reinterpret_cast<int16_t*>(off + p.q.num_seg + 1);
@@ -1282,6 +1280,8 @@ __global__ void __launch_bounds__(256) adapter_grad_sum_kernel(const GradParams 
   int* first = rows + p.q.num_adapters;
   load_requests(p.q, off, ad, p.status);
   load_parts(p.q, off, ad, p.part_rows, rows, first);
+  pdl_wait();  // (the request table is older than the call's first kernel, which waited for it)
+  pdl_trigger();
   const int a = blockIdx.y;
   const int n = first[a + 1] - first[a];
   if (n == 1 && !p.accumulate) return;
