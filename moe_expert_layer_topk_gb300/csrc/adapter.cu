@@ -26,8 +26,9 @@
 //   517 rows, mixed, r = 64, 768 x 2048            22.9     the same
 //   16384 rows, 2048 x 4096                        164-180  tensor cores: 1.5 PFLOP/s of
 //                                                  the wide product's 0.28 TFLOP in 146
-//   8192 rows, 2048 x 2048, backward               122.5 with the forward: narrow 13 and
-//                                                  wide 44 each way, gradients 17 + 6
+//   8192 rows, 2048 x 2048, backward               117.7 with the forward: narrow 13 and
+//                                                  wide 44 each way, gradients 17 + 5, in part
+//                                                  beside them
 #include <cuda.h>
 
 #include "tc_common.cuh"
@@ -1004,7 +1005,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
 // tile is 128 rows of the output (columns of x or dy) times the hidden columns
 // of all parts, over at most part_rows of the adapter's rows; the parts'
 // products are added in the epilogue.  An adapter's rows are those of all its
-// requests in order.  A run's last block may reach into the next request's
+// requests in order, neighbouring ones as one run.  A run's last block may reach into the next request's
 // rows: those are overwritten with zeros in shared memory.
 //
 // Bound by reading x and dy once, 67 MB at 8192 x (2048 + 2048): 17 us, 3.9 TB/s
@@ -1038,45 +1039,87 @@ struct GradCtl {
   int abort_flag;
 };
 
-// Shared-memory table: rows of each adapter -> first part of each adapter
-// (first[num_adapters] = all parts).
-__device__ __forceinline__ void load_parts(const Reqs& q, const int* off, const int16_t* ad, int part_rows, int* rows, int* first) {
-  for (int a = threadIdx.x; a < q.num_adapters; a += blockDim.x) rows[a] = 0;
-  __syncthreads();
-  for (int s = threadIdx.x; s < q.num_seg; s += blockDim.x)
-    if (ad[s] >= 0 && off[s + 1] > off[s]) atomicAdd(&rows[ad[s]], off[s + 1] - off[s]);
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    int carry = 0;
-    for (int b = 0; b < q.num_adapters; b += 32) {
-      const int a = b + lane, n = a < q.num_adapters ? (rows[a] + part_rows - 1) / part_rows : 0;
-      int m = n;
+// Sums of a warp's values over all adapters, 32 at a time: v[a] becomes f(v[a]),
+// f(0) + ... + f(v[a]) or the sum before it; returns the whole.
+template <bool kBefore, class F>
+__device__ __forceinline__ int scan_adapters(int n, const int* v, int* out, F&& f) {
+  const int lane = threadIdx.x & 31;
+  int carry = 0;
+  for (int b = 0; b < n; b += 32) {
+    const int a = b + lane, x = a < n ? f(v[a]) : 0;
+    int m = x;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, m, d);
-        if (lane >= d) m += o;
-      }
-      if (a < q.num_adapters) first[a] = carry + m - n;
-      carry += __shfl_sync(0xffffffffu, m, 31);
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, m, d);
+      if (lane >= d) m += o;
     }
-    if (lane == 0) first[q.num_adapters] = carry;
+    if (a < n) out[a] = carry + m - (kBefore ? x : 0);
+    carry += __shfl_sync(0xffffffffu, m, 31);
+  }
+  return carry;
+}
+
+// Shared-memory tables (all threads call it): the rows of each adapter and from
+// them its first part, first[num_adapters] all parts.
+// kRuns: also its rows as runs, requests that follow one another with one adapter
+// taken together: list[begin[a]..begin[a + 1]) are a's, in row order, each its
+// first request and the one past its last (walking all requests for each tile made
+// the kernel's time grow with their number: 1000 requests over 48 adapters 637 us,
+// 345 with the runs).  They are counted, then placed from the last request back,
+// where the end of each is known.
+template <bool kRuns>
+__device__ __forceinline__ void load_parts(const Reqs& q, const int* off, const int16_t* ad, int part_rows, int* rows, int* first,
+                                           int* begin = nullptr, uint32_t* list = nullptr) {
+  for (int a = threadIdx.x; a < q.num_adapters; a += blockDim.x) {
+    rows[a] = 0;
+    if (kRuns) begin[a] = 0;
+  }
+  __syncthreads();
+  for (int s = threadIdx.x; s < q.num_seg; s += blockDim.x) {
+    const int a = ad[s];
+    if (a < 0) continue;
+    if (off[s + 1] > off[s]) atomicAdd(&rows[a], off[s + 1] - off[s]);
+    if (kRuns && (s == 0 || ad[s - 1] != a)) atomicAdd(&begin[a], 1);
+  }
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    const int parts = scan_adapters<true>(q.num_adapters, rows, first, [&](int n) { return (n + part_rows - 1) / part_rows; });
+    if (lane == 0) first[q.num_adapters] = parts;
+  }
+  if (kRuns && warp == 2) {
+    const int runs = scan_adapters<false>(q.num_adapters, begin, begin, [](int n) { return n; });  // where they end
+    if (lane == 0) begin[q.num_adapters] = runs;
+    __syncwarp();
+    int after = q.num_seg;  // the next request with another adapter
+    for (int b = (q.num_seg - 1) / 32 * 32; b >= 0; b -= 32) {
+      const int s = b + lane, a = s < q.num_seg ? ad[s] : -1;
+      const unsigned other = __ballot_sync(0xffffffffu, s < q.num_seg && (s == 0 || ad[s - 1] != a));
+      const bool start = ((other >> lane) & 1u) && a >= 0;
+      const unsigned above = lane == 31 ? 0u : 0xffffffffu << (lane + 1), later = other & above;
+      const unsigned peers = __match_any_sync(0xffffffffu, start ? a : -1 - lane);
+      if (start)
+        list[begin[a] - 1 - __popc(peers & above)] = (uint32_t)s | (uint32_t)(later ? b + __ffs(later) - 1 : after) << 16;
+      __syncwarp();
+      if (start && (peers & ((1u << lane) - 1u)) == 0) begin[a] -= __popc(peers);
+      __syncwarp();
+      if (other) after = b + __ffs(other) - 1;
+    }
   }
   __syncthreads();
 }
 
-// f(first row, valid rows <= 64) -> bool for the blocks of part `part` of adapter a.
+// f(first row, valid rows <= 64) -> bool for the blocks of part `part` of the adapter with runs [i0, i1).
 template <class F>
-__device__ __forceinline__ void for_each_block(const Reqs& q, const int* off, const int16_t* ad, int a, int part, int part_rows, F&& f) {
+__device__ __forceinline__ void for_each_block(const int* off, const uint32_t* list, int i0, int i1, int part, int part_rows, F&& f) {
   const long long lo = (long long)part * part_rows, hi = lo + part_rows;
-  long long at = 0;  // adapter rows before request s
-  for (int s = 0; s < q.num_seg && at < hi; ++s) {
-    if (ad[s] != a) continue;
-    const int n = off[s + 1] - off[s];
-    if (n <= 0) continue;
+  long long at = 0;  // adapter rows before this run
+  for (int i = i0; i < i1 && at < hi; ++i) {
+    const uint32_t run = list[i];
+    const int first = off[run & 0xffffu], n = off[run >> 16] - first;
     const int b = (int)max(lo - at, 0ll), e = (int)min(hi - at, (long long)n);
     for (int t = b; t < e; t += BK)
-      if (!f(off[s] + t, min(BK, e - t))) return;
+      if (!f(first + t, min(BK, e - t))) return;
     at += n;
   }
 }
@@ -1109,12 +1152,12 @@ __global__ void __launch_bounds__(192) adapter_grad_kernel(const __grid_constant
   int16_t* ad = reinterpret_cast<int16_t*>(off + p.q.num_seg + 1);
   int* rows = reinterpret_cast<int*>(ad + (p.q.num_seg + 1) / 2 * 2);
   int* first = rows + p.q.num_adapters;
+  int* begin = first + p.q.num_adapters + 1;
+  uint32_t* runs = reinterpret_cast<uint32_t*>(begin + p.q.num_adapters + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int bufs = hc <= 96 ? 2 : 1;
   const uint32_t cols = grad_tmem_cols(p.r);
-  load_requests(p.q, off, ad, p.status);
-  load_parts(p.q, off, ad, p.part_rows, rows, first);
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 160) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(smem_u32(&ctl.full[i]), 1);
       mbar_init(smem_u32(&ctl.empty[i]), 1);
@@ -1132,6 +1175,8 @@ __global__ void __launch_bounds__(192) adapter_grad_kernel(const __grid_constant
     prefetch_tmap(&tmV);
   }
   if (warp == 1) tmem_alloc_n<1>(smem_u32(&ctl.tmem_base), cols);
+  load_requests(p.q, off, ad, p.status);
+  load_parts<true>(p.q, off, ad, p.part_rows, rows, first, begin, runs);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1152,7 +1197,7 @@ __global__ void __launch_bounds__(192) adapter_grad_kernel(const __grid_constant
         const CUtensorMap* ml = is_a ? &tmX : &tmDy;
         const CUtensorMap* mr = is_a ? &tmU : &tmV;
         const int ck = (is_a ? mt : mt - p.tiles_a) * 2;
-        for_each_block(p.q, off, ad, a, part - first[a], p.part_rows, [&](int row, int) {
+        for_each_block(off, runs, begin[a], begin[a + 1], part - first[a], p.part_rows, [&](int row, int) {
           if (!(ok = wait_bar(smem_u32(&ctl.empty[st]), ph ^ 1u, &ctl.abort_flag, p.status))) return false;
           const uint32_t fb = smem_u32(&ctl.full[st]), sA = base + st * stage_bytes;
           mbar_arrive_expect_tx(fb, stage_bytes);
@@ -1176,7 +1221,7 @@ __global__ void __launch_bounds__(192) adapter_grad_kernel(const __grid_constant
       tc_fence_after();
       const uint32_t d = tmem + buf * (cols / bufs);
       uint32_t started = 0;
-      for_each_block(p.q, off, ad, a, part - first[a], p.part_rows, [&](int, int valid) {
+      for_each_block(off, runs, begin[a], begin[a + 1], part - first[a], p.part_rows, [&](int, int valid) {
         ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&ctl.full[st]), ph, &ctl.abort_flag, p.status));
         if (!ok) return false;
         const int steps = (valid + 15) / 16;
@@ -1279,7 +1324,7 @@ __global__ void __launch_bounds__(256) adapter_grad_sum_kernel(const GradParams 
   int* rows = reinterpret_cast<int*>(ad + (p.q.num_seg + 1) / 2 * 2);
   int* first = rows + p.q.num_adapters;
   load_requests(p.q, off, ad, p.status);
-  load_parts(p.q, off, ad, p.part_rows, rows, first);
+  load_parts<false>(p.q, off, ad, p.part_rows, rows, first);
   pdl_wait();  // (the request table is older than the call's first kernel, which waited for it)
   pdl_trigger();
   const int a = blockIdx.y;
@@ -1336,11 +1381,11 @@ int map_mn(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64
   return make_map(m, ptr, 3, d, s, b);
 }
 
-int set_smem(const void* kern, bool* done, const char* fn) {
+int set_smem(const void* kern, bool* done, const char* fn, size_t most = kAdapterSmem) {
   const int dev = current_device();
   if (dev < 0) return fail(MOE_ERR_CUDA, "%s: no current CUDA device", fn);
   if (done[dev]) return MOE_OK;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAdapterSmem);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
   done[dev] = true;
   return MOE_OK;
@@ -1652,21 +1697,21 @@ int moe_adapter_linear_bwd(const void* dy, long long lddy, const void* x, long l
   p.stages = nck == 1 ? 4 : (nck == 2 ? 3 : (nck == 3 ? 5 : 3));
   p.status = status_word();
   static bool attr[64] = {};
-  if (int rc = set_smem(reinterpret_cast<const void*>(adapter_grad_kernel), attr, fn)) return rc;
+  if (int rc = set_smem(reinterpret_cast<const void*>(adapter_grad_kernel), attr, fn, kSmemMax - 1024)) return rc;
   CUtensorMap tx, tu, td, tv;
   if (int rc = map_mn(&tx, x, K, T, ldx, 2)) return rc;
   if (int rc = map_mn(&tu, u, hp, T, hp, nck)) return rc;
   if (int rc = map_mn(&td, dy, N, T, lddy, 2)) return rc;
   if (int rc = map_mn(&tv, hidden, hp, T, hp, nck)) return rc;
   const size_t table = table_bytes(num_seg) + sizeof(int) * (size_t)(2 * num_adapters + 2);
-  const size_t smem = 1024 + (size_t)p.stages * (BM * BK * 2 + nck * CHUNK_BYTES) + table;
+  const size_t smem = 1024 + (size_t)p.stages * (BM * BK * 2 + nck * CHUNK_BYTES) + table + sizeof(int) * (size_t)(num_adapters + 1 + num_seg);
   const int per_sm = nck <= 2 ? 2 : 1;
   const long long most = ((long long)T / kPartRows + num_seg) * (p.tiles_a + p.tiles_b);
   const int sms = sm_count() > 0 ? sm_count() : 148;
   const int grid = (int)(most < (long long)sms * per_sm ? most : (long long)sms * per_sm);
   if (int rc = launch_adapter(fn, adapter_grad_kernel, dim3(grid), 192, smem, 0, s, tx, tu, td, tv, p)) return rc;
   const size_t vec = (size_t)r * (K + N) / 4;
-  const int gx = (int)((vec + 255) / 256 < 64 ? (vec + 255) / 256 : 64);
+  const int gx = (int)((vec + 255) / 256 < 256 ? (vec + 255) / 256 : 256);
   return launch_adapter(fn, adapter_grad_sum_kernel, dim3(gx, num_adapters), 256, table, 0, s, p);
 }
 

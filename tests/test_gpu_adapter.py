@@ -131,6 +131,22 @@ def test_every_row_its_own_request():
         near(y, ref, "y", True)
 
 
+@pytest.mark.parametrize("T,n,r,nA,same", [(1300, 1024, 64, 1024, 0), (3000, 1000, 16, 48, 0), (3000, 1000, 40, 1, 1), (900, 70, 128, 5, 6)])
+def test_gradients_of_many_requests(T, n, r, nA, same):
+    """The most requests and adapters of a call; neighbours with one adapter (in groups of `same`), empty requests between."""
+    K, N = 64, 128
+    d, c = make(T, K, N, r, nA, seed=n + nA, dy=True)
+    offsets, which = requests(T, n, nA, seed=n)
+    if same:
+        which = [which[i // same * same] % nA if i % 11 else which[i] for i in range(n)]
+    ref = ops_ref.adapter(*(d[k].double().numpy() for k in ("x", "W", "A", "B", "scale")), offsets, which, d["dy"].double().numpy())
+    y, hid = forward(c, offsets, which, T, K, N, r, nA)
+    dx, dA, dB = backward(c, hid, offsets, which, T, K, N, r, nA)
+    for got, name, bf16 in ((y, "y", True), (dx, "dx", True), (dA, "dA", False), (dB, "dB", False)):
+        near(got, ref, name, bf16)
+    assert m.moe_read_device_status(reset=True) == 0
+
+
 def test_no_requests_no_adapters_no_scale():
     T, K, N, r, nA = 150, 192, 128, 16, 2
     d, c = make(T, K, N, r, nA, dy=True)
