@@ -515,12 +515,12 @@ int moe_combine_dropout_bwd(const void* dy, const void* y_perm, const float* top
  * W bf16 [N,K]; A bf16 [num_adapters,r,K]; B bf16 [num_adapters,N,r]; scale
  * fp32 [num_adapters] or NULL (1).  x, y bf16 with row strides ldx >= K,
  * ldy >= N (elements, multiples of 8).  hidden receives v, each fp32 value as
- * three bf16 parts that add up to it, for the backward; its layout is the
- * library's own, moe_adapter_hidden_size(T, r) bytes.  y takes two of the
- * parts (16 bits).  y may not overlap x.
+ * three bf16 parts that add up to it, for y and for the backward; its layout
+ * is the library's own, moe_adapter_hidden_size(T, r) bytes.  y may not
+ * overlap x.
  *
  * moe_adapter_linear_bwd, W frozen:
- *   u[t]  = scale[a] B[a]^T dy[t]  (three bf16 parts; dx takes two)
+ *   u[t]  = scale[a] B[a]^T dy[t]  (kept as v is)
  *   dx[t] = W^T dy[t] + A[a]^T u[t]                                      -> bf16 [T,K]
  *   dA[a] = sum over a's rows of u[t] x[t]^T     fp32 [num_adapters,r,K]
  *   dB[a] = sum over a's rows of dy[t] v[t]^T    fp32 [num_adapters,N,r]

@@ -11,8 +11,7 @@
 // bound by reading x or dy) writes its fp32 result as three bf16 parts whose
 // sum is that value (8 bits each), so the products that take it stay on the
 // tensor cores without losing what the first one computed: the gradients of
-// A and B, kept in fp32, take all three, the wide product, rounded to bf16 at
-// its end, the first two (16 bits).  The wide one appends the
+// A and B and the wide product take all three.  The wide one appends the
 // adapter to the shared projection's reduction: after the W blocks, the same
 // accumulator tile takes v_t's parts times B_a for every run of rows with one
 // adapter, with the tile's other rows switched off by the MMA's lane mask
@@ -38,20 +37,21 @@ namespace tc {
 namespace {
 
 constexpr int kPlanes = 3;        // bf16 parts of v, u
-constexpr int kWidePlanes = 2;    // of them in the wide product
 constexpr int kMaxRank = 128;
 constexpr int kMaxAdapters = 1024;
 
 __host__ __device__ constexpr int round_up(int v, int to) { return (v + to - 1) / to * to; }
-// Columns of one part in the hidden tensor: whole 16-wide MMA steps when the
-// wide product's parts fit one 64-column block, else whole 64-column blocks.
-__host__ __device__ constexpr int plane_cols(int r) {
-  return kWidePlanes * round_up(r, 16) <= 64 ? round_up(r, 16) : round_up(r, 64);
-}
+// Columns of one part in the hidden tensor: whole 16-wide MMA steps when all
+// parts fit two 64-column blocks (and no part crosses from one to the next),
+// else whole 64-column blocks.
+__host__ __device__ constexpr bool parts_packed(int r) { return r <= 32; }
+__host__ __device__ constexpr int plane_cols(int r) { return parts_packed(r) ? round_up(r, 16) : round_up(r, 64); }
 // Columns of all parts, and of a row of the hidden tensor (whole 64-column
 // blocks; what pads a row is never used).
 __host__ __device__ constexpr int hidden_cols(int r) { return kPlanes * plane_cols(r); }
 __host__ __device__ constexpr int hidden_pitch(int r) { return round_up(hidden_cols(r), 64); }
+// 64-column blocks that hold the parts of up to 64 ranks.
+__host__ __device__ constexpr int hidden_blocks(int r) { return parts_packed(r) ? hidden_pitch(r) / 64 : kPlanes; }
 
 // ------------------------------------------------------------ request table
 
@@ -650,18 +650,23 @@ struct WideCfg {
   static constexpr int CTAS = BN == 256 ? 2 : 1;
   static constexpr int B_BYTES = BN / CTAS * BK * 2;       // a CTA's share of a block of W
   static constexpr int WB = BN / CTAS > 64 && CTAS == 1 ? BN : 64;  // W rows (columns) of one TMA box
-  static constexpr int VBUF = 2;                  // hidden blocks held at a time
   static constexpr int EP_BYTES = kSplit ? 0 : 4 * EP_SLOTS * EP_BOX_BYTES;
-  static constexpr int STAGES = BN == 64 ? 6 : 5;
-  static constexpr size_t smem(int a_rows, int stages) {
+  // three blocks of hidden cost the wider tiles' ring a stage
+  static constexpr int stages(int vblocks) { return BN == 64 ? 6 : (vblocks <= 2 ? 5 : 4); }
+  static constexpr size_t smem(int a_rows, int vblocks, int stages) {
     // the MMA reads 128 rows from a hidden block's start, however few it holds
-    return 1024 + (size_t)stages * (a_rows * BK * 2 + B_BYTES) + (size_t)((VBUF - 1) * a_rows + BM) * BK * 2 + EP_BYTES +
+    return 1024 + (size_t)stages * (a_rows * BK * 2 + B_BYTES) + (size_t)((vblocks - 1) * a_rows + BM) * BK * 2 + EP_BYTES +
            table_bytes(kMaxSegments);
   }
+  static constexpr bool fits(int vblocks);
 };
 constexpr size_t kAdapterSmem = kSmemMax - 4096;  // dynamic; the rest is for static tables
-static_assert(WideCfg<256, false>::smem(BM, 5) <= kAdapterSmem && WideCfg<128, false>::smem(BM, 5) <= kAdapterSmem &&
-                  WideCfg<64, false>::smem(BM, 6) <= kAdapterSmem,
+template <int BN, bool kSplit>
+constexpr bool WideCfg<BN, kSplit>::fits(int vblocks) {
+  return smem(BM, vblocks, stages(vblocks)) <= kAdapterSmem;
+}
+static_assert(WideCfg<256, false>::fits(2) && WideCfg<256, false>::fits(3) && WideCfg<128, false>::fits(2) &&
+                  WideCfg<128, false>::fits(3) && WideCfg<64, false>::fits(3) && WideCfg<64, true>::fits(3),
               "shared memory budget exceeded");
 
 struct WideCtl {
@@ -690,10 +695,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
   const uint32_t base = align1k(smem_u32(smem_raw));
   uint8_t* bytes = smem_raw + (base - smem_u32(smem_raw));
   const int a_bytes = kSplit ? p.a_rows * (BK * 2) : BM * BK * 2;
-  const int nst = kSplit ? p.stages : C::STAGES;
+  const int nst = p.stages;
   const int stage_bytes = a_bytes + C::B_BYTES;
   const uint32_t sV = base + nst * stage_bytes;
-  uint8_t* ep = bytes + (size_t)nst * stage_bytes + (C::VBUF - 1) * a_bytes + BM * BK * 2;
+  uint8_t* ep = bytes + (size_t)nst * stage_bytes + (hidden_blocks(p.r) - 1) * a_bytes + BM * BK * 2;
   int* off = reinterpret_cast<int*>(ep + C::EP_BYTES);
   int16_t* ad = reinterpret_cast<int16_t*>(off + p.q.num_seg + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -740,13 +745,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
   const int nkb = p.red / BK;
   const int kb0 = kSplit ? (int)((long long)nkb * rank / nrank) : 0;
   const int kb1 = kSplit ? (int)((long long)nkb * (rank + 1) / nrank) : nkb;
-  // Passes: 64 ranks of F at a time, times two parts of hidden, which share one
-  // 64-column block up to r = 32 and are two blocks beyond.
+  // Passes: 64 ranks of F at a time, with the blocks that hold hidden's three
+  // parts of them.
   const int rp = plane_cols(p.r);
-  const bool one_block = kWidePlanes * rp <= 64;
-  const int vset = one_block ? 1 : kWidePlanes;
+  const bool packed = parts_packed(p.r);
   const int passes = (p.r + 63) / 64;
-  static_assert(C::VBUF == kWidePlanes, "room for both parts of hidden");
+  const int vblocks = hidden_blocks(p.r), vcol = packed ? 64 : rp;  // columns from one block to the next
   // A stage holds F's blocks of several runs: one in W's place, the others in in's
   // (a barrier wait and a commit a run cost about what its MMAs do).
   const int per_stage = 1 + a_bytes / C::B_BYTES;
@@ -842,9 +846,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
           for (int ps = 0; ps < passes; ++ps, ph ^= 1u) {
             if (!(ok = wait_bar(smem_u32(&ctl.vempty), ph ^ 1u, &ctl.abort_flag, p.status))) break;
             const uint32_t fb = at_leader(smem_u32(&ctl.vfull));
-            if (leader) mbar_arrive_expect_tx(smem_u32(&ctl.vfull), CTAS * vset * a_bytes);
-            for (int v = 0; v < vset; ++v)
-              tma_load<CTAS>(sV + v * a_bytes, &tmH, fb, v * rp + ps * 64, t.m0 + pair_rank * BM);
+            if (leader) mbar_arrive_expect_tx(smem_u32(&ctl.vfull), CTAS * vblocks * a_bytes);
+            for (int v = 0; v < vblocks; ++v)
+              tma_load<CTAS>(sV + v * a_bytes, &tmH, fb, v * vcol + ps * 64, t.m0 + pair_rank * BM);
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -888,8 +892,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
           for (int ps = 0; ok && n > r0 && ps < passes; ++ps, vph ^= 1u) {
             if (!(ok = wait_bar(smem_u32(&ctl.vfull), vph, &ctl.abort_flag, p.status))) break;
             const int steps = min(4, (p.r - ps * 64 + 15) / 16);  // 16-wide steps of this block of F
-            const int pstep = one_block ? rp * 2 : a_bytes;        // bytes from one part of hidden to the next
+            // where the parts of hidden start, in the descriptors' 16-byte units
             const uint64_t vd = sdesc(sV, 16, 1024);
+            const uint64_t vp[kPlanes] = {vd, vd + (uint64_t)((packed ? rp * 2 : a_bytes) >> 4),
+                                          vd + (uint64_t)((packed ? (rp == 16 ? 64 : a_bytes) : 2 * a_bytes) >> 4)};
             for (int i = r0; i < n; i += dr * per_stage) {
               if (!(ok = wait_bar(smem_u32(&ctl.full[st]), ph, &ctl.abort_flag, p.status))) break;
               tc_fence_after();
@@ -904,8 +910,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) adapter_wide_kernel(const __g
                 for (int kk = 0; kk < BK / 16; ++kk) {
                   if (kk >= steps) break;
 #pragma unroll
-                  for (int pl = 0; pl < kWidePlanes; ++pl)
-                    mma_lanes(d, vd + (uint64_t)(pl * (pstep >> 4) + kk * 2), bd + (uint64_t)(kk * (kMN ? 128 : 2)), idesc, 1u, m);
+                  for (int pl = 0; pl < kPlanes; ++pl)
+                    mma_lanes(d, vp[pl] + (uint64_t)(kk * 2), bd + (uint64_t)(kk * (kMN ? 128 : 2)), idesc, 1u, m);
                 }
               }
               mma_commit_to<CTAS>(smem_u32(&ctl.empty[st]));
@@ -1517,14 +1523,15 @@ int run_wide_bn(const char* fn, const Reqs& q, const void* in, long long ld, con
   p.out = static_cast<__nv_bfloat16*>(out);
   p.ldo = ldo;
   p.status = status_word();
-  p.stages = C::STAGES;
+  const int vblocks = hidden_blocks(r);
+  p.stages = C::stages(vblocks);
   if (kSplit) {
     // a slice's blocks all in flight where they fit; four hold the accumulator afterwards
-    while (p.stages < kWideStagesMax && C::smem(p.a_rows, p.stages + 1) <= kAdapterSmem) ++p.stages;
-    return launch_adapter(fn, kern, dim3(nrank, p.n_tiles, rows), kWideThreads, C::smem(p.a_rows, p.stages), nrank, s, tx, tw,
-                          th, tf, to, p);
+    while (p.stages < kWideStagesMax && C::smem(p.a_rows, vblocks, p.stages + 1) <= kAdapterSmem) ++p.stages;
+    return launch_adapter(fn, kern, dim3(nrank, p.n_tiles, rows), kWideThreads, C::smem(p.a_rows, vblocks, p.stages), nrank, s, tx,
+                          tw, th, tf, to, p);
   }
-  return launch_adapter(fn, kern, dim3((p.units < places ? p.units : places) * C::CTAS), kWideThreads, C::smem(BM, p.stages),
+  return launch_adapter(fn, kern, dim3((p.units < places ? p.units : places) * C::CTAS), kWideThreads, C::smem(BM, vblocks, p.stages),
                         C::CTAS == 2 ? 2 : 0, s, tx, tw, th, tf,
                         to, p);
 }

@@ -108,3 +108,38 @@ def test_gradients_keep_every_bit_of_u_and_v(r):
     wantB = s[1] * f(d["dy"])[25][:, None] * f(d["A"])[1, :, k0][None, :]
     for got, want in ((dA[0], wantA), (dB[1], wantB)):
         assert np.all(np.abs(got.double().cpu().numpy() - want) <= 2.0 ** -22 * np.abs(want))
+
+
+@pytest.mark.parametrize("T", [4, 40, 517, 1333, 3001])
+@pytest.mark.parametrize("r", [8, 16, 32, 64, 128])
+def test_outputs_keep_every_bit_of_u_and_v(T, r):
+    """W x takes the first 16 bits of v = s away again: what is left of y is s
+    less its two largest bf16 parts, a bf16 number itself, and every step to
+    it is exact in fp32 (2^-8 of it allowed).  The same for dx with u."""
+    K, N, nA, j = 1280, 2048 if T > 1500 else 1024, 2, r - 1
+    _, c = make(1, K, N, r, nA, dy=True)
+    s = np.float32(1.2345678)
+    parts, rest = [], float(s)
+    for _ in range(2):
+        parts.append(float(torch.tensor(rest).bfloat16()))
+        rest -= parts[-1]
+    assert rest != 0 and abs(rest) <= 2.0 ** -16 and float(torch.tensor(rest).bfloat16()) == rest
+    z = lambda *shape: torch.zeros(*shape, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    c.update(x=z(T, K), dy=z(T, N), W=z(N, K), A=z(nA, r, K), B=z(nA, N, r), scale=torch.full((nA,), float(s), device="cuda"))
+    half = T // 2
+    offsets, which = [0, half, T], [1, -1]
+    c["x"][:, [70, 700]] = 1
+    c["W"][:, 70], c["W"][:, 700] = -parts[0], -parts[1]
+    c["A"][1, j, 70], c["B"][1, :, j] = 1, 1
+    y, hid = forward(c, offsets, which, T, K, N, r, nA)
+    assert (y[:half].double() - rest).abs().max() <= 2.0 ** -8 * abs(rest)
+    assert torch.all(y[half:] == torch.tensor(-(parts[0] + parts[1])).bfloat16())
+    c["dy"][:, [5, 600]] = 1
+    c["W"].zero_()
+    c["W"][5], c["W"][600] = -parts[0], -parts[1]
+    c["B"].zero_()
+    c["A"].zero_()
+    c["B"][1, 5, j], c["A"][1, j] = 1, 1
+    dx, _, _ = backward(c, hid, offsets, which, T, K, N, r, nA)
+    assert (dx[:half].double() - rest).abs().max() <= 2.0 ** -8 * abs(rest)
+    assert torch.all(dx[half:] == torch.tensor(-(parts[0] + parts[1])).bfloat16())
