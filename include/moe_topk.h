@@ -493,6 +493,7 @@ int moe_balance_loss_bwd(const float* logits, const uint8_t* mask, int T, int E,
  * moe_combine_dropout_bwd: its backward, with g = D(dy) in fp32:
  *   dy_perm[row(t,j)] = topk_w[t,j] g[t]                      -> bf16
  *   d_w[t,j]          = sum_h g[t,h] y_perm[row(t,j),h]       (fp32)
+ *   (over the h that stay: what y_perm holds under the mask does not matter)
  *   (the residual's gradient is dy). */
 int moe_dropout(const void* x, const void* residual, long long n, int fp32, double p, const int64_t* rng, void* out,
                 void* stream);

@@ -241,9 +241,37 @@ __device__ __forceinline__ uint4 select8(uint4 v, const uint4& bits, uint32_t dr
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// A warp's sum of dy . y_perm over the elements that stay, both rows' dropped
+// elements selected away: added up as the kernel below does.
+__device__ __noinline__ float dot_of_kept(const uint4* dy, const uint4* y, const unsigned long long* rng, uint32_t drop,
+                                          unsigned long long block0, int nvec) {
+  const PhiloxKey key = load_key(rng);
+  float sum = 0.f;
+#pragma unroll 1
+  for (int v0 = 0; v0 < nvec; v0 += 256) {
+    float p = 0.f;
+#pragma unroll 1
+    for (int v = v0 + (threadIdx.x & 31); v < min(nvec, v0 + 256); v += 32) {
+      const uint4 bits = philox8(key, block0 + v);
+      float g[8], yv[8];
+      unpack8(select8(__ldg(dy + v), bits, drop), g);
+      unpack8(select8(__ldg(y + v), bits, drop), yv);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p = __fmaf_rn(g[i], yv[i], p);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) p += __shfl_xor_sync(0xffffffffu, p, off);
+    sum += p;
+  }
+  return sum;
+}
+
 // Warp per token: the token's dy row with its dropped elements zeroed sits in
 // registers; for every slot the warp writes dy_perm[row] = (w scale) dy[t] and
-// reduces dy[t] . y_perm[row]; the scale is applied to the sum once.
+// reduces dy[t] . y_perm[row]; the scale is applied to the sum once.  A dropped
+// element of y_perm meets a zero of dy there, which an infinity or a NaN turns
+// into NaN: a sum that is not finite is taken again over the elements that stay
+// (selecting them away each time cost 6% at 2048 columns, 26% at 512).
 __global__ void __launch_bounds__(64) combine_dropout_bwd_kernel(
     const __nv_bfloat16* __restrict__ dy, const __nv_bfloat16* __restrict__ y_perm,
     const float* __restrict__ topk_w, const int32_t* __restrict__ row_of_slot, int T, int H, int k, int R,
@@ -304,6 +332,12 @@ __global__ void __launch_bounds__(64) combine_dropout_bwd_kernel(
         for (int off = 16; off > 0; off >>= 1) p += __shfl_xor_sync(0xffffffffu, p, off);
         if (lane == j) my_dw += p;
       }
+    }
+    for (unsigned again = __ballot_sync(0xffffffffu, !isfinite(my_dw)); again; again &= again - 1) {
+      const int j = __ffs(again) - 1, row = __shfl_sync(0xffffffffu, my_row, j);
+      const float p = dot_of_kept(reinterpret_cast<const uint4*>(dy + (size_t)t * H), reinterpret_cast<const uint4*>(y_perm + (size_t)row * H),
+                                  rng, dp.drop, (unsigned long long)t * nvec, nvec);
+      if (lane == j) my_dw = p;
     }
     if (lane < k) d_w[(size_t)t * k + lane] = my_dw * dp.scale;
   }
