@@ -725,20 +725,27 @@ Layout layout(int T, int E, int num_seq) {
 
 template <bool kSum, bool kGrad, bool kInline>
 struct Main {
+  // nv: values a lane holds
+  static constexpr size_t smem_bytes(int num_seq, int E, int nv) {
+    return sizeof(int) * (((2 * num_seq + 5) & ~3) + ((E + 3) & ~3)) + (kSum ? sizeof(float) * (kWarps * (E + 1) + nv * kThreads) : 0);
+  }
   template <int LPT, int VEC, int NQ, bool kFull>
   static int go(const char* fn, int grid, const Tokens& tk, const float* logits, const int32_t* idx, const Work& w, const Out& o,
                 const Grad& gr, cudaStream_t s) {
-    const size_t smem = sizeof(int) * (((2 * tk.num_seq + 5) & ~3) + ((tk.E + 3) & ~3)) + (kSum ? sizeof(float) * (kWarps * (tk.E + 1) + VEC * NQ * kThreads) : 0);
+    const size_t smem = smem_bytes(tk.num_seq, tk.E, VEC * NQ);
     auto kern = balance_main_kernel<LPT, VEC, NQ, kFull, kSum, kGrad, kInline>;
-    if (smem > 48 * 1024) {
-      static bool set[64] = {};
-      const int dev = current_device();
-      if (dev < 0) return fail(MOE_ERR_CUDA, "%s: no current CUDA device", fn);
-      if (!set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-        if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
-        set[dev] = true;
-      }
+    // Asked for once per device whatever this call's size: beside the kernel's
+    // static variables even 48 KB of dynamic shared memory are more than a launch
+    // has unasked.  The most that an accepted shape takes is below it.
+    constexpr size_t kMost = 160 * 1024;
+    static_assert(smem_bytes(kMaxSeq, kMaxExperts, VEC * NQ) <= kMost, "shared memory limit exceeded");
+    static bool set[64] = {};
+    const int dev = current_device();
+    if (dev < 0) return fail(MOE_ERR_CUDA, "%s: no current CUDA device", fn);
+    if (!set[dev]) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
+      if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+      set[dev] = true;
     }
     launch_pdl(kern, grid, kThreads, smem, s, tk, logits, idx, w, o, gr, status_word());
     return check_launch(fn, "main kernel");
