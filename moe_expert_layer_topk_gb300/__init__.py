@@ -116,13 +116,16 @@ def lib(path: Path | str | None = None) -> ctypes.CDLL:
             raise RuntimeError(f"CUDA library {p} is not built: run "
                                f"`python -c 'import __graft_entry__ as g; g.build()'`")
         L = ctypes.CDLL(str(p))
+        version = getattr(L, "moe_abi_version", None)
+        if version is None or version() != ABI_VERSION:
+            raise RuntimeError(f"CUDA library {p} has ABI version {version and version()}, this binding "
+                               f"expects {ABI_VERSION}: rebuild it")
         for name, (args, res) in ENTRY_POINTS.items():
-            f = getattr(L, name)
+            f = getattr(L, name, None)
+            if f is None:  # added calls leave the version as it is
+                raise RuntimeError(f"CUDA library {p} has no {name}, it is older than this binding: rebuild it")
             f.argtypes = args
             f.restype = res
-        if L.moe_abi_version() != ABI_VERSION:
-            raise RuntimeError(f"CUDA library {p} has ABI version {L.moe_abi_version()}, this binding "
-                               f"expects {ABI_VERSION}: rebuild it")
         _lib = L
     return _lib
 
