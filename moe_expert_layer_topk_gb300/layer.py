@@ -223,7 +223,8 @@ class MoELayer:
             self.combine(stream, y, residual)
         return self.y if y is None else y
 
-    def capture_forward(self, x, Wr, bias, Wg, Wu, Wd) -> "torch.cuda.CUDAGraph":
+    def capture_forward(self, x, Wr, bias, Wg, Wu, Wd, *, residual=None, mask=None,
+                        seg_offsets=None) -> "torch.cuda.CUDAGraph":
         """Record forward() on these tensors as a CUDA graph and return it.
 
         `graph.replay()` then re-runs the whole forward (all its kernels,
@@ -232,11 +233,12 @@ class MoELayer:
         host issuing one call per kernel.  One forward runs first, outside
         the capture, so that each call's first-use set-up (kernel
         attributes, the device status word) is done before it."""
-        self.forward(x, Wr, bias, Wg, Wu, Wd)
+        opts = dict(residual=residual, mask=mask, seg_offsets=seg_offsets)
+        self.forward(x, Wr, bias, Wg, Wu, Wd, **opts)
         torch.cuda.synchronize(self.y.device)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            self.forward(x, Wr, bias, Wg, Wu, Wd)
+            self.forward(x, Wr, bias, Wg, Wu, Wd, **opts)
         return graph
 
     # --------------------------------------------------------------- backward
