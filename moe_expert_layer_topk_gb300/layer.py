@@ -190,9 +190,18 @@ class MoELayer:
                          self.seq_counts, self.seq_tokens, self.prob_sum, self.loss, self.balance_coef, self.z_coef,
                          self.dlogits, self.ws_balance, stream)
 
-    def advance_rng(self):
-        """Move the dropout's offset past one forward's counters (on the current stream)."""
-        self.rng[1] += self.T * self.H // 8
+    def advance_rng(self, stream=None):
+        """Move the dropout's offset past one forward's counters, on `stream` like the other
+        calls (a layer without dropout has none)."""
+        if not self.dropout:
+            return
+        if stream is None:
+            self.rng[1] += self.T * self.H // 8
+            return
+        handle = getattr(stream, "cuda_stream", stream)
+        dev = self.rng.device
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle, dev) if handle else torch.cuda.default_stream(dev)):
+            self.rng[1] += self.T * self.H // 8
 
     def combine(self, stream=None, y=None, residual=None):
         if self.dropout or residual is not None:

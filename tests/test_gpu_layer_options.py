@@ -1,8 +1,10 @@
-"""The layer's options through its own calls: recorded as a graph."""
+"""The layer's options through its own calls: recorded as a graph, on another
+stream."""
 import pytest
 import torch
 
 import moe_expert_layer_topk_gb300 as m
+import ops_ref
 from gpu_util import inputs, to_dev
 
 pytestmark = pytest.mark.gpu
@@ -58,3 +60,41 @@ def test_graph_of_a_residual_without_dropout():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(L.y, M.forward(g["x"], *weights(g), residual=opts["residual"]))
+
+
+def test_advance_rng_without_dropout_is_nothing():
+    _, g = parts()
+    L = m.MoELayer(T, H, I, E, k, balance_coef=0.5)
+    L.advance_rng()
+    y = L.forward(g["x"], *weights(g)).clone()
+    L.advance_rng()
+    assert torch.equal(y, L.forward(g["x"], *weights(g)))
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_advance_rng_on_the_calls_stream(raw):
+    """Ordered after the work of that stream, not of the current one: a forward
+    that a long kernel holds up still takes the words it was given."""
+    opts, g = parts()
+    L = layer()
+    want0 = torch.from_numpy(ops_ref.keep(99, 0, 0, T * H, 0.25).reshape(T, H)).cuda()
+    want1 = torch.from_numpy(ops_ref.keep(99, T * H // 8, 0, T * H, 0.25).reshape(T, H)).cuda()
+    opts["residual"].zero_()
+    L.forward(g["x"], *weights(g), **opts)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    big = torch.randn(4096, 4096, device="cuda")
+    out = torch.empty_like(big)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(20):
+            torch.mm(big, big, out=out)
+    handle = s.cuda_stream if raw else s
+    y0, y1 = torch.empty_like(L.y), torch.empty_like(L.y)
+    L.forward(g["x"], *weights(g), handle, y0, **opts)
+    L.advance_rng(handle)
+    L.forward(g["x"], *weights(g), handle, y1, **opts)
+    s.synchronize()
+    assert not y0[~want0].any() and not y1[~want1].any()
+    assert y0[want0].ne(0).float().mean() > 0.9 and y1[want1].ne(0).float().mean() > 0.9
+    assert L.rng.tolist() == [99, T * H // 8]
