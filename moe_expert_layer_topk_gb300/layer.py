@@ -11,7 +11,8 @@ from __future__ import annotations
 import torch
 
 from . import (moe_adapter_hidden_size, moe_adapter_linear, moe_adapter_linear_bwd,
-               moe_adapter_linear_bwd_workspace_size, moe_balance_loss, moe_balance_loss_workspace_size, moe_combine, moe_combine_bwd,
+               moe_adapter_linear_bwd_workspace_size, moe_balance_loss, moe_balance_loss_bwd, moe_balance_loss_workspace_size,
+               moe_combine, moe_combine_bwd,
                moe_combine_dropout, moe_combine_dropout_bwd, moe_dispatch_bwd, moe_dispatch_chunked,
                moe_dispatch_e4m3_chunked, moe_grouped_gemm_bwd_workspace_size,
                moe_grouped_gemm_down, moe_grouped_gemm_down_bwd, moe_grouped_gemm_down_combine,
@@ -51,7 +52,8 @@ class MoELayer:
     the backward adds to the router's (moe_balance_loss).  `sequences`
     packed sequences of the T tokens, told apart by the forward's
     seg_offsets, are each balanced on their own; tokens whose mask byte is 0
-    take no part in the two losses.
+    take no part in the two losses.  The backward's dloss scales the two
+    gradients.
 
     dropout (training): y = residual + D(combined rows) with the
     counter-based dropout of moe_combine_dropout; the backward computes the
@@ -81,6 +83,7 @@ class MoELayer:
         self.balance_coef, self.z_coef, self.sequences, self.dropout = balance_coef, z_coef, sequences, dropout
         self.balanced = bool(balance_coef or z_coef)
         self._x = None
+        self._upstream = False  # whether dlogits holds a backward's dloss
         self._side = None  # side stream of the backward's tail (created on first use)
         dev = torch.device(device)
         i32, f32, bf = torch.int32, torch.float32, torch.bfloat16
@@ -189,6 +192,7 @@ class MoELayer:
         moe_balance_loss(self.logits, self.topk_idx, mask, self.T, self.E, self.k, self.sequences, seg_offsets,
                          self.seq_counts, self.seq_tokens, self.prob_sum, self.loss, self.balance_coef, self.z_coef,
                          self.dlogits, self.ws_balance, stream)
+        self._losses_of, self._upstream = (mask, seg_offsets), False
 
     def advance_rng(self, stream=None):
         """Move the dropout's offset past one forward's counters, on `stream` like the other
@@ -258,8 +262,13 @@ class MoELayer:
     TAIL_SMS = 16
 
     def backward(self, dy, x, Wr, Wg, Wu, Wd, accumulate: bool = False, stream=None, dx=None,
-                 overlap: bool = True):
+                 overlap: bool = True, dloss=None):
         """dx: optional bf16 [T,H] output tensor (default: the layer's own).
+
+        dloss: fp32 [2] on the device, the upstream gradients of the two
+        router losses (loss scaling, the weight of a micro-batch; default
+        1), which balance_coef and z_coef are multiplied by; the forward's
+        mask and seg_offsets have to hold what they held then.
 
         overlap: run the dispatch and router backward on a side stream beside
         the gate/up weight gradient (which then leaves TAIL_SMS SMs free);
@@ -268,6 +277,13 @@ class MoELayer:
         assert self.training, "layer was built without backward buffers"
         dx = self.dx if dx is None else dx
         T, H, I, E, k, R = self.T, self.H, self.I, self.E, self.k, self.R
+        if dloss is not None and not self.balanced:
+            raise ValueError("dloss belongs to a layer with a balance loss or a z-loss")
+        if self.balanced and (dloss is not None or self._upstream):  # else dlogits is the forward's
+            mask, seg_offsets = self._losses_of
+            moe_balance_loss_bwd(self.logits, mask, T, E, k, self.sequences, seg_offsets, self.seq_counts, self.seq_tokens,
+                                 self.balance_coef, self.z_coef, dloss, self.dlogits, stream)
+            self._upstream = dloss is not None
         if self.dropout:
             moe_combine_dropout_bwd(dy, self.y_perm, self.topk_w, self.row_of_slot, T, H, k, self.dropout, self.rng,
                                     self.dy_perm, self.d_w, stream)

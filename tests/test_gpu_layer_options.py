@@ -1,5 +1,5 @@
 """The layer's options through its own calls: recorded as a graph, on another
-stream."""
+stream, with an upstream gradient of the router losses."""
 import pytest
 import torch
 
@@ -98,3 +98,42 @@ def test_advance_rng_on_the_calls_stream(raw):
     assert not y0[~want0].any() and not y1[~want1].any()
     assert y0[want0].ne(0).float().mean() > 0.9 and y1[want1].ne(0).float().mean() > 0.9
     assert L.rng.tolist() == [99, T * H // 8]
+
+
+@pytest.mark.parametrize("overlap", [False, True])
+def test_upstream_gradient_of_the_router_losses(overlap):
+    """dloss scales the two losses' parts of the gradient: the backward with it
+    is the one of a layer whose coefficients are the products.  The scales are
+    powers of two, so the gradients are the same to the bit."""
+    opts, g = parts()
+    up = torch.tensor([4.0, 0.125], device="cuda")
+    L = layer()
+    M = m.MoELayer(T, H, I, E, k, balance_coef=2.0, z_coef=0.0025, sequences=3, dropout=0.25, seed=99)
+    args = (g["dy"], g["x"], g["Wr"], g["Wg"], g["Wu"], g["Wd"])
+    for lay in (L, M):
+        lay.forward(g["x"], *weights(g), **opts)
+    L.backward(*args, overlap=overlap, dloss=up)
+    M.backward(*args, overlap=overlap)
+    torch.cuda.synchronize()
+    assert torch.equal(L.dlogits, M.dlogits) and torch.equal(L.dx, M.dx) and torch.equal(L.dWr, M.dWr)
+    assert torch.equal(L.dWg, M.dWg)
+    # without it: the forward's own coefficients, after a backward with it as well
+    ref = layer()
+    ref.forward(g["x"], *weights(g), **opts)
+    ref.backward(*args, overlap=overlap)
+    for again in (False, True):
+        if again:
+            L.backward(*args, overlap=overlap, dloss=up)
+            L.forward(g["x"], *weights(g), **opts)
+        L.backward(*args, overlap=overlap)
+        torch.cuda.synchronize()
+        assert torch.equal(L.dx, ref.dx) and torch.equal(L.dWr, ref.dWr) and not torch.equal(L.dWr, M.dWr)
+    assert m.moe_read_device_status(reset=True) == 0
+
+
+def test_upstream_gradient_needs_the_losses():
+    _, g = parts()
+    L = m.MoELayer(T, H, I, E, k)
+    L.forward(g["x"], *weights(g))
+    with pytest.raises(ValueError):
+        L.backward(g["dy"], g["x"], g["Wr"], g["Wg"], g["Wu"], g["Wd"], dloss=torch.ones(2, device="cuda"))
