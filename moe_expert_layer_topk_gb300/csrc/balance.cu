@@ -28,6 +28,7 @@
 #include <cfloat>
 
 #include "common.cuh"
+#include "packed_cut.cuh"
 
 namespace moe {
 namespace {
@@ -109,56 +110,19 @@ __device__ __forceinline__ void load_table(const Tokens& k, int* off, int* nb, i
   __syncthreads();
 }
 
-// The sequences' tokens cut into equal chunks, where a sequence counts for `pad`
-// tokens more than it has: a chunk pays for each piece it holds (its counts, its
-// sums, its ticket), and with chunks of equal tokens the one with the most pieces
-// sets the time (65519 x 128: 37 sequences 28.9 us, 150 38.8; with the pad 24.1
-// and 28.9; 8192 x 128 in 64 sequences 34.6 and 16.8).  Sequence s takes places [start(s), start(s + 1)), the first pad
-// of them without a token.
-struct Cut {
-  const int *off, *nb;
-  int num_seq;
-  unsigned pad, chunk;
-  __device__ __forceinline__ Cut(const int* off, const int* nb, int num_seq, int chunks, int pad)
-      : off(off), nb(nb), num_seq(num_seq), pad(nb[num_seq] > 1 ? pad : 0) {
-    chunk = max(1u, (start(num_seq) + chunks - 1) / chunks);
-  }
-  __device__ __forceinline__ unsigned start(int s) const { return (unsigned)(off[s] - off[0]) + pad * nb[s]; }
-  // the chunks that hold tokens of s (which has some)
-  __device__ __forceinline__ int first(int s) const { return (start(s) + pad) / chunk; }
-  __device__ __forceinline__ int last(int s) const { return (start(s + 1) - 1) / chunk; }
-  // f(seq, first token, end) for every piece of chunk c
-  template <class F>
-  __device__ __forceinline__ void pieces(int c, F&& f) const {
-    const unsigned all = start(num_seq), v0 = c * chunk, v1 = min(all, v0 + chunk);
-    if (v0 >= all) return;
-    int lo = 0, hi = num_seq - 1;  // last s with start(s) <= v0
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (start(mid) <= v0) lo = mid; else hi = mid - 1;
-    }
-    for (int s = lo; s < num_seq && start(s) < v1; ++s) {
-      const unsigned v = start(s) + pad;  // its first token's place
-      const int a = off[s] + (v0 > v ? (int)(v0 - v) : 0);
-      const int b = min(off[s + 1], off[s] + (v1 > v ? (int)(v1 - v) : 0));
-      if (a < b) f(s, a, b);
-    }
-  }
-};
-
 // ------------------------------------------------------------------ counts
 // hist[e], *live: the slots and tokens of [a, b) that count (all threads).
 // Four slots' loads are under way before the first is counted; a token is
 // counted with its first slot.
-__device__ __forceinline__ void count_slots(const Tokens& tk, const int32_t* __restrict__ topk_idx, int a, int b, int* hist,
+__device__ __forceinline__ void count_slots(const Tokens& tk, const int32_t* __restrict__ topk_idx, unsigned a, unsigned b, int* hist,
                                             int* live, int* status) {
   constexpr int kSlots = 4;
   for (int e = threadIdx.x; e < tk.E; e += kThreads) hist[e] = 0;
   if (threadIdx.x == 0) *live = 0;
   __syncthreads();
   int mine = 0;
-  const unsigned q1 = (unsigned)b * tk.k;  // T k < 2^31
-  for (unsigned q0 = (unsigned)a * tk.k + threadIdx.x; q0 < q1; q0 += kSlots * kThreads) {
+  const unsigned q1 = b * tk.k;  // T k < 2^31
+  for (unsigned q0 = a * tk.k + threadIdx.x; q0 < q1; q0 += kSlots * kThreads) {
     int e[kSlots];
     bool on[kSlots];
 #pragma unroll
@@ -185,7 +149,7 @@ __device__ __forceinline__ void count_slots(const Tokens& tk, const int32_t* __r
     mine = __reduce_add_sync(0xffffffffu, mine);
     if ((threadIdx.x & 31) == 0 && mine) atomicAdd(live, mine);
   } else if (threadIdx.x == 0) {
-    *live = b - a;
+    *live = (int)(b - a);
   }
   __syncthreads();
 }
@@ -215,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) balance_count_kernel(const Tokens tk
   load_table(tk, off, nb, status);
   const int c = blockIdx.x;
   int total = 0;
-  Cut(off, nb, tk.num_seq, gridDim.x, kCountPad).pieces(c, [&](int s, int a, int b) {
+  Cut(off, nb, tk.num_seq, gridDim.x, kCountPad).pieces(c, [&](int s, unsigned a, unsigned b) {
     count_slots(tk, topk_idx, a, b, hist, &live, status);
     for (int e = threadIdx.x; e < tk.E; e += kThreads) w.cnt_part[(size_t)(c + s) * tk.E + e] = hist[e];
     if (threadIdx.x == 0) w.tok_part[c + s] = live;
@@ -342,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
   // read and replaced.
   float ln[NV];
   bool onn = false;
-  auto load = [&](int t) {
+  auto load = [&](unsigned t) {
     onn = !tk.mask || __ldg(tk.mask + t);
     const float* src = logits + (size_t)t * E + el * VEC;
 #pragma unroll
@@ -357,14 +321,14 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
     }
   };
 
-  cut.pieces(chunk, [&](int s, int a, int b) {
+  cut.pieces(chunk, [&](int s, unsigned a, unsigned b) {
     float acc[kSum ? NV : 1];
     float cf[kGrad ? NV : 1];
     float z = 0.f, z_fold = 0.f;
     int since = 0;
     bool folded = false;
-    int t = a + warp * TPW + sub;
-    if (t < b) load(t);  // under way while the counts are added up
+    TokenWalk walk{a + warp * TPW + sub, b, (unsigned)step};
+    if (walk.more()) load(walk.t);  // under way while the counts are added up
     const int cc0 = kCounted ? counted.first(s) : 0, cc1 = kCounted ? counted.last(s) + 1 : 0;
     if constexpr (kCounted)
       if (!ready) pdl_wait();
@@ -459,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
 #pragma unroll
       for (int i = 0; i < NV; ++i) acc[i] = 0.f;
     }
-    while (t < b) {
+    while (walk.more()) {
       float l[NV];
       const bool on = onn;
 #pragma unroll
@@ -468,9 +432,9 @@ __global__ void __launch_bounds__(kThreads, 1) balance_main_kernel(const Tokens 
 #pragma unroll
         for (int i = 0; i < NV; ++i) l[i] = 0.f;
       }
-      const int here = t;
-      t += step;
-      if (t < b) load(t);
+      const unsigned here = walk.t;
+      walk.next();
+      if (walk.more()) load(walk.t);
       float m = l[0], sum = 0.f, dot = 0.f;
 #pragma unroll
       for (int i = 1; i < NV; ++i) m = fmaxf(m, l[i]);

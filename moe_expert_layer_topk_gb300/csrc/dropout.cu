@@ -282,8 +282,8 @@ __global__ void __launch_bounds__(64) combine_dropout_bwd_kernel(
   const PhiloxKey key = load_key(rng);
   const int lane = threadIdx.x & 31;
   const int nvec = H / 8;
-  const int nw = (int)((gridDim.x * blockDim.x) >> 5);
-  for (int t = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5); t < T; t += nw) {
+  const unsigned nw = (gridDim.x * blockDim.x) >> 5;
+  for (unsigned t = (blockIdx.x * blockDim.x + threadIdx.x) >> 5; t < (unsigned)T; t += nw) {
     int my_row = lane < k ? __ldg(row_of_slot + (size_t)t * k + lane) : -1;
     const float my_w = lane < k ? __ldg(topk_w + (size_t)t * k + lane) * dp.scale : 0.f;
     if (lane < k && (my_row < 0 || my_row >= R)) {
