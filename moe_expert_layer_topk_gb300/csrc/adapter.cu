@@ -1392,7 +1392,7 @@ int set_smem(const void* kern, bool* done, const char* fn, size_t most = kAdapte
   if (dev < 0) return fail(MOE_ERR_CUDA, "%s: no current CUDA device", fn);
   if (done[dev]) return MOE_OK;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
-  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+  if (e != cudaSuccess) return fail_cuda(fn, e);
   done[dev] = true;
   return MOE_OK;
 }
@@ -1415,7 +1415,7 @@ int launch_adapter(const char* fn, void (*kern)(KArgs...), dim3 grid, int thread
   cfg.attrs = at;
   cfg.numAttrs = cluster_x > 0 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
-  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+  if (e != cudaSuccess) return fail_cuda(fn, e);
   return check_launch(fn);
 }
 
@@ -1677,7 +1677,7 @@ int moe_adapter_linear_bwd(const void* dy, long long lddy, const void* x, long l
     if (!accumulate) {
       cudaError_t e = cudaMemsetAsync(dA, 0, sizeof(float) * (size_t)num_adapters * r * K, s);
       if (e == cudaSuccess) e = cudaMemsetAsync(dB, 0, sizeof(float) * (size_t)num_adapters * r * N, s);
-      if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+      if (e != cudaSuccess) return fail_cuda(fn, e);
     }
     if (T == 0) return MOE_OK;
     return run_wide<true>(fn, q, dy, lddy, W, nullptr, A, N, K, r, dx, lddx, false, s);

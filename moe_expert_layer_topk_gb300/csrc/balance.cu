@@ -708,7 +708,7 @@ struct Main {
     if (dev < 0) return fail(MOE_ERR_CUDA, "%s: no current CUDA device", fn);
     if (!set[dev]) {
       const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
-      if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+      if (e != cudaSuccess) return fail_cuda(fn, e);
       set[dev] = true;
     }
     launch_pdl(kern, grid, kThreads, smem, s, tk, logits, idx, w, o, gr, status_word());
@@ -783,7 +783,7 @@ int moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t
     if (e == cudaSuccess) e = cudaMemsetAsync(tokens, 0, sizeof(int32_t) * (size_t)num_seg, s);
     if (e == cudaSuccess) e = cudaMemsetAsync(prob_sum, 0, sizeof(float) * (size_t)num_seg * E, s);
     if (e == cudaSuccess) e = cudaMemsetAsync(loss, 0, 2 * sizeof(float), s);
-    if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+    if (e != cudaSuccess) return fail_cuda(fn, e);
     return MOE_OK;
   }
   const Tokens tk{T, E, k, num_seg, L.ncount, seg_offsets, mask};

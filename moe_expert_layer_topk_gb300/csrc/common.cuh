@@ -59,6 +59,13 @@ inline int check_launch(const char* fn, const char* kernel) {
   return MOE_OK;
 }
 
+// Reports an error that a runtime call returned, and takes it off the runtime:
+// left there, the next call's check would report it as its own.
+inline int fail_cuda(const char* fn, cudaError_t e) {
+  cudaGetLastError();
+  return fail(MOE_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+}
+
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
 constexpr int kMaxSegments = 1024;
