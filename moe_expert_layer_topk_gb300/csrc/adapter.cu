@@ -266,6 +266,8 @@ __device__ __forceinline__ bool elect_one() {
 
 __device__ __forceinline__ uint32_t align1k(uint32_t a) { return (a + 1023u) & ~1023u; }
 
+constexpr float kLargestBf16 = 0x1.FEp127f;
+
 // v split into kPlanes bf16 parts, largest first, 8 columns: one 16-byte vector a part
 __device__ __forceinline__ void split8(const float (&v)[8], uint4 (&out)[kPlanes]) {
   float rest[8];
@@ -276,9 +278,12 @@ __device__ __forceinline__ void split8(const float (&v)[8], uint4 (&out)[kPlanes
     float h[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      h[i] = __bfloat162float(__float2bfloat16_rn(rest[i]));
-      // of an infinity or a NaN, whose difference would be NaN, only the first part is kept
-      rest[i] = isfinite(rest[i]) ? rest[i] - h[i] : 0.f;
+      // A finite value above the largest bf16 number starts with that one (the
+      // nearest would be infinity); of an infinity or a NaN, whose difference would
+      // be NaN, only the first part is kept.
+      const bool finite = isfinite(rest[i]);
+      h[i] = __bfloat162float(__float2bfloat16_rn(finite ? fminf(fmaxf(rest[i], -kLargestBf16), kLargestBf16) : rest[i]));
+      rest[i] = finite ? rest[i] - h[i] : 0.f;
     }
     out[p] = pack8(h);
   }

@@ -143,3 +143,30 @@ def test_outputs_keep_every_bit_of_u_and_v(T, r):
     dx, _, _ = backward(c, hid, offsets, which, T, K, N, r, nA)
     assert (dx[:half].double() - rest).abs().max() <= 2.0 ** -8 * abs(rest)
     assert torch.all(dx[half:] == torch.tensor(-(parts[0] + parts[1])).bfloat16())
+
+
+@pytest.mark.parametrize("T", [4, 40])
+def test_largest_values_stay_finite(T):
+    """v = u = 3.3999e38 is a finite fp32 number whose nearest bf16 number
+    would be infinity: y and dx are v and u times 2^-100, dA and dB v and u
+    times 2^-20.  2^-8 of a bf16 result, 2^-22 of an fp32 one."""
+    K, N, r, nA = 64, 128, 8, 1
+    big, s = float(torch.tensor(3.3895e38).bfloat16()), np.float32(1.003)
+    want = float(np.float32(big) * s)
+    assert np.isfinite(want) and not np.isfinite(float(torch.tensor(want).bfloat16()))
+    _, c = make(1, K, N, r, nA, dy=True)
+    z = lambda *shape: torch.zeros(*shape, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    c.update(x=z(T, K), dy=z(T, N), W=z(N, K), A=z(nA, r, K), B=z(nA, N, r), scale=torch.full((nA,), float(s), device="cuda"))
+    offsets, which = [0, T], [0]
+    c["x"][0, 3], c["A"][0, 2, 3], c["B"][0, :, 2] = 1, big, 2.0 ** -100
+    y, hid = forward(c, offsets, which, T, K, N, r, nA)
+    assert (y[0].double() / (want * 2.0 ** -100) - 1).abs().max() <= 2.0 ** -8
+    c["dy"][0, 7] = 2.0 ** -20
+    _, _, dB = backward(c, hid, offsets, which, T, K, N, r, nA)
+    assert abs(float(dB[0, 7, 2]) / (want * 2.0 ** -20) - 1) <= 2.0 ** -22
+    c["A"].zero_(), c["B"].zero_()
+    c["dy"][0, 7], c["B"][0, 7, 2], c["A"][0, 2] = 1, big, 2.0 ** -100
+    c["x"][0, 3] = 2.0 ** -20
+    dx, dA, _ = backward(c, hid, offsets, which, T, K, N, r, nA)
+    assert (dx[0].double() / (want * 2.0 ** -100) - 1).abs().max() <= 2.0 ** -8
+    assert abs(float(dA[0, 2, 3]) / (want * 2.0 ** -20) - 1) <= 2.0 ** -22
