@@ -20,14 +20,19 @@
 // one request's row or adapter reaches no other row.
 //
 // Measured (r = 16 unless said; graph replays, cold L2 not forced):
-//   1 row, 2048 x 2048, one request                6.7 us   launches and latency
-//   64 rows of 64 requests, 48 adapters            11.1     masked MMAs, one run a row
-//   517 rows, mixed, r = 64, 768 x 2048            22.9     the same
-//   16384 rows, 2048 x 4096                        164-180  tensor cores: 1.5 PFLOP/s of
-//                                                  the wide product's 0.28 TFLOP in 146
-//   8192 rows, 2048 x 2048, backward               117.7 with the forward: narrow 13 and
-//                                                  wide 44 each way, gradients 17 + 5, in part
-//                                                  beside them
+//   1 row, 2048 x 2048, one request                7.2 us   launches and latency
+//   64 rows of 64 requests, 48 adapters            11.5     masked MMAs, one run a row
+//   517 rows, mixed, r = 64, 768 x 2048            26.0     the same
+//   16381 rows, 2048 x 4096, r = 32                170-181  tensor cores: 0.28 TFLOP of the
+//                                                  wide product in 149, narrow 24 before it
+//   8192 rows, 2048 x 2048, backward               121.8 with the forward: narrow 14 and
+//                                                  wide 44 each way, gradients 18 + 6, in part
+//                                                  beside them (r = 64: 149.1)
+//
+// With v and u at 16 bits in the wide product (two parts) these took 11.9 (12.3
+// now, in turn with it), 23.6 (26.6), 177.3 (180.1), 120.7 (121.8) and 140.5
+// (149.1); but where W x cancels the adapter's term, those 16 bits were all that
+// y had.
 #include <cuda.h>
 
 #include "tc_common.cuh"
@@ -656,7 +661,10 @@ struct WideCfg {
   static constexpr int B_BYTES = BN / CTAS * BK * 2;       // a CTA's share of a block of W
   static constexpr int WB = BN / CTAS > 64 && CTAS == 1 ? BN : 64;  // W rows (columns) of one TMA box
   static constexpr int EP_BYTES = kSplit ? 0 : 4 * EP_SLOTS * EP_BOX_BYTES;
-  // three blocks of hidden cost the wider tiles' ring a stage
+  // three blocks of hidden cost the wider tiles' ring a stage (with two held and
+  // the third part in a pass of its own, F's blocks loaded again, 8192 rows forward
+  // and backward at r = 64 took 153.7 us instead of 149.1, 517 mixed rows 30.8
+  // instead of 26.6)
   static constexpr int stages(int vblocks) { return BN == 64 ? 6 : (vblocks <= 2 ? 5 : 4); }
   static constexpr size_t smem(int a_rows, int vblocks, int stages) {
     // the MMA reads 128 rows from a hidden block's start, however few it holds
@@ -1434,8 +1442,8 @@ int run_shrink(const char* fn, const Reqs& q, const void* in, long long ld, cons
   const int tiles = (q.T + BM - 1) / BM, nkb = red / BK, sms = sm_count() > 0 ? sm_count() : 148;
   const int rN = round_up(r, 16), f_bytes = kMN ? (r + 63) / 64 * CHUNK_BYTES : r * 128;
   // as many slices as run at a time: two CTAs an SM where both fit (r = 64, of which one fits, with slices
-  // for two: 155 us instead of 144 for 8192 x 2048 x 2048 in both directions; 33.1 instead of 34.6 for the
-  // narrow product of 16384 x 2048 alone, whose 128 tiles leave SMs idle)
+  // for two: 159 us instead of 150 for 8192 x 2048 x 2048 in both directions, 113.5 instead of 107.6 for
+  // the forward of 16384 x 2048 x 2048)
   const int least = 1024 + 2 * kShrinkXBytes + rN * BM * 4 + (int)table_bytes(q.num_seg) + 2 * kShrinkK * f_bytes;
   const bool two = least <= 110 * 1024;
   int cs = 1;
@@ -1553,8 +1561,10 @@ int run_wide(const char* fn, const Reqs& q, const void* in, long long ld, const 
     return run_wide_bn<64, kMN, true>(fn, q, in, ld, W, hidden, F, red, out_cols, r, out, ldo, has_hidden, nrank, s);
   // else the tile whose waves cost least: a block's time goes with the columns it multiplies plus half of
   // the 128 rows it loads; a pair's last wave may be one of halves, which cost what a 128-column tile does
-  // (517 rows, 768 x 2048: 23.9 us on 128 columns, 26.6 on halves of 256, 23.5 on 64 with four times the
-  // loads; 8192 rows, 2048 x 2048: 40 us on 256 and a wave of halves)
+  // (forward, narrow product included: 517 rows of 40 requests, 768 x 2048, r = 16: 18.5 us on 128 columns,
+  // 20.6 on halves of 256, 18.0 on 64 with four times the loads; r = 64: 26.8, 27.6, 24.2, since the
+  // adapters' MMAs, which the rule does not count, weigh more; 8192 rows, 2048 x 2048, r = 16: 50.5 on 256
+  // and a wave of halves, 64.1 on 128, 102 on 64)
   int best = (tiles + sms - 1) / sms * (64 + 64), bn = 64;
   if (out_cols % 128 == 0) {
     const int w128 = (tiles / 2 + sms - 1) / sms * (128 + 64);

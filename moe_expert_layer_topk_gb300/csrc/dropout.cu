@@ -100,9 +100,10 @@ struct Vec8<float> {
 };
 
 // x may be out (every element is read before it is written by its thread).
-// One generator block of eight elements a thread (16.8 M bf16 elements with a
-// residual: 16.8 us; two a thread 18.3, four 19.4: the registers they take cost
-// more warps than their loads are worth).
+// One generator block of eight elements a thread, their vectors held as they lie
+// in memory (16.8 M bf16 elements with a residual: 15.1 us, 6.7 TB/s, fp32 30.8;
+// unpacked first 16.8, and then with two blocks a thread 18.3, four 19.4: the
+// registers they take cost more warps than their loads are worth).
 template <typename T>
 __global__ void __launch_bounds__(256) dropout_kernel(const T* x, const T* residual, long long n, DropParams dp,
                                                       const unsigned long long* __restrict__ rng, T* out) {
@@ -272,6 +273,11 @@ __device__ __noinline__ float dot_of_kept(const uint4* dy, const uint4* y, const
 // element of y_perm meets a zero of dy there, which an infinity or a NaN turns
 // into NaN: a sum that is not finite is taken again over the elements that stay
 // (selecting them away each time cost 6% at 2048 columns, 26% at 512).
+//
+// Bound by HBM at 2048 columns (8192 tokens, top-8: 89.6 us, 6.4 TB/s; top-2
+// 31.1).  The eight vectors a lane holds are 2048 columns: narrower rows leave
+// some of them empty, and a token's slots follow one another (top-8: 1024 columns
+// 57.0 us, 512 43.7, 256 27.9, 128 25.9, of which HBM needs 42, 21, 11 and 5).
 __global__ void __launch_bounds__(64) combine_dropout_bwd_kernel(
     const __nv_bfloat16* __restrict__ dy, const __nv_bfloat16* __restrict__ y_perm,
     const float* __restrict__ topk_w, const int32_t* __restrict__ row_of_slot, int T, int H, int k, int R,

@@ -17,8 +17,8 @@ namespace moe {
 // The sequences' tokens cut into equal chunks, where a sequence counts for `pad`
 // tokens more than it has: a chunk pays for each piece it holds (its counts, its
 // sums, its ticket), and with chunks of equal tokens the one with the most pieces
-// sets the time (65519 x 128: 37 sequences 28.9 us, 150 38.8; with the pad 24.1
-// and 28.9; 8192 x 128 in 64 sequences 34.6 and 16.8).  Sequence s takes places
+// sets the time (65519 x 128: 37 sequences 29.5 us, 150 36.6; with the pad 23.3
+// and 28.0; 8192 x 128 in 64 sequences 24.9 and 16.3).  Sequence s takes places
 // [start(s), start(s + 1)), the first pad of them without a token.
 // off[0..num_seq]: the sequences' first tokens and the last one's end, rising;
 // nb[0..num_seq]: sequences with tokens before each.
