@@ -540,6 +540,108 @@ int moe_adapter_linear_bwd(const void* dy, long long lddy, const void* x, long l
                            int num_adapters, void* dx, long long lddx, float* dA, float* dB, int accumulate, void* ws,
                            size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The norms around a block (no counterpart on the pages): the root-mean-square
+ * norm before it, and the norm after it with the block's gate, the residual and
+ * a scale for each.
+ *
+ * The residual stream (x, dres, dx, residual, out, dout) is bf16 (fp32 = 0) or
+ * fp32 (fp32 = 1); what enters and leaves the block (y, dy, z, dz, next_y) is
+ * bf16.  gain fp32 [H], NULL: ones.  fp32 arithmetic, each output rounded once.
+ * H a multiple of 8, at most 8192; eps > 0.  A row whose squares leave fp32's
+ * range is summed again on a smaller scale.  Row strides ld* in elements,
+ * multiples of 8 (of 4 for fp32 rows), at least H; without one, rows are
+ * contiguous.
+ *
+ * moe_pre_norm:     rstd[t] = 1 / sqrt(mean_h x[t,h]^2 + eps)   (rstd fp32 [T], may be NULL)
+ *                   y[t,h]  = x[t,h] rstd[t] gain[h]
+ * moe_pre_norm_bwd: with n = x rstd and dn = dy gain,
+ *                   dx[t,h]  = res_scale dres[t,h] + rstd[t] (dn[t,h] - n[t,h] mean_j dn[t,j] n[t,j])
+ *                   dgain[h] = sum_t dy[t,h] n[t,h]             (fp32 [H], NULL: not computed)
+ *                   dres: gradient of the residual path, or NULL (0); dx may be dres.
+ *                   y may not overlap x, nor dx overlap x or dy.
+ *
+ * moe_post_norm: with n = z rstd (norm = 1, rstd as above, of z) or n = z (norm = 0),
+ *                   out[t,h] = res_scale residual[t,h] + out_scale G[t,h] n[t,h] gain[h]
+ *   residual may be NULL (0); out may be residual.  G by gate_kind:
+ *     0: 1;  1: sigmoid(gate[t]), gate fp32 [T];  2: sigmoid(gate[t,h]), gate bf16 [T,H].
+ *   rstd: NULL or where z's rstd is left (norm = 1).  next_y not NULL: the next
+ *   block's moe_pre_norm of out as stored is computed on the way,
+ *   next_y = norm(out) next_gain, next_rstd its rstd (may be NULL).
+ * moe_combine_post_norm: the same of z[t] = sum_j topk_w[t,j] y_perm[row_of_slot[t,j]]
+ *   (fp32, slots in order, as moe_combine); z NULL, or where it is kept in bf16
+ *   for the backward.  H a multiple of 64, k <= 32.
+ * moe_post_norm_bwd: with dv = out_scale G dout and dn = dv gain,
+ *                   dz[t,h]  = rstd[t] (dn[t,h] - n[t,h] mean_j dn[t,j] n[t,j])  (norm = 1) or dn
+ *                   dgain[h] = sum_t dv[t,h] n[t,h]             (fp32 [H], NULL: not computed)
+ *                   dgate    = out_scale dout n gain G (1 - G), summed over h for gate_kind 1
+ *                              (fp32 [T]) or of each element (bf16 [T,H]); NULL: not computed
+ *   The residual's gradient is res_scale dout: moe_pre_norm_bwd's dres is dout.
+ *   rstd of z as the forward left it (norm = 1).  dz may be z.
+ * dgain is overwritten, or added to when accumulate != 0.  Results are
+ * deterministic.  Workspaces (for dgain only): moe_*_norm_bwd_workspace_size. */
+int moe_pre_norm(const void* x, long long ldx, int fp32, const float* gain, float eps, int T, int H, void* y,
+                 long long ldy, float* rstd, void* stream);
+size_t moe_pre_norm_bwd_workspace_size(int T, int H);
+int moe_pre_norm_bwd(const void* dy, long long lddy, const void* x, long long ldx, int fp32, const float* gain,
+                     const float* rstd, const void* dres, long long lddres, float res_scale, int T, int H, void* dx,
+                     long long lddx, float* dgain, int accumulate, void* ws, size_t ws_bytes, void* stream);
+int moe_post_norm(const void* z, const void* residual, int fp32, const float* gain, int norm, float eps, int gate_kind,
+                  const void* gate, float res_scale, float out_scale, int T, int H, void* out, float* rstd,
+                  const float* next_gain, void* next_y, float* next_rstd, void* stream);
+int moe_combine_post_norm(const void* y_perm, const float* topk_w, const int32_t* row_of_slot, const void* residual,
+                          int fp32, const float* gain, int norm, float eps, int gate_kind, const void* gate,
+                          float res_scale, float out_scale, int T, int H, int k, void* z, void* out, float* rstd,
+                          const float* next_gain, void* next_y, float* next_rstd, void* stream);
+size_t moe_post_norm_bwd_workspace_size(int T, int H);
+int moe_post_norm_bwd(const void* dout, int fp32, const void* z, const float* gain, int norm, const float* rstd,
+                      int gate_kind, const void* gate, float out_scale, int T, int H, void* dz, float* dgain,
+                      void* dgate, int accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Activations kept in 8 bits for the backward (no counterpart on the pages).
+ *
+ * Each 32 columns of a row share a scale, a bf16 number:
+ *   s = amax(|a|) / 127 (IEEE fp32 division), rounded up to bf16, at least 2^-126
+ *   q = a * (1/s) (fp32, 1/s IEEE) rounded to the nearest whole number, ties to even
+ *   a ~ q s, off by at most s/2
+ * q int8 [rows, cols] row-major, scale bf16 [rows, cols/32]: 1.0625 bytes an
+ * element.  Where a group holds an infinity or a NaN its scale is NaN and all its
+ * values come back as NaN.  cols a multiple of 32.
+ *
+ * moe_ckpt_pack, moe_ckpt_unpack: rows in bf16 to codes, and codes to bf16
+ *   (q s rounded once).
+ * moe_dispatch_rows: x_perm[row_of_slot[t,j]] = x[t] (bf16 [T*k,H]), from bf16
+ *   tokens (scale NULL) or from tokens kept in 8 bits; row_w[row_of_slot[t,j]] =
+ *   topk_w[t,j] (both NULL, or both given).  Rows that no slot names are left as
+ *   they were; a row outside [0, T*k) is skipped and sets MOE_STATUS_BAD_INDEX.
+ * moe_grouped_gemm_swiglu_ckpt: moe_grouped_gemm_swiglu that keeps g and u so,
+ *   of their fp32 values: gu_q int8 [R,2I], gu_scale bf16 [R,2I/32].
+ * moe_grouped_gemm_down_bwd_ckpt: the backward through them.  dy_perm holds the
+ *   tokens' dy as they are (not weighted), row_w fp32 [R] the rows' routing
+ *   weights (NULL: 1).  For row r of expert e, g and u decoded, s = sigmoid(g):
+ *     dh      = dy_perm[r] . Wd[e]                                 (fp32)
+ *     dgu[r]  = row_w[r] [dh u s (1 + g (1 - s)) | dh g s]         -> bf16 [R,2I]
+ *     h_w[r]  = row_w[r] g s u                                     -> bf16 [R,I]
+ *     d_w(r)  = sum_i dh[i] g s u                                  (fp32)
+ *   d_w is what moe_combine_bwd computes as dy . y_perm[r], so that y_perm need
+ *   not be kept: d_w[t,j] = d_w(row_of_slot[t,j]) (fp32 [T,k], T*k <= R), or
+ *   d_w[r] (fp32 [R]) when row_of_slot is NULL; 0 for a row outside every segment.
+ *   With dy_perm and h_w moe_grouped_gemm_down_bwd_dw gives dWd.
+ *   ws: moe_grouped_gemm_down_bwd_ckpt_workspace_size(R, I) bytes, 16-byte aligned. */
+int moe_ckpt_pack(const void* a, int rows, int cols, void* q, void* scale, void* stream);
+int moe_ckpt_unpack(const void* q, const void* scale, int rows, int cols, void* a, void* stream);
+int moe_dispatch_rows(const void* x, const void* scale, const int32_t* row_of_slot, const float* topk_w, int T, int H,
+                      int k, void* x_perm, float* row_w, void* stream);
+int moe_grouped_gemm_swiglu_ckpt(const void* x_perm, const void* Wg, const void* Wu, int num_seg,
+                                 const int32_t* seg_offsets, const int32_t* seg_expert, int R, int H, int I, int E,
+                                 void* h, void* gu_q, void* gu_scale, void* stream);
+size_t moe_grouped_gemm_down_bwd_ckpt_workspace_size(int R, int I);
+int moe_grouped_gemm_down_bwd_ckpt(const void* dy_perm, const float* row_w, const void* gu_q, const void* gu_scale,
+                                   const void* Wd, int num_seg, const int32_t* seg_offsets, const int32_t* seg_expert,
+                                   int R, int H, int I, int E, void* dgu, void* h_w, const int32_t* row_of_slot, int T,
+                                   int k, float* d_w, void* ws, size_t ws_bytes, void* stream);
+
 /* Persistent-grid limit of the grouped GEMMs (no counterpart on the pages).
  * Every grouped GEMM kernel (the forward, backward and router-backward
  * GEMMs of the calls above) runs one CTA per SM over its tiles.  After

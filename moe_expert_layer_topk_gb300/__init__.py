@@ -35,6 +35,10 @@ __all__ = ["lib", "MoEError", "LIB_PATH", "ENTRY_POINTS",
            "moe_dropout", "moe_combine_dropout", "moe_combine_dropout_bwd",
            "moe_adapter_hidden_size", "moe_adapter_linear", "moe_adapter_linear_bwd_workspace_size",
            "moe_adapter_linear_bwd",
+           "moe_pre_norm", "moe_pre_norm_bwd_workspace_size", "moe_pre_norm_bwd", "moe_post_norm",
+           "moe_combine_post_norm", "moe_post_norm_bwd_workspace_size", "moe_post_norm_bwd",
+           "moe_ckpt_pack", "moe_ckpt_unpack", "moe_dispatch_rows", "moe_grouped_gemm_swiglu_ckpt",
+           "moe_grouped_gemm_down_bwd_ckpt_workspace_size", "moe_grouped_gemm_down_bwd_ckpt",
            "moe_read_device_status", "moe_abi_version", "moe_probe_fma", "moe_set_gemm_sm_limit", "sm_count"]
 
 LIB_PATH: Path = _build_mod.LIB
@@ -94,6 +98,20 @@ ENTRY_POINTS = {
     "moe_adapter_linear_bwd_workspace_size": ([_I, _I, _I, _I, _I], _Z),
     "moe_adapter_linear_bwd": ([_P, _L, _P, _L, _P, _P, _P, _P, _P, _Z, _I, _P, _P, _I, _I, _I, _I, _I, _P, _L, _P, _P,
                                 _I, _P, _Z, _P], _I),
+    "moe_pre_norm": ([_P, _L, _I, _P, _F, _I, _I, _P, _L, _P, _P], _I),
+    "moe_pre_norm_bwd_workspace_size": ([_I, _I], _Z),
+    "moe_pre_norm_bwd": ([_P, _L, _P, _L, _I, _P, _P, _P, _L, _F, _I, _I, _P, _L, _P, _I, _P, _Z, _P], _I),
+    "moe_post_norm": ([_P, _P, _I, _P, _I, _F, _I, _P, _F, _F, _I, _I, _P, _P, _P, _P, _P, _P], _I),
+    "moe_combine_post_norm": ([_P, _P, _P, _P, _I, _P, _I, _F, _I, _P, _F, _F, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P], _I),
+    "moe_post_norm_bwd_workspace_size": ([_I, _I], _Z),
+    "moe_post_norm_bwd": ([_P, _I, _P, _P, _I, _P, _I, _P, _F, _I, _I, _P, _P, _P, _I, _P, _Z, _P], _I),
+    "moe_ckpt_pack": ([_P, _I, _I, _P, _P, _P], _I),
+    "moe_ckpt_unpack": ([_P, _P, _I, _I, _P, _P], _I),
+    "moe_dispatch_rows": ([_P, _P, _P, _P, _I, _I, _I, _P, _P, _P], _I),
+    "moe_grouped_gemm_swiglu_ckpt": ([_P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P], _I),
+    "moe_grouped_gemm_down_bwd_ckpt_workspace_size": ([_I, _I], _Z),
+    "moe_grouped_gemm_down_bwd_ckpt": ([_P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _P, _P, _P, _I, _I, _P, _P, _Z,
+                                        _P], _I),
     "moe_probe_fma": ([_I, _I, _I, _P, ctypes.POINTER(ctypes.c_longlong), _P], _I),
     "moe_set_gemm_sm_limit": ([_I, ctypes.POINTER(ctypes.c_int)], _I),
 }
@@ -438,6 +456,107 @@ def moe_adapter_linear_bwd(dy, x, W, A, B, scale, hidden, num_seg, seg_offsets, 
     _call("moe_adapter_linear_bwd", pd, lddy, px, ldx, _ptr(W), _ptr(A), _ptr(B), _ptr(scale), _ptr(hidden),
           _nbytes(hidden), num_seg, _ptr(seg_offsets), _ptr(seg_adapter), T, K, N, r, num_adapters, po, lddx, _ptr(dA),
           _ptr(dB), int(accumulate), _ptr(ws), _nbytes(ws), _stream(stream))
+
+
+def _stream_type(*tensors) -> int:
+    """0 where the residual stream's tensors are bf16, 1 where they are fp32."""
+    dt = tensors[0].dtype
+    if dt not in (torch.bfloat16, torch.float32) or any(t is not None and t.dtype != dt for t in tensors):
+        raise ValueError("the residual stream's tensors must all be bf16 or all fp32")
+    return int(dt == torch.float32)
+
+
+def _gate_kind(gate, T, H) -> int:
+    """0 without a gate, 1 for fp32 logits of T tokens, 2 for bf16 logits of T x H elements."""
+    if gate is None:
+        return 0
+    if gate.dtype == torch.float32 and gate.numel() == T:
+        return 1
+    if gate.dtype == torch.bfloat16 and gate.numel() == T * H:
+        return 2
+    raise ValueError("gate must be fp32 logits of the tokens or bf16 logits of their elements")
+
+
+def moe_pre_norm(x, gain, eps, T, H, y, rstd=None, stream=None):
+    """y = x / rms(x) * gain; x bf16 or fp32, x and y may be row slices of wider tensors."""
+    px, ldx = _rows(x)
+    py, ldy = _rows(y)
+    _call("moe_pre_norm", px, ldx, _stream_type(x), _ptr(gain), eps, T, H, py, ldy, _ptr(rstd), _stream(stream))
+
+
+def moe_pre_norm_bwd_workspace_size(T, H) -> int:
+    return lib().moe_pre_norm_bwd_workspace_size(T, H)
+
+
+def moe_pre_norm_bwd(dy, x, gain, rstd, dres, res_scale, T, H, dx, dgain=None, accumulate=0, ws=None, stream=None):
+    pd, lddy = _rows(dy)
+    px, ldx = _rows(x)
+    pr, lddres = (None, H) if dres is None else _rows(dres)
+    po, lddx = _rows(dx)
+    _call("moe_pre_norm_bwd", pd, lddy, px, ldx, _stream_type(x, dres, dx), _ptr(gain), _ptr(rstd), pr, lddres, res_scale,
+          T, H, po, lddx, _ptr(dgain), int(accumulate), _ptr(ws), _nbytes(ws), _stream(stream))
+
+
+def moe_post_norm(z, residual, gain, norm, eps, gate, res_scale, out_scale, T, H, out, rstd=None, next_gain=None,
+                  next_y=None, next_rstd=None, stream=None):
+    """out = res_scale residual + out_scale sigmoid(gate) norm(z) gain, and the next norm of out where next_y is given;
+    the stream's type is out's, the gate's kind its own (fp32 [T] or bf16 [T,H])."""
+    _call("moe_post_norm", _ptr(z), _ptr(residual), _stream_type(out, residual), _ptr(gain), int(norm), eps,
+          _gate_kind(gate, T, H), _ptr(gate), res_scale, out_scale, T, H, _ptr(out), _ptr(rstd), _ptr(next_gain),
+          _ptr(next_y), _ptr(next_rstd), _stream(stream))
+
+
+def moe_combine_post_norm(y_perm, topk_w, row_of_slot, residual, gain, norm, eps, gate, res_scale, out_scale, T, H, k, z,
+                          out, rstd=None, next_gain=None, next_y=None, next_rstd=None, stream=None):
+    _call("moe_combine_post_norm", _ptr(y_perm), _ptr(topk_w), _ptr(row_of_slot), _ptr(residual),
+          _stream_type(out, residual), _ptr(gain), int(norm), eps, _gate_kind(gate, T, H), _ptr(gate), res_scale, out_scale,
+          T, H, k, _ptr(z), _ptr(out), _ptr(rstd), _ptr(next_gain), _ptr(next_y), _ptr(next_rstd), _stream(stream))
+
+
+def moe_post_norm_bwd_workspace_size(T, H) -> int:
+    return lib().moe_post_norm_bwd_workspace_size(T, H)
+
+
+def moe_post_norm_bwd(dout, z, gain, norm, rstd, gate, out_scale, T, H, dz, dgain=None, dgate=None, accumulate=0, ws=None,
+                      stream=None):
+    if dgate is not None and (gate is None or dgate.dtype != gate.dtype):
+        raise ValueError("dgate must have the gate's type")
+    _call("moe_post_norm_bwd", _ptr(dout), _stream_type(dout), _ptr(z), _ptr(gain), int(norm), _ptr(rstd),
+          _gate_kind(gate, T, H), _ptr(gate), out_scale, T, H, _ptr(dz), _ptr(dgain), _ptr(dgate), int(accumulate), _ptr(ws),
+          _nbytes(ws), _stream(stream))
+
+
+def moe_ckpt_pack(a, rows, cols, q, scale, stream=None):
+    _call("moe_ckpt_pack", _ptr(a), rows, cols, _ptr(q), _ptr(scale), _stream(stream))
+
+
+def moe_ckpt_unpack(q, scale, rows, cols, a, stream=None):
+    _call("moe_ckpt_unpack", _ptr(q), _ptr(scale), rows, cols, _ptr(a), _stream(stream))
+
+
+def moe_dispatch_rows(x, scale, row_of_slot, topk_w, T, H, k, x_perm, row_w=None, stream=None):
+    """x: bf16 tokens (scale None), or int8 codes with their scales."""
+    if x.element_size() != (2 if scale is None else 1):
+        raise ValueError("x must be bf16 tokens, or 8-bit codes with their scales")
+    _call("moe_dispatch_rows", _ptr(x), _ptr(scale), _ptr(row_of_slot), _ptr(topk_w), T, H, k, _ptr(x_perm), _ptr(row_w),
+          _stream(stream))
+
+
+def moe_grouped_gemm_swiglu_ckpt(x_perm, Wg, Wu, num_seg, seg_offsets, seg_expert, R, H, I, E, h, gu_q, gu_scale,
+                                 stream=None):
+    _call("moe_grouped_gemm_swiglu_ckpt", _ptr(x_perm), _ptr(Wg), _ptr(Wu), num_seg, _ptr(seg_offsets), _ptr(seg_expert),
+          R, H, I, E, _ptr(h), _ptr(gu_q), _ptr(gu_scale), _stream(stream))
+
+
+def moe_grouped_gemm_down_bwd_ckpt_workspace_size(R, I) -> int:
+    return lib().moe_grouped_gemm_down_bwd_ckpt_workspace_size(R, I)
+
+
+def moe_grouped_gemm_down_bwd_ckpt(dy_perm, row_w, gu_q, gu_scale, Wd, num_seg, seg_offsets, seg_expert, R, H, I, E, dgu,
+                                   h_w, d_w, row_of_slot=None, T=0, k=0, ws=None, stream=None):
+    _call("moe_grouped_gemm_down_bwd_ckpt", _ptr(dy_perm), _ptr(row_w), _ptr(gu_q), _ptr(gu_scale), _ptr(Wd), num_seg,
+          _ptr(seg_offsets), _ptr(seg_expert), R, H, I, E, _ptr(dgu), _ptr(h_w), _ptr(row_of_slot), T, k, _ptr(d_w), _ptr(ws),
+          _nbytes(ws), _stream(stream))
 
 
 def moe_set_gemm_sm_limit(max_sms: int) -> int:

@@ -121,6 +121,42 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7]));
 }
 
+// Eight elements as they lie in memory.
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<__nv_bfloat16> {
+  uint4 q;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ float at(int i) const {
+    const uint32_t w = i < 2 ? q.x : (i < 4 ? q.y : (i < 6 ? q.z : q.w));
+    return (i & 1) ? bf16hi(w) : bf16lo(w);
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
+    *reinterpret_cast<uint4*>(p) = pack8(f);
+  }
+  static __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  static __device__ __forceinline__ __nv_bfloat16 round(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct Vec8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ float at(int i) const {
+    const float4& v = i < 4 ? a : b;
+    return (i & 3) == 0 ? v.x : ((i & 3) == 1 ? v.y : ((i & 3) == 2 ? v.z : v.w));
+  }
+  static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+  static __device__ __forceinline__ float one(const float* p) { return *p; }
+  static __device__ __forceinline__ float round(float v) { return v; }
+};
+
 __device__ __forceinline__ void set_status(int* status, int bits) {
   if (status) atomicOr(status, bits);
 }
@@ -149,5 +185,43 @@ __device__ __forceinline__ uint2 e4m3_codes8(uint4 v, float s) {
   }
   return make_uint2(out[0], out[1]);
 }
+
+// Activations kept in 8 bits: 32 columns share a bf16 scale s, the smallest bf16
+// number that is at least amax/127 (and 2^-126, whose reciprocal is finite), and
+// are whole numbers of at most 7 bits and a sign times it.
+constexpr int kCkptGroup = 32;
+
+// The larger magnitude, or NaN where there is one.
+__device__ __forceinline__ float amax_nan(float m, float a) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(a)));
+  return r;
+}
+// An amax that is infinite or NaN gives a NaN: all the group's values come back as NaN.
+__device__ __forceinline__ float ckpt_scale(float amax) {
+  const float q = __fdiv_rn(amax, 127.0f);
+  const float up = __uint_as_float((__float_as_uint(q) + 0xFFFFu) & 0xFFFF0000u);
+  return !(q <= 3.402823466e+38f) ? __uint_as_float(0x7FC00000u) : (up < 1.17549435e-38f ? 1.17549435e-38f : up);
+}
+// Four codes, lowest first: a * inv rounded to nearest even by adding 1.5 * 2^23,
+// whose lowest byte is then the two's complement code (|a * inv| is at most 127
+// and a few units of the last place).
+__device__ __forceinline__ uint32_t ckpt_codes4(float a, float b, float c, float d, float inv) {
+  const uint32_t x = __float_as_uint(__fadd_rn(__fmul_rn(a, inv), 12582912.0f));
+  const uint32_t y = __float_as_uint(__fadd_rn(__fmul_rn(b, inv), 12582912.0f));
+  const uint32_t z = __float_as_uint(__fadd_rn(__fmul_rn(c, inv), 12582912.0f));
+  const uint32_t w = __float_as_uint(__fadd_rn(__fmul_rn(d, inv), 12582912.0f));
+  return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
+}
+// The values of four codes: the byte with its sign bit flipped is code + 128, put
+// into the low mantissa bits of 2^23, whose difference from 2^23 + 128 is exact.
+__device__ __forceinline__ void ckpt_decode4(uint32_t w, float s, float (&f)[4]) {
+  const uint32_t v = w ^ 0x80808080u;
+  f[0] = (__uint_as_float(__byte_perm(v, 0x4B000000u, 0x7440)) - 8388736.0f) * s;
+  f[1] = (__uint_as_float(__byte_perm(v, 0x4B000000u, 0x7441)) - 8388736.0f) * s;
+  f[2] = (__uint_as_float(__byte_perm(v, 0x4B000000u, 0x7442)) - 8388736.0f) * s;
+  f[3] = (__uint_as_float(__byte_perm(v, 0x4B000000u, 0x7443)) - 8388736.0f) * s;
+}
+__device__ __forceinline__ float bf16_bits(uint32_t h) { return __uint_as_float(h << 16); }
 
 }  // namespace moe

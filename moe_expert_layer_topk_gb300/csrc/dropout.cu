@@ -63,42 +63,6 @@ __device__ __forceinline__ bool stays(const uint4& w, int i, uint32_t drop) {
 
 // ------------------------------------------------------------- elementwise
 // out = residual + D(x), fp32 arithmetic, one rounding.
-// Eight elements as they lie in memory.
-template <typename T>
-struct Vec8;
-template <>
-struct Vec8<__nv_bfloat16> {
-  uint4 q;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { q = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ float at(int i) const {
-    const uint32_t w = i < 2 ? q.x : (i < 4 ? q.y : (i < 6 ? q.z : q.w));
-    return (i & 1) ? bf16hi(w) : bf16lo(w);
-  }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
-    *reinterpret_cast<uint4*>(p) = pack8(f);
-  }
-  static __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-  static __device__ __forceinline__ __nv_bfloat16 round(float v) { return __float2bfloat16_rn(v); }
-};
-template <>
-struct Vec8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
-  }
-  __device__ __forceinline__ float at(int i) const {
-    const float4& v = i < 4 ? a : b;
-    return (i & 3) == 0 ? v.x : ((i & 3) == 1 ? v.y : ((i & 3) == 2 ? v.z : v.w));
-  }
-  static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-  }
-  static __device__ __forceinline__ float one(const float* p) { return *p; }
-  static __device__ __forceinline__ float round(float v) { return v; }
-};
-
 // x may be out (every element is read before it is written by its thread).
 // One generator block of eight elements a thread, their vectors held as they lie
 // in memory (16.8 M bf16 elements with a residual: 15.1 us, 6.7 TB/s, fp32 30.8;

@@ -11,7 +11,7 @@
 // [E,I,H], down [E,H,I]).  fp32 weight gradients: "TorchTitan FSDP2 完全指南",
 // mixed-precision section.
 //
-// One kernel template serves ten GEMM shapes (`Kind`):
+// One kernel template serves thirteen GEMM shapes (`Kind`):
 //   GATE_UP_FWD    h = silu(A Wg^T) * (A Wu^T)  (+ save g, u)     A, B K-major
 //   GATE_UP_GATHER the same with A row r = x[token_of_row[r]]
 //   GATE_UP_FP8, GATE_UP_GATHER_FP8, DOWN_FP8: the forward kinds on e4m3
@@ -23,6 +23,8 @@
 //                  added into its token's fp32 output row (fused combine)
 //   DOWN_BWD_DX    dh = A Wd; SwiGLU backward in the epilogue     B MN-major
 //   GATE_UP_BWD_DX dx = dg Wg + du Wu (K = 2I, two B tensors)      B MN-major
+//   GATE_UP_CKPT, DOWN_BWD_CKPT: GATE_UP_FWD and DOWN_BWD_DX that write and
+//                  read g, u as 8-bit codes with a scale for each 32 columns
 //   DW             dW[g] = sum over group g's rows of A^T B (fp32) A, B MN-major
 //   DENSE_ADD      out = bf16(A B^T + add)  (router backward)     A, B K-major
 //
@@ -72,17 +74,21 @@ enum Kind : int {
   GATE_UP_FP8 = 7,
   GATE_UP_GATHER_FP8 = 8,
   DOWN_FP8 = 9,
-  DOWN_COMBINE = 10
+  DOWN_COMBINE = 10,
+  GATE_UP_CKPT = 11,
+  DOWN_BWD_CKPT = 12
 };
-constexpr int kNumKinds = 11;
+constexpr int kNumKinds = 13;
 __host__ __device__ constexpr bool is_fp8(int k) {
   return k == GATE_UP_FP8 || k == GATE_UP_GATHER_FP8 || k == DOWN_FP8;
 }
 // the gate/up forward kinds (same tiles and epilogue; they differ in how A
 // arrives and in the operand type)
 __host__ __device__ constexpr bool is_gate_up(int k) {
-  return k == GATE_UP_FWD || k == GATE_UP_GATHER || k == GATE_UP_FP8 || k == GATE_UP_GATHER_FP8;
+  return k == GATE_UP_FWD || k == GATE_UP_GATHER || k == GATE_UP_FP8 || k == GATE_UP_GATHER_FP8 || k == GATE_UP_CKPT;
 }
+// the SwiGLU-backward kinds (same tiles and operands)
+__host__ __device__ constexpr bool is_down_bwd(int k) { return k == DOWN_BWD_DX || k == DOWN_BWD_CKPT; }
 __host__ __device__ constexpr bool is_gather(int k) { return k == GATE_UP_GATHER || k == GATE_UP_GATHER_FP8; }
 // the down-projection kinds (same tiles and operands)
 __host__ __device__ constexpr bool is_down_fwd(int k) { return k == DOWN_FWD || k == DOWN_FP8 || k == DOWN_COMBINE; }
@@ -128,6 +134,12 @@ struct Params {
   float* comb_out;             // [comb_T, ldo]
   int comb_T;
   int comb_k;
+  // GATE_UP_CKPT, DOWN_BWD_CKPT: the scales of g, u [M, 2I/32] (bf16 bits).  DOWN_BWD_CKPT
+  // too: the rows' weights (null: 1), h_w, and the partial sums of d_w [2 n_tiles, M]
+  unsigned short* ckpt_scale;
+  const float* row_w;
+  void* h_w;
+  float* dw_part;
 };
 
 struct Ctl {
@@ -161,7 +173,7 @@ constexpr size_t kMaxTableBytes = seg_table_bytes(kMaxSegments, kMaxExperts, tru
 template <int KIND>
 struct Traits {
   static constexpr bool a_mn = (KIND == DW);
-  static constexpr bool b_mn = (KIND == DOWN_BWD_DX || KIND == GATE_UP_BWD_DX || KIND == DW);
+  static constexpr bool b_mn = (is_down_bwd(KIND) || KIND == GATE_UP_BWD_DX || KIND == DW);
   static constexpr bool rows = (KIND != DW);
 };
 
@@ -186,7 +198,7 @@ struct Cfg {
   // output columns per tile from a short reduction, K = I) run eight
   // epilogue warps, two per TMEM lane quadrant sharing the columns (a
   // one-box store ring each).
-  static constexpr bool EP8 = KIND == DW || KIND == DOWN_BWD_DX || is_down_fwd(KIND);
+  static constexpr bool EP8 = KIND == DW || is_down_bwd(KIND) || is_down_fwd(KIND);
   static constexpr int EPW = EP8 ? 8 : 4;
   // row-gathering kinds: four more warps share the row gather
   static constexpr int GW = is_gather(KIND) ? 4 : 0;
@@ -205,6 +217,9 @@ static_assert(Cfg<GATE_UP_FWD, 1>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
                   Cfg<DOWN_FP8, 1>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
                   Cfg<DOWN_FWD, 1>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
                   Cfg<DOWN_BWD_DX, 1>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
+                  Cfg<DOWN_BWD_CKPT, 1>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
+                  Cfg<GATE_UP_CKPT, 1>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
+                  Cfg<GATE_UP_CKPT, 2>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
                   Cfg<GATE_UP_BWD_DX, 1>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
                   Cfg<GATE_UP_BWD_DX, 2>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
                   Cfg<GATE_UP_FWD, 2>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
@@ -531,7 +546,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CTAS>::NTHREADS, 1)
             } else if constexpr (is_down_fwd(KIND) || KIND == DENSE_ADD) {
               tma_load<CTAS>(sB, &tmB0, fb, row0,
                              t.group * p.b_group_rows + t.n0 + rank * (p.BN / CTAS));
-            } else if constexpr (KIND == DOWN_BWD_DX) {
+            } else if constexpr (is_down_bwd(KIND)) {
               tma_load_mn<CTAS>(sB, &tmB0, fb, t.group * p.b_group_rows + row0, t.n0 / 64 + ck0);
             } else {  // GATE_UP_BWD_DX: k < I from Wg, k >= I from Wu
               const bool up = row0 >= p.I;
@@ -703,7 +718,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CTAS>::NTHREADS, 1)
       // that both halves of each 128-byte row segment of g, u (read) and of
       // dg, du (written) are touched at about the same time; the other kinds
       // split the columns in halves (warps 2..5 the first, 6..9 the second).
-      constexpr bool kAlt = KIND == DOWN_BWD_DX;
+      constexpr bool kAlt = is_down_bwd(KIND);
       const int sub = (warp - 2) >> 2, nsub = C::EPW / 4;
       const int cbeg = kAlt ? 32 * sub : sub * (p.BN / nsub);
       const int cstep = kAlt ? 32 * nsub : 32;
@@ -723,6 +738,30 @@ __global__ void __launch_bounds__(Cfg<KIND, CTAS>::NTHREADS, 1)
       };
       if constexpr (KIND == DOWN_BWD_DX) {
         if (any) ld_gu(cbeg, gq, uq);
+      }
+      // The same in 8 bits: 32 bytes of codes each, and the two scales.
+      uint32_t gc[8], uc[8], gsc = 0, usc = 0;
+      auto ld_codes = [&](int c, uint32_t (&g8)[8], uint32_t (&u8)[8], uint32_t& gs, uint32_t& us) {
+        const bool ok = lane < nvalid;
+        const size_t r = (size_t)(ok ? rb + lane : 0);
+        const uint4* row = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.aux) + r * 2 * p.I);
+        const int v = (t.n0 + c) >> 4, vu = (p.I + t.n0 + c) >> 4;
+        const unsigned short* sc = p.ckpt_scale + r * (p.I / 16) + ((t.n0 + c) >> 5);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 a = __ldg(row + v + i), b = __ldg(row + vu + i);
+          g8[4 * i] = a.x, g8[4 * i + 1] = a.y, g8[4 * i + 2] = a.z, g8[4 * i + 3] = a.w;
+          u8[4 * i] = b.x, u8[4 * i + 1] = b.y, u8[4 * i + 2] = b.z, u8[4 * i + 3] = b.w;
+        }
+        gs = __ldg(sc);
+        us = __ldg(sc + p.I / 32);
+      };
+      float row_w = 1.0f, row_dw = 0.0f;
+      if constexpr (KIND == DOWN_BWD_CKPT) {
+        if (any) {
+          ld_codes(cbeg, gc, uc, gsc, usc);
+          if (p.row_w && lane < nvalid) row_w = __ldg(p.row_w + rb + lane);
+        }
       }
       // FP8 kinds: this lane's row scale (the scale of its token when
       // gathering) and the expert's output-channel scales, lane L holding
@@ -749,7 +788,67 @@ __global__ void __launch_bounds__(Cfg<KIND, CTAS>::NTHREADS, 1)
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * ACC_COLS);
 
 
-      if constexpr (is_gate_up(KIND)) {
+      if constexpr (KIND == GATE_UP_CKPT) {
+        // h as below; g and u as codes: a lane holds a row's 32 columns, so a
+        // group's amax is its own.  The box takes 32 bytes of g's codes and 32 of
+        // u's a row; the tile's scales (2 or 4 each of g and u) leave together.
+        const size_t hp_pitch = (size_t)p.I * 2;
+        uint32_t gsc[2] = {0, 0}, usc[2] = {0, 0};
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          const int c = 32 * cc;
+          if (!any || c >= p.NH) break;
+          uint32_t g[32], u[32];
+          tmem_ld32(taddr + c, g);
+          tmem_ld32(taddr + p.NH + c, u);
+          tmem_wait_ld();
+          uint32_t hp[16], code[16];
+          float gm = 0.f, um = 0.f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float g0 = f32(g[2 * i]), g1 = f32(g[2 * i + 1]);
+            const float u0 = f32(u[2 * i]), u1 = f32(u[2 * i + 1]);
+            hp[i] = pack_bf16x2(__fdividef(g0, 1.0f + __expf(-g0)) * u0, __fdividef(g1, 1.0f + __expf(-g1)) * u1);
+            gm = amax_nan(amax_nan(gm, g0), g1);
+            um = amax_nan(amax_nan(um, u0), u1);
+          }
+          const float gs = ckpt_scale(gm), us = ckpt_scale(um);
+          const float gi = __frcp_rn(gs), ui = __frcp_rn(us);
+          gsc[cc >> 1] |= (__float_as_uint(gs) >> 16) << (16 * (cc & 1));
+          usc[cc >> 1] |= (__float_as_uint(us) >> 16) << (16 * (cc & 1));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            code[i] = ckpt_codes4(f32(g[4 * i]), f32(g[4 * i + 1]), f32(g[4 * i + 2]), f32(g[4 * i + 3]), gi);
+            code[8 + i] = ckpt_codes4(f32(u[4 * i]), f32(u[4 * i + 1]), f32(u[4 * i + 2]), f32(u[4 * i + 3]), ui);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) put(ep_base, i, make_uint4(hp[4 * i], hp[4 * i + 1], hp[4 * i + 2], hp[4 * i + 3]));
+          flush(ep_base, p.out0, hp_pitch, (size_t)(t.n0 + c) * 2, rb, nvalid, false);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            put(ep_base, i, make_uint4(code[4 * i], code[4 * i + 1], code[4 * i + 2], code[4 * i + 3]));
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int rr = (lane >> 2) + 8 * j, piece = lane & 3;
+            const uint4 v = *reinterpret_cast<const uint4*>(ep_base + rr * 64 + ((piece ^ ((rr >> 1) & 3)) << 4));
+            if (rr < nvalid)
+              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out1) + (size_t)(rb + rr) * 2 * p.I +
+                                        (piece < 2 ? 0 : p.I) + t.n0 + c + 16 * (piece & 1)) = v;
+          }
+          __syncwarp();
+        }
+        if (lane < nvalid) {
+          unsigned short* sc = p.ckpt_scale + (size_t)(rb + lane) * (p.I / 16) + (t.n0 >> 5);
+          if (p.NH == 128) {
+            *reinterpret_cast<uint2*>(sc) = make_uint2(gsc[0], gsc[1]);
+            *reinterpret_cast<uint2*>(sc + p.I / 32) = make_uint2(usc[0], usc[1]);
+          } else {
+            *reinterpret_cast<uint32_t*>(sc) = gsc[0];
+            *reinterpret_cast<uint32_t*>(sc + p.I / 32) = usc[0];
+          }
+        }
+      } else if constexpr (is_gate_up(KIND)) {
         const size_t hp_pitch = (size_t)p.I * 2, gu_pitch = (size_t)p.I * 4;
         for (int c = 0; any && c < p.NH; c += 32) {
           float nx0 = 0.0f, nx1 = 0.0f;  // FP8: the next chunk's column scales
@@ -954,6 +1053,60 @@ __global__ void __launch_bounds__(Cfg<KIND, CTAS>::NTHREADS, 1)
             uq[i] = un[i];
           }
         }
+      } else if constexpr (KIND == DOWN_BWD_CKPT) {
+        // As the kind above, with g and u decoded from codes (loaded one chunk
+        // ahead) and the row's weight applied here: dgu, the weighted h (the
+        // weight gradient's operand), and the row's sum of dh h over this warp's
+        // columns, one of 2 n_tiles parts of it.
+        const size_t pitch = (size_t)p.I * 4;
+        for (int c = cbeg; any && c < cend; c += cstep) {
+          uint32_t gn[8], un[8], gsn = 0, usn = 0;
+          if (c + cstep < cend) ld_codes(c + cstep, gn, un, gsn, usn);
+          uint32_t a[32];
+          tmem_ld32(taddr + c, a);
+          tmem_wait_ld();
+          const float gs = bf16_bits(gsc), us = bf16_bits(usc);
+          uint32_t og[16], ou[16], oh[16];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float g4[4], u4[4], dg[4], du[4], hw[4];
+            ckpt_decode4(gc[i], gs, g4);
+            ckpt_decode4(uc[i], us, u4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float g = g4[j], u = u4[j], dh = f32(a[4 * i + j]);
+              const float sg = __fdividef(1.0f, 1.0f + __expf(-g));
+              const float silu = g * sg, h = silu * u, dhw = dh * row_w;
+              row_dw = __fmaf_rn(dh, h, row_dw);
+              dg[j] = dhw * u * sg * (1.0f + g * (1.0f - sg));
+              du[j] = dhw * silu;
+              hw[j] = row_w * h;
+            }
+            og[2 * i] = pack_bf16x2(dg[0], dg[1]), og[2 * i + 1] = pack_bf16x2(dg[2], dg[3]);
+            ou[2 * i] = pack_bf16x2(du[0], du[1]), ou[2 * i + 1] = pack_bf16x2(du[2], du[3]);
+            oh[2 * i] = pack_bf16x2(hw[0], hw[1]), oh[2 * i + 1] = pack_bf16x2(hw[2], hw[3]);
+          }
+          auto leave = [&](const uint32_t (&o)[16], const CUtensorMap* map, void* base, size_t row_bytes, int col) {
+            uint8_t* bx = ring.acquire();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) put(bx, i, make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]));
+            if (nvalid == 32)
+              ring.issue(bx, map, col, rb);
+            else  // the last rows of a segment: masked row stores
+              flush(bx, base, row_bytes, (size_t)col * 2, rb, nvalid, false);
+          };
+          leave(og, &tmO0, p.out0, pitch, t.n0 + c);
+          leave(ou, &tmO0, p.out0, pitch, p.I + t.n0 + c);
+          leave(oh, &tmO1, p.h_w, (size_t)p.I * 2, t.n0 + c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            gc[i] = gn[i];
+            uc[i] = un[i];
+          }
+          gsc = gsn;
+          usc = usn;
+        }
+        if (lane < nvalid) p.dw_part[(size_t)(2 * (t.n0 / p.BN) + sub) * p.M + rb + lane] = row_dw;
       } else {  // DW: fp32 [group, M, N] (optionally split at split_m over two tensors)
         const bool nonempty = ctl->grp_rows[t.group] > 0;
         if (any && (nonempty || !p.accumulate)) {
@@ -1013,6 +1166,24 @@ __global__ void __launch_bounds__(Cfg<KIND, CTAS>::NTHREADS, 1)
 // address is moved to segment s's first row and whose row extent is the
 // segment's length (rows clamped to [0, rows) like the kernel's own table).
 // An empty segment keeps the template unchanged; no k-block ever reads it.
+// d_w of the 8-bit SwiGLU backward: a row's parts added in their order, for each slot
+// (row_of_slot) or each row.
+__global__ void __launch_bounds__(256) ckpt_dw_kernel(const float* __restrict__ part, int parts, int R,
+                                                      const int32_t* __restrict__ row_of_slot, int n, float* __restrict__ d_w,
+                                                      int* status) {
+  pdl_wait();
+  pdl_trigger();
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) {
+    const int row = row_of_slot ? __ldg(row_of_slot + i) : i;
+    float v = 0.f;
+    if (row < 0 || row >= R)
+      set_status(status, MOE_STATUS_BAD_INDEX);
+    else
+      for (int q = 0; q < parts; ++q) v += __ldg(part + (size_t)q * R + row);
+    d_w[i] = v;
+  }
+}
+
 // y = bf16(acc) (round to nearest even), eight elements per step.
 __global__ void __launch_bounds__(256) f32_to_bf16_kernel(const float* __restrict__ acc, __nv_bfloat16* __restrict__ y,
                                                           size_t n8) {
@@ -1094,7 +1265,7 @@ template <int KIND, int CTAS>
 int launch(Params p, const CUtensorMap& a, const CUtensorMap& b0, const CUtensorMap& b1,
            const CUtensorMap& o0, const CUtensorMap& o1, cudaStream_t s, const char* what) {
   constexpr bool a_mn = KIND == DW;
-  constexpr bool b_mn = KIND == DOWN_BWD_DX || KIND == GATE_UP_BWD_DX || KIND == DW;
+  constexpr bool b_mn = is_down_bwd(KIND) || KIND == GATE_UP_BWD_DX || KIND == DW;
   p.idesc = make_idesc(p.BN, BM * CTAS, a_mn, b_mn, is_fp8(KIND));
   long long upper;
   if (KIND == DW) {
@@ -1148,7 +1319,8 @@ int launch(Params p, const CUtensorMap& a, const CUtensorMap& b0, const CUtensor
 template <int KIND>
 int run(bool pair, const Params& p, const CUtensorMap& a, const CUtensorMap& b0, const CUtensorMap& b1,
         const CUtensorMap& o0, const CUtensorMap& o1, cudaStream_t s, const char* what) {
-  if constexpr (KIND == GATE_UP_BWD_DX || KIND == GATE_UP_FWD || KIND == DOWN_FWD || KIND == DOWN_COMBINE) {
+  if constexpr (KIND == GATE_UP_BWD_DX || KIND == GATE_UP_FWD || KIND == GATE_UP_CKPT || KIND == DOWN_FWD ||
+                KIND == DOWN_COMBINE) {
     if (pair) return launch<KIND, 2>(p, a, b0, b1, o0, o1, s, what);
   }
   return launch<KIND, 1>(p, a, b0, b1, o0, o1, s, what);
@@ -1265,7 +1437,7 @@ namespace tc {
 // x[gather_rows[r]] (rows copied by cp.async in the producer warp).
 int swiglu_impl(const void* a_src, const int32_t* gather_rows, int T, const void* Wg, const void* Wu,
                 int num_seg, const int32_t* seg_offsets, const int32_t* seg_expert, int R, int H,
-                int I, int E, void* h, void* gu_save, cudaStream_t s, const char* fn) {
+                int I, int E, void* h, void* gu_save, cudaStream_t s, const char* fn, void* gu_scale = nullptr) {
   Params p = base_params(num_seg, seg_offsets, seg_expert, E);
   p.M = R;
   p.N = I;
@@ -1290,13 +1462,17 @@ int swiglu_impl(const void* a_src, const int32_t* gather_rows, int T, const void
   if (int rc = make_tmap(&tu, Wu, H, (uint64_t)E * I, 64, p.NH)) return rc;
   CUtensorMap th, tgu;
   if (int rc = make_out_map(&th, h, I, R, false)) return rc;
-  if (int rc = make_out_map(&tgu, gu_save ? gu_save : h, gu_save ? 2 * I : I, R, false)) return rc;
+  if (int rc = make_out_map(&tgu, gu_save && !gu_scale ? gu_save : h, gu_save && !gu_scale ? 2 * I : I, R, false)) return rc;
   if (gather_rows) return run<GATE_UP_GATHER>(false, p, ta, tg, tu, th, tgu, s, fn);
   // Cluster pairs (the leader loads the gate rows of B, the peer the up rows)
   // by pair_for_rows.  With several segments per expert (the EP receive
   // layout) each expert's weights stay in L2 across its segments and the
   // 256-row tiles waste more rows: single CTAs measured faster there.
   const bool pair = pair_for_rows(p.BN, R, num_seg, E);
+  if (gu_scale) {
+    p.ckpt_scale = static_cast<unsigned short*>(gu_scale);
+    return run<GATE_UP_CKPT>(pair, p, ta, tg, tu, th, th, s, fn);
+  }
   return run<GATE_UP_FWD>(pair, p, ta, tg, tu, th, tgu, s, fn);
 }
 
@@ -1375,6 +1551,20 @@ int moe_grouped_gemm_swiglu(const void* x_perm, const void* Wg, const void* Wu, 
   if (R == 0 || num_seg == 0) return MOE_OK;
   return swiglu_impl(x_perm, nullptr, 0, Wg, Wu, num_seg, seg_offsets, seg_expert, R, H, I, E, h,
                      gu_save, static_cast<cudaStream_t>(stream), fn);
+}
+
+int moe_grouped_gemm_swiglu_ckpt(const void* x_perm, const void* Wg, const void* Wu, int num_seg,
+                                 const int32_t* seg_offsets, const int32_t* seg_expert, int R, int H, int I, int E,
+                                 void* h, void* gu_q, void* gu_scale, void* stream) {
+  clear_error();
+  const char* fn = "moe_grouped_gemm_swiglu_ckpt";
+  if (int rc = check_grouped(fn, num_seg, seg_offsets, R, H, I, E)) return rc;
+  if (R == 0 || num_seg == 0) return MOE_OK;
+  if (!x_perm || !Wg || !Wu || !h || !gu_q || !gu_scale) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer argument", fn);
+  if (!aligned16(x_perm) || !aligned16(Wg) || !aligned16(Wu) || !aligned16(h) || !aligned16(gu_q) || !aligned16(gu_scale))
+    return fail(MOE_ERR_ALIGNMENT, "%s: tensors must be 16-byte aligned", fn);
+  return swiglu_impl(x_perm, nullptr, 0, Wg, Wu, num_seg, seg_offsets, seg_expert, R, H, I, E, h, gu_q,
+                     static_cast<cudaStream_t>(stream), fn, gu_scale);
 }
 
 int moe_grouped_gemm_swiglu_gather(const void* x, const int32_t* token_of_row, int T,
@@ -1556,6 +1746,63 @@ static int down_bwd_dx(const void* dy_perm, const void* gu_save, const void* Wd,
   CUtensorMap to;
   if (int rc = make_out_map(&to, dgu, 2 * I, R, false)) return rc;
   return run<DOWN_BWD_DX>(false, p, ta, tb, tb, to, to, s, fn);
+}
+
+// two parts (the two warps of a TMEM lane quadrant) for each column tile
+static size_t ckpt_dw_bytes(int R, int I) {
+  return R > 0 && I > 0 && I % 64 == 0 ? sizeof(float) * 2 * (size_t)(I / pick_bn(I)) * R : 0;
+}
+
+size_t moe_grouped_gemm_down_bwd_ckpt_workspace_size(int R, int I) { return ckpt_dw_bytes(R, I); }
+
+int moe_grouped_gemm_down_bwd_ckpt(const void* dy_perm, const float* row_w, const void* gu_q, const void* gu_scale,
+                                   const void* Wd, int num_seg, const int32_t* seg_offsets, const int32_t* seg_expert,
+                                   int R, int H, int I, int E, void* dgu, void* h_w, const int32_t* row_of_slot, int T,
+                                   int k, float* d_w, void* ws, size_t ws_bytes, void* stream) {
+  clear_error();
+  const char* fn = "moe_grouped_gemm_down_bwd_ckpt";
+  if (int rc = check_grouped(fn, num_seg, seg_offsets, R, H, I, E)) return rc;
+  if (row_of_slot && (T < 0 || k < 1 || k > kMaxTopK || (long long)T * k > R))
+    return fail(MOE_ERR_INVALID_ARG, "%s: need T>=0, 1<=k<=32, T*k<=R", fn);
+  if (R == 0) return MOE_OK;
+  if (!dy_perm || !gu_q || !gu_scale || !Wd || !dgu || !h_w || !d_w) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer argument", fn);
+  if (!aligned16(dy_perm) || !aligned16(gu_q) || !aligned16(gu_scale) || !aligned16(Wd) || !aligned16(dgu) || !aligned16(h_w))
+    return fail(MOE_ERR_ALIGNMENT, "%s: tensors must be 16-byte aligned", fn);
+  const size_t need = ckpt_dw_bytes(R, I);
+  if (!ws || ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws ? ws_bytes : (size_t)0, need);
+  if (!aligned16(ws)) return fail(MOE_ERR_ALIGNMENT, "%s: ws must be 16-byte aligned", fn);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // rows outside every segment leave no part
+  cudaError_t e = cudaMemsetAsync(ws, 0, need, s);
+  if (e != cudaSuccess) return fail_cuda(fn, e);
+  const int bn = pick_bn(I);
+  if (num_seg > 0) {
+    Params p = base_params(num_seg, seg_offsets, seg_expert, E);
+    p.M = R;
+    p.N = I;
+    p.K = H;
+    p.BN = bn;
+    p.n_tiles = I / bn;
+    p.b_group_rows = H;
+    p.I = I;
+    p.out0 = dgu;
+    p.aux = gu_q;
+    p.ckpt_scale = static_cast<unsigned short*>(const_cast<void*>(gu_scale));
+    p.row_w = row_w;
+    p.h_w = h_w;
+    p.dw_part = static_cast<float*>(ws);
+    CUtensorMap ta, tb, to, th;
+    if (int rc = make_tmap(&ta, dy_perm, H, R, 64, BM)) return rc;
+    if (int rc = make_tmap_mn(&tb, Wd, I, (uint64_t)E * H, bn / 64)) return rc;
+    if (int rc = make_out_map(&to, dgu, 2 * I, R, false)) return rc;
+    if (int rc = make_out_map(&th, h_w, I, R, false)) return rc;
+    if (int rc = run<DOWN_BWD_CKPT>(false, p, ta, tb, tb, to, th, s, fn)) return rc;
+  }
+  const int n = row_of_slot ? T * k : R;
+  if (n == 0) return MOE_OK;
+  launch_pdl(ckpt_dw_kernel, (n + 255) / 256, 256, 0, s, static_cast<const float*>(ws), 2 * (I / bn), R, row_of_slot, n, d_w,
+             status_word());
+  return check_launch(fn);
 }
 
 // dWd[e] = dy_perm[rows of e]^T . h[rows of e]
