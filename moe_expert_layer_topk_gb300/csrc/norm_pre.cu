@@ -130,10 +130,10 @@ __global__ void __launch_bounds__(256) norm_gain_sum_kernel(const float* __restr
   s[y][x] = v;
   __syncthreads();
   if (y == 0 && h < H) {
-    v = accumulate ? dgain[h] : 0.f;
+    v = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v += s[i][x];
-    dgain[h] = v;
+    dgain[h] = accumulate ? dgain[h] + v : v;
   }
 }
 

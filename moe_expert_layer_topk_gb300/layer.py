@@ -1,5 +1,6 @@
-"""Buffers and call order of one MoE expert layer, and of a projection with
-per-request adapters, over the C entry points.
+"""Buffers and call order of one MoE expert layer, of the block around it
+(norms, gate, residual), and of a projection with per-request adapters, over
+the C entry points.
 
 `MoELayer` owns the device tensors one layer needs for a fixed token count
 (outputs, activations kept for the backward pass, gradients, workspaces),
@@ -12,13 +13,15 @@ import torch
 
 from . import (moe_adapter_hidden_size, moe_adapter_linear, moe_adapter_linear_bwd,
                moe_adapter_linear_bwd_workspace_size, moe_balance_loss, moe_balance_loss_bwd, moe_balance_loss_workspace_size,
-               moe_combine, moe_combine_bwd,
-               moe_combine_dropout, moe_combine_dropout_bwd, moe_dispatch_bwd, moe_dispatch_chunked,
-               moe_dispatch_e4m3_chunked, moe_grouped_gemm_bwd_workspace_size,
-               moe_grouped_gemm_down, moe_grouped_gemm_down_bwd, moe_grouped_gemm_down_combine,
+               moe_ckpt_pack, moe_ckpt_unpack, moe_combine, moe_combine_bwd,
+               moe_combine_dropout, moe_combine_dropout_bwd, moe_combine_post_norm, moe_dispatch_bwd, moe_dispatch_chunked,
+               moe_dispatch_e4m3_chunked, moe_dispatch_rows, moe_dropout, moe_grouped_gemm_bwd_workspace_size,
+               moe_grouped_gemm_down, moe_grouped_gemm_down_bwd, moe_grouped_gemm_down_bwd_ckpt,
+               moe_grouped_gemm_down_bwd_ckpt_workspace_size, moe_grouped_gemm_down_bwd_dw, moe_grouped_gemm_down_combine,
                moe_grouped_gemm_down_fp8,
                moe_grouped_gemm_swiglu, moe_grouped_gemm_swiglu_bwd_dw, moe_grouped_gemm_swiglu_bwd_dx,
-               moe_grouped_gemm_swiglu_fp8, moe_set_gemm_sm_limit, sm_count,
+               moe_grouped_gemm_swiglu_ckpt, moe_grouped_gemm_swiglu_fp8, moe_post_norm_bwd, moe_post_norm_bwd_workspace_size,
+               moe_pre_norm, moe_pre_norm_bwd, moe_pre_norm_bwd_workspace_size, moe_set_gemm_sm_limit, sm_count,
                moe_grouped_gemm_swiglu_gather, moe_quantize_rows_e4m3, moe_route_topk_bwd,
                moe_route_topk_bwd_workspace_size, moe_route_topk_chunks,
                moe_route_topk_chunks_workspace_size, moe_route_topk_logits, moe_route_topk_logits_bwd)
@@ -59,13 +62,31 @@ class MoELayer:
     counter-based dropout of moe_combine_dropout; the backward computes the
     same mask again from `rng` (int64 [2] on the device: seed, offset), so
     rng has to hold the forward's words until the backward has run.
-    `advance_rng` moves the offset past the layer's own counters."""
+    `advance_rng` moves the offset past the layer's own counters.
+
+    checkpoint (training): between forward and backward the layer keeps g and
+    u in 8 bits (moe_grouped_gemm_swiglu_ckpt) and the routing, and nothing
+    else of its activations; x_perm, h and y_perm are scratch, made again in
+    the backward where it needs them.  share: another checkpointed layer of
+    the same sizes on the same device, whose scratch this one uses as well
+    (the layers of a model run one after another on one stream), so that
+    only the kept tensors, the outputs and the gradients are a layer's own.
+    checkpoint_input: x is kept in 8 bits too, and the backward's x may be
+    None.  Gradients are those of the kept values: about 1% off."""
 
     def __init__(self, T: int, H: int, I: int, E: int, k: int, ep_size: int = 1, *,
                  training: bool = True, fused_dispatch: bool = False, fp8: bool = False,
                  fused_combine: bool = False, balance_coef: float = 0.0, z_coef: float = 0.0,
                  sequences: int = 1, dropout: float = 0.0, seed: int = 0,
+                 checkpoint: bool = False, checkpoint_input: bool = False, share: "MoELayer | None" = None,
                  device: str | torch.device = "cuda"):
+        if checkpoint and not training:
+            raise ValueError("checkpoint belongs to a training layer")
+        if (checkpoint_input or share is not None) and not checkpoint:
+            raise ValueError("checkpoint_input and share belong to a checkpointed layer")
+        if share is not None and (not share.checkpoint or (share.T, share.H, share.I, share.E, share.k) != (T, H, I, E, k)
+                                  or share.y.device != torch.empty(0, device=device).device):
+            raise ValueError("share must be a checkpointed layer of the same sizes on the same device")
         if fp8 and training:
             raise ValueError("the e4m3 path is forward only")
         if fused_combine and (training or fp8):
@@ -80,6 +101,7 @@ class MoELayer:
         self.fused_dispatch = fused_dispatch
         self.fused_combine = fused_combine
         self.fp8 = fp8
+        self.checkpoint, self.checkpoint_input = checkpoint, checkpoint_input
         self.balance_coef, self.z_coef, self.sequences, self.dropout = balance_coef, z_coef, sequences, dropout
         self.balanced = bool(balance_coef or z_coef)
         self._x = None
@@ -93,34 +115,44 @@ class MoELayer:
         self.counts = e(E, dt=i32)
         self.offsets = e(E + 1, dt=i32)
         self.rank_offsets = e(ep_size + 1, dt=i32)
-        self.ws_route = _ws(moe_route_topk_chunks_workspace_size(T, H, E), dev)
+        own = share is None
+        self.ws_route = _ws(moe_route_topk_chunks_workspace_size(T, H, E), dev) if own else share.ws_route
         # where each 16-token chunk starts in each expert's rows (from the route, for the dispatch)
         self.chunk_prefix = e(E, (T + 15) // 16, dt=i32)
-        self.x_perm = None if (fused_dispatch or fp8) else e(R, H, dt=bf)
+        self.x_perm = None if (fused_dispatch or fp8) else e(R, H, dt=bf) if own else share.x_perm
         self.row_of_slot = e(T, k, dt=i32)
         self.token_of_row = e(R, dt=i32)
-        self.h = e(R, I, dt=bf)
-        self.gu = e(R, 2 * I, dt=bf) if training else None
-        self.y_perm = None if fused_combine else e(R, H, dt=bf)
+        self.h = e(R, I, dt=bf) if own else share.h
+        self.gu = e(R, 2 * I, dt=bf) if training and not checkpoint else None
+        self.y_perm = None if fused_combine else e(R, H, dt=bf) if own else share.y_perm
         self.y_acc = e(T, H, dt=f32) if fused_combine else None
         self.y = e(T, H, dt=bf)
         if fp8:
             u8 = torch.uint8
             self.x_q, self.x_scale = e(R, H, dt=u8), e(R, dt=f32)  # permuted rows, their tokens' scales
             self.h_q, self.h_scale = e(R, I, dt=u8), e(R, dt=f32)
+        if checkpoint:
+            i8 = torch.int8
+            self.gu_q, self.gu_scale = e(R, 2 * I, dt=i8), e(R, 2 * I // 32, dt=bf)
+            if checkpoint_input:
+                self.x_kept, self.x_kept_scale = e(T, H, dt=i8), e(T, H // 32, dt=bf)
+            # the tokens' values where they are made again: x from its codes, or dy under the dropout's mask
+            self.tokens = e(T, H, dt=bf) if own else share.tokens
+            self.row_w = e(R, dt=f32) if own else share.row_w
+            self.ws_ckpt = _ws(moe_grouped_gemm_down_bwd_ckpt_workspace_size(R, I), dev) if own else share.ws_ckpt
         if training:
-            self.dy_perm = e(R, H, dt=bf)
+            self.dy_perm = e(R, H, dt=bf) if own else share.dy_perm
             self.d_w = e(T, k, dt=f32)
-            self.dgu = e(R, 2 * I, dt=bf)
-            self.dx_perm = e(R, H, dt=bf)
-            self.dx_acc = e(T, H, dt=f32)
+            self.dgu = e(R, 2 * I, dt=bf) if own else share.dgu
+            self.dx_perm = e(R, H, dt=bf) if own else share.dx_perm
+            self.dx_acc = e(T, H, dt=f32) if own else share.dx_acc
             self.dx = e(T, H, dt=bf)
             self.dWg = e(E, I, H, dt=f32)
             self.dWu = e(E, I, H, dt=f32)
             self.dWd = e(E, H, I, dt=f32)
             self.dWr = e(H, E, dt=f32)
-            self.ws_route_bwd = _ws(moe_route_topk_bwd_workspace_size(T, H, E), dev)
-            self.ws_gemm_bwd = _ws(moe_grouped_gemm_bwd_workspace_size(E), dev)
+            self.ws_route_bwd = _ws(moe_route_topk_bwd_workspace_size(T, H, E), dev) if own else share.ws_route_bwd
+            self.ws_gemm_bwd = _ws(moe_grouped_gemm_bwd_workspace_size(E), dev) if own else share.ws_gemm_bwd
         if self.balanced:
             self.logits, self.dlogits = e(T, E, dt=f32), e(T, E, dt=f32)
             self.seq_counts, self.seq_tokens = e(sequences, E, dt=i32), e(sequences, dt=i32)
@@ -156,6 +188,8 @@ class MoELayer:
             moe_dispatch_e4m3_chunked(x, self.topk_idx, self.offsets, self.chunk_prefix, self.T, self.H, self.E,
                                       self.k, self.x_q, self.x_scale, self.row_of_slot, self.token_of_row, stream)
             return
+        if self.checkpoint_input:
+            moe_ckpt_pack(x, self.T, self.H, self.x_kept, self.x_kept_scale, stream)
         moe_dispatch_chunked(x, self.topk_idx, self.offsets, self.chunk_prefix, self.T, self.H, self.E, self.k,
                              self.x_perm, self.row_of_slot, self.token_of_row, stream)
 
@@ -177,8 +211,12 @@ class MoELayer:
                                            self.offsets, None, self.R, self.H, self.I, self.E, self.h,
                                            None, stream)
         else:
-            moe_grouped_gemm_swiglu(self.x_perm, Wg, Wu, self.E, self.offsets, None, self.R, self.H,
-                                    self.I, self.E, self.h, self.gu, None, stream)
+            if self.checkpoint:
+                moe_grouped_gemm_swiglu_ckpt(self.x_perm, Wg, Wu, self.E, self.offsets, None, self.R, self.H, self.I, self.E,
+                                             self.h, self.gu_q, self.gu_scale, stream)
+            else:
+                moe_grouped_gemm_swiglu(self.x_perm, Wg, Wu, self.E, self.offsets, None, self.R, self.H,
+                                        self.I, self.E, self.h, self.gu, None, stream)
         if self.fused_combine:
             moe_grouped_gemm_down_combine(self.h, Wd, self.E, self.offsets, None, self.R, self.H, self.I,
                                           self.E, self.token_of_row, self.row_of_slot, self.topk_w, self.T,
@@ -264,6 +302,7 @@ class MoELayer:
     def backward(self, dy, x, Wr, Wg, Wu, Wd, accumulate: bool = False, stream=None, dx=None,
                  overlap: bool = True, dloss=None):
         """dx: optional bf16 [T,H] output tensor (default: the layer's own).
+        x: the forward's, or None for a checkpoint_input layer.
 
         dloss: fp32 [2] on the device, the upstream gradients of the two
         router losses (loss scaling, the weight of a micro-batch; default
@@ -284,14 +323,19 @@ class MoELayer:
             moe_balance_loss_bwd(self.logits, mask, T, E, k, self.sequences, seg_offsets, self.seq_counts, self.seq_tokens,
                                  self.balance_coef, self.z_coef, dloss, self.dlogits, stream)
             self._upstream = dloss is not None
-        if self.dropout:
+        if x is None and not self.checkpoint_input:
+            raise ValueError("the backward needs x unless the layer keeps it (checkpoint_input)")
+        if self.checkpoint:
+            x = self._experts_bwd_checkpointed(dy, x, Wd, accumulate, stream)
+        elif self.dropout:
             moe_combine_dropout_bwd(dy, self.y_perm, self.topk_w, self.row_of_slot, T, H, k, self.dropout, self.rng,
                                     self.dy_perm, self.d_w, stream)
         else:
             moe_combine_bwd(dy, self.y_perm, self.topk_w, self.row_of_slot, T, H, k, self.dy_perm,
                             self.d_w, stream)
-        moe_grouped_gemm_down_bwd(self.dy_perm, self.h, self.gu, Wd, E, self.offsets, None, R, H, I,
-                                  E, self.dgu, self.dWd, accumulate, self.ws_gemm_bwd, stream)
+        if not self.checkpoint:
+            moe_grouped_gemm_down_bwd(self.dy_perm, self.h, self.gu, Wd, E, self.offsets, None, R, H, I,
+                                      E, self.dgu, self.dWd, accumulate, self.ws_gemm_bwd, stream)
         moe_grouped_gemm_swiglu_bwd_dx(self.dgu, Wg, Wu, E, self.offsets, None, R, H, I, E, self.dx_perm,
                                        stream)
         tail = stream
@@ -322,6 +366,133 @@ class MoELayer:
         if overlap:
             self._ev_join.record(self._side)
             main.wait_event(self._ev_join)
+        return dx
+
+
+    def _experts_bwd_checkpointed(self, dy, x, Wd, accumulate, stream):
+        """The backward of combine and down projection from the kept codes (fills d_w, dgu and
+        dWd), and the experts' rows of x made again; returns the x that the router's backward uses."""
+        T, H, I, E, k, R = self.T, self.H, self.I, self.E, self.k, self.R
+        if self.dropout:
+            moe_dropout(dy, None, T * H, self.dropout, self.rng, self.tokens, stream)
+            dy = self.tokens
+        moe_dispatch_rows(dy, None, self.row_of_slot, self.topk_w, T, H, k, self.dy_perm, self.row_w, stream)
+        moe_grouped_gemm_down_bwd_ckpt(self.dy_perm, self.row_w, self.gu_q, self.gu_scale, Wd, E, self.offsets, None, R, H, I,
+                                       E, self.dgu, self.h, self.d_w, self.row_of_slot, T, k, self.ws_ckpt, stream)
+        moe_grouped_gemm_down_bwd_dw(self.dy_perm, self.h, E, self.offsets, None, R, H, I, E, self.dWd, accumulate,
+                                     self.ws_gemm_bwd, stream)
+        if x is None:
+            moe_ckpt_unpack(self.x_kept, self.x_kept_scale, T, H, self.tokens, stream)
+            x = self.tokens
+        moe_dispatch_rows(x, None, self.row_of_slot, None, T, H, k, self.x_perm, None, stream)
+        return x
+
+
+class MoEBlock:
+    """An MoE layer between its norms, with the block's gate and the residual:
+
+        out = res_scale x + out_scale sigmoid(gate) norm(MoE(norm(x) pre_gain)) post_gain
+
+    over moe_pre_norm, MoELayer and moe_combine_post_norm.  The residual
+    stream (x, out, dout, dx) is bf16, or fp32 with fp32=True.  gate: None,
+    "token" (fp32 logits [T]) or "element" (bf16 logits [T,H]).  post_norm
+    False leaves the second norm out (its gain stays).  Further options are
+    MoELayer's (`checkpoint` and `share`, the router losses; no dropout).
+
+    Gains are fp32 [H] or None (ones).  Blocks one after another: with
+    next_norm=True a block also computes the next one's normed input on the
+    way, with that one's pre_gain as next_gain, and leaves it and its rstd in
+    `next_normed`, which that one's forward takes as `normed`.
+
+    After the backward: d_pre_gain, d_post_gain (fp32 [H]), d_gate (like the
+    gate), and the layer's gradients (`layer.dWg` ...).  A checkpointed
+    block keeps z (bf16 [T,H]) beside what its layer keeps, and norms x
+    again in the backward."""
+
+    def __init__(self, T: int, H: int, I: int, E: int, k: int, ep_size: int = 1, *, gate: str | None = None,
+                 post_norm: bool = True, eps: float = 1e-6, res_scale: float = 1.0, out_scale: float = 1.0, fp32: bool = False,
+                 next_norm: bool = False, training: bool = True, share: "MoEBlock | None" = None,
+                 device: str | torch.device = "cuda", **options):
+        if gate not in (None, "token", "element"):
+            raise ValueError("gate must be None, 'token' or 'element'")
+        if options.get("dropout") or options.get("fused_combine") or options.get("checkpoint_input"):
+            raise ValueError("a block takes no dropout, fused_combine or checkpoint_input")
+        self.layer = MoELayer(T, H, I, E, k, ep_size, training=training, share=share.layer if share is not None else None,
+                              device=device, **options)
+        self.T, self.H, self.training, self.gate, self.post_norm = T, H, training, gate, post_norm
+        self.eps, self.res_scale, self.out_scale = eps, res_scale, out_scale
+        dev = torch.device(device)
+        e = lambda *s, dt: torch.empty(*s, dtype=dt, device=dev)  # noqa: E731
+        f32, bf = torch.float32, torch.bfloat16
+        stream_type = f32 if fp32 else bf
+        self.checkpoint = self.layer.checkpoint
+        self.n = share.n if share is not None else e(T, H, dt=bf)
+        self.rstd = e(T, dt=f32)
+        self.out = e(T, H, dt=stream_type)
+        # a checkpointed block has no more use for n by then
+        self.next_n = (self.n if self.checkpoint else e(T, H, dt=bf)) if next_norm else None
+        self.next_rstd = e(T, dt=f32) if next_norm else None
+        self._normed = None
+        self.z = self.post_rstd = None
+        if training:
+            self.z, self.post_rstd = e(T, H, dt=bf), e(T, dt=f32) if post_norm else None
+            self.dz = e(T, H, dt=bf) if share is None else share.dz
+            self.dx = e(T, H, dt=stream_type)
+            self.d_pre_gain, self.d_post_gain = e(H, dt=f32), e(H, dt=f32)
+            self.d_gate = e(T, dt=f32) if gate == "token" else e(T, H, dt=bf) if gate == "element" else None
+            self.ws_norm = _ws(max(moe_pre_norm_bwd_workspace_size(T, H), moe_post_norm_bwd_workspace_size(T, H)), dev)
+
+    @property
+    def next_normed(self):
+        """The next block's normed input and its rstd (after a forward, with next_norm)."""
+        return self.next_n, self.next_rstd
+
+    def _check_gate(self, gate):
+        if (gate is None) != (self.gate is None):
+            raise ValueError("the block was built %s a gate" % ("without" if self.gate is None else "with"))
+        if gate is not None and gate.dtype != (torch.float32 if self.gate == "token" else torch.bfloat16):
+            raise ValueError("a token's gate is fp32, an element's bf16")
+
+    def forward(self, x, pre_gain, post_gain, Wr, bias, Wg, Wu, Wd, gate=None, stream=None, out=None, *, normed=None,
+                next_gain=None, mask=None, seg_offsets=None):
+        """out (default: the block's own) of x.  normed: (n, rstd) as the block before left them
+        (its next_normed, for this block's pre_gain); else the block norms x itself.  next_gain:
+        the next block's pre_gain, of a block with next_norm."""
+        self._check_gate(gate)
+        if next_gain is not None and self.next_n is None:
+            raise ValueError("next_gain belongs to a block built with next_norm")
+        T, H, L = self.T, self.H, self.layer
+        out = self.out if out is None else out
+        n, rstd = (self.n, self.rstd) if normed is None else normed
+        if normed is None:
+            moe_pre_norm(x, pre_gain, self.eps, T, H, n, rstd, stream)
+        self._normed = n, rstd
+        L.route(n, Wr, bias, stream)
+        if L.balanced:
+            L.balance(mask, seg_offsets, stream)
+        L.dispatch(n, stream)
+        L.experts(Wg, Wu, Wd, stream)
+        moe_combine_post_norm(L.y_perm, L.topk_w, L.row_of_slot, x, post_gain, self.post_norm, self.eps, gate, self.res_scale,
+                              self.out_scale, T, H, L.k, self.z, out, self.post_rstd, next_gain, self.next_n, self.next_rstd,
+                              stream)
+        return out
+
+    def backward(self, dout, x, pre_gain, post_gain, Wr, Wg, Wu, Wd, gate=None, accumulate: bool = False, stream=None, dx=None,
+                 overlap: bool = True, dloss=None):
+        """After the forward of the same x: the gradients of the parameters and of the gate, and dx
+        (default: the block's own), which may be dout."""
+        assert self.training, "block was built without backward buffers"
+        self._check_gate(gate)
+        T, H, L = self.T, self.H, self.layer
+        dx = self.dx if dx is None else dx
+        n, rstd = self._normed
+        moe_post_norm_bwd(dout, self.z, post_gain, self.post_norm, self.post_rstd, gate, self.out_scale, T, H, self.dz,
+                          self.d_post_gain, self.d_gate, accumulate, self.ws_norm, stream)
+        if self.checkpoint:  # n was scratch
+            n = self.n
+            moe_pre_norm(x, pre_gain, self.eps, T, H, n, None, stream)
+        dn = L.backward(self.dz, n, Wr, Wg, Wu, Wd, accumulate, stream, overlap=overlap, dloss=dloss)
+        moe_pre_norm_bwd(dn, x, pre_gain, rstd, dout, self.res_scale, T, H, dx, self.d_pre_gain, accumulate, self.ws_norm, stream)
         return dx
 
 
