@@ -72,6 +72,38 @@ struct RowGroup {
   }
 };
 
+// A thread's own stretch of shared memory, through which the 16-byte vectors of its
+// next rows arrive while it works on one: no other thread reads it, so that waiting
+// for one's own copies is all the synchronisation there is.  A stage holds UNITS
+// vectors; STAGES - 1 of them are under way.
+template <int UNITS, int STAGES>
+struct RowRing {
+  static constexpr size_t kBytes = (size_t)UNITS * STAGES * kNormThreads * 16;
+  uint8_t* mine;
+  __device__ __forceinline__ explicit RowRing(uint8_t* smem) : mine(smem + threadIdx.x * 16) {}
+  // unit u of `stage` = the 16 bytes at src, or zeros
+  __device__ __forceinline__ void fetch(int stage, int u, const void* src, bool there) {
+    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(mine + (size_t)(stage * UNITS + u) * (kNormThreads * 16));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+  }
+  __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory"); }
+  __device__ __forceinline__ const uint4& at(int stage, int u) const {
+    return *reinterpret_cast<const uint4*>(mine + (size_t)(stage * UNITS + u) * (kNormThreads * 16));
+  }
+  // the vector whose (first) unit is u
+  template <typename S>
+  __device__ __forceinline__ Vec8<S> vec(int stage, int u) const {
+    Vec8<S> v;
+    uint4* w = reinterpret_cast<uint4*>(&v);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(Vec8<S>) / 16); ++i) w[i] = at(stage, u + i);
+    return v;
+  }
+};
+// stages that leave room for two blocks an SM (up to 12 units)
+__host__ __device__ constexpr int ring_stages(int units) { return units <= 6 ? 4 : (units <= 8 ? 3 : 2); }
+
 template <typename S>
 __device__ __forceinline__ Vec8<S> zero_vec() {
   Vec8<S> v;
@@ -127,6 +159,21 @@ int with_row_shape(int H, F&& f) {
   return f(integral_constant<int, 256>{}, integral_constant<int, 4>{});
 }
 
+// The same for the backward kernels, which hold the gain's gradient of their columns as
+// well: fewer vectors a lane.
+template <class F>
+int with_bwd_shape(int H, F&& f) {
+  using std::integral_constant;
+  if (H <= 64) return f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+  if (H <= 128) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  if (H <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  if (H <= 512) return f(integral_constant<int, 32>{}, integral_constant<int, 2>{});
+  if (H <= 1024) return f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  if (H <= 2048) return f(integral_constant<int, 128>{}, integral_constant<int, 2>{});
+  if (H <= 4096) return f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  return f(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+}
+
 inline int norm_grid(long long T, int rows_per_block, int per_sm, int most) {
   const long long b = (T + rows_per_block - 1) / rows_per_block;
   const long long cap = (long long)(sm_count() > 0 ? sm_count() : 148) * per_sm;
@@ -139,6 +186,14 @@ inline size_t norm_parts_bytes(int T, int H) {
   if (T <= 0 || H <= 0) return 0;
   return (size_t)(T < kNormParts ? T : kNormParts) * H * sizeof(float);
 }
+
+// shared memory of a backward: its ring, in which the gain's gradients are folded too
+constexpr size_t norm_smem(size_t ring, int nv) {
+  const size_t fold = sizeof(float) * kNormThreads * 8 * nv;
+  return ring > fold ? ring : fold;
+}
+// lets a kernel have that much (an attribute of the kernel, set on every call: cheap, and right on every device)
+int allow_smem(const char* fn, const void* kernel, size_t bytes);
 
 // H, eps and a call's gradient of the gain
 int check_norm(const char* fn, int T, int H, int fp32);

@@ -44,107 +44,179 @@ __device__ __forceinline__ Gate sigmoid(float x) {
   return {x >= 0.f ? t : e * t, e * t * t};
 }
 
-template <typename S, int L, int NV, bool kCombine>
+// What follows a row's z: norm, gate, residual, and the next norm.  res, gate2: the row's
+// vectors of the residual and of an element's gate (zeros without).
+template <typename S, int L, int NV>
+__device__ __forceinline__ void finish_row(const PostArgs& p, RowGroup<L>& rg, long long t, float (&z)[NV][8], const Vec8<S> (&res)[NV],
+                                           const uint4 (&gate2)[NV], float tok_logit) {
+  const int H = p.H, nvec = H / 8;
+  const float inv_h = 1.0f / (float)H;
+  const bool live = t < p.T;
+  float r = 1.f;
+  if (p.norm) {
+    r = rg.template rstd<NV>(inv_h, p.eps, [&](int i, int j) { return z[i][j]; });
+    if (p.rstd && live && rg.l == 0) p.rstd[t] = r;
+  }
+  const float tok = p.gate_kind == 1 ? p.out_scale * sigmoid(tok_logit).g : p.out_scale;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = rg.l + i * L;
+    if (!live || c >= nvec) continue;
+    const Gain8 w(p.gain, c, true);
+    float g[8];
+    unpack8(gate2[i], g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float v = z[i][j] * r * w.at(j) * tok;
+      if (p.gate_kind == 2) v *= sigmoid(g[j]).g;
+      if (p.residual) v = __fmaf_rn(p.res_scale, res[i].at(j), v);
+      z[i][j] = v;
+    }
+    Vec8<S>::store(static_cast<S*>(p.out) + t * H + 8 * c, z[i]);
+    if (sizeof(S) == 2) {  // the next norm is of what is stored
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[i][j] = __bfloat162float(__float2bfloat16_rn(z[i][j]));
+    }
+  }
+  if (p.next_y) {
+    const float q = rg.template rstd<NV>(inv_h, p.eps, [&](int i, int j) { return z[i][j]; });
+    if (p.next_rstd && live && rg.l == 0) p.next_rstd[t] = q;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = rg.l + i * L;
+      if (!live || c >= nvec) continue;
+      const Gain8 w(p.next_gain, c, true);
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = z[i][j] * q * w.at(j);
+      Vec8<__nv_bfloat16>::store(p.next_y + t * H + 8 * c, o);
+    }
+  }
+}
+
+// The row's vectors of the residual and of an element's gate.
+template <typename S, int L, int NV>
+__device__ __forceinline__ void load_sides(const PostArgs& p, const RowGroup<L>& rg, long long t, Vec8<S> (&res)[NV], uint4 (&gate2)[NV]) {
+  const int nvec = p.H / 8;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = rg.l + i * L;
+    const bool there = t < p.T && c < nvec;
+    res[i] = zero_vec<S>();
+    gate2[i] = make_uint4(0, 0, 0, 0);
+    if (p.residual && there) res[i].load(static_cast<const S*>(p.residual) + t * p.H + 8 * c);
+    if (p.gate_kind == 2 && there)
+      gate2[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.gate) + t * p.H) + c);
+  }
+}
+
+template <typename S, int L, int NV>
 __global__ void __launch_bounds__(kNormThreads) post_norm_kernel(const PostArgs p) {
   pdl_wait();
   pdl_trigger();
   __shared__ float sm[16];
   RowGroup<L> rg(sm);
-  const int H = p.H, nvec = H / 8, T = p.T;
-  const float inv_h = 1.0f / (float)H;
-  const S* residual = static_cast<const S*>(p.residual);
-  S* out = static_cast<S*>(p.out);
-  for (long long base = (long long)blockIdx.x * rg.kRows; base < T; base += (long long)gridDim.x * rg.kRows) {
+  const int nvec = p.H / 8;
+  for (long long base = (long long)blockIdx.x * rg.kRows; base < p.T; base += (long long)gridDim.x * rg.kRows) {
     const long long t = base + rg.g;
-    const bool live = t < T;
     float z[NV][8];
     Vec8<S> res[NV];
+    uint4 gate2[NV], zv[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = rg.l + i * L;
-      res[i] = zero_vec<S>();
-      if (residual && live && c < nvec) res[i].load(residual + t * H + 8 * c);
+      zv[i] = t < p.T && c < nvec ? __ldg(reinterpret_cast<const uint4*>(p.z + t * p.H) + c) : make_uint4(0, 0, 0, 0);
+    }
+    load_sides<S, L, NV>(p, rg, t, res, gate2);
+    const float logit = p.gate_kind == 1 && t < p.T ? __ldg(static_cast<const float*>(p.gate) + t) : 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) unpack8(zv[i], z[i]);
+    finish_row<S, L, NV>(p, rg, t, z, res, gate2, logit);
+  }
+}
+
+// Combine: KB of a token's rows are under way in each lane at a time, the first of the
+// next token while this one's sums are taken and its outputs written; the row ids and
+// weights (lane j of a warp holds slot j's) a token further ahead.
+template <typename S, int L, int NV, int KB>
+__global__ void __launch_bounds__(kNormThreads, NV == 4 ? 1 : 2) combine_post_norm_kernel(const PostArgs p) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float sm[16];
+  RowGroup<L> rg(sm);
+  const int H = p.H, nvec = H / 8, k = p.k, lane = threadIdx.x & 31;
+  const long long step = (long long)gridDim.x * rg.kRows;
+  int row, next_row;
+  float w, next_w, logit, next_logit = 0.f;
+  auto ids = [&](long long t, int& row, float& w, float& logit) {
+    row = -1;
+    w = 0.f;
+    if (t < p.T && lane < k) {
+      row = __ldg(p.row_of_slot + t * k + lane);
+      w = __ldg(p.topk_w + t * k + lane);
+    }
+    logit = p.gate_kind == 1 && t < p.T ? __ldg(static_cast<const float*>(p.gate) + t) : 0.f;
+  };
+  uint4 buf[KB][NV];
+  // rows of slots j0 .. j0 + KB - 1; one that is out of range counts as zeros
+  auto rows = [&](int row, int j0) {
+#pragma unroll
+    for (int u = 0; u < KB; ++u) {
+      const int q = __shfl_sync(0xffffffffu, row, (j0 + u) & 31);
+      const bool there = j0 + u < k && q >= 0 && q < p.R;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = rg.l + i * L;
+        buf[u][i] = there && c < nvec ? __ldg(reinterpret_cast<const uint4*>(p.z + (size_t)q * H) + c) : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  const long long first = (long long)blockIdx.x * rg.kRows;
+  ids(first + rg.g, row, w, logit);
+  rows(row, 0);
+  ids(first + step + rg.g, next_row, next_w, next_logit);
+  for (long long base = first; base < p.T; base += step) {
+    const long long t = base + rg.g;
+    if (t < p.T && lane < k && (row < 0 || row >= p.R)) set_status(p.status, MOE_STATUS_BAD_INDEX);
+    if (row < 0 || row >= p.R) w = 0.f;
+    Vec8<S> res[NV];
+    uint4 gate2[NV];
+    load_sides<S, L, NV>(p, rg, t, res, gate2);
+    float z[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[i][j] = 0.f;
-    }
-    if constexpr (kCombine) {
-      constexpr int KB = NV == 1 ? 8 : (NV == 2 ? 4 : 2);
-      for (int j0 = 0; j0 < p.k; j0 += KB) {
-        uint4 buf[KB][NV];
-        float w[KB];
+    for (int j0 = 0; j0 < k; j0 += KB) {
+      if (j0) rows(row, j0);
 #pragma unroll
-        for (int u = 0; u < KB; ++u) {
-          const bool slot = live && j0 + u < p.k;
-          const int row = slot ? __ldg(p.row_of_slot + t * p.k + j0 + u) : -1;
-          const bool there = row >= 0 && row < p.R;
-          if (slot && !there) set_status(p.status, MOE_STATUS_BAD_INDEX);
-          w[u] = there ? __ldg(p.topk_w + t * p.k + j0 + u) : 0.f;
-#pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            const int c = rg.l + i * L;
-            buf[u][i] = there && c < nvec ? __ldg(reinterpret_cast<const uint4*>(p.z + (size_t)row * H) + c) : make_uint4(0, 0, 0, 0);
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < KB; ++u)
+      for (int u = 0; u < KB; ++u) {
+        const float wu = __shfl_sync(0xffffffffu, w, (j0 + u) & 31);
+        if (j0 + u < k) {
 #pragma unroll
           for (int i = 0; i < NV; ++i) {
             float f[8];
             unpack8(buf[u][i], f);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) z[i][j] = __fmaf_rn(w[u], f[j], z[i][j]);
+            for (int j = 0; j < 8; ++j) z[i][j] = __fmaf_rn(wu, f[j], z[i][j]);
           }
+        }
       }
-    } else {
+    }
+    const float gate = logit;
+    row = next_row;
+    w = next_w;
+    logit = next_logit;
+    rows(row, 0);
+    ids(t + 2 * step, next_row, next_w, next_logit);
+    if (p.z_out && t < p.T) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = rg.l + i * L;
-        if (live && c < nvec) unpack8(*(reinterpret_cast<const uint4*>(p.z + t * H) + c), z[i]);
+        if (c < nvec) Vec8<__nv_bfloat16>::store(p.z_out + t * H + 8 * c, z[i]);
       }
     }
-    float r = 1.f;
-    if (p.norm) {
-      r = rg.template rstd<NV>(inv_h, p.eps, [&](int i, int j) { return z[i][j]; });
-      if (p.rstd && live && rg.l == 0) p.rstd[t] = r;
-    }
-    float tok = p.out_scale;
-    if (p.gate_kind == 1 && live) tok *= sigmoid(__ldg(static_cast<const float*>(p.gate) + t)).g;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = rg.l + i * L;
-      const bool there = live && c < nvec;
-      if (!there) continue;
-      if (kCombine && p.z_out) Vec8<__nv_bfloat16>::store(p.z_out + t * H + 8 * c, z[i]);
-      const Gain8 w(p.gain, c, true);
-      float g[8];
-      if (p.gate_kind == 2) unpack8(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.gate) + t * H) + c), g);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        float v = z[i][j] * r * w.at(j) * tok;
-        if (p.gate_kind == 2) v *= sigmoid(g[j]).g;
-        if (residual) v = __fmaf_rn(p.res_scale, res[i].at(j), v);
-        z[i][j] = v;
-      }
-      Vec8<S>::store(out + t * H + 8 * c, z[i]);
-      if (sizeof(S) == 2) {  // the next norm is of what is stored
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[i][j] = __bfloat162float(__float2bfloat16_rn(z[i][j]));
-      }
-    }
-    if (p.next_y) {
-      const float q = rg.template rstd<NV>(inv_h, p.eps, [&](int i, int j) { return z[i][j]; });
-      if (p.next_rstd && live && rg.l == 0) p.next_rstd[t] = q;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = rg.l + i * L;
-        if (!live || c >= nvec) continue;
-        const Gain8 w(p.next_gain, c, true);
-        float o[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = z[i][j] * q * w.at(j);
-        Vec8<__nv_bfloat16>::store(p.next_y + t * H + 8 * c, o);
-      }
-    }
+    finish_row<S, L, NV>(p, rg, t, z, res, gate2, gate);
   }
 }
 
@@ -163,63 +235,89 @@ struct PostBwdArgs {
   void* dgate;
 };
 
-// dz may be z: a row's vectors are read before they are written by the same lane.
-template <typename S, int L, int NV>
-__global__ void __launch_bounds__(kNormThreads) post_norm_bwd_kernel(const PostBwdArgs p) {
+// dz may be z: each vector is read before it is written, by the same thread.
+template <typename S, int L, int NV, bool kElement>
+struct PostBwd {
+  static constexpr int SU = sizeof(Vec8<S>) / 16;                // units of a stream vector
+  static constexpr int PER = 1 + SU + (kElement ? 1 : 0);        // z, dout, gate
+  using Ring = RowRing<NV * PER, ring_stages(NV * PER)>;
+};
+template <typename S, int L, int NV, bool kElement>
+__global__ void __launch_bounds__(kNormThreads, NV == 4 ? 1 : 2) post_norm_bwd_kernel(const PostBwdArgs p) {
   pdl_wait();
   pdl_trigger();
+  using P = PostBwd<S, L, NV, kElement>;
+  constexpr int SU = P::SU, STAGES = ring_stages(NV * P::PER);
   __shared__ float sm[16];
-  __shared__ float fold[kNormThreads * NV * 8];
+  extern __shared__ __align__(16) uint8_t ring_smem[];
+  typename P::Ring ring(ring_smem);
   RowGroup<L> rg(sm);
   const int H = p.H, nvec = H / 8, T = p.T;
   const float inv_h = 1.0f / (float)H;
   const S* dout = static_cast<const S*>(p.dout);
-  const __nv_bfloat16* gate2 = p.gate_kind == 2 ? static_cast<const __nv_bfloat16*>(p.gate) : nullptr;
+  const long long step = (long long)gridDim.x * rg.kRows;
   float acc[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
-  for (long long base = (long long)blockIdx.x * rg.kRows; base < T; base += (long long)gridDim.x * rg.kRows) {
+  auto fetch = [&](int stage, long long t) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = rg.l + i * L;
+      const bool there = t < T && c < nvec;
+      const long long at = there ? t * H + 8 * c : 0;
+      const int u = i * P::PER;
+      ring.fetch(stage, u, p.z + at, there);
+#pragma unroll
+      for (int q = 0; q < SU; ++q) ring.fetch(stage, u + 1 + q, reinterpret_cast<const uint4*>(dout + at) + q, there);
+      if (kElement) ring.fetch(stage, u + 1 + SU, static_cast<const __nv_bfloat16*>(p.gate) + at, there);
+    }
+    ring.commit();
+  };
+  const long long first = (long long)blockIdx.x * rg.kRows;
+#pragma unroll
+  for (int q = 0; q < STAGES - 1; ++q) fetch(q, first + q * step + rg.g);
+  int stage = 0;
+  for (long long base = first; base < T; base += step) {
     const long long t = base + rg.g;
     const bool live = t < T;
-    Vec8<__nv_bfloat16> zv[NV], gv[NV];
-    Vec8<S> d[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = rg.l + i * L;
-      zv[i] = gv[i] = zero_vec<__nv_bfloat16>();
-      d[i] = zero_vec<S>();
-      if (live && c < nvec) {
-        zv[i].load(p.z + t * H + 8 * c);
-        d[i].load(dout + t * H + 8 * c);
-        if (gate2) gv[i].load(gate2 + t * H + 8 * c);
-      }
-    }
     const float r = p.norm && live ? __ldg(p.rstd + t) : 1.f;
     Gate tok = {1.f, 0.f};
-    if (p.gate_kind == 1 && live) tok = sigmoid(__ldg(static_cast<const float*>(p.gate) + t));
+    if (!kElement && p.gate_kind == 1 && live) tok = sigmoid(__ldg(static_cast<const float*>(p.gate) + t));
+    ring.wait();
+    const int cur = stage;
     float m = 0.f, dg = 0.f;  // sums of dn n, and of dout n gain
+    float n[NV][8], dn[NV][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = rg.l + i * L;
+      const int c = rg.l + i * L, u = i * P::PER;
       const bool there = live && c < nvec;
       const Gain8 w(p.gain, c, c < nvec);
+      const Vec8<__nv_bfloat16> zv = ring.template vec<__nv_bfloat16>(cur, u);
+      const Vec8<S> d = ring.template vec<S>(cur, u + 1);
+      const Vec8<__nv_bfloat16> gv = kElement ? ring.template vec<__nv_bfloat16>(cur, u + 1 + SU) : zero_vec<__nv_bfloat16>();
       float ds[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float n = zv[i].at(j) * r, e = p.out_scale * d[i].at(j);
-        const Gate G = gate2 ? sigmoid(gv[i].at(j)) : tok;
+        n[i][j] = zv.at(j) * r;
+        const float e = p.out_scale * d.at(j), en = e * n[i][j];
+        const Gate G = kElement ? sigmoid(gv.at(j)) : tok;
         const float dv = e * G.g;
-        acc[i][j] = __fmaf_rn(dv, n, acc[i][j]);
-        m = __fmaf_rn(dv * w.at(j), n, m);
-        dg = __fmaf_rn(e * w.at(j), n, dg);
-        ds[j] = e * w.at(j) * n * G.d;
+        acc[i][j] = __fmaf_rn(dv, n[i][j], acc[i][j]);
+        dn[i][j] = dv * w.at(j);
+        m = __fmaf_rn(dn[i][j], n[i][j], m);
+        if (kElement)
+          ds[j] = en * w.at(j) * G.d;
+        else
+          dg = __fmaf_rn(en, w.at(j), dg);
       }
-      if (gate2 && p.dgate && there) Vec8<__nv_bfloat16>::store(static_cast<__nv_bfloat16*>(p.dgate) + t * H + 8 * c, ds);
+      if (kElement && p.dgate && there) Vec8<__nv_bfloat16>::store(static_cast<__nv_bfloat16*>(p.dgate) + t * H + 8 * c, ds);
     }
+    fetch(stage == 0 ? STAGES - 1 : stage - 1, t + (STAGES - 1) * step);
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
     if (p.norm) m = rg.sum(m) * inv_h;
-    if (p.gate_kind == 1 && p.dgate) {
+    if (!kElement && p.gate_kind == 1 && p.dgate) {
       dg = rg.sum(dg);
       if (live && rg.l == 0) static_cast<float*>(p.dgate)[t] = dg * tok.d;
     }
@@ -228,43 +326,42 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_bwd_kernel(const PostB
     for (int i = 0; i < NV; ++i) {
       const int c = rg.l + i * L;
       if (c >= nvec) continue;
-      const Gain8 w(p.gain, c, true);
       float o[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float dn = p.out_scale * d[i].at(j) * (gate2 ? sigmoid(gv[i].at(j)).g : tok.g) * w.at(j);
-        o[j] = p.norm ? r * (dn - zv[i].at(j) * r * m) : dn;
-      }
+      for (int j = 0; j < 8; ++j) o[j] = p.norm ? r * (dn[i][j] - n[i][j] * m) : dn[i][j];
       Vec8<__nv_bfloat16>::store(p.dz + t * H + 8 * c, o);
     }
   }
-  if (p.part) leave_part<L, NV>(acc, fold, H, p.part);
+  if (p.part) {  // the ring's memory is free: copies still under way are of rows behind the last, zeros
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    leave_part<L, NV>(acc, reinterpret_cast<float*>(ring_smem), H, p.part);
+  }
 }
 
-// The combine keeps a token's k rows in flight in each lane: one vector a lane as
-// long as a block's lanes can hold the row.
+// Lanes of a token's row, vectors of a lane and rows under way at a time in the combine.
 template <class F>
 int with_combine_shape(int H, F&& f) {
   using std::integral_constant;
-  if (H <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-  if (H <= 512) return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-  if (H <= 1024) return f(integral_constant<int, 128>{}, integral_constant<int, 1>{});
-  if (H <= 2048) return f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
-  if (H <= 4096) return f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-  return f(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  if (H <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{}, integral_constant<int, 8>{});
+  if (H <= 512) return f(integral_constant<int, 32>{}, integral_constant<int, 2>{}, integral_constant<int, 8>{});
+  if (H <= 1024) return f(integral_constant<int, 64>{}, integral_constant<int, 2>{}, integral_constant<int, 8>{});
+  if (H <= 2048) return f(integral_constant<int, 128>{}, integral_constant<int, 2>{}, integral_constant<int, 8>{});
+  if (H <= 4096) return f(integral_constant<int, 256>{}, integral_constant<int, 2>{}, integral_constant<int, 8>{});
+  return f(integral_constant<int, 256>{}, integral_constant<int, 4>{}, integral_constant<int, 4>{});
 }
 
 template <typename S>
 int run_post_norm(const char* fn, const PostArgs& a, bool combine, cudaStream_t s) {
   if (combine)
-    return with_combine_shape(a.H, [&](auto l, auto nv) {
-      constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
-      launch_pdl(post_norm_kernel<S, L, NV, true>, norm_grid(a.T, kNormThreads / L, 8, 1 << 30), kNormThreads, 0, s, a);
+    return with_combine_shape(a.H, [&](auto l, auto nv, auto kb) {
+      constexpr int L = decltype(l)::value, NV = decltype(nv)::value, KB = decltype(kb)::value;
+      launch_pdl(combine_post_norm_kernel<S, L, NV, KB>, norm_grid(a.T, kNormThreads / L, 2, 1 << 30), kNormThreads, 0, s, a);
       return check_launch(fn);
     });
   return with_row_shape(a.H, [&](auto l, auto nv) {
     constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
-    launch_pdl(post_norm_kernel<S, L, NV, false>, norm_grid(a.T, kNormThreads / L, 8, 1 << 30), kNormThreads, 0, s, a);
+    launch_pdl(post_norm_kernel<S, L, NV>, norm_grid(a.T, kNormThreads / L, 8, 1 << 30), kNormThreads, 0, s, a);
     return check_launch(fn);
   });
 }
@@ -357,14 +454,22 @@ int moe_post_norm_bwd(const void* dout, int fp32, const void* z, const float* ga
   if (int rc = check_gain_grad(fn, T, H, dgain, ws, ws_bytes)) return rc;
   const PostBwdArgs a = {dout, static_cast<const __nv_bfloat16*>(z), gain, norm, rstd, gate_kind, gate, out_scale, T, H,
                          static_cast<__nv_bfloat16*>(dz), dgain ? static_cast<float*>(ws) : nullptr, dgate};
-  return with_row_shape(H, [&](auto l, auto nv) {
+  return with_bwd_shape(H, [&](auto l, auto nv) {
     constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
-    const int grid = norm_grid(T, kNormThreads / L, 2, kNormParts);
-    if (fp32)
-      launch_pdl(post_norm_bwd_kernel<float, L, NV>, grid, kNormThreads, 0, s, a);
-    else
-      launch_pdl(post_norm_bwd_kernel<__nv_bfloat16, L, NV>, grid, kNormThreads, 0, s, a);
-    if (int rc = check_launch(fn)) return rc;
+    int grid = 0;
+    auto run = [&](auto type, auto element) {
+      using S = decltype(type);
+      constexpr bool kElement = decltype(element)::value;
+      auto kern = post_norm_bwd_kernel<S, L, NV, kElement>;
+      const size_t smem = norm_smem(PostBwd<S, L, NV, kElement>::Ring::kBytes, NV);
+      grid = norm_grid(T, kNormThreads / L, smem <= 110 * 1024 ? 2 : 1, kNormParts);
+      if (int rc = allow_smem(fn, reinterpret_cast<const void*>(kern), smem)) return rc;
+      launch_pdl(kern, grid, kNormThreads, smem, s, a);
+      return check_launch(fn);
+    };
+    const int rc = gate_kind == 2 ? (fp32 ? run(float(), std::true_type()) : run(__nv_bfloat16(), std::true_type()))
+                                  : (fp32 ? run(float(), std::false_type()) : run(__nv_bfloat16(), std::false_type()));
+    if (rc) return rc;
     return dgain ? launch_gain_sum(fn, static_cast<const float*>(ws), grid, H, dgain, accumulate, s) : MOE_OK;
   });
 }

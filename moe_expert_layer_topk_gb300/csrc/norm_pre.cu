@@ -11,7 +11,8 @@
 namespace moe {
 namespace {
 
-template <typename S, int L, int NV>
+// RU rows a group at a time, so that short rows too have several loads a thread under way.
+template <typename S, int L, int NV, int RU>
 __global__ void __launch_bounds__(kNormThreads) pre_norm_kernel(const S* __restrict__ x, long long ldx,
                                                                 const float* __restrict__ gain, float eps, int T, int H,
                                                                 __nv_bfloat16* __restrict__ y, long long ldy,
@@ -22,68 +23,102 @@ __global__ void __launch_bounds__(kNormThreads) pre_norm_kernel(const S* __restr
   RowGroup<L> rg(sm);
   const int nvec = H / 8;
   const float inv_h = 1.0f / (float)H;
-  for (long long base = (long long)blockIdx.x * rg.kRows; base < T; base += (long long)gridDim.x * rg.kRows) {
-    const long long t = base + rg.g;
-    const bool live = t < T;
-    Vec8<S> v[NV];
+  for (long long base = (long long)blockIdx.x * (RU * rg.kRows); base < T; base += (long long)gridDim.x * (RU * rg.kRows)) {
+    Vec8<S> v[RU][NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = rg.l + i * L;
-      v[i] = zero_vec<S>();
-      if (live && c < nvec) v[i].load(x + t * ldx + 8 * c);
+    for (int u = 0; u < RU; ++u) {
+      const long long t = base + u * rg.kRows + rg.g;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = rg.l + i * L;
+        v[u][i] = zero_vec<S>();
+        if (t < T && c < nvec) v[u][i].load(x + t * ldx + 8 * c);
+      }
     }
-    const float r = rg.template rstd<NV>(inv_h, eps, [&](int i, int j) { return v[i].at(j); });
-    if (!live) continue;
-    if (rstd && rg.l == 0) rstd[t] = r;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = rg.l + i * L;
-      if (c >= nvec) continue;
-      const Gain8 w(gain, c, true);
-      float o[8];
+    for (int u = 0; u < RU; ++u) {
+      const long long t = base + u * rg.kRows + rg.g;
+      const float r = rg.template rstd<NV>(inv_h, eps, [&](int i, int j) { return v[u][i].at(j); });
+      if (t >= T) continue;
+      if (rstd && rg.l == 0) rstd[t] = r;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = v[i].at(j) * r * w.at(j);
-      Vec8<__nv_bfloat16>::store(y + t * ldy + 8 * c, o);
+      for (int i = 0; i < NV; ++i) {
+        const int c = rg.l + i * L;
+        if (c >= nvec) continue;
+        const Gain8 w(gain, c, true);
+        float o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = v[u][i].at(j) * r * w.at(j);
+        Vec8<__nv_bfloat16>::store(y + t * ldy + 8 * c, o);
+      }
     }
   }
 }
 
-// dx may be dres: a row's vectors are read before they are written by the same lane.
+// dx may be dres: each vector is read before it is written, by the same thread.
 template <typename S, int L, int NV>
-__global__ void __launch_bounds__(kNormThreads) pre_norm_bwd_kernel(
+struct PreBwd {
+  static constexpr int SU = sizeof(Vec8<S>) / 16;         // units of a stream vector
+  static constexpr int UNITS = NV * (1 + 2 * SU);         // dy, x, dres
+  using Ring = RowRing<UNITS, ring_stages(UNITS)>;
+};
+template <typename S, int L, int NV>
+__global__ void __launch_bounds__(kNormThreads, NV == 4 ? 1 : 2) pre_norm_bwd_kernel(
     const __nv_bfloat16* __restrict__ dy, long long lddy, const S* __restrict__ x, long long ldx, const float* __restrict__ gain,
     const float* __restrict__ rstd, const S* dres, long long lddres, float res_scale, int T, int H, S* dx, long long lddx,
     float* __restrict__ part) {
   pdl_wait();
   pdl_trigger();
+  using P = PreBwd<S, L, NV>;
+  constexpr int SU = P::SU, STAGES = ring_stages(P::UNITS);
   __shared__ float sm[16];
-  __shared__ float fold[kNormThreads * NV * 8];
+  extern __shared__ __align__(16) uint8_t ring_smem[];
+  typename P::Ring ring(ring_smem);
   RowGroup<L> rg(sm);
   const int nvec = H / 8;
   const float inv_h = 1.0f / (float)H;
+  const long long step = (long long)gridDim.x * rg.kRows;
   float acc[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
-  for (long long base = (long long)blockIdx.x * rg.kRows; base < T; base += (long long)gridDim.x * rg.kRows) {
+  auto fetch = [&](int stage, long long t) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = rg.l + i * L;
+      const bool there = t < T && c < nvec;
+      const int u = i * (1 + 2 * SU);
+      ring.fetch(stage, u, dy + (there ? t * lddy + 8 * c : 0), there);
+#pragma unroll
+      for (int q = 0; q < SU; ++q) {
+        ring.fetch(stage, u + 1 + q, reinterpret_cast<const uint4*>(x + (there ? t * ldx + 8 * c : 0)) + q, there);
+        if (dres)
+          ring.fetch(stage, u + 1 + SU + q, reinterpret_cast<const uint4*>(dres + (there ? t * lddres + 8 * c : 0)) + q, there);
+      }
+    }
+    ring.commit();
+  };
+  const long long first = (long long)blockIdx.x * rg.kRows;
+#pragma unroll
+  for (int q = 0; q < STAGES - 1; ++q) fetch(q, first + q * step + rg.g);
+  int stage = 0;
+  for (long long base = first; base < T; base += step) {
     const long long t = base + rg.g;
     const bool live = t < T;
+    const float r = live ? __ldg(rstd + t) : 0.f;
+    ring.wait();
     Vec8<S> v[NV], res[NV];
     Vec8<__nv_bfloat16> d[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = rg.l + i * L;
-      v[i] = zero_vec<S>();
-      res[i] = zero_vec<S>();
-      d[i] = zero_vec<__nv_bfloat16>();
-      if (live && c < nvec) {
-        v[i].load(x + t * ldx + 8 * c);
-        d[i].load(dy + t * lddy + 8 * c);
-        if (dres) res[i].load(dres + t * lddres + 8 * c);
-      }
+      const int u = i * (1 + 2 * SU);
+      d[i] = ring.template vec<__nv_bfloat16>(stage, u);
+      v[i] = ring.template vec<S>(stage, u + 1);
+      res[i] = dres ? ring.template vec<S>(stage, u + 1 + SU) : zero_vec<S>();
     }
-    const float r = live ? __ldg(rstd + t) : 0.f;
+    fetch(stage == 0 ? STAGES - 1 : stage - 1, t + (STAGES - 1) * step);
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -113,7 +148,11 @@ __global__ void __launch_bounds__(kNormThreads) pre_norm_bwd_kernel(
       Vec8<S>::store(dx + t * lddx + 8 * c, o);
     }
   }
-  if (part) leave_part<L, NV>(acc, fold, H, part);
+  if (part) {  // the ring's memory is free: copies still under way are of rows behind the last, zeros
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    leave_part<L, NV>(acc, reinterpret_cast<float*>(ring_smem), H, part);
+  }
 }
 
 // dgain[h] (+)= the parts' sums, in their order: 32 columns a block, eight threads a
@@ -148,7 +187,8 @@ int run_pre_norm(const char* fn, const S* x, long long ldx, const float* gain, f
                  long long ldy, float* rstd, cudaStream_t s) {
   return with_row_shape(H, [&](auto l, auto nv) {
     constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
-    launch_pdl(pre_norm_kernel<S, L, NV>, norm_grid(T, kNormThreads / L, 8, 1 << 30), kNormThreads, 0, s, x, ldx, gain, eps, T, H,
+    constexpr int RU = NV == 1 ? 4 : (NV == 2 ? 2 : 1);
+    launch_pdl(pre_norm_kernel<S, L, NV, RU>, norm_grid(T, RU * kNormThreads / L, 8, 1 << 30), kNormThreads, 0, s, x, ldx, gain, eps, T, H,
                y, ldy, rstd);
     return check_launch(fn);
   });
@@ -158,10 +198,13 @@ template <typename S>
 int run_pre_norm_bwd(const char* fn, const __nv_bfloat16* dy, long long lddy, const S* x, long long ldx, const float* gain,
                      const float* rstd, const S* dres, long long lddres, float res_scale, int T, int H, S* dx, long long lddx,
                      float* dgain, int accumulate, float* ws, cudaStream_t s) {
-  return with_row_shape(H, [&](auto l, auto nv) {
+  return with_bwd_shape(H, [&](auto l, auto nv) {
     constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
-    const int grid = norm_grid(T, kNormThreads / L, 2, kNormParts);
-    launch_pdl(pre_norm_bwd_kernel<S, L, NV>, grid, kNormThreads, 0, s, dy, lddy, x, ldx, gain, rstd, dres, lddres, res_scale, T, H,
+    auto kern = pre_norm_bwd_kernel<S, L, NV>;
+    const size_t smem = norm_smem(PreBwd<S, L, NV>::Ring::kBytes, NV);
+    const int grid = norm_grid(T, kNormThreads / L, smem <= 110 * 1024 ? 2 : 1, kNormParts);
+    if (int rc = allow_smem(fn, reinterpret_cast<const void*>(kern), smem)) return rc;
+    launch_pdl(kern, grid, kNormThreads, smem, s, dy, lddy, x, ldx, gain, rstd, dres, lddres, res_scale, T, H,
                dx, lddx, dgain ? ws : nullptr);
     if (int rc = check_launch(fn)) return rc;
     return dgain ? launch_gain_sum(fn, ws, grid, H, dgain, accumulate, s) : MOE_OK;
@@ -182,6 +225,12 @@ int check_gain_grad(const char* fn, int T, int H, const float* dgain, const void
   if (!ws || ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws ? ws_bytes : (size_t)0, need);
   if (!aligned16(ws) || !aligned16(dgain)) return fail(MOE_ERR_ALIGNMENT, "%s: dgain and ws must be 16-byte aligned", fn);
   return MOE_OK;
+}
+
+int allow_smem(const char* fn, const void* kernel, size_t bytes) {
+  if (bytes <= 48 * 1024) return MOE_OK;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  return e == cudaSuccess ? MOE_OK : fail_cuda(fn, e);
 }
 
 int launch_gain_sum(const char* fn, const float* part, int parts, int H, float* dgain, int accumulate, cudaStream_t s) {
