@@ -42,54 +42,75 @@ struct RowGroup {
     }
     return v;
   }
-  // 1/sqrt(mean + eps) of the squares of a row's values, at(i, j) for element j of this
-  // lane's i-th vector (0 where it has none).  Squares beyond fp32's range are added
-  // again of values times 2^-80 (8192 of the largest, 2^48 each, add up to 2^109); eps
-  // is nothing beside those.  An infinity gives 0, a NaN NaN.
-  template <int NV, class At>
-  __device__ __forceinline__ float rstd(float inv_h, float eps, At&& at) {
-    float ss = 0.f;
+  // 1/sqrt(mean + eps) of the squares of RU rows' values, at(u, i, j) for element j of
+  // row u's i-th vector of this lane (0 where it has none).  Squares beyond fp32's range
+  // are added again of values times 2^-80 (8192 of the largest, 2^48 each, add up to
+  // 2^109); eps is nothing beside those.  An infinity gives 0, a NaN NaN.
+  template <int RU, int NV, class At>
+  __device__ __forceinline__ void rstds(float (&r)[RU], float inv_h, float eps, At&& at) {
+    bool big = false;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = __fmaf_rn(at(i, j), at(i, j), ss);
-    ss = sum(ss);
-    float r = __frsqrt_rn(__fmaf_rn(ss, inv_h, eps));
-    const bool big = !(ss <= 3.402823466e+38f);
-    if (L <= 32 ? __any_sync(0xffffffffu, big) : big) {
-      float s2 = 0.f;
+    for (int u = 0; u < RU; ++u) {
+      float ss = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float v = at(i, j) * 0x1p-80f;
-          s2 = __fmaf_rn(v, v, s2);
-        }
-      s2 = sum(s2);
-      if (big) r = __frsqrt_rn(s2 * inv_h) * 0x1p-80f;
+        for (int j = 0; j < 8; ++j) ss = __fmaf_rn(at(u, i, j), at(u, i, j), ss);
+      r[u] = sum(ss);
     }
-    return r;
+#pragma unroll
+    for (int u = 0; u < RU; ++u) {
+      big |= !(r[u] <= 3.402823466e+38f);
+    }
+    if (L <= 32 ? __any_sync(0xffffffffu, big) : big) {
+#pragma unroll
+      for (int u = 0; u < RU; ++u) {
+        float s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float v = at(u, i, j) * 0x1p-80f;
+            s2 = __fmaf_rn(v, v, s2);
+          }
+        s2 = sum(s2);
+        r[u] = r[u] <= 3.402823466e+38f ? __frsqrt_rn(__fmaf_rn(r[u], inv_h, eps)) : __frsqrt_rn(s2 * inv_h) * 0x1p-80f;
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < RU; ++u) r[u] = __frsqrt_rn(__fmaf_rn(r[u], inv_h, eps));
+    }
+  }
+  template <int NV, class At>
+  __device__ __forceinline__ float rstd(float inv_h, float eps, At&& at) {
+    float r[1];
+    rstds<1, NV>(r, inv_h, eps, [&](int, int i, int j) { return at(i, j); });
+    return r[0];
   }
 };
 
 // A thread's own stretch of shared memory, through which the 16-byte vectors of its
 // next rows arrive while it works on one: no other thread reads it, so that waiting
-// for one's own copies is all the synchronisation there is.  A stage holds UNITS
-// vectors; STAGES - 1 of them are under way.
-template <int UNITS, int STAGES>
+// for one's own copies is all the synchronisation there is.  A stage holds `units`
+// vectors.
+constexpr int kRingUnitBytes = kNormThreads * 16;  // a vector of each thread
 struct RowRing {
-  static constexpr size_t kBytes = (size_t)UNITS * STAGES * kNormThreads * 16;
   uint8_t* mine;
-  __device__ __forceinline__ explicit RowRing(uint8_t* smem) : mine(smem + threadIdx.x * 16) {}
+  int units;
+  __device__ __forceinline__ RowRing(uint8_t* smem, int units) : mine(smem + threadIdx.x * 16), units(units) {}
   // unit u of `stage` = the 16 bytes at src, or zeros
   __device__ __forceinline__ void fetch(int stage, int u, const void* src, bool there) {
-    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(mine + (size_t)(stage * UNITS + u) * (kNormThreads * 16));
+    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(mine + (stage * units + u) * kRingUnitBytes);
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
   }
   __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-  __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory"); }
+  // all but the last BUT stages' copies have arrived
+  template <int BUT>
+  __device__ __forceinline__ void wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(BUT) : "memory");
+  }
   __device__ __forceinline__ const uint4& at(int stage, int u) const {
-    return *reinterpret_cast<const uint4*>(mine + (size_t)(stage * UNITS + u) * (kNormThreads * 16));
+    return *reinterpret_cast<const uint4*>(mine + (stage * units + u) * kRingUnitBytes);
   }
   // the vector whose (first) unit is u
   template <typename S>
@@ -159,6 +180,9 @@ int with_row_shape(int H, F&& f) {
   return f(integral_constant<int, 256>{}, integral_constant<int, 4>{});
 }
 
+// Blocks an SM that a backward kernel's registers leave room for.
+__host__ __device__ constexpr int bwd_blocks(int nv) { return nv == 4 ? 1 : 2; }
+
 // The same for the backward kernels, which hold the gain's gradient of their columns as
 // well: fewer vectors a lane.
 template <class F>
@@ -188,9 +212,14 @@ inline size_t norm_parts_bytes(int T, int H) {
 }
 
 // shared memory of a backward: its ring, in which the gain's gradients are folded too
-constexpr size_t norm_smem(size_t ring, int nv) {
-  const size_t fold = sizeof(float) * kNormThreads * 8 * nv;
+constexpr size_t norm_smem(int units, int nv) {
+  const size_t ring = (size_t)units * ring_stages(units) * kRingUnitBytes, fold = sizeof(float) * kNormThreads * 8 * nv;
   return ring > fold ? ring : fold;
+}
+// blocks of so much shared memory that an SM holds (228 KB, 1 KB of it a block's own)
+inline int blocks_per_sm(size_t smem, int most) {
+  const int n = (int)(228 * 1024 / (smem + 1024));
+  return n < most ? (n > 0 ? n : 1) : most;
 }
 // lets a kernel have that much (an attribute of the kernel, set on every call: cheap, and right on every device)
 int allow_smem(const char* fn, const void* kernel, size_t bytes);

@@ -44,11 +44,22 @@ __device__ __forceinline__ Gate sigmoid(float x) {
   return {x >= 0.f ? t : e * t, e * t * t};
 }
 
+// The two gains of a lane's vectors: kept in registers where that is one vector (the
+// same for every row), else read for each row.
+template <int L, int NV>
+struct Gains {
+  Gain8 own, next;
+  __device__ __forceinline__ Gains(const PostArgs& p, int l)
+      : own(p.gain, l, NV == 1 && l < p.H / 8), next(p.next_gain, l, NV == 1 && l < p.H / 8) {}
+  __device__ __forceinline__ Gain8 of(const PostArgs& p, int c) const { return NV == 1 ? own : Gain8(p.gain, c, true); }
+  __device__ __forceinline__ Gain8 of_next(const PostArgs& p, int c) const { return NV == 1 ? next : Gain8(p.next_gain, c, true); }
+};
+
 // What follows a row's z: norm, gate, residual, and the next norm.  res, gate2: the row's
 // vectors of the residual and of an element's gate (zeros without).
 template <typename S, int L, int NV>
-__device__ __forceinline__ void finish_row(const PostArgs& p, RowGroup<L>& rg, long long t, float (&z)[NV][8], const Vec8<S> (&res)[NV],
-                                           const uint4 (&gate2)[NV], float tok_logit) {
+__device__ __forceinline__ void finish_row(const PostArgs& p, RowGroup<L>& rg, const Gains<L, NV>& gains, long long t, float (&z)[NV][8],
+                                           const Vec8<S> (&res)[NV], const uint4 (&gate2)[NV], float tok_logit) {
   const int H = p.H, nvec = H / 8;
   const float inv_h = 1.0f / (float)H;
   const bool live = t < p.T;
@@ -62,7 +73,7 @@ __device__ __forceinline__ void finish_row(const PostArgs& p, RowGroup<L>& rg, l
   for (int i = 0; i < NV; ++i) {
     const int c = rg.l + i * L;
     if (!live || c >= nvec) continue;
-    const Gain8 w(p.gain, c, true);
+    const Gain8 w = gains.of(p, c);
     float g[8];
     unpack8(gate2[i], g);
 #pragma unroll
@@ -85,7 +96,7 @@ __device__ __forceinline__ void finish_row(const PostArgs& p, RowGroup<L>& rg, l
     for (int i = 0; i < NV; ++i) {
       const int c = rg.l + i * L;
       if (!live || c >= nvec) continue;
-      const Gain8 w(p.next_gain, c, true);
+      const Gain8 w = gains.of_next(p, c);
       float o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = z[i][j] * q * w.at(j);
@@ -116,6 +127,7 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_kernel(const PostArgs 
   pdl_trigger();
   __shared__ float sm[16];
   RowGroup<L> rg(sm);
+  const Gains<L, NV> gains(p, rg.l);
   const int nvec = p.H / 8;
   for (long long base = (long long)blockIdx.x * rg.kRows; base < p.T; base += (long long)gridDim.x * rg.kRows) {
     const long long t = base + rg.g;
@@ -131,68 +143,140 @@ __global__ void __launch_bounds__(kNormThreads) post_norm_kernel(const PostArgs 
     const float logit = p.gate_kind == 1 && t < p.T ? __ldg(static_cast<const float*>(p.gate) + t) : 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) unpack8(zv[i], z[i]);
-    finish_row<S, L, NV>(p, rg, t, z, res, gate2, logit);
+    finish_row<S, L, NV>(p, rg, gains, t, z, res, gate2, logit);
   }
 }
 
-// Combine: KB of a token's rows are under way in each lane at a time, the first of the
-// next token while this one's sums are taken and its outputs written; the row ids and
-// weights (lane j of a warp holds slot j's) a token further ahead.
-template <typename S, int L, int NV, int KB>
-__global__ void __launch_bounds__(kNormThreads, NV == 4 ? 1 : 2) combine_post_norm_kernel(const PostArgs p) {
+// Combine: the rows of a token's first eight slots, its residual and its element gate come
+// through the lanes' own rings of shared memory while the token before is summed (a
+// token's further slots are read when their turn comes); the row ids, a token further
+// ahead, and the weights sit in registers, lane j of a warp holding slot j's.
+template <typename S, int NV>
+struct CombineRing {
+  static constexpr int KB = NV == 4 ? 4 : 8;  // four vectors a lane: the first four slots
+  static constexpr int SU = sizeof(Vec8<S>) / 16;
+  static constexpr int STAGES = 2;
+  // a vector's units: rows, residual, element gate
+  static __host__ __device__ int per(int gate_kind) { return KB + SU + (gate_kind == 2 ? 1 : 0); }
+  static size_t bytes(int gate_kind) { return (size_t)NV * per(gate_kind) * STAGES * kRingUnitBytes; }
+};
+template <typename S, int L, int NV>
+__global__ void __launch_bounds__(kNormThreads, NV == 1 ? 3 : 1) combine_post_norm_kernel(const PostArgs p) {
   pdl_wait();
   pdl_trigger();
+  using C = CombineRing<S, NV>;
+  constexpr int KB = C::KB, SU = C::SU, STAGES = C::STAGES;
   __shared__ float sm[16];
+  extern __shared__ __align__(16) uint8_t ring_smem[];
+  const int per = C::per(p.gate_kind);
+  RowRing ring(ring_smem, NV * per);
   RowGroup<L> rg(sm);
+  const Gains<L, NV> gains(p, rg.l);
   const int H = p.H, nvec = H / 8, k = p.k, lane = threadIdx.x & 31;
   const long long step = (long long)gridDim.x * rg.kRows;
-  int row, next_row;
-  float w, next_w, logit, next_logit = 0.f;
-  auto ids = [&](long long t, int& row, float& w, float& logit) {
+  // this lane's slot of token t; a row out of range counts as none
+  auto ids = [&](long long t, int& row, float& w) {
     row = -1;
     w = 0.f;
     if (t < p.T && lane < k) {
       row = __ldg(p.row_of_slot + t * k + lane);
       w = __ldg(p.topk_w + t * k + lane);
     }
-    logit = p.gate_kind == 1 && t < p.T ? __ldg(static_cast<const float*>(p.gate) + t) : 0.f;
   };
-  uint4 buf[KB][NV];
-  // rows of slots j0 .. j0 + KB - 1; one that is out of range counts as zeros
-  auto rows = [&](int row, int j0) {
+  auto checked = [&](long long t, int& row, float& w) {
+    if (t < p.T && lane < k && (row < 0 || row >= p.R)) {
+      set_status(p.status, MOE_STATUS_BAD_INDEX);
+      row = -1;
+      w = 0.f;
+    }
+  };
+  auto fetch = [&](int stage, long long t, int row) {
 #pragma unroll
     for (int u = 0; u < KB; ++u) {
-      const int q = __shfl_sync(0xffffffffu, row, (j0 + u) & 31);
-      const bool there = j0 + u < k && q >= 0 && q < p.R;
+      if (u >= k) break;
+      const int q = __shfl_sync(0xffffffffu, row, u);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = rg.l + i * L;
-        buf[u][i] = there && c < nvec ? __ldg(reinterpret_cast<const uint4*>(p.z + (size_t)q * H) + c) : make_uint4(0, 0, 0, 0);
+        const bool there = q >= 0 && c < nvec;
+        ring.fetch(stage, i * per + u, p.z + (there ? (size_t)q * H + 8 * c : 0), there);
       }
     }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = rg.l + i * L;
+      const bool there = t < p.T && c < nvec;
+      const size_t at = there ? (size_t)t * H + 8 * c : 0;
+      if (p.residual) {
+#pragma unroll
+        for (int v = 0; v < SU; ++v)
+          ring.fetch(stage, i * per + KB + v, reinterpret_cast<const uint4*>(static_cast<const S*>(p.residual) + at) + v, there);
+      }
+      if (p.gate_kind == 2) ring.fetch(stage, i * per + KB + SU, static_cast<const __nv_bfloat16*>(p.gate) + at, there);
+    }
+    ring.commit();
   };
-  const long long first = (long long)blockIdx.x * rg.kRows;
-  ids(first + rg.g, row, w, logit);
-  rows(row, 0);
-  ids(first + step + rg.g, next_row, next_w, next_logit);
-  for (long long base = first; base < p.T; base += step) {
+  const long long first = (long long)blockIdx.x * rg.kRows + rg.g;
+  float w[STAGES];  // of the token in hand and the STAGES - 1 behind it
+  int ahead_row;
+  float ahead_w;
+#pragma unroll
+  for (int q = 0; q < STAGES - 1; ++q) {
+    int row;
+    ids(first + q * step, row, w[q]);
+    checked(first + q * step, row, w[q]);
+    fetch(q, first + q * step, row);
+  }
+  ids(first + (STAGES - 1) * step, ahead_row, ahead_w);
+  float logit = p.gate_kind == 1 && first < p.T ? __ldg(static_cast<const float*>(p.gate) + first) : 0.f;
+  int stage = 0;
+  for (long long base = (long long)blockIdx.x * rg.kRows; base < p.T; base += step) {
     const long long t = base + rg.g;
-    if (t < p.T && lane < k && (row < 0 || row >= p.R)) set_status(p.status, MOE_STATUS_BAD_INDEX);
-    if (row < 0 || row >= p.R) w = 0.f;
-    Vec8<S> res[NV];
-    uint4 gate2[NV];
-    load_sides<S, L, NV>(p, rg, t, res, gate2);
+    checked(t + (STAGES - 1) * step, ahead_row, ahead_w);
+    fetch(stage == 0 ? STAGES - 1 : stage - 1, t + (STAGES - 1) * step, ahead_row);
+    w[STAGES - 1] = ahead_w;
+    ids(t + STAGES * step, ahead_row, ahead_w);
+    const float gate = logit;
+    logit = p.gate_kind == 1 && t + step < p.T ? __ldg(static_cast<const float*>(p.gate) + t + step) : 0.f;
+    ring.template wait<STAGES - 1>();
     float z[NV][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) z[i][j] = 0.f;
-    for (int j0 = 0; j0 < k; j0 += KB) {
-      if (j0) rows(row, j0);
 #pragma unroll
-      for (int u = 0; u < KB; ++u) {
-        const float wu = __shfl_sync(0xffffffffu, w, (j0 + u) & 31);
-        if (j0 + u < k) {
+    for (int u = 0; u < KB; ++u) {
+      if (u >= k) break;
+      const float wu = __shfl_sync(0xffffffffu, w[0], u);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float f[8];
+        unpack8(ring.at(stage, i * per + u), f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[i][j] = __fmaf_rn(wu, f[j], z[i][j]);
+      }
+    }
+    if (k > KB) {
+      int row;
+      float unused;
+      ids(t, row, unused);
+      if (row >= p.R) row = -1;
+      for (int j0 = KB; j0 < k; j0 += 4) {
+        uint4 buf[4][NV];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int q = __shfl_sync(0xffffffffu, row, (j0 + u) & 31);
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            const int c = rg.l + i * L;
+            buf[u][i] = j0 + u < k && q >= 0 && c < nvec ? __ldg(reinterpret_cast<const uint4*>(p.z + (size_t)q * H) + c)
+                                                         : make_uint4(0, 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float wu = __shfl_sync(0xffffffffu, w[0], (j0 + u) & 31);
+          if (j0 + u >= k) break;
 #pragma unroll
           for (int i = 0; i < NV; ++i) {
             float f[8];
@@ -203,12 +287,16 @@ __global__ void __launch_bounds__(kNormThreads, NV == 4 ? 1 : 2) combine_post_no
         }
       }
     }
-    const float gate = logit;
-    row = next_row;
-    w = next_w;
-    logit = next_logit;
-    rows(row, 0);
-    ids(t + 2 * step, next_row, next_w, next_logit);
+    Vec8<S> res[NV];
+    uint4 gate2[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      res[i] = p.residual ? ring.template vec<S>(stage, i * per + KB) : zero_vec<S>();
+      gate2[i] = p.gate_kind == 2 ? ring.at(stage, i * per + KB + SU) : make_uint4(0, 0, 0, 0);
+    }
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+#pragma unroll
+    for (int q = 0; q + 1 < STAGES; ++q) w[q] = w[q + 1];
     if (p.z_out && t < p.T) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -216,7 +304,7 @@ __global__ void __launch_bounds__(kNormThreads, NV == 4 ? 1 : 2) combine_post_no
         if (c < nvec) Vec8<__nv_bfloat16>::store(p.z_out + t * H + 8 * c, z[i]);
       }
     }
-    finish_row<S, L, NV>(p, rg, t, z, res, gate2, gate);
+    finish_row<S, L, NV>(p, rg, gains, t, z, res, gate2, gate);
   }
 }
 
@@ -240,17 +328,17 @@ template <typename S, int L, int NV, bool kElement>
 struct PostBwd {
   static constexpr int SU = sizeof(Vec8<S>) / 16;                // units of a stream vector
   static constexpr int PER = 1 + SU + (kElement ? 1 : 0);        // z, dout, gate
-  using Ring = RowRing<NV * PER, ring_stages(NV * PER)>;
+  static constexpr int UNITS = NV * PER;
 };
 template <typename S, int L, int NV, bool kElement>
-__global__ void __launch_bounds__(kNormThreads, NV == 4 ? 1 : 2) post_norm_bwd_kernel(const PostBwdArgs p) {
+__global__ void __launch_bounds__(kNormThreads, bwd_blocks(NV)) post_norm_bwd_kernel(const PostBwdArgs p) {
   pdl_wait();
   pdl_trigger();
   using P = PostBwd<S, L, NV, kElement>;
-  constexpr int SU = P::SU, STAGES = ring_stages(NV * P::PER);
+  constexpr int SU = P::SU, STAGES = ring_stages(P::UNITS);
   __shared__ float sm[16];
   extern __shared__ __align__(16) uint8_t ring_smem[];
-  typename P::Ring ring(ring_smem);
+  RowRing ring(ring_smem, P::UNITS);
   RowGroup<L> rg(sm);
   const int H = p.H, nvec = H / 8, T = p.T;
   const float inv_h = 1.0f / (float)H;
@@ -285,7 +373,7 @@ __global__ void __launch_bounds__(kNormThreads, NV == 4 ? 1 : 2) post_norm_bwd_k
     const float r = p.norm && live ? __ldg(p.rstd + t) : 1.f;
     Gate tok = {1.f, 0.f};
     if (!kElement && p.gate_kind == 1 && live) tok = sigmoid(__ldg(static_cast<const float*>(p.gate) + t));
-    ring.wait();
+    ring.template wait<STAGES - 2>();
     const int cur = stage;
     float m = 0.f, dg = 0.f;  // sums of dn n, and of dout n gain
     float n[NV][8], dn[NV][8];
@@ -339,24 +427,27 @@ __global__ void __launch_bounds__(kNormThreads, NV == 4 ? 1 : 2) post_norm_bwd_k
   }
 }
 
-// Lanes of a token's row, vectors of a lane and rows under way at a time in the combine.
+// Lanes of a token's row and vectors of a lane in the combine.
 template <class F>
 int with_combine_shape(int H, F&& f) {
   using std::integral_constant;
-  if (H <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{}, integral_constant<int, 8>{});
-  if (H <= 512) return f(integral_constant<int, 32>{}, integral_constant<int, 2>{}, integral_constant<int, 8>{});
-  if (H <= 1024) return f(integral_constant<int, 64>{}, integral_constant<int, 2>{}, integral_constant<int, 8>{});
-  if (H <= 2048) return f(integral_constant<int, 128>{}, integral_constant<int, 2>{}, integral_constant<int, 8>{});
-  if (H <= 4096) return f(integral_constant<int, 256>{}, integral_constant<int, 2>{}, integral_constant<int, 8>{});
-  return f(integral_constant<int, 256>{}, integral_constant<int, 4>{}, integral_constant<int, 4>{});
+  if (H <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  if (H <= 512) return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  if (H <= 1024) return f(integral_constant<int, 128>{}, integral_constant<int, 1>{});
+  if (H <= 2048) return f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+  if (H <= 4096) return f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  return f(integral_constant<int, 256>{}, integral_constant<int, 4>{});
 }
 
 template <typename S>
 int run_post_norm(const char* fn, const PostArgs& a, bool combine, cudaStream_t s) {
   if (combine)
-    return with_combine_shape(a.H, [&](auto l, auto nv, auto kb) {
-      constexpr int L = decltype(l)::value, NV = decltype(nv)::value, KB = decltype(kb)::value;
-      launch_pdl(combine_post_norm_kernel<S, L, NV, KB>, norm_grid(a.T, kNormThreads / L, 2, 1 << 30), kNormThreads, 0, s, a);
+    return with_combine_shape(a.H, [&](auto l, auto nv) {
+      constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
+      auto kern = combine_post_norm_kernel<S, L, NV>;
+      const size_t smem = CombineRing<S, NV>::bytes(a.gate_kind);
+      if (int rc = allow_smem(fn, reinterpret_cast<const void*>(kern), smem)) return rc;
+      launch_pdl(kern, norm_grid(a.T, kNormThreads / L, blocks_per_sm(smem, NV == 1 ? 3 : 1), 1 << 30), kNormThreads, smem, s, a);
       return check_launch(fn);
     });
   return with_row_shape(a.H, [&](auto l, auto nv) {
@@ -461,8 +552,8 @@ int moe_post_norm_bwd(const void* dout, int fp32, const void* z, const float* ga
       using S = decltype(type);
       constexpr bool kElement = decltype(element)::value;
       auto kern = post_norm_bwd_kernel<S, L, NV, kElement>;
-      const size_t smem = norm_smem(PostBwd<S, L, NV, kElement>::Ring::kBytes, NV);
-      grid = norm_grid(T, kNormThreads / L, smem <= 110 * 1024 ? 2 : 1, kNormParts);
+      const size_t smem = norm_smem(PostBwd<S, L, NV, kElement>::UNITS, NV);
+      grid = norm_grid(T, kNormThreads / L, blocks_per_sm(smem, bwd_blocks(NV)), kNormParts);
       if (int rc = allow_smem(fn, reinterpret_cast<const void*>(kern), smem)) return rc;
       launch_pdl(kern, grid, kNormThreads, smem, s, a);
       return check_launch(fn);
