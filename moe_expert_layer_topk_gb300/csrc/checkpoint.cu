@@ -51,7 +51,9 @@ __global__ void __launch_bounds__(256) ckpt_unpack_kernel(const uint2* __restric
     a[v] = unpack_codes8(__ldg(q + v), __ldg(scale + (v >> 2)));
 }
 
-// Thread = eight columns of one token, written to its k rows.
+// Warp = 64 vectors (512 columns) of one token, written to its k rows, whose ids its
+// lanes hold.  8192 x 2048 from codes, top-8: 47.4 us (6.1 TB/s); a vector a lane 50.2, with
+// the ids read by every thread 51.5; four vectors 47.7, eight 49.0.
 template <bool kCodes>
 __global__ void __launch_bounds__(256) dispatch_rows_kernel(const void* __restrict__ x, const unsigned short* __restrict__ scale,
                                                             const int32_t* __restrict__ row_of_slot, const float* __restrict__ topk_w,
@@ -59,24 +61,34 @@ __global__ void __launch_bounds__(256) dispatch_rows_kernel(const void* __restri
                                                             float* __restrict__ row_w, int* status) {
   pdl_wait();
   pdl_trigger();
-  const int nvec = H / 8;
-  const size_t total = (size_t)T * nvec;
-  for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < total; i += (size_t)gridDim.x * blockDim.x) {
-    const size_t t = i / nvec;
-    const int v = (int)(i - t * nvec);
-    uint4 val;
-    if (kCodes)
-      val = unpack_codes8(__ldg(static_cast<const uint2*>(x) + i), __ldg(scale + (i >> 2)));
-    else
-      val = __ldg(static_cast<const uint4*>(x) + i);
-    for (int j = 0; j < k; ++j) {
-      const int row = __ldg(row_of_slot + t * k + j);
-      if (row < 0 || row >= R) {
-        if (v == 0) set_status(status, MOE_STATUS_BAD_INDEX);
-        continue;
+  constexpr int NV = 2;
+  const int lane = threadIdx.x & 31, nvec = H / 8, pieces = (nvec + 32 * NV - 1) / (32 * NV);
+  const size_t total = (size_t)T * pieces, nw = (size_t)gridDim.x * 8;
+  for (size_t i = blockIdx.x * (size_t)8 + (threadIdx.x >> 5); i < total; i += nw) {
+    const size_t t = i / pieces;
+    const int v0 = (int)(i - t * pieces) * 32 * NV + lane;
+    int row = lane < k ? __ldg(row_of_slot + t * k + lane) : 0;
+    uint4 val[NV];
+#pragma unroll
+    for (int q = 0; q < NV; ++q) {
+      const int v = v0 + 32 * q;
+      val[q] = make_uint4(0, 0, 0, 0);
+      if (v < nvec) {
+        const size_t at = t * nvec + v;
+        val[q] = kCodes ? unpack_codes8(__ldg(static_cast<const uint2*>(x) + at), __ldg(scale + (at >> 2))) : __ldg(static_cast<const uint4*>(x) + at);
       }
-      x_perm[(size_t)row * nvec + v] = val;
-      if (v == 0 && row_w) row_w[row] = __ldg(topk_w + t * k + j);
+    }
+    if (row < 0 || row >= R) {
+      set_status(status, MOE_STATUS_BAD_INDEX);
+      row = -1;
+    }
+    if (v0 == lane && row_w && lane < k && row >= 0) row_w[row] = __ldg(topk_w + t * k + lane);
+    for (int j = 0; j < k; ++j) {
+      const int r = __shfl_sync(0xffffffffu, row, j);
+      if (r < 0) continue;
+#pragma unroll
+      for (int q = 0; q < NV; ++q)
+        if (v0 + 32 * q < nvec) x_perm[(size_t)r * nvec + v0 + 32 * q] = val[q];
     }
   }
 }
@@ -138,7 +150,7 @@ int moe_dispatch_rows(const void* x, const void* scale, const int32_t* row_of_sl
   if (!aligned16(x) || !aligned16(x_perm) || (scale && !aligned16(scale)))
     return fail(MOE_ERR_ALIGNMENT, "%s: tensors must be 16-byte aligned", fn);
   auto run = [&](auto kern) {
-    launch_pdl(kern, grid_of((size_t)T * (H / 8), 16), 256, 0, static_cast<cudaStream_t>(stream), x,
+    launch_pdl(kern, grid_of((size_t)T * ((H / 8 + 63) / 64) * 32, 16), 256, 0, static_cast<cudaStream_t>(stream), x,
                static_cast<const unsigned short*>(scale), row_of_slot, topk_w, T, H, k, T * k, static_cast<uint4*>(x_perm), row_w,
                status_word());
   };

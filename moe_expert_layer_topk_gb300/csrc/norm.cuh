@@ -42,50 +42,33 @@ struct RowGroup {
     }
     return v;
   }
-  // 1/sqrt(mean + eps) of the squares of RU rows' values, at(u, i, j) for element j of
-  // row u's i-th vector of this lane (0 where it has none).  Squares beyond fp32's range
-  // are added again of values times 2^-80 (8192 of the largest, 2^48 each, add up to
-  // 2^109); eps is nothing beside those.  An infinity gives 0, a NaN NaN.
-  template <int RU, int NV, class At>
-  __device__ __forceinline__ void rstds(float (&r)[RU], float inv_h, float eps, At&& at) {
-    bool big = false;
+  // 1/sqrt(mean + eps) of the squares of a row's values, at(i, j) for element j of this
+  // lane's i-th vector (0 where it has none).  Squares beyond fp32's range are added
+  // again of values times 2^-80 (8192 of the largest, 2^48 each, add up to 2^109); eps
+  // is nothing beside those.  An infinity gives 0, a NaN NaN.
+  template <int NV, class At>
+  __device__ __forceinline__ float rstd(float inv_h, float eps, At&& at) {
+    float ss = 0.f;
 #pragma unroll
-    for (int u = 0; u < RU; ++u) {
-      float ss = 0.f;
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = __fmaf_rn(at(i, j), at(i, j), ss);
+    ss = sum(ss);
+    float r = __frsqrt_rn(__fmaf_rn(ss, inv_h, eps));
+    const bool big = !(ss <= 3.402823466e+38f);
+    if (L <= 32 ? __any_sync(0xffffffffu, big) : big) {
+      float s2 = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = __fmaf_rn(at(u, i, j), at(u, i, j), ss);
-      r[u] = sum(ss);
+        for (int j = 0; j < 8; ++j) {
+          const float v = at(i, j) * 0x1p-80f;
+          s2 = __fmaf_rn(v, v, s2);
+        }
+      s2 = sum(s2);
+      if (big) r = __frsqrt_rn(s2 * inv_h) * 0x1p-80f;
     }
-#pragma unroll
-    for (int u = 0; u < RU; ++u) {
-      big |= !(r[u] <= 3.402823466e+38f);
-    }
-    if (L <= 32 ? __any_sync(0xffffffffu, big) : big) {
-#pragma unroll
-      for (int u = 0; u < RU; ++u) {
-        float s2 = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float v = at(u, i, j) * 0x1p-80f;
-            s2 = __fmaf_rn(v, v, s2);
-          }
-        s2 = sum(s2);
-        r[u] = r[u] <= 3.402823466e+38f ? __frsqrt_rn(__fmaf_rn(r[u], inv_h, eps)) : __frsqrt_rn(s2 * inv_h) * 0x1p-80f;
-      }
-    } else {
-#pragma unroll
-      for (int u = 0; u < RU; ++u) r[u] = __frsqrt_rn(__fmaf_rn(r[u], inv_h, eps));
-    }
-  }
-  template <int NV, class At>
-  __device__ __forceinline__ float rstd(float inv_h, float eps, At&& at) {
-    float r[1];
-    rstds<1, NV>(r, inv_h, eps, [&](int, int i, int j) { return at(i, j); });
-    return r[0];
+    return r;
   }
 };
 
