@@ -135,7 +135,7 @@ struct Params {
   int comb_T;
   int comb_k;
   // GATE_UP_CKPT, DOWN_BWD_CKPT: the scales of g, u [M, 2I/32] (bf16 bits).  DOWN_BWD_CKPT
-  // too: the rows' weights (null: 1), h_w, and the partial sums of d_w [2 n_tiles, M]
+  // too: the rows' weights (null: 1), h_w, and the partial sums of d_w [M, 2 n_tiles]
   unsigned short* ckpt_scale;
   const float* row_w;
   void* h_w;
@@ -189,7 +189,8 @@ template <int KIND, int CTAS>
 struct Cfg {
   static constexpr bool gu_tma = KIND == DENSE_ADD;
   static constexpr int GU_SETS = EP_GU_SETS;
-  static constexpr int STAGES = CTAS == 1 ? (gu_tma ? 3 : 4) : (gu_tma ? 4 : 6);
+  // (the 8-bit SwiGLU backward's pairs: one stage fewer, for a second box a warp)
+  static constexpr int STAGES = CTAS == 1 ? (gu_tma ? 3 : 4) : (gu_tma ? 4 : (KIND == DOWN_BWD_CKPT ? 5 : 6));
   static constexpr int B_BYTES = B_BYTES_MAX / CTAS;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int TILE_M = BM * CTAS;
@@ -203,7 +204,7 @@ struct Cfg {
   // row-gathering kinds: four more warps share the row gather
   static constexpr int GW = is_gather(KIND) ? 4 : 0;
   static constexpr int NTHREADS = 64 + 32 * (EPW + GW);
-  static constexpr int RING = EP8 ? 1 : EP_SLOTS;
+  static constexpr int RING = EP8 && !(KIND == DOWN_BWD_CKPT && CTAS == 2) ? 1 : EP_SLOTS;
   static constexpr int EP_WARP = gu_tma ? EP_BOX_BYTES * 2 * GU_SETS : EP_BOX_BYTES * RING;
   static constexpr int EP_TOTAL = EPW * EP_WARP;
   // without the segment tables
@@ -218,6 +219,7 @@ static_assert(Cfg<GATE_UP_FWD, 1>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
                   Cfg<DOWN_FWD, 1>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
                   Cfg<DOWN_BWD_DX, 1>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
                   Cfg<DOWN_BWD_CKPT, 1>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
+                  Cfg<DOWN_BWD_CKPT, 2>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
                   Cfg<GATE_UP_CKPT, 1>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
                   Cfg<GATE_UP_CKPT, 2>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
                   Cfg<GATE_UP_BWD_DX, 1>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
@@ -739,27 +741,38 @@ __global__ void __launch_bounds__(Cfg<KIND, CTAS>::NTHREADS, 1)
       if constexpr (KIND == DOWN_BWD_DX) {
         if (any) ld_gu(cbeg, gq, uq);
       }
-      // The same in 8 bits: 32 bytes of codes each, and the two scales.
-      uint32_t gc[8], uc[8], gsc = 0, usc = 0;
-      auto ld_codes = [&](int c, uint32_t (&g8)[8], uint32_t (&u8)[8], uint32_t& gs, uint32_t& us) {
+      // The same in 8 bits: 32 bytes of codes each a chunk; the scales of the tile's
+      // columns (2, 4 or 8 groups each of g and u) at once, the two of a word belonging to
+      // the two warps of a lane quadrant.
+      uint32_t gc[8], uc[8];
+      uint4 gsc = make_uint4(0, 0, 0, 0), usc = gsc;
+      auto ld_codes = [&](int c, uint32_t (&g8)[8], uint32_t (&u8)[8]) {
         const bool ok = lane < nvalid;
         const size_t r = (size_t)(ok ? rb + lane : 0);
         const uint4* row = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.aux) + r * 2 * p.I);
         const int v = (t.n0 + c) >> 4, vu = (p.I + t.n0 + c) >> 4;
-        const unsigned short* sc = p.ckpt_scale + r * (p.I / 16) + ((t.n0 + c) >> 5);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint4 a = __ldg(row + v + i), b = __ldg(row + vu + i);
           g8[4 * i] = a.x, g8[4 * i + 1] = a.y, g8[4 * i + 2] = a.z, g8[4 * i + 3] = a.w;
           u8[4 * i] = b.x, u8[4 * i + 1] = b.y, u8[4 * i + 2] = b.z, u8[4 * i + 3] = b.w;
         }
-        gs = __ldg(sc);
-        us = __ldg(sc + p.I / 32);
       };
       float row_w = 1.0f, row_dw = 0.0f;
       if constexpr (KIND == DOWN_BWD_CKPT) {
         if (any) {
-          ld_codes(cbeg, gc, uc, gsc, usc);
+          ld_codes(cbeg, gc, uc);
+          const unsigned short* sc = p.ckpt_scale + (size_t)(lane < nvalid ? rb + lane : 0) * (p.I / 16) + (t.n0 >> 5);
+          auto ld_scales = [&](const unsigned short* q) {
+            if (p.BN == 256) return __ldg(reinterpret_cast<const uint4*>(q));
+            if (p.BN == 128) {
+              const uint2 w = __ldg(reinterpret_cast<const uint2*>(q));
+              return make_uint4(w.x, w.y, 0, 0);
+            }
+            return make_uint4(__ldg(reinterpret_cast<const uint32_t*>(q)), 0, 0, 0);
+          };
+          gsc = ld_scales(sc);
+          usc = ld_scales(sc + p.I / 32);
           if (p.row_w && lane < nvalid) row_w = __ldg(p.row_w + rb + lane);
         }
       }
@@ -1060,12 +1073,12 @@ __global__ void __launch_bounds__(Cfg<KIND, CTAS>::NTHREADS, 1)
         // columns, one of 2 n_tiles parts of it.
         const size_t pitch = (size_t)p.I * 4;
         for (int c = cbeg; any && c < cend; c += cstep) {
-          uint32_t gn[8], un[8], gsn = 0, usn = 0;
-          if (c + cstep < cend) ld_codes(c + cstep, gn, un, gsn, usn);
+          uint32_t gn[8], un[8];
+          if (c + cstep < cend) ld_codes(c + cstep, gn, un);
           uint32_t a[32];
           tmem_ld32(taddr + c, a);
           tmem_wait_ld();
-          const float gs = bf16_bits(gsc), us = bf16_bits(usc);
+          const float gs = sub ? bf16hi(gsc.x) : bf16lo(gsc.x), us = sub ? bf16hi(usc.x) : bf16lo(usc.x);
           uint32_t og[16], ou[16], oh[16];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -1103,10 +1116,10 @@ __global__ void __launch_bounds__(Cfg<KIND, CTAS>::NTHREADS, 1)
             gc[i] = gn[i];
             uc[i] = un[i];
           }
-          gsc = gsn;
-          usc = usn;
+          gsc = make_uint4(gsc.y, gsc.z, gsc.w, 0);
+          usc = make_uint4(usc.y, usc.z, usc.w, 0);
         }
-        if (lane < nvalid) p.dw_part[(size_t)(2 * (t.n0 / p.BN) + sub) * p.M + rb + lane] = row_dw;
+        if (lane < nvalid) p.dw_part[(size_t)(rb + lane) * (2 * p.n_tiles) + 2 * (t.n0 / p.BN) + sub] = row_dw;
       } else {  // DW: fp32 [group, M, N] (optionally split at split_m over two tensors)
         const bool nonempty = ctl->grp_rows[t.group] > 0;
         if (any && (nonempty || !p.accumulate)) {
@@ -1167,21 +1180,33 @@ __global__ void __launch_bounds__(Cfg<KIND, CTAS>::NTHREADS, 1)
 // segment's length (rows clamped to [0, rows) like the kernel's own table).
 // An empty segment keeps the template unchanged; no k-block ever reads it.
 // d_w of the 8-bit SwiGLU backward: a row's parts added in their order, for each slot
-// (row_of_slot) or each row.
+// (row_of_slot) or each row; 0 where no segment of an expert holds the row.
 __global__ void __launch_bounds__(256) ckpt_dw_kernel(const float* __restrict__ part, int parts, int R,
-                                                      const int32_t* __restrict__ row_of_slot, int n, float* __restrict__ d_w,
-                                                      int* status) {
+                                                      const int32_t* __restrict__ seg_offsets, const int32_t* __restrict__ seg_expert,
+                                                      int num_seg, int E, const int32_t* __restrict__ row_of_slot, int n,
+                                                      float* __restrict__ d_w, int* status) {
   pdl_wait();
   pdl_trigger();
-  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) {
-    const int row = row_of_slot ? __ldg(row_of_slot + i) : i;
-    float v = 0.f;
-    if (row < 0 || row >= R)
-      set_status(status, MOE_STATUS_BAD_INDEX);
-    else
-      for (int q = 0; q < parts; ++q) v += __ldg(part + (size_t)q * R + row);
-    d_w[i] = v;
+  extern __shared__ int off[];  // [num_seg + 1]
+  for (int s = threadIdx.x; num_seg > 0 && s <= num_seg; s += blockDim.x) off[s] = __ldg(seg_offsets + s);
+  __syncthreads();
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= n) return;
+  const int row = row_of_slot ? __ldg(row_of_slot + i) : i;
+  float v = 0.f;
+  if (row < 0 || row >= R) {
+    set_status(status, MOE_STATUS_BAD_INDEX);
+  } else if (num_seg > 0 && row >= off[0] && row < off[num_seg]) {
+    int lo = 0, hi = num_seg - 1;  // the last segment that starts at or before the row
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (off[mid] <= row) lo = mid; else hi = mid - 1;
+    }
+    const int e = seg_expert ? __ldg(seg_expert + lo) : lo;
+    if (e >= 0 && e < E)
+      for (int q = 0; q < parts; ++q) v += __ldg(part + (size_t)row * parts + q);
   }
+  d_w[i] = v;
 }
 
 // y = bf16(acc) (round to nearest even), eight elements per step.
@@ -1319,8 +1344,8 @@ int launch(Params p, const CUtensorMap& a, const CUtensorMap& b0, const CUtensor
 template <int KIND>
 int run(bool pair, const Params& p, const CUtensorMap& a, const CUtensorMap& b0, const CUtensorMap& b1,
         const CUtensorMap& o0, const CUtensorMap& o1, cudaStream_t s, const char* what) {
-  if constexpr (KIND == GATE_UP_BWD_DX || KIND == GATE_UP_FWD || KIND == GATE_UP_CKPT || KIND == DOWN_FWD ||
-                KIND == DOWN_COMBINE) {
+  if constexpr (KIND == GATE_UP_BWD_DX || KIND == GATE_UP_FWD || KIND == GATE_UP_CKPT || KIND == DOWN_BWD_CKPT ||
+                KIND == DOWN_FWD || KIND == DOWN_COMBINE) {
     if (pair) return launch<KIND, 2>(p, a, b0, b1, o0, o1, s, what);
   }
   return launch<KIND, 1>(p, a, b0, b1, o0, o1, s, what);
@@ -1772,9 +1797,6 @@ int moe_grouped_gemm_down_bwd_ckpt(const void* dy_perm, const float* row_w, cons
   if (!ws || ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, ws ? ws_bytes : (size_t)0, need);
   if (!aligned16(ws)) return fail(MOE_ERR_ALIGNMENT, "%s: ws must be 16-byte aligned", fn);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // rows outside every segment leave no part
-  cudaError_t e = cudaMemsetAsync(ws, 0, need, s);
-  if (e != cudaSuccess) return fail_cuda(fn, e);
   const int bn = pick_bn(I);
   if (num_seg > 0) {
     Params p = base_params(num_seg, seg_offsets, seg_expert, E);
@@ -1792,16 +1814,20 @@ int moe_grouped_gemm_down_bwd_ckpt(const void* dy_perm, const float* row_w, cons
     p.h_w = h_w;
     p.dw_part = static_cast<float*>(ws);
     CUtensorMap ta, tb, to, th;
+    // Pairs by the forward kinds' rule: with 512 rows per expert 232 us against 243 (three
+    // outputs beside the operands; with one box a warp and six stages 252), with 128 rows
+    // per segment the same.
+    const bool pair = pair_for_rows(bn, R, num_seg, E);
     if (int rc = make_tmap(&ta, dy_perm, H, R, 64, BM)) return rc;
-    if (int rc = make_tmap_mn(&tb, Wd, I, (uint64_t)E * H, bn / 64)) return rc;
+    if (int rc = make_tmap_mn(&tb, Wd, I, (uint64_t)E * H, bn / 64 / (pair ? 2 : 1))) return rc;
     if (int rc = make_out_map(&to, dgu, 2 * I, R, false)) return rc;
     if (int rc = make_out_map(&th, h_w, I, R, false)) return rc;
-    if (int rc = run<DOWN_BWD_CKPT>(false, p, ta, tb, tb, to, th, s, fn)) return rc;
+    if (int rc = run<DOWN_BWD_CKPT>(pair, p, ta, tb, tb, to, th, s, fn)) return rc;
   }
   const int n = row_of_slot ? T * k : R;
   if (n == 0) return MOE_OK;
-  launch_pdl(ckpt_dw_kernel, (n + 255) / 256, 256, 0, s, static_cast<const float*>(ws), 2 * (I / bn), R, row_of_slot, n, d_w,
-             status_word());
+  launch_pdl(ckpt_dw_kernel, (n + 255) / 256, 256, sizeof(int) * (num_seg + 1), s, static_cast<const float*>(ws), 2 * (I / bn), R,
+             seg_offsets, seg_expert, num_seg, E, row_of_slot, n, d_w, status_word());
   return check_launch(fn);
 }
 

@@ -121,6 +121,7 @@ def table(kind, R, E):
 
 
 CASES = [("experts", 7, 64, 64, 2), ("experts", 300, 128, 64, 8), ("experts", 700, 512, 320, 4), ("experts", 2500, 256, 128, 3),
+         ("experts", 2600, 128, 256, 5), ("experts", 900, 64, 512, 2),
          ("experts", 129, 64, 192, 1), ("blocks", 400, 128, 128, 3), ("blocks", 1000, 256, 768, 5)]
 
 
@@ -201,6 +202,9 @@ def test_no_rows_or_segments():
     x, W, h = e(R, H, dt=BF), e(E, I, H, dt=BF), e(R, I, dt=BF).fill_(9.0)
     q, s, off = torch.full((R, 2 * I), 7, dtype=torch.int8, device="cuda"), e(R, 4, dt=BF).fill_(9.0), torch.zeros(E + 1, dtype=torch.int32, device="cuda")
     ws, dw, dgu = torch.empty(m.moe_grouped_gemm_down_bwd_ckpt_workspace_size(R, I), dtype=torch.uint8, device="cuda"), e(R).fill_(9.0), e(R, 2 * I, dt=BF).fill_(9.0)
+    m.moe_grouped_gemm_down_bwd_ckpt(x, None, q, s, W, 0, None, None, R, H, I, E, dgu, h, dw, ws=ws)
+    assert (dw == 0).all()
+    dw.fill_(9.0)
     for n in (0, E):  # no segment, and empty ones
         m.moe_grouped_gemm_swiglu_ckpt(x, W, W, n, off, None, R, H, I, E, h, q, s)
         m.moe_grouped_gemm_down_bwd_ckpt(x, None, q, s, W, n, off, None, R, H, I, E, dgu, h, dw, ws=ws)
