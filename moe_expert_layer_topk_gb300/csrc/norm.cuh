@@ -1,5 +1,6 @@
-// Rows spread over groups of lanes, their sums, and the root-mean-square norm's
-// statistics: shared by the norms before and after a block.
+// Rows spread over groups of lanes, their sums, the root-mean-square norm's
+// statistics, and rings of rows in shared memory: shared by the norms before and
+// after a block.
 #pragma once
 
 #include <type_traits>
@@ -8,38 +9,70 @@
 
 namespace moe {
 
-constexpr int kNormThreads = 256;
 constexpr int kNormMaxH = 8192;
 // rows of partial gain gradients that a backward leaves at most
 constexpr int kNormParts = 512;
 
-// A row belongs to L lanes (a part of a warp, a warp, or several warps), lane l of
-// them holding the 16-byte vectors l, l + L, ... of it (NV at most).  A block of 256
-// threads works on 256/L rows; every thread of a block makes the same number of
-// steps, so that full-warp shuffles and the rows' barriers always meet.
+// floats of shared memory that a block's row sums take: two slots of two sums, for each
+// group of at most eight places for sixteen warps
+constexpr int kSumFloats = 2 * 2 * 8 * 16;
+
+// A row belongs to a group of lanes: L of them (8, 16 or 32, parts of a warp), or W
+// whole warps (L = 0); lane l of n holds the 16-byte vectors l, l + n, ... of it.  Every
+// thread of a block makes the same number of steps, so that full-warp shuffles and the
+// groups' barriers always meet.
 template <int L>
 struct RowGroup {
-  static constexpr int kRows = kNormThreads / L;
-  int g, l, slot;
-  float* sm;  // [2][8]
-  __device__ __forceinline__ explicit RowGroup(float* s) : g(threadIdx.x / L), l(threadIdx.x % L), slot(0), sm(s) {}
-  // The row's sum in each of its lanes, always added in the same order.  Two slots:
-  // a warp writes one again only behind the next sum's barrier, which the row's other
-  // warps reach with this sum read.
-  __device__ __forceinline__ float sum(float v) {
-#pragma unroll
-    for (int off = (L < 32 ? L : 32) / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    if constexpr (L > 32) {
-      constexpr int W = L / 32;
-      const int warp = threadIdx.x >> 5;
-      float* p = sm + 8 * slot;
-      slot ^= 1;
-      if ((threadIdx.x & 31) == 0) p[warp] = v;
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "n"(L) : "memory");
-      v = 0.f;
-#pragma unroll
-      for (int i = 0; i < W; ++i) v += p[g * W + i];
+  int W, g, l, slot;
+  float* sm;
+  __device__ __forceinline__ RowGroup(float* s, int w) : W(w), slot(0), sm(s) {
+    const int n = lanes();
+    g = threadIdx.x / n;
+    l = threadIdx.x - g * n;
+    if constexpr (L == 0) {  // places of warps that a group does not have stay zero
+      for (int i = threadIdx.x; i < kSumFloats; i += blockDim.x) sm[i] = 0.f;
+      __syncthreads();
     }
+  }
+  __device__ __forceinline__ int lanes() const { return L ? L : 32 * W; }
+  __device__ __forceinline__ int rows() const { return blockDim.x / lanes(); }
+  // The row's sums of a and b in each of its lanes, always added in the same order.  Two
+  // slots: a warp writes one again only behind the next sum's barrier, which the row's
+  // other warps reach with this sum read.
+  template <bool kTwo>
+  __device__ __forceinline__ void sums(float& a, float& b) {
+#pragma unroll
+    for (int off = (L ? L : 32) / 2; off > 0; off >>= 1) {
+      a += __shfl_xor_sync(0xffffffffu, a, off);
+      if (kTwo) b += __shfl_xor_sync(0xffffffffu, b, off);
+    }
+    if constexpr (L == 0) {
+      if (W == 1) return;
+      float* p = sm + slot * (kSumFloats / 2) + g * 16;
+      slot ^= 1;
+      const int w = (threadIdx.x >> 5) - g * W;
+      if ((threadIdx.x & 31) == 0) {
+        p[w] = a;
+        if (kTwo) p[w + kSumFloats / 4] = b;
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "r"(32 * W) : "memory");
+      a = places(p);
+      if (kTwo) b = places(p + kSumFloats / 4);
+    }
+  }
+  __device__ __forceinline__ float places(const float* p) const {
+    const float4* q = reinterpret_cast<const float4*>(p);
+    const float4 x = q[0], y = q[1];
+    float v = ((x.x + x.y) + (x.z + x.w)) + ((y.x + y.y) + (y.z + y.w));
+    if (W > 8) {
+      const float4 z = q[2], u = q[3];
+      v += ((z.x + z.y) + (z.z + z.w)) + ((u.x + u.y) + (u.z + u.w));
+    }
+    return v;
+  }
+  __device__ __forceinline__ float sum(float v) {
+    float none = 0.f;
+    sums<false>(v, none);
     return v;
   }
   // 1/sqrt(mean + eps) of the squares of a row's values, at(i, j) for element j of this
@@ -56,7 +89,7 @@ struct RowGroup {
     ss = sum(ss);
     float r = __frsqrt_rn(__fmaf_rn(ss, inv_h, eps));
     const bool big = !(ss <= 3.402823466e+38f);
-    if (L <= 32 ? __any_sync(0xffffffffu, big) : big) {
+    if (L ? __any_sync(0xffffffffu, big) : big) {
       float s2 = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
@@ -72,19 +105,27 @@ struct RowGroup {
   }
 };
 
+template <typename S>
+__device__ __forceinline__ Vec8<S> zero_vec() {
+  Vec8<S> v;
+  memset(&v, 0, sizeof v);
+  return v;
+}
+
 // A thread's own stretch of shared memory, through which the 16-byte vectors of its
 // next rows arrive while it works on one: no other thread reads it, so that waiting
 // for one's own copies is all the synchronisation there is.  A stage holds `units`
 // vectors.
-constexpr int kRingUnitBytes = kNormThreads * 16;  // a vector of each thread
 struct RowRing {
-  uint8_t* mine;
-  int units;
-  __device__ __forceinline__ RowRing(uint8_t* smem, int units) : mine(smem + threadIdx.x * 16), units(units) {}
+  uint32_t mine;  // shared-memory address
+  int pitch, stage_bytes;
+  __device__ __forceinline__ RowRing(uint8_t* smem, int units)
+      : mine((uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16), pitch(blockDim.x * 16), stage_bytes(units * pitch) {}
   // unit u of `stage` = the 16 bytes at src, or zeros
   __device__ __forceinline__ void fetch(int stage, int u, const void* src, bool there) {
-    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(mine + (stage * units + u) * kRingUnitBytes);
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(mine + stage * stage_bytes + u * pitch), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
   }
   __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
   // all but the last BUT stages' copies have arrived
@@ -92,8 +133,13 @@ struct RowRing {
   __device__ __forceinline__ void wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(BUT) : "memory");
   }
-  __device__ __forceinline__ const uint4& at(int stage, int u) const {
-    return *reinterpret_cast<const uint4*>(mine + (stage * units + u) * kRingUnitBytes);
+  __device__ __forceinline__ uint4 at(int stage, int u) const {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(mine + stage * stage_bytes + u * pitch)
+                 : "memory");
+    return v;
   }
   // the vector whose (first) unit is u
   template <typename S>
@@ -105,15 +151,8 @@ struct RowRing {
     return v;
   }
 };
-// stages that leave room for two blocks an SM (up to 12 units)
-__host__ __device__ constexpr int ring_stages(int units) { return units <= 6 ? 4 : (units <= 8 ? 3 : 2); }
-
-template <typename S>
-__device__ __forceinline__ Vec8<S> zero_vec() {
-  Vec8<S> v;
-  memset(&v, 0, sizeof v);
-  return v;
-}
+// stages of a backward's ring: about 64 KB of 256 threads
+__host__ __device__ constexpr int ring_stages(int units) { return units <= 4 ? 4 : (units <= 6 ? 3 : 2); }
 
 // Eight gains (ones without a tensor).
 struct Gain8 {
@@ -132,55 +171,57 @@ struct Gain8 {
 };
 
 // Leaves this block's sums over its rows, acc of each lane's vectors, as one row of
-// part [blocks][H].  fold: shared, 256 * NV * 8 floats.
+// part [blocks][H].  fold: shared, 8 NV floats a thread.
 template <int L, int NV>
-__device__ __forceinline__ void leave_part(const float (&acc)[NV][8], float* fold, int H, float* part) {
-  constexpr int kCols = L * NV * 8;
-  const int g = threadIdx.x / L, l = threadIdx.x % L;
+__device__ __forceinline__ void leave_part(const RowGroup<L>& rg, const float (&acc)[NV][8], float* fold, int H, float* part) {
+  const int n = rg.lanes(), cols = n * NV * 8, rows = rg.rows();
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) fold[g * kCols + (l + i * L) * 8 + j] = acc[i][j];
+    for (int j = 0; j < 8; ++j) fold[rg.g * cols + (rg.l + i * n) * 8 + j] = acc[i][j];
   __syncthreads();
-  for (int c = threadIdx.x; c < H; c += kNormThreads) {
+  for (int c = threadIdx.x; c < H; c += blockDim.x) {
     float v = 0.f;
-    for (int r = 0; r < RowGroup<L>::kRows; ++r) v += fold[r * kCols + c];
+    for (int r = 0; r < rows; ++r) v += fold[r * cols + c];
     part[(size_t)blockIdx.x * H + c] = v;
   }
 }
 
-// Calls f(lanes of a row, vectors of a lane) for rows of H elements.
-template <class F>
-int with_row_shape(int H, F&& f) {
+// How rows of H elements lie: lanes of a row (0: whole warps, W of them), rows and
+// threads of a block.
+struct RowShape {
+  int L, W, rows, threads;
+};
+// nv vectors a lane; blocks of about 256 threads
+inline RowShape row_shape(int H, int nv) {
+  const int nvec = H / 8;
+  if (nvec <= 8) return {8, 1, 32, 256};
+  if (nvec <= 16) return {16, 1, 16, 256};
+  if (nvec <= 32) return {32, 1, 8, 256};
+  const int W = (nvec + 32 * nv - 1) / (32 * nv), rows = W >= 8 ? 1 : 8 / W;
+  return {0, W, rows, 32 * W * rows};
+}
+// Calls f(L) for the lanes of a row (kLong: rows of whole warps too).
+template <bool kLong, class F>
+int with_lanes(int L, F&& f) {
   using std::integral_constant;
-  if (H <= 64) return f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
-  if (H <= 128) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
-  if (H <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-  if (H <= 512) return f(integral_constant<int, 32>{}, integral_constant<int, 2>{});
-  if (H <= 1024) return f(integral_constant<int, 32>{}, integral_constant<int, 4>{});
-  if (H <= 2048) return f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
-  if (H <= 4096) return f(integral_constant<int, 128>{}, integral_constant<int, 4>{});
-  return f(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+  if (L == 8) return f(integral_constant<int, 8>{});
+  if (L == 16) return f(integral_constant<int, 16>{});
+  if constexpr (kLong) {
+    if (L == 0) return f(integral_constant<int, 0>{});
+  }
+  return f(integral_constant<int, 32>{});
 }
 
-// Blocks an SM that a backward kernel's registers leave room for.
-__host__ __device__ constexpr int bwd_blocks(int nv) { return nv == 4 ? 1 : 2; }
-
-// The same for the backward kernels, which hold the gain's gradient of their columns as
-// well: fewer vectors a lane.
-template <class F>
-int with_bwd_shape(int H, F&& f) {
-  using std::integral_constant;
-  if (H <= 64) return f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
-  if (H <= 128) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
-  if (H <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-  if (H <= 512) return f(integral_constant<int, 32>{}, integral_constant<int, 2>{});
-  if (H <= 1024) return f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-  if (H <= 2048) return f(integral_constant<int, 128>{}, integral_constant<int, 2>{});
-  if (H <= 4096) return f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-  return f(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+// Blocks that an SM holds: 228 KB of shared memory (1 KB of it a block's own), registers
+// of `regs` a thread, and 2048 threads.
+inline int blocks_per_sm(size_t smem, int threads, int regs) {
+  int n = 2048 / threads;
+  const int by_smem = (int)(228 * 1024 / (smem + 1024 + 256)), by_regs = 65536 / (regs * threads);
+  n = n < by_smem ? n : by_smem;
+  n = n < by_regs ? n : by_regs;
+  return n > 0 ? n : 1;
 }
-
 inline int norm_grid(long long T, int rows_per_block, int per_sm, int most) {
   const long long b = (T + rows_per_block - 1) / rows_per_block;
   const long long cap = (long long)(sm_count() > 0 ? sm_count() : 148) * per_sm;
@@ -188,26 +229,21 @@ inline int norm_grid(long long T, int rows_per_block, int per_sm, int most) {
   if (g > most) g = most;
   return (int)(g > 0 ? g : 1);
 }
+// shared memory of a backward: its ring, in which the gain's gradients are folded too
+inline size_t bwd_smem(int units, int nv, int threads) {
+  const size_t ring = (size_t)units * ring_stages(units) * threads * 16, fold = sizeof(float) * 8 * nv * threads;
+  return ring > fold ? ring : fold;
+}
 
 inline size_t norm_parts_bytes(int T, int H) {
   if (T <= 0 || H <= 0) return 0;
   return (size_t)(T < kNormParts ? T : kNormParts) * H * sizeof(float);
 }
 
-// shared memory of a backward: its ring, in which the gain's gradients are folded too
-constexpr size_t norm_smem(int units, int nv) {
-  const size_t ring = (size_t)units * ring_stages(units) * kRingUnitBytes, fold = sizeof(float) * kNormThreads * 8 * nv;
-  return ring > fold ? ring : fold;
-}
-// blocks of so much shared memory that an SM holds (228 KB, 1 KB of it a block's own)
-inline int blocks_per_sm(size_t smem, int most) {
-  const int n = (int)(228 * 1024 / (smem + 1024));
-  return n < most ? (n > 0 ? n : 1) : most;
-}
-// lets a kernel have that much (an attribute of the kernel, set on every call: cheap, and right on every device)
+// lets a kernel have so much shared memory (an attribute of the kernel, set on every call: cheap, and right on
+// every device)
 int allow_smem(const char* fn, const void* kernel, size_t bytes);
-
-// H, eps and a call's gradient of the gain
+// H, and a call's gradient of the gain
 int check_norm(const char* fn, int T, int H, int fp32);
 int check_gain_grad(const char* fn, int T, int H, const float* dgain, const void* ws, size_t ws_bytes);
 // dgain (+)= sum over the rows of part

@@ -11,27 +11,27 @@
 namespace moe {
 namespace {
 
-// Short rows (a vector a lane): registers for eight blocks an SM.  65521 rows of 128 with
-// a row stride of 192: 9.4 us, of which a kernel of one row takes 2.9; four rows a group
-// at a time in four blocks 10.8, two in six 10.1.
+// A vector a lane for rows within a warp (registers for eight blocks an SM: 65521 rows of
+// 128 with a row stride of 192 take 9.4 us, of which a kernel of one row takes 2.9), up to
+// four for longer ones.
 template <typename S, int L, int NV>
-__global__ void __launch_bounds__(kNormThreads, NV == 1 ? 8 : 1) pre_norm_kernel(const S* __restrict__ x, long long ldx,
-                                                                                 const float* __restrict__ gain, float eps, int T,
-                                                                                 int H, __nv_bfloat16* __restrict__ y,
-                                                                                 long long ldy, float* __restrict__ rstd) {
+__global__ void __launch_bounds__(256, NV == 1 ? 8 : 4) pre_norm_kernel(const S* __restrict__ x, long long ldx,
+                                                                        const float* __restrict__ gain, float eps, int T, int H, int W,
+                                                                        __nv_bfloat16* __restrict__ y, long long ldy,
+                                                                        float* __restrict__ rstd) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float sm[16];
-  RowGroup<L> rg(sm);
-  const int nvec = H / 8;
+  __shared__ __align__(16) float sm[kSumFloats];
+  RowGroup<L> rg(sm, W);
+  const int nvec = H / 8, n = rg.lanes(), rows = rg.rows();
   const float inv_h = 1.0f / (float)H;
-  for (long long base = (long long)blockIdx.x * rg.kRows; base < T; base += (long long)gridDim.x * rg.kRows) {
+  for (long long base = (long long)blockIdx.x * rows; base < T; base += (long long)gridDim.x * rows) {
     const long long t = base + rg.g;
     const bool live = t < T;
     Vec8<S> v[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = rg.l + i * L;
+      const int c = rg.l + i * n;
       v[i] = zero_vec<S>();
       if (live && c < nvec) v[i].load(x + t * ldx + 8 * c);
     }
@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kNormThreads, NV == 1 ? 8 : 1) pre_norm_kernel
     if (rstd && rg.l == 0) rstd[t] = r;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = rg.l + i * L;
+      const int c = rg.l + i * n;
       if (c >= nvec) continue;
       const Gain8 w(gain, c, true);
       float o[8];
@@ -52,27 +52,29 @@ __global__ void __launch_bounds__(kNormThreads, NV == 1 ? 8 : 1) pre_norm_kernel
 }
 
 // dx may be dres: each vector is read before it is written, by the same thread.
-template <typename S, int L, int NV>
+template <typename S, int NV>
 struct PreBwd {
   static constexpr int SU = sizeof(Vec8<S>) / 16;         // units of a stream vector
   static constexpr int UNITS = NV * (1 + 2 * SU);         // dy, x, dres
 };
+// A vector a lane for rows within a warp, two for longer ones (512 threads for more than
+// 4096 columns).
 template <typename S, int L, int NV>
-__global__ void __launch_bounds__(kNormThreads, bwd_blocks(NV)) pre_norm_bwd_kernel(
+__global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1) pre_norm_bwd_kernel(
     const __nv_bfloat16* __restrict__ dy, long long lddy, const S* __restrict__ x, long long ldx, const float* __restrict__ gain,
-    const float* __restrict__ rstd, const S* dres, long long lddres, float res_scale, int T, int H, S* dx, long long lddx,
+    const float* __restrict__ rstd, const S* dres, long long lddres, float res_scale, int T, int H, int W, S* dx, long long lddx,
     float* __restrict__ part) {
   pdl_wait();
   pdl_trigger();
-  using P = PreBwd<S, L, NV>;
+  using P = PreBwd<S, NV>;
   constexpr int SU = P::SU, STAGES = ring_stages(P::UNITS);
-  __shared__ float sm[16];
+  __shared__ __align__(16) float sm[kSumFloats];
   extern __shared__ __align__(16) uint8_t ring_smem[];
   RowRing ring(ring_smem, P::UNITS);
-  RowGroup<L> rg(sm);
-  const int nvec = H / 8;
+  RowGroup<L> rg(sm, W);
+  const int nvec = H / 8, n_lanes = rg.lanes();
   const float inv_h = 1.0f / (float)H;
-  const long long step = (long long)gridDim.x * rg.kRows;
+  const long long step = (long long)gridDim.x * rg.rows();
   float acc[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -81,7 +83,7 @@ __global__ void __launch_bounds__(kNormThreads, bwd_blocks(NV)) pre_norm_bwd_ker
   auto fetch = [&](int stage, long long t) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = rg.l + i * L;
+      const int c = rg.l + i * n_lanes;
       const bool there = t < T && c < nvec;
       const int u = i * (1 + 2 * SU);
       ring.fetch(stage, u, dy + (there ? t * lddy + 8 * c : 0), there);
@@ -94,7 +96,7 @@ __global__ void __launch_bounds__(kNormThreads, bwd_blocks(NV)) pre_norm_bwd_ker
     }
     ring.commit();
   };
-  const long long first = (long long)blockIdx.x * rg.kRows;
+  const long long first = (long long)blockIdx.x * rg.rows();
 #pragma unroll
   for (int q = 0; q < STAGES - 1; ++q) fetch(q, first + q * step + rg.g);
   int stage = 0;
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(kNormThreads, bwd_blocks(NV)) pre_norm_bwd_ker
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = rg.l + i * L;
+      const int c = rg.l + i * n_lanes;
       const Gain8 w(gain, c, c < nvec);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(kNormThreads, bwd_blocks(NV)) pre_norm_bwd_ker
     if (!live) continue;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = rg.l + i * L;
+      const int c = rg.l + i * n_lanes;
       if (c >= nvec) continue;
       const Gain8 w(gain, c, true);
       float o[8];
@@ -146,7 +148,7 @@ __global__ void __launch_bounds__(kNormThreads, bwd_blocks(NV)) pre_norm_bwd_ker
   if (part) {  // the ring's memory is free: copies still under way are of rows behind the last, zeros
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    leave_part<L, NV>(acc, reinterpret_cast<float*>(ring_smem), H, part);
+    leave_part<L, NV>(rg, acc, reinterpret_cast<float*>(ring_smem), H, part);
   }
 }
 
@@ -191,10 +193,11 @@ bool row_strides_ok(const T* p, long long ld, int H) {
 template <typename S>
 int run_pre_norm(const char* fn, const S* x, long long ldx, const float* gain, float eps, int T, int H, __nv_bfloat16* y,
                  long long ldy, float* rstd, cudaStream_t s) {
-  return with_row_shape(H, [&](auto l, auto nv) {
-    constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
-    launch_pdl(pre_norm_kernel<S, L, NV>, norm_grid(T, kNormThreads / L, 8, 1 << 30), kNormThreads, 0, s, x, ldx, gain, eps, T, H,
-               y, ldy, rstd);
+  const RowShape sh = row_shape(H, 4);
+  return with_lanes<true>(sh.L, [&](auto l) {
+    constexpr int L = decltype(l)::value, NV = L ? 1 : 4;
+    launch_pdl(pre_norm_kernel<S, L, NV>, norm_grid(T, sh.rows, 8, 1 << 30), sh.threads, 0, s, x, ldx, gain, eps, T, H, sh.W, y, ldy,
+               rstd);
     return check_launch(fn);
   });
 }
@@ -203,17 +206,20 @@ template <typename S>
 int run_pre_norm_bwd(const char* fn, const __nv_bfloat16* dy, long long lddy, const S* x, long long ldx, const float* gain,
                      const float* rstd, const S* dres, long long lddres, float res_scale, int T, int H, S* dx, long long lddx,
                      float* dgain, int accumulate, float* ws, cudaStream_t s) {
-  return with_bwd_shape(H, [&](auto l, auto nv) {
-    constexpr int L = decltype(l)::value, NV = decltype(nv)::value;
+  auto run = [&](auto l, auto v) {
+    constexpr int L = decltype(l)::value, NV = decltype(v)::value;
+    const RowShape sh = row_shape(H, NV);
     auto kern = pre_norm_bwd_kernel<S, L, NV>;
-    const size_t smem = norm_smem(PreBwd<S, L, NV>::UNITS, NV);
-    const int grid = norm_grid(T, kNormThreads / L, blocks_per_sm(smem, bwd_blocks(NV)), kNormParts);
+    const size_t smem = bwd_smem(PreBwd<S, NV>::UNITS, NV, sh.threads);
+    const int grid = norm_grid(T, sh.rows, blocks_per_sm(smem, sh.threads, NV == 1 ? 80 : 128), kNormParts);
     if (int rc = allow_smem(fn, reinterpret_cast<const void*>(kern), smem)) return rc;
-    launch_pdl(kern, grid, kNormThreads, smem, s, dy, lddy, x, ldx, gain, rstd, dres, lddres, res_scale, T, H,
-               dx, lddx, dgain ? ws : nullptr);
+    launch_pdl(kern, grid, sh.threads, smem, s, dy, lddy, x, ldx, gain, rstd, dres, lddres, res_scale, T, H, sh.W, dx, lddx,
+               dgain ? ws : nullptr);
     if (int rc = check_launch(fn)) return rc;
     return dgain ? launch_gain_sum(fn, ws, grid, H, dgain, accumulate, s) : MOE_OK;
-  });
+  };
+  if (H > 256) return run(std::integral_constant<int, 0>{}, std::integral_constant<int, 2>{});
+  return with_lanes<false>(row_shape(H, 1).L, [&](auto l) { return run(l, std::integral_constant<int, 1>{}); });
 }
 
 }  // namespace
