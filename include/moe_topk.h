@@ -613,8 +613,9 @@ int moe_post_norm_bwd(const void* dout, int fp32, const void* z, const float* ga
  *   (q s rounded once).
  * moe_dispatch_rows: x_perm[row_of_slot[t,j]] = x[t] (bf16 [T*k,H]), from bf16
  *   tokens (scale NULL) or from tokens kept in 8 bits; row_w[row_of_slot[t,j]] =
- *   topk_w[t,j] (both NULL, or both given).  Rows that no slot names are left as
- *   they were; a row outside [0, T*k) is skipped and sets MOE_STATUS_BAD_INDEX.
+ *   topk_w[t,j] (both NULL, or both given).  No two slots name the same row (else it
+ *   holds a mix of theirs); rows that no slot names are left as they were; a row
+ *   outside [0, T*k) is skipped and sets MOE_STATUS_BAD_INDEX.
  * moe_grouped_gemm_swiglu_ckpt: moe_grouped_gemm_swiglu that keeps g and u so,
  *   of their fp32 values: gu_q int8 [R,2I], gu_scale bf16 [R,2I/32].
  * moe_grouped_gemm_down_bwd_ckpt: the backward through them.  dy_perm holds the
@@ -625,7 +626,8 @@ int moe_post_norm_bwd(const void* dout, int fp32, const void* z, const float* ga
  *     h_w[r]  = row_w[r] g s u                                     -> bf16 [R,I]
  *     d_w(r)  = sum_i dh[i] g s u                                  (fp32)
  *   d_w is what moe_combine_bwd computes as dy . y_perm[r], so that y_perm need
- *   not be kept: d_w[t,j] = d_w(row_of_slot[t,j]) (fp32 [T,k], T*k <= R), or
+ *   not be kept (and is not rounded to bf16 in between: off by 2e-6 of its size at
+ *   H = 2048, by the tensor cores' fp32 sums): d_w[t,j] = d_w(row_of_slot[t,j]) (fp32 [T,k], T*k <= R), or
  *   d_w[r] (fp32 [R]) when row_of_slot is NULL; 0 for a row outside every segment.
  *   With dy_perm and h_w moe_grouped_gemm_down_bwd_dw gives dWd.
  *   ws: moe_grouped_gemm_down_bwd_ckpt_workspace_size(R, I) bytes, 16-byte aligned. */

@@ -461,9 +461,14 @@ def moe_adapter_linear_bwd(dy, x, W, A, B, scale, hidden, num_seg, seg_offsets, 
 def _stream_type(*tensors) -> int:
     """0 where the residual stream's tensors are bf16, 1 where they are fp32."""
     dt = tensors[0].dtype
-    if dt not in (torch.bfloat16, torch.float32) or any(t is not None and t.dtype != dt for t in tensors):
-        raise ValueError("the residual stream's tensors must all be bf16 or all fp32")
-    return int(dt == torch.float32)
+    for t in tensors:
+        if t is not None and t.dtype is not dt:
+            raise ValueError("the residual stream's tensors must all be bf16 or all fp32")
+    if dt is torch.bfloat16:
+        return 0
+    if dt is torch.float32:
+        return 1
+    raise ValueError("the residual stream's tensors must all be bf16 or all fp32")
 
 
 def _gate_kind(gate, T, H) -> int:
@@ -477,11 +482,25 @@ def _gate_kind(gate, T, H) -> int:
     raise ValueError("gate must be fp32 logits of the tokens or bf16 logits of their elements")
 
 
+def _fp32(t):
+    """Pointer of an fp32 tensor (a gain, or its gradient), which a bf16 parameter is not."""
+    if t is not None and t.dtype is not torch.float32:
+        raise ValueError("gains and their gradients are fp32")
+    return _ptr(t)
+
+
+def _codes(q, scale):
+    """Pointers of 8-bit codes and their bf16 scales."""
+    if q.element_size() != 1 or scale.dtype is not torch.bfloat16:
+        raise ValueError("codes are 8-bit, their scales bf16")
+    return _ptr(q), _ptr(scale)
+
+
 def moe_pre_norm(x, gain, eps, T, H, y, rstd=None, stream=None):
     """y = x / rms(x) * gain; x bf16 or fp32, x and y may be row slices of wider tensors."""
     px, ldx = _rows(x)
     py, ldy = _rows(y)
-    _call("moe_pre_norm", px, ldx, _stream_type(x), _ptr(gain), eps, T, H, py, ldy, _ptr(rstd), _stream(stream))
+    _call("moe_pre_norm", px, ldx, _stream_type(x), _fp32(gain), eps, T, H, py, ldy, _ptr(rstd), _stream(stream))
 
 
 def moe_pre_norm_bwd_workspace_size(T, H) -> int:
@@ -493,24 +512,24 @@ def moe_pre_norm_bwd(dy, x, gain, rstd, dres, res_scale, T, H, dx, dgain=None, a
     px, ldx = _rows(x)
     pr, lddres = (None, H) if dres is None else _rows(dres)
     po, lddx = _rows(dx)
-    _call("moe_pre_norm_bwd", pd, lddy, px, ldx, _stream_type(x, dres, dx), _ptr(gain), _ptr(rstd), pr, lddres, res_scale,
-          T, H, po, lddx, _ptr(dgain), int(accumulate), _ptr(ws), _nbytes(ws), _stream(stream))
+    _call("moe_pre_norm_bwd", pd, lddy, px, ldx, _stream_type(x, dres, dx), _fp32(gain), _ptr(rstd), pr, lddres, res_scale,
+          T, H, po, lddx, _fp32(dgain), int(accumulate), _ptr(ws), _nbytes(ws), _stream(stream))
 
 
 def moe_post_norm(z, residual, gain, norm, eps, gate, res_scale, out_scale, T, H, out, rstd=None, next_gain=None,
                   next_y=None, next_rstd=None, stream=None):
     """out = res_scale residual + out_scale sigmoid(gate) norm(z) gain, and the next norm of out where next_y is given;
     the stream's type is out's, the gate's kind its own (fp32 [T] or bf16 [T,H])."""
-    _call("moe_post_norm", _ptr(z), _ptr(residual), _stream_type(out, residual), _ptr(gain), int(norm), eps,
-          _gate_kind(gate, T, H), _ptr(gate), res_scale, out_scale, T, H, _ptr(out), _ptr(rstd), _ptr(next_gain),
+    _call("moe_post_norm", _ptr(z), _ptr(residual), _stream_type(out, residual), _fp32(gain), int(norm), eps,
+          _gate_kind(gate, T, H), _ptr(gate), res_scale, out_scale, T, H, _ptr(out), _ptr(rstd), _fp32(next_gain),
           _ptr(next_y), _ptr(next_rstd), _stream(stream))
 
 
 def moe_combine_post_norm(y_perm, topk_w, row_of_slot, residual, gain, norm, eps, gate, res_scale, out_scale, T, H, k, z,
                           out, rstd=None, next_gain=None, next_y=None, next_rstd=None, stream=None):
     _call("moe_combine_post_norm", _ptr(y_perm), _ptr(topk_w), _ptr(row_of_slot), _ptr(residual),
-          _stream_type(out, residual), _ptr(gain), int(norm), eps, _gate_kind(gate, T, H), _ptr(gate), res_scale, out_scale,
-          T, H, k, _ptr(z), _ptr(out), _ptr(rstd), _ptr(next_gain), _ptr(next_y), _ptr(next_rstd), _stream(stream))
+          _stream_type(out, residual), _fp32(gain), int(norm), eps, _gate_kind(gate, T, H), _ptr(gate), res_scale, out_scale,
+          T, H, k, _ptr(z), _ptr(out), _ptr(rstd), _fp32(next_gain), _ptr(next_y), _ptr(next_rstd), _stream(stream))
 
 
 def moe_post_norm_bwd_workspace_size(T, H) -> int:
@@ -521,17 +540,17 @@ def moe_post_norm_bwd(dout, z, gain, norm, rstd, gate, out_scale, T, H, dz, dgai
                       stream=None):
     if dgate is not None and (gate is None or dgate.dtype != gate.dtype):
         raise ValueError("dgate must have the gate's type")
-    _call("moe_post_norm_bwd", _ptr(dout), _stream_type(dout), _ptr(z), _ptr(gain), int(norm), _ptr(rstd),
-          _gate_kind(gate, T, H), _ptr(gate), out_scale, T, H, _ptr(dz), _ptr(dgain), _ptr(dgate), int(accumulate), _ptr(ws),
+    _call("moe_post_norm_bwd", _ptr(dout), _stream_type(dout), _ptr(z), _fp32(gain), int(norm), _ptr(rstd),
+          _gate_kind(gate, T, H), _ptr(gate), out_scale, T, H, _ptr(dz), _fp32(dgain), _ptr(dgate), int(accumulate), _ptr(ws),
           _nbytes(ws), _stream(stream))
 
 
 def moe_ckpt_pack(a, rows, cols, q, scale, stream=None):
-    _call("moe_ckpt_pack", _ptr(a), rows, cols, _ptr(q), _ptr(scale), _stream(stream))
+    _call("moe_ckpt_pack", _ptr(a), rows, cols, *_codes(q, scale), _stream(stream))
 
 
 def moe_ckpt_unpack(q, scale, rows, cols, a, stream=None):
-    _call("moe_ckpt_unpack", _ptr(q), _ptr(scale), rows, cols, _ptr(a), _stream(stream))
+    _call("moe_ckpt_unpack", *_codes(q, scale), rows, cols, _ptr(a), _stream(stream))
 
 
 def moe_dispatch_rows(x, scale, row_of_slot, topk_w, T, H, k, x_perm, row_w=None, stream=None):
@@ -545,7 +564,7 @@ def moe_dispatch_rows(x, scale, row_of_slot, topk_w, T, H, k, x_perm, row_w=None
 def moe_grouped_gemm_swiglu_ckpt(x_perm, Wg, Wu, num_seg, seg_offsets, seg_expert, R, H, I, E, h, gu_q, gu_scale,
                                  stream=None):
     _call("moe_grouped_gemm_swiglu_ckpt", _ptr(x_perm), _ptr(Wg), _ptr(Wu), num_seg, _ptr(seg_offsets), _ptr(seg_expert),
-          R, H, I, E, _ptr(h), _ptr(gu_q), _ptr(gu_scale), _stream(stream))
+          R, H, I, E, _ptr(h), *_codes(gu_q, gu_scale), _stream(stream))
 
 
 def moe_grouped_gemm_down_bwd_ckpt_workspace_size(R, I) -> int:
@@ -554,7 +573,7 @@ def moe_grouped_gemm_down_bwd_ckpt_workspace_size(R, I) -> int:
 
 def moe_grouped_gemm_down_bwd_ckpt(dy_perm, row_w, gu_q, gu_scale, Wd, num_seg, seg_offsets, seg_expert, R, H, I, E, dgu,
                                    h_w, d_w, row_of_slot=None, T=0, k=0, ws=None, stream=None):
-    _call("moe_grouped_gemm_down_bwd_ckpt", _ptr(dy_perm), _ptr(row_w), _ptr(gu_q), _ptr(gu_scale), _ptr(Wd), num_seg,
+    _call("moe_grouped_gemm_down_bwd_ckpt", _ptr(dy_perm), _ptr(row_w), *_codes(gu_q, gu_scale), _ptr(Wd), num_seg,
           _ptr(seg_offsets), _ptr(seg_expert), R, H, I, E, _ptr(dgu), _ptr(h_w), _ptr(row_of_slot), T, k, _ptr(d_w), _ptr(ws),
           _nbytes(ws), _stream(stream))
 

@@ -1190,9 +1190,9 @@ __global__ void __launch_bounds__(256) ckpt_dw_kernel(const float* __restrict__ 
   extern __shared__ int off[];  // [num_seg + 1]
   for (int s = threadIdx.x; num_seg > 0 && s <= num_seg; s += blockDim.x) off[s] = __ldg(seg_offsets + s);
   __syncthreads();
-  const int i = blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= n) return;
-  const int row = row_of_slot ? __ldg(row_of_slot + i) : i;
+  const unsigned i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= (unsigned)n) return;
+  const int row = row_of_slot ? __ldg(row_of_slot + i) : (int)i;
   float v = 0.f;
   if (row < 0 || row >= R) {
     set_status(status, MOE_STATUS_BAD_INDEX);
@@ -1485,19 +1485,19 @@ int swiglu_impl(const void* a_src, const int32_t* gather_rows, int T, const void
   }
   if (int rc = make_tmap(&tg, Wg, H, (uint64_t)E * I, 64, p.NH)) return rc;
   if (int rc = make_tmap(&tu, Wu, H, (uint64_t)E * I, 64, p.NH)) return rc;
-  CUtensorMap th, tgu;
-  if (int rc = make_out_map(&th, h, I, R, false)) return rc;
-  if (int rc = make_out_map(&tgu, gu_save && !gu_scale ? gu_save : h, gu_save && !gu_scale ? 2 * I : I, R, false)) return rc;
-  if (gather_rows) return run<GATE_UP_GATHER>(false, p, ta, tg, tu, th, tgu, s, fn);
   // Cluster pairs (the leader loads the gate rows of B, the peer the up rows)
   // by pair_for_rows.  With several segments per expert (the EP receive
   // layout) each expert's weights stay in L2 across its segments and the
   // 256-row tiles waste more rows: single CTAs measured faster there.
   const bool pair = pair_for_rows(p.BN, R, num_seg, E);
-  if (gu_scale) {
+  if (gu_scale) {  // its epilogue stores without maps (the A map fills the slots)
     p.ckpt_scale = static_cast<unsigned short*>(gu_scale);
-    return run<GATE_UP_CKPT>(pair, p, ta, tg, tu, th, th, s, fn);
+    return run<GATE_UP_CKPT>(pair, p, ta, tg, tu, ta, ta, s, fn);
   }
+  CUtensorMap th, tgu;
+  if (int rc = make_out_map(&th, h, I, R, false)) return rc;
+  if (int rc = make_out_map(&tgu, gu_save ? gu_save : h, gu_save ? 2 * I : I, R, false)) return rc;
+  if (gather_rows) return run<GATE_UP_GATHER>(false, p, ta, tg, tu, th, tgu, s, fn);
   return run<GATE_UP_FWD>(pair, p, ta, tg, tu, th, tgu, s, fn);
 }
 
@@ -1826,7 +1826,7 @@ int moe_grouped_gemm_down_bwd_ckpt(const void* dy_perm, const float* row_w, cons
   }
   const int n = row_of_slot ? T * k : R;
   if (n == 0) return MOE_OK;
-  launch_pdl(ckpt_dw_kernel, (n + 255) / 256, 256, sizeof(int) * (num_seg + 1), s, static_cast<const float*>(ws), 2 * (I / bn), R,
+  launch_pdl(ckpt_dw_kernel, (n - 1) / 256 + 1, 256, sizeof(int) * (num_seg + 1), s, static_cast<const float*>(ws), 2 * (I / bn), R,
              seg_offsets, seg_expert, num_seg, E, row_of_slot, n, d_w, status_word());
   return check_launch(fn);
 }

@@ -217,7 +217,7 @@ int with_lanes(int L, F&& f) {
 // of `regs` a thread, and 2048 threads.
 inline int blocks_per_sm(size_t smem, int threads, int regs) {
   int n = 2048 / threads;
-  const int by_smem = (int)(228 * 1024 / (smem + 1024 + 256)), by_regs = 65536 / (regs * threads);
+  const int by_smem = (int)(228 * 1024 / (smem + 1024 + sizeof(float) * kSumFloats)), by_regs = 65536 / (regs * threads);
   n = n < by_smem ? n : by_smem;
   n = n < by_regs ? n : by_regs;
   return n > 0 ? n : 1;
@@ -240,9 +240,10 @@ inline size_t norm_parts_bytes(int T, int H) {
   return (size_t)(T < kNormParts ? T : kNormParts) * H * sizeof(float);
 }
 
-// lets a kernel have so much shared memory (an attribute of the kernel, set on every call: cheap, and right on
-// every device)
-int allow_smem(const char* fn, const void* kernel, size_t bytes);
+// Lets a kernel that is launched with `bytes` of shared memory have what a block can
+// have beside its static sums; done: the kernel's own flags, one a device.
+constexpr int kMaxDevices = 64;
+int allow_smem(const char* fn, const void* kernel, size_t bytes, bool (&done)[kMaxDevices]);
 // H, and a call's gradient of the gain
 int check_norm(const char* fn, int T, int H, int fp32);
 int check_gain_grad(const char* fn, int T, int H, const float* dgain, const void* ws, size_t ws_bytes);

@@ -319,7 +319,8 @@ int run_combine_post_norm(const char* fn, const PostArgs& a, cudaStream_t s) {
     if (L == 32) sh = {32, 1, 8, 256};  // short rows too: a warp's lanes hold a token's slots
     auto kern = combine_post_norm_kernel<S, L, NV, kWide, STAGES>;
     const size_t smem = (size_t)NV * PostRing<S, NV>::per(a.k, a.gate_kind) * STAGES * sh.threads * 16;
-    if (int rc = allow_smem(fn, reinterpret_cast<const void*>(kern), smem)) return rc;
+    static bool done[kMaxDevices];
+    if (int rc = allow_smem(fn, reinterpret_cast<const void*>(kern), smem, done)) return rc;
     launch_pdl(kern, norm_grid(a.T, sh.rows, blocks_per_sm(smem, sh.threads, PostBlock<NV, kWide>::REGS), 1 << 30), sh.threads, smem, s, a,
                sh.W);
     return check_launch(fn);

@@ -169,7 +169,8 @@ int moe_post_norm_bwd(const void* dout, int fp32, const void* z, const float* ga
     auto kern = post_norm_bwd_kernel<S, L, NV, kElement>;
     const size_t smem = bwd_smem(PostBwd<S, NV, kElement>::UNITS, NV, sh.threads);
     const int grid = norm_grid(T, sh.rows, blocks_per_sm(smem, sh.threads, NV == 1 ? 80 : 128), kNormParts);
-    if (int rc = allow_smem(fn, reinterpret_cast<const void*>(kern), smem)) return rc;
+    static bool done[kMaxDevices];
+    if (int rc = allow_smem(fn, reinterpret_cast<const void*>(kern), smem, done)) return rc;
     launch_pdl(kern, grid, sh.threads, smem, s, a, sh.W);
     if (int rc = check_launch(fn)) return rc;
     return dgain ? launch_gain_sum(fn, static_cast<const float*>(ws), grid, H, dgain, accumulate, s) : MOE_OK;

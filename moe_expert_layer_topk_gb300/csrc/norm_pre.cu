@@ -212,7 +212,8 @@ int run_pre_norm_bwd(const char* fn, const __nv_bfloat16* dy, long long lddy, co
     auto kern = pre_norm_bwd_kernel<S, L, NV>;
     const size_t smem = bwd_smem(PreBwd<S, NV>::UNITS, NV, sh.threads);
     const int grid = norm_grid(T, sh.rows, blocks_per_sm(smem, sh.threads, NV == 1 ? 80 : 128), kNormParts);
-    if (int rc = allow_smem(fn, reinterpret_cast<const void*>(kern), smem)) return rc;
+    static bool done[kMaxDevices];
+    if (int rc = allow_smem(fn, reinterpret_cast<const void*>(kern), smem, done)) return rc;
     launch_pdl(kern, grid, sh.threads, smem, s, dy, lddy, x, ldx, gain, rstd, dres, lddres, res_scale, T, H, sh.W, dx, lddx,
                dgain ? ws : nullptr);
     if (int rc = check_launch(fn)) return rc;
@@ -238,10 +239,16 @@ int check_gain_grad(const char* fn, int T, int H, const float* dgain, const void
   return MOE_OK;
 }
 
-int allow_smem(const char* fn, const void* kernel, size_t bytes) {
-  if (bytes <= 47 * 1024) return MOE_OK;  // with the static kilobyte at most, what every kernel may have
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  return e == cudaSuccess ? MOE_OK : fail_cuda(fn, e);
+int allow_smem(const char* fn, const void* kernel, size_t bytes, bool (&done)[kMaxDevices]) {
+  const size_t most = 232448 - sizeof(float) * kSumFloats;
+  if (bytes > most) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: needs %zu bytes of shared memory", fn, bytes);
+  const int dev = current_device();
+  if (dev < 0) return fail(MOE_ERR_CUDA, "%s: no current CUDA device", fn);
+  if (done[dev]) return MOE_OK;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  if (e != cudaSuccess) return fail_cuda(fn, e);
+  done[dev] = true;
+  return MOE_OK;
 }
 
 int launch_gain_sum(const char* fn, const float* part, int parts, int H, float* dgain, int accumulate, cudaStream_t s) {

@@ -123,3 +123,8 @@ def test_binding_types():
             m._gate_kind(bad, 2, 8)
     with pytest.raises(ValueError):
         m.moe_dispatch_rows(z(2, 64), z(2, 2), None, None, 2, 64, 1, None)
+    f, b, i8 = z(8, dt=torch.float32), z(2, 64), z(2, 64, dt=torch.int8)
+    for call in (lambda: m._fp32(z(8)), lambda: m._codes(b, z(2, 2)), lambda: m._codes(i8, f),
+                 lambda: m.moe_grouped_gemm_swiglu_ckpt(None, None, None, 1, None, None, 2, 64, 32, 1, None, i8, f)):
+        with pytest.raises(ValueError, match="fp32|8-bit"):
+            call()
