@@ -93,6 +93,38 @@ __global__ void __launch_bounds__(256) dispatch_rows_kernel(const void* __restri
   }
 }
 
+// Rows within less than a warp's 32 vectors (H < 256): thread = one vector of a token, the ids
+// read by each.  65536 tokens, top-2, from codes: H = 64 5.6 us, 128 13.1; with the kernel
+// above, whose lanes are then mostly idle, 14.7 and 17.0 (H = 256, top-4: 17.3 against 16.1).
+template <bool kCodes>
+__global__ void __launch_bounds__(256) dispatch_short_rows_kernel(const void* __restrict__ x, const unsigned short* __restrict__ scale,
+                                                            const int32_t* __restrict__ row_of_slot, const float* __restrict__ topk_w,
+                                                            int T, int H, int k, int R, uint4* __restrict__ x_perm,
+                                                            float* __restrict__ row_w, int* status) {
+  pdl_wait();
+  pdl_trigger();
+  const int nvec = H / 8;
+  const size_t total = (size_t)T * nvec;
+  for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < total; i += (size_t)gridDim.x * blockDim.x) {
+    const size_t t = i / nvec;
+    const int v = (int)(i - t * nvec);
+    uint4 val;
+    if (kCodes)
+      val = unpack_codes8(__ldg(static_cast<const uint2*>(x) + i), __ldg(scale + (i >> 2)));
+    else
+      val = __ldg(static_cast<const uint4*>(x) + i);
+    for (int j = 0; j < k; ++j) {
+      const int row = __ldg(row_of_slot + t * k + j);
+      if (row < 0 || row >= R) {
+        if (v == 0) set_status(status, MOE_STATUS_BAD_INDEX);
+        continue;
+      }
+      x_perm[(size_t)row * nvec + v] = val;
+      if (v == 0 && row_w) row_w[row] = __ldg(topk_w + t * k + j);
+    }
+  }
+}
+
 int grid_of(size_t work, int per_sm) {
   const size_t b = (work + 255) / 256, cap = (size_t)(sm_count() > 0 ? sm_count() : 148) * per_sm;
   return (int)(b < cap ? b : cap);
@@ -149,15 +181,14 @@ int moe_dispatch_rows(const void* x, const void* scale, const int32_t* row_of_sl
   if (!topk_w != !row_w) return fail(MOE_ERR_INVALID_ARG, "%s: topk_w and row_w are given together", fn);
   if (!aligned16(x) || !aligned16(x_perm) || (scale && !aligned16(scale)))
     return fail(MOE_ERR_ALIGNMENT, "%s: tensors must be 16-byte aligned", fn);
-  auto run = [&](auto kern) {
-    launch_pdl(kern, grid_of((size_t)T * ((H / 8 + 63) / 64) * 32, 16), 256, 0, static_cast<cudaStream_t>(stream), x,
-               static_cast<const unsigned short*>(scale), row_of_slot, topk_w, T, H, k, T * k, static_cast<uint4*>(x_perm), row_w,
-               status_word());
+  auto run = [&](auto kern, size_t threads) {
+    launch_pdl(kern, grid_of(threads, 16), 256, 0, static_cast<cudaStream_t>(stream), x, static_cast<const unsigned short*>(scale),
+               row_of_slot, topk_w, T, H, k, T * k, static_cast<uint4*>(x_perm), row_w, status_word());
   };
-  if (scale)
-    run(dispatch_rows_kernel<true>);
+  if (H < 256)
+    run(scale ? dispatch_short_rows_kernel<true> : dispatch_short_rows_kernel<false>, (size_t)T * (H / 8));
   else
-    run(dispatch_rows_kernel<false>);
+    run(scale ? dispatch_rows_kernel<true> : dispatch_rows_kernel<false>, (size_t)T * ((H / 8 + 63) / 64) * 32);
   return check_launch(fn);
 }
 
