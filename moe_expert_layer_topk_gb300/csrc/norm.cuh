@@ -151,8 +151,10 @@ struct RowRing {
     return v;
   }
 };
-// stages of a backward's ring: about 64 KB of 256 threads
-__host__ __device__ constexpr int ring_stages(int units) { return units <= 4 ? 4 : (units <= 6 ? 3 : 2); }
+// Stages of a backward's ring.  What the rings of an SM's blocks leave of its 256 KB caches
+// the gains: 8192 x 2048, three blocks an SM, with three stages of 24 KB in each takes 31.2
+// us, with two 28.4.  hold: two blocks an SM at most.
+__host__ __device__ constexpr int ring_stages(int units, bool hold) { return !hold ? 2 : (units <= 4 ? 4 : (units <= 6 ? 3 : 2)); }
 
 // Eight gains (ones without a tensor).
 struct Gain8 {
@@ -230,8 +232,8 @@ inline int norm_grid(long long T, int rows_per_block, int per_sm, int most) {
   return (int)(g > 0 ? g : 1);
 }
 // shared memory of a backward: its ring, in which the gain's gradients are folded too
-inline size_t bwd_smem(int units, int nv, int threads) {
-  const size_t ring = (size_t)units * ring_stages(units) * threads * 16, fold = sizeof(float) * 8 * nv * threads;
+inline size_t bwd_smem(int units, int nv, int threads, bool hold) {
+  const size_t ring = (size_t)units * ring_stages(units, hold) * threads * 16, fold = sizeof(float) * 8 * nv * threads;
   return ring > fold ? ring : fold;
 }
 

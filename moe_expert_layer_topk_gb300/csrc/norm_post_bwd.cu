@@ -33,12 +33,18 @@ struct PostBwd {
   static constexpr int PER = 1 + SU + (kElement ? 1 : 0);        // z, dout, gate
   static constexpr int UNITS = NV * PER;
 };
-template <typename S, int L, int NV, bool kElement>
-__global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1) post_norm_bwd_kernel(const PostBwdArgs p, int W) {
+// As the backward of the norm before a block; with an element's gate a row is held too (two
+// blocks an SM), since its sigmoids would be computed twice (8192 x 2048, fp32 stream: 44.5
+// against 48.9 us; without that gate, bf16: 29.9 held, 28.5 read twice).
+__host__ __device__ constexpr bool holds_row(bool element, bool wide, int nv) { return wide || (element && nv > 1); }
+template <typename S, int L, int NV, bool kElement, bool kWide>
+__global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : (holds_row(kElement, kWide, NV) ? 2 : 3))
+    post_norm_bwd_kernel(const PostBwdArgs p, int W) {
   pdl_wait();
   pdl_trigger();
   using P = PostBwd<S, NV, kElement>;
-  constexpr int SU = P::SU, STAGES = ring_stages(P::UNITS);
+  constexpr int SU = P::SU, STAGES = ring_stages(P::UNITS, holds_row(kElement, kWide, NV));
+  constexpr bool kHold = holds_row(kElement, kWide, NV);
   __shared__ __align__(16) float sm[kSumFloats];
   extern __shared__ __align__(16) uint8_t ring_smem[];
   RowRing ring(ring_smem, P::UNITS);
@@ -76,8 +82,8 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1) post_nor
     const float r = p.norm && live ? __ldg(p.rstd + t) : 1.f;
     Gate tok = {1.f, 0.f};
     if (!kElement && p.gate_kind == 1 && live) tok = sigmoid(__ldg(static_cast<const float*>(p.gate) + t));
-    ring.template wait<STAGES - 2>();
-    const int cur = stage;
+    fetch(stage == 0 ? STAGES - 1 : stage - 1, t + (STAGES - 1) * step);
+    ring.template wait<STAGES - 1>();
     float m = 0.f, dg = 0.f;  // sums of dn n, and of dout n gain
     float n[NV][8], dn[NV][8];
 #pragma unroll
@@ -85,28 +91,26 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1) post_nor
       const int c = rg.l + i * lanes, u = i * P::PER;
       const bool there = live && c < nvec;
       const Gain8 w(p.gain, c, c < nvec);
-      const Vec8<__nv_bfloat16> zv = ring.template vec<__nv_bfloat16>(cur, u);
-      const Vec8<S> d = ring.template vec<S>(cur, u + 1);
-      const Vec8<__nv_bfloat16> gv = kElement ? ring.template vec<__nv_bfloat16>(cur, u + 1 + SU) : zero_vec<__nv_bfloat16>();
+      const Vec8<__nv_bfloat16> zv = ring.template vec<__nv_bfloat16>(stage, u);
+      const Vec8<S> d = ring.template vec<S>(stage, u + 1);
+      const Vec8<__nv_bfloat16> gv = kElement ? ring.template vec<__nv_bfloat16>(stage, u + 1 + SU) : zero_vec<__nv_bfloat16>();
       float ds[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         n[i][j] = zv.at(j) * r;
-        const float e = p.out_scale * d.at(j), en = e * n[i][j];
+        const float e = p.out_scale * d.at(j);
         const Gate G = kElement ? sigmoid(gv.at(j)) : tok;
-        const float dv = e * G.g;
-        acc[i][j] = __fmaf_rn(dv, n[i][j], acc[i][j]);
-        dn[i][j] = dv * w.at(j);
+        const float ew = e * w.at(j);
+        acc[i][j] = __fmaf_rn(e * G.g, n[i][j], acc[i][j]);
+        dn[i][j] = ew * G.g;
         m = __fmaf_rn(dn[i][j], n[i][j], m);
         if (kElement)
-          ds[j] = en * w.at(j) * G.d;
+          ds[j] = ew * n[i][j] * G.d;
         else
-          dg = __fmaf_rn(en, w.at(j), dg);
+          dg = __fmaf_rn(ew, n[i][j], dg);
       }
       if (kElement && p.dgate && there) Vec8<__nv_bfloat16>::store(static_cast<__nv_bfloat16*>(p.dgate) + t * H + 8 * c, ds);
     }
-    fetch(stage == 0 ? STAGES - 1 : stage - 1, t + (STAGES - 1) * step);
-    stage = stage + 1 == STAGES ? 0 : stage + 1;
     if (!kElement && p.gate_kind == 1 && p.dgate) {
       rg.template sums<true>(m, dg);
       if (live && rg.l == 0) static_cast<float*>(p.dgate)[t] = dg * tok.d;
@@ -114,16 +118,27 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1) post_nor
       m = rg.sum(m);
     }
     m *= inv_h;
-    if (!live) continue;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = rg.l + i * lanes;
-      if (c >= nvec) continue;
+      const int c = rg.l + i * lanes, u = i * P::PER;
+      if (!live || c >= nvec) continue;
+      if (!kHold) {
+        const Gain8 w(p.gain, c, true);
+        const Vec8<__nv_bfloat16> zv = ring.template vec<__nv_bfloat16>(stage, u);
+        const Vec8<S> d = ring.template vec<S>(stage, u + 1);
+        const Vec8<__nv_bfloat16> gv = kElement ? ring.template vec<__nv_bfloat16>(stage, u + 1 + SU) : zero_vec<__nv_bfloat16>();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          n[i][j] = zv.at(j) * r;
+          dn[i][j] = p.out_scale * d.at(j) * w.at(j) * (kElement ? sigmoid(gv.at(j)).g : tok.g);
+        }
+      }
       float o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = p.norm ? r * (dn[i][j] - n[i][j] * m) : dn[i][j];
       Vec8<__nv_bfloat16>::store(p.dz + t * H + 8 * c, o);
     }
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
   }
   if (p.part) {  // the ring's memory is free: copies still under way are of rows behind the last, zeros
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -161,26 +176,27 @@ int moe_post_norm_bwd(const void* dout, int fp32, const void* z, const float* ga
   if (int rc = check_gain_grad(fn, T, H, dgain, ws, ws_bytes)) return rc;
   const PostBwdArgs a = {dout, static_cast<const __nv_bfloat16*>(z), gain, norm, rstd, gate_kind, gate, out_scale, T, H,
                          static_cast<__nv_bfloat16*>(dz), dgain ? static_cast<float*>(ws) : nullptr, dgate};
-  auto run = [&](auto type, auto l, auto v, auto element) {
+  auto run = [&](auto type, auto l, auto v, auto wide, auto element) {
     using S = decltype(type);
     constexpr int L = decltype(l)::value, NV = decltype(v)::value;
-    constexpr bool kElement = decltype(element)::value;
+    constexpr bool kElement = decltype(element)::value, kWide = decltype(wide)::value;
     const RowShape sh = row_shape(H, NV);
-    auto kern = post_norm_bwd_kernel<S, L, NV, kElement>;
-    const size_t smem = bwd_smem(PostBwd<S, NV, kElement>::UNITS, NV, sh.threads);
-    const int grid = norm_grid(T, sh.rows, blocks_per_sm(smem, sh.threads, NV == 1 ? 80 : 128), kNormParts);
+    auto kern = post_norm_bwd_kernel<S, L, NV, kElement, kWide>;
+    const size_t smem = bwd_smem(PostBwd<S, NV, kElement>::UNITS, NV, sh.threads, holds_row(kElement, kWide, NV));
+    const int grid = norm_grid(T, sh.rows, blocks_per_sm(smem, sh.threads, holds_row(kElement, kWide, NV) ? 128 : 80), kNormParts);
     static bool done[kMaxDevices];
     if (int rc = allow_smem(fn, reinterpret_cast<const void*>(kern), smem, done)) return rc;
     launch_pdl(kern, grid, sh.threads, smem, s, a, sh.W);
     if (int rc = check_launch(fn)) return rc;
     return dgain ? launch_gain_sum(fn, static_cast<const float*>(ws), grid, H, dgain, accumulate, s) : MOE_OK;
   };
-  auto typed = [&](auto l, auto v) {
-    if (gate_kind == 2) return fp32 ? run(float(), l, v, std::true_type()) : run(__nv_bfloat16(), l, v, std::true_type());
-    return fp32 ? run(float(), l, v, std::false_type()) : run(__nv_bfloat16(), l, v, std::false_type());
+  auto typed = [&](auto l, auto v, auto wide) {
+    if (gate_kind == 2) return fp32 ? run(float(), l, v, wide, std::true_type()) : run(__nv_bfloat16(), l, v, wide, std::true_type());
+    return fp32 ? run(float(), l, v, wide, std::false_type()) : run(__nv_bfloat16(), l, v, wide, std::false_type());
   };
-  if (H > 256) return typed(std::integral_constant<int, 0>{}, std::integral_constant<int, 2>{});
-  return with_lanes<false>(row_shape(H, 1).L, [&](auto l) { return typed(l, std::integral_constant<int, 1>{}); });
+  if (H > 4096) return typed(std::integral_constant<int, 0>{}, std::integral_constant<int, 2>{}, std::true_type{});
+  if (H > 256) return typed(std::integral_constant<int, 0>{}, std::integral_constant<int, 2>{}, std::false_type{});
+  return with_lanes<false>(row_shape(H, 1).L, [&](auto l) { return typed(l, std::integral_constant<int, 1>{}, std::false_type{}); });
 }
 
 }  // extern "C"

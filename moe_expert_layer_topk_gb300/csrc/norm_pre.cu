@@ -57,17 +57,20 @@ struct PreBwd {
   static constexpr int SU = sizeof(Vec8<S>) / 16;         // units of a stream vector
   static constexpr int UNITS = NV * (1 + 2 * SU);         // dy, x, dres
 };
-// A vector a lane for rows within a warp, two for longer ones (512 threads for more than
-// 4096 columns).
-template <typename S, int L, int NV>
-__global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1) pre_norm_bwd_kernel(
+// A vector a lane for rows within a warp, two for longer ones (kWide: 512 threads, for more
+// than 4096 columns).  A row's vectors stay in the ring while it is worked on and are read
+// twice: in registers they would leave an SM two blocks instead of three (8192 x 2048: 28.4
+// against 31.0 us).  The wide kernel has one block an SM anyway and holds them (2048 x 8192:
+// 36.3 against 39.5).
+template <typename S, int L, int NV, bool kWide>
+__global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : 3) pre_norm_bwd_kernel(
     const __nv_bfloat16* __restrict__ dy, long long lddy, const S* __restrict__ x, long long ldx, const float* __restrict__ gain,
     const float* __restrict__ rstd, const S* dres, long long lddres, float res_scale, int T, int H, int W, S* dx, long long lddx,
     float* __restrict__ part) {
   pdl_wait();
   pdl_trigger();
   using P = PreBwd<S, NV>;
-  constexpr int SU = P::SU, STAGES = ring_stages(P::UNITS);
+  constexpr int SU = P::SU, STAGES = ring_stages(P::UNITS, kWide);
   __shared__ __align__(16) float sm[kSumFloats];
   extern __shared__ __align__(16) uint8_t ring_smem[];
   RowRing ring(ring_smem, P::UNITS);
@@ -104,22 +107,16 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1) pre_norm
     const long long t = base + rg.g;
     const bool live = t < T;
     const float r = live ? __ldg(rstd + t) : 0.f;
-    ring.template wait<STAGES - 2>();
-    Vec8<S> v[NV], res[NV];
-    Vec8<__nv_bfloat16> d[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int u = i * (1 + 2 * SU);
-      d[i] = ring.template vec<__nv_bfloat16>(stage, u);
-      v[i] = ring.template vec<S>(stage, u + 1);
-      res[i] = dres ? ring.template vec<S>(stage, u + 1 + SU) : zero_vec<S>();
-    }
     fetch(stage == 0 ? STAGES - 1 : stage - 1, t + (STAGES - 1) * step);
-    stage = stage + 1 == STAGES ? 0 : stage + 1;
+    ring.template wait<STAGES - 1>();
+    Vec8<__nv_bfloat16> d[NV];
+    Vec8<S> v[NV];
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = rg.l + i * n_lanes;
+      const int c = rg.l + i * n_lanes, u = i * (1 + 2 * SU);
+      d[i] = ring.template vec<__nv_bfloat16>(stage, u);
+      v[i] = ring.template vec<S>(stage, u + 1);
       const Gain8 w(gain, c, c < nvec);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -129,21 +126,26 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1) pre_norm
       }
     }
     m = rg.sum(m) * inv_h;
-    if (!live) continue;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = rg.l + i * n_lanes;
-      if (c >= nvec) continue;
+      const int c = rg.l + i * n_lanes, u = i * (1 + 2 * SU);
+      if (!live || c >= nvec) continue;
+      if (!kWide) {
+        d[i] = ring.template vec<__nv_bfloat16>(stage, u);
+        v[i] = ring.template vec<S>(stage, u + 1);
+      }
       const Gain8 w(gain, c, true);
       float o[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float n = v[i].at(j) * r;
-        o[j] = r * (d[i].at(j) * w.at(j) - n * m);
-        if (dres) o[j] = __fmaf_rn(res_scale, res[i].at(j), o[j]);
+      for (int j = 0; j < 8; ++j) o[j] = r * (d[i].at(j) * w.at(j) - v[i].at(j) * r * m);
+      if (dres) {
+        const Vec8<S> res = ring.template vec<S>(stage, u + 1 + SU);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = __fmaf_rn(res_scale, res.at(j), o[j]);
       }
       Vec8<S>::store(dx + t * lddx + 8 * c, o);
     }
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
   }
   if (part) {  // the ring's memory is free: copies still under way are of rows behind the last, zeros
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -152,34 +154,37 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1) pre_norm
   }
 }
 
-// dgain[h] (+)= the parts' sums: 32 columns a block, four a thread, 32 threads a column,
-// each with every 32nd part, eight of them under way at a time; their sums in order.
-__global__ void __launch_bounds__(256) norm_gain_sum_kernel(const float* __restrict__ part, int parts, int H, float* dgain,
+// dgain[h] (+)= the parts' sums: 32 columns a block, four a thread, 64 threads a column,
+// each with every 64th of the 512 parts at most, all eight under way at once; their sums in
+// a fixed order.
+__global__ void __launch_bounds__(512) norm_gain_sum_kernel(const float* __restrict__ part, int parts, int H, float* dgain,
                                                             int accumulate) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float s[32][33];
+  __shared__ float s[64][33];
+  __shared__ float s2[16][33];
   const int x = threadIdx.x & 7, y = threadIdx.x >> 3, h = blockIdx.x * 32 + 4 * x;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (h < H) {
-#pragma unroll 1
-    for (int p0 = y; p0 < parts; p0 += 256) {
-      float4 a[8];
+    float4 a[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        a[u] = p0 + 32 * u < parts ? __ldg(reinterpret_cast<const float4*>(part + (size_t)(p0 + 32 * u) * H + h))
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int u = 0; u < 8; ++u)
+      a[u] = y + 64 * u < parts ? __ldg(reinterpret_cast<const float4*>(part + (size_t)(y + 64 * u) * H + h)) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v.x += a[u].x, v.y += a[u].y, v.z += a[u].z, v.w += a[u].w;
-    }
+    for (int u = 0; u < 8; ++u) v.x += a[u].x, v.y += a[u].y, v.z += a[u].z, v.w += a[u].w;
   }
   s[y][4 * x] = v.x, s[y][4 * x + 1] = v.y, s[y][4 * x + 2] = v.z, s[y][4 * x + 3] = v.w;
+  __syncthreads();
+  {
+    const int c = threadIdx.x & 31, q = threadIdx.x >> 5;
+    s2[q][c] = (s[4 * q][c] + s[4 * q + 1][c]) + (s[4 * q + 2][c] + s[4 * q + 3][c]);
+  }
   __syncthreads();
   const int c = blockIdx.x * 32 + threadIdx.x;
   if (threadIdx.x < 32 && c < H) {
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) sum += s[i][threadIdx.x];
+    for (int i = 0; i < 16; ++i) sum += s2[i][threadIdx.x];
     dgain[c] = accumulate ? dgain[c] + sum : sum;
   }
 }
@@ -206,12 +211,13 @@ template <typename S>
 int run_pre_norm_bwd(const char* fn, const __nv_bfloat16* dy, long long lddy, const S* x, long long ldx, const float* gain,
                      const float* rstd, const S* dres, long long lddres, float res_scale, int T, int H, S* dx, long long lddx,
                      float* dgain, int accumulate, float* ws, cudaStream_t s) {
-  auto run = [&](auto l, auto v) {
+  auto run = [&](auto l, auto v, auto wide) {
     constexpr int L = decltype(l)::value, NV = decltype(v)::value;
+    constexpr bool kWide = decltype(wide)::value;
     const RowShape sh = row_shape(H, NV);
-    auto kern = pre_norm_bwd_kernel<S, L, NV>;
-    const size_t smem = bwd_smem(PreBwd<S, NV>::UNITS, NV, sh.threads);
-    const int grid = norm_grid(T, sh.rows, blocks_per_sm(smem, sh.threads, NV == 1 ? 80 : 128), kNormParts);
+    auto kern = pre_norm_bwd_kernel<S, L, NV, kWide>;
+    const size_t smem = bwd_smem(PreBwd<S, NV>::UNITS, NV, sh.threads, kWide);
+    const int grid = norm_grid(T, sh.rows, blocks_per_sm(smem, sh.threads, kWide ? 128 : 80), kNormParts);
     static bool done[kMaxDevices];
     if (int rc = allow_smem(fn, reinterpret_cast<const void*>(kern), smem, done)) return rc;
     launch_pdl(kern, grid, sh.threads, smem, s, dy, lddy, x, ldx, gain, rstd, dres, lddres, res_scale, T, H, sh.W, dx, lddx,
@@ -219,8 +225,9 @@ int run_pre_norm_bwd(const char* fn, const __nv_bfloat16* dy, long long lddy, co
     if (int rc = check_launch(fn)) return rc;
     return dgain ? launch_gain_sum(fn, ws, grid, H, dgain, accumulate, s) : MOE_OK;
   };
-  if (H > 256) return run(std::integral_constant<int, 0>{}, std::integral_constant<int, 2>{});
-  return with_lanes<false>(row_shape(H, 1).L, [&](auto l) { return run(l, std::integral_constant<int, 1>{}); });
+  if (H > 4096) return run(std::integral_constant<int, 0>{}, std::integral_constant<int, 2>{}, std::true_type{});
+  if (H > 256) return run(std::integral_constant<int, 0>{}, std::integral_constant<int, 2>{}, std::false_type{});
+  return with_lanes<false>(row_shape(H, 1).L, [&](auto l) { return run(l, std::integral_constant<int, 1>{}, std::false_type{}); });
 }
 
 }  // namespace
@@ -252,7 +259,7 @@ int allow_smem(const char* fn, const void* kernel, size_t bytes, bool (&done)[kM
 }
 
 int launch_gain_sum(const char* fn, const float* part, int parts, int H, float* dgain, int accumulate, cudaStream_t s) {
-  launch_pdl(norm_gain_sum_kernel, (H + 31) / 32, 256, 0, s, part, parts, H, dgain, accumulate);
+  launch_pdl(norm_gain_sum_kernel, (H + 31) / 32, 512, 0, s, part, parts, H, dgain, accumulate);
   return check_launch(fn);
 }
 
