@@ -195,11 +195,7 @@ __global__ void __launch_bounds__(PostBlock<NV, kWide>::THREADS, PostBlock<NV, k
       const int c = rg.l + i * n;
       const bool there = t < p.T && c < nvec;
       const size_t at = there ? (size_t)t * H + 8 * c : 0;
-      if (p.residual) {
-#pragma unroll
-        for (int v = 0; v < SU; ++v)
-          ring.fetch(stage, i * per + kr + v, reinterpret_cast<const uint4*>(static_cast<const S*>(p.residual) + at) + v, there);
-      }
+      if (p.residual) ring.fetch(stage, i * per + kr, static_cast<const S*>(p.residual) + at, there);
       if (p.gate_kind == 2) ring.fetch(stage, i * per + kr + SU, static_cast<const __nv_bfloat16*>(p.gate) + at, there);
     }
     ring.commit();

@@ -66,8 +66,7 @@ __global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : (holds_row(kEle
       const long long at = there ? t * H + 8 * c : 0;
       const int u = i * P::PER;
       ring.fetch(stage, u, p.z + at, there);
-#pragma unroll
-      for (int q = 0; q < SU; ++q) ring.fetch(stage, u + 1 + q, reinterpret_cast<const uint4*>(dout + at) + q, there);
+      ring.fetch(stage, u + 1, dout + at, there);
       if (kElement) ring.fetch(stage, u + 1 + SU, static_cast<const __nv_bfloat16*>(p.gate) + at, there);
     }
     ring.commit();

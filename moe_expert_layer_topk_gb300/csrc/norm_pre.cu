@@ -90,12 +90,8 @@ __global__ void __launch_bounds__(kWide ? 512 : 256, kWide ? 1 : 3) pre_norm_bwd
       const bool there = t < T && c < nvec;
       const int u = i * (1 + 2 * SU);
       ring.fetch(stage, u, dy + (there ? t * lddy + 8 * c : 0), there);
-#pragma unroll
-      for (int q = 0; q < SU; ++q) {
-        ring.fetch(stage, u + 1 + q, reinterpret_cast<const uint4*>(x + (there ? t * ldx + 8 * c : 0)) + q, there);
-        if (dres)
-          ring.fetch(stage, u + 1 + SU + q, reinterpret_cast<const uint4*>(dres + (there ? t * lddres + 8 * c : 0)) + q, there);
-      }
+      ring.fetch(stage, u + 1, x + (there ? t * ldx + 8 * c : 0), there);
+      if (dres) ring.fetch(stage, u + 1 + SU, dres + (there ? t * lddres + 8 * c : 0), there);
     }
     ring.commit();
   };
