@@ -140,6 +140,9 @@ struct Params {
   const float* row_w;
   void* h_w;
   float* dw_part;
+  // GATE_UP_CKPT, DOWN_BWD_CKPT, single CTAs: a tile is four pieces of up to 32 rows of one
+  // expert, from any of its segments (A comes in boxes of 32 rows, through tmO0 or tmB1)
+  int pieces;
 };
 
 struct Ctl {
@@ -157,13 +160,20 @@ struct Ctl {
   int* seg_tiles;                   // prefix sum of tiles per segment (row kinds)
   int* seg_exp;
   int* grp_rows;                    // DW: rows per output group
+  int* seg_ord;                     // pieces: segments by expert; seg_tiles counts pieces in this order
   unsigned long long ep_bar[4][EP_GU_SETS];  // g,u / addend box loads per epilogue warp
 };
 
 // Bytes of the segment tables that follow Ctl.
-__host__ __device__ constexpr size_t seg_table_bytes(int num_seg, int num_groups, bool dw) {
-  return ((size_t)(3 * num_seg + 2 + (dw ? num_groups : 0)) * 4 + 15) / 16 * 16;
+__host__ __device__ constexpr size_t seg_table_bytes(int num_seg, int num_groups, bool dw, bool pieces = false) {
+  return ((size_t)(3 * num_seg + 2 + (dw ? num_groups : 0) + (pieces ? num_seg : 0)) * 4 + 15) / 16 * 16;
 }
+// the kinds whose tiles may be made of pieces, and segments up to which they are (the order
+// by expert costs each CTA num_seg^2 / 320 comparisons)
+__host__ __device__ constexpr bool has_pieces(int kind, int ctas) {
+  return (kind == DOWN_BWD_CKPT || kind == GATE_UP_CKPT) && ctas == 1;
+}
+constexpr int kMaxPieceSegs = 256;
 constexpr size_t kMaxTableBytes = seg_table_bytes(kMaxSegments, kMaxExperts, true);
 
 
@@ -238,11 +248,42 @@ struct Tile {
   int n0;      // first output column of the tile
   int row_end; // row kinds: end of the segment (exclusive)
   int seg;     // row kinds: segment index
+  int ord;     // pieces: the first one's segment's place in the order by expert
 };
+
+// Piece `i` in the order by expert: its first row and how many of its 32 rows are a
+// segment's (0: a piece that fills up an expert's last tile).
+// ord: a place at or before its segment's, from where it is looked for.
+struct Piece {
+  int row, rows;
+};
+__device__ __forceinline__ Piece find_piece(int i, int& ord, const Params& p, const Ctl* ctl) {
+  while (ord + 1 < p.num_seg && ctl->seg_tiles[ord + 1] <= i) ++ord;
+  const int seg = ctl->seg_ord[ord], row = ctl->seg_off[seg] + 32 * (i - ctl->seg_tiles[ord]);
+  const int left = ctl->seg_off[seg + 1] - row;
+  return {left > 0 ? row : 0, left < 0 ? 0 : (left > 32 ? 32 : left)};
+}
 
 template <int KIND, int CTAS>
 __device__ __forceinline__ Tile decode_tile(int tile, const Params& p, const Ctl* ctl, int rank) {
   Tile t;
+  if constexpr (has_pieces(KIND, CTAS)) {
+    if (p.pieces) {
+      const int i = 4 * (tile / p.n_tiles);
+      int lo = 0, hi = p.num_seg - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (ctl->seg_tiles[mid] <= i) lo = mid; else hi = mid - 1;
+      }
+      t.ord = lo;
+      t.seg = ctl->seg_ord[lo];
+      t.group = ctl->seg_exp[t.seg];
+      t.m0 = 0;
+      t.row_end = 0;
+      t.n0 = tile % p.n_tiles * (is_gate_up(KIND) ? p.NH : p.BN);
+      return t;
+    }
+  }
   if constexpr (Traits<KIND>::rows) {
     const int gm = tile / p.n_tiles, nt = tile % p.n_tiles;
     int lo = 0, hi = p.num_seg - 1;
@@ -325,6 +366,7 @@ __global__ void __launch_bounds__(Cfg<KIND, CTAS>::NTHREADS, 1)
       ctl->seg_tiles = tab + p.num_seg + 1;
       ctl->seg_exp = tab + 2 * (p.num_seg + 1);
       ctl->grp_rows = tab + 3 * p.num_seg + 2;
+      ctl->seg_ord = tab + 3 * p.num_seg + 2;
     }
     __syncthreads();
   }
@@ -356,8 +398,70 @@ __global__ void __launch_bounds__(Cfg<KIND, CTAS>::NTHREADS, 1)
   if (!Traits<KIND>::rows)
     for (int s = threadIdx.x; s < p.num_seg; s += C::NTHREADS)
       if (ctl->seg_exp[s] >= 0) atomicAdd(&ctl->grp_rows[ctl->seg_exp[s]], ctl->seg_off[s + 1] - ctl->seg_off[s]);
+  if constexpr (has_pieces(KIND, CTAS)) {
+    if (p.pieces) {  // segments by expert, each expert's in their order; those of none last
+      for (int s = threadIdx.x; s < p.num_seg; s += C::NTHREADS) {
+        const unsigned key = (unsigned)ctl->seg_exp[s];
+        int rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < p.num_seg; ++j) {
+          const unsigned other = (unsigned)ctl->seg_exp[j];
+          rank += other < key || (other == key && j < s);
+        }
+        ctl->seg_ord[rank] = s;
+      }
+      __syncthreads();
+    }
+  }
+  const bool by_pieces = has_pieces(KIND, CTAS) && p.pieces;
+  if (warp == 0 && by_pieces) {
+    // First piece of each segment in that order, every expert's first at a multiple of four:
+    // a running sum of the segments' pieces, and one of what fills up each expert's last tile.
+    int sum = 0, start = 0, pad = 0;
+    for (int base = 0; base < p.num_seg; base += 32) {
+      const int i = base + lane;
+      int n = 0, e = -1, before = -2, behind = -2;
+      if (i < p.num_seg) {
+        const int s = ctl->seg_ord[i];
+        e = ctl->seg_exp[s];
+        const int len = ctl->seg_off[s + 1] - ctl->seg_off[s];
+        if (e >= 0 && len > 0) n = (len + 31) / 32;
+        if (i > 0) before = ctl->seg_exp[ctl->seg_ord[i - 1]];
+        if (i + 1 < p.num_seg) behind = ctl->seg_exp[ctl->seg_ord[i + 1]];
+      }
+      int incl = n;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+      }
+      incl += sum;
+      int from = e != before ? incl - n : 0;  // the expert's first piece (never falls along the order)
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, from, off);
+        if (lane >= off && o > from) from = o;
+      }
+      if (start > from) from = start;
+      const int fill = i < p.num_seg && e != behind ? (-(incl - from)) & 3 : 0;
+      int fills = fill;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, fills, off);
+        if (lane >= off) fills += o;
+      }
+      fills += pad;
+      if (i < p.num_seg) ctl->seg_tiles[i] = incl - n + fills - fill;
+      sum = __shfl_sync(0xffffffffu, incl, 31);
+      start = __shfl_sync(0xffffffffu, from, 31);
+      pad = __shfl_sync(0xffffffffu, fills, 31);
+    }
+    if (lane == 0) ctl->total_tiles = (sum + pad) / 4 * p.n_tiles;
+    __syncwarp();
+  }
   if (warp == 0) {
-    if constexpr (Traits<KIND>::rows) {
+    if (by_pieces) {
+    } else if constexpr (Traits<KIND>::rows) {
       int carry = 0;
       for (int base = 0; base < p.num_seg; base += 32) {
         const int s = base + lane;
@@ -495,6 +599,14 @@ __global__ void __launch_bounds__(Cfg<KIND, CTAS>::NTHREADS, 1)
       int map_seg = -1, this_seg = -1, next_seg = -1;
       for (int tile = unit; ok && tile < total; tile += nunits) {
         const Tile t = decode_tile<KIND, CTAS>(tile, p, ctl, rank);
+        int piece_row[4] = {0, 0, 0, 0};
+        if constexpr (has_pieces(KIND, CTAS)) {
+          if (p.pieces) {
+            int ord = t.ord;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) piece_row[i] = find_piece(4 * (tile / p.n_tiles) + i, ord, p, ctl).row;
+          }
+        }
         if constexpr (KIND == DW) {
           // with one segment per group, the next tile's maps are acquired
           // and prefetched now, so their fetch overlaps this tile's loads
@@ -535,7 +647,12 @@ __global__ void __launch_bounds__(Cfg<KIND, CTAS>::NTHREADS, 1)
             tma_load_mn<CTAS>(sA, ma, fb, row0, t.m0 / 64);
             tma_load_mn<CTAS>(sB, ma + 1, fb, row0, t.n0 / 64 + ck0);
           } else {
-            tma_load<CTAS>(sA, &tmA, fb, row0, t.m0);
+            if (by_pieces) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) tma_load<CTAS>(sA + i * (A_BYTES / 4), KIND == GATE_UP_CKPT ? &tmO0 : &tmB1, fb, row0, piece_row[i]);
+            } else {
+              tma_load<CTAS>(sA, &tmA, fb, row0, t.m0);
+            }
             if constexpr (is_gate_up(KIND)) {
               const int brow = t.group * p.b_group_rows + t.n0;
               if (CTAS == 1) {
@@ -688,9 +805,17 @@ __global__ void __launch_bounds__(Cfg<KIND, CTAS>::NTHREADS, 1)
       const Tile t = decode_tile<KIND, CTAS>(tile, p, ctl, rank);
       const int buf = local & 1;
       const uint32_t use = (uint32_t)(local >> 1);
-      const int rb = t.m0 + q * 32;
+      int rb = t.m0 + q * 32;
       const int lim = Traits<KIND>::rows ? t.row_end : p.M;
-      const int nvalid = lim - rb < 0 ? 0 : (lim - rb > 32 ? 32 : lim - rb);
+      int nvalid = lim - rb < 0 ? 0 : (lim - rb > 32 ? 32 : lim - rb);
+      if constexpr (has_pieces(KIND, CTAS)) {
+        if (p.pieces) {
+          int ord = t.ord;
+          const Piece mine = find_piece(4 * (tile / p.n_tiles) + q, ord, p, ctl);
+          rb = mine.row;
+          nvalid = mine.rows;
+        }
+      }
       const bool any = nvalid > 0;
       // Router dX: the fp32 addend, which does not depend on the
       // accumulator (two boxes of 32 rows x 16 columns per 32-column
@@ -1281,6 +1406,24 @@ bool pair_for_rows(int bn, int R, int num_seg, int E) {
 bool g_attr[kNumKinds][2][64] = {};
 // SMs the persistent GEMM grids may use, for launches from this thread (0: all)
 thread_local int g_gemm_sm_limit = 0;
+int gemm_sms() {
+  const int sms = sm_count();
+  return g_gemm_sm_limit > 0 && g_gemm_sm_limit < sms ? g_gemm_sm_limit : sms;
+}
+
+// Several segments an expert (rows received from several ranks): tiles of pieces, where the
+// kind has them and they come to fewer rounds of tiles, each segment counted with half a
+// tile or half a piece of padding, each expert with half a tile.  Forward / backward, 2048 x
+// 768, us: 16381 rows of 16 experts from 8 ranks 98 / 75 against 129 / 88 by rows, 32768
+// 169 / 123 against 194 / 140, 3000 of 32 experts 67 / 59 against 240 / 110; where the
+// rounds are as many, the order by expert costs 2 to 3 (4000 rows of 8 experts from 4
+// ranks 39 / 37 against 36 / 35).
+bool tiles_of_pieces(bool pair, int num_seg, int E, int R, int n_tiles) {
+  if (pair || num_seg <= E || num_seg > kMaxPieceSegs) return false;
+  const long long sms = gemm_sms() > 0 ? gemm_sms() : 1, rows = R / BM;
+  const long long by_rows = (rows + num_seg / 2) * n_tiles, by_pieces = (rows + num_seg / 8 + E / 2) * n_tiles;
+  return (by_pieces + sms - 1) / sms < (by_rows + sms - 1) / sms;
+}
 
 // Launches grouped_gemm_kernel<KIND, CTAS>: completes the CTAS-dependent
 // parameters, sizes the shared memory to the segment tables and the
@@ -1297,12 +1440,13 @@ int launch(Params p, const CUtensorMap& a, const CUtensorMap& b0, const CUtensor
     p.m_tiles = (p.M + BM * CTAS - 1) / (BM * CTAS);
     upper = (long long)p.num_groups * p.m_tiles * p.n_tiles;
   } else {
-    upper = ((long long)(p.M + BM * CTAS - 1) / (BM * CTAS) + p.num_seg) * p.n_tiles;
+    upper = ((long long)(p.M + BM * CTAS - 1) / (BM * CTAS) + p.num_seg) * p.n_tiles;  // (pieces need no more tiles)
   }
   const int dev = current_device();
   if (dev < 0) return fail(MOE_ERR_CUDA, "%s: no current CUDA device", what);
   auto kern = grouped_gemm_kernel<KIND, CTAS>;
-  const size_t smem_sz = Cfg<KIND, CTAS>::SMEM_FIXED + seg_table_bytes(p.num_seg, p.num_groups, KIND == DW);
+  const size_t smem_sz = Cfg<KIND, CTAS>::SMEM_FIXED +
+                         seg_table_bytes(p.num_seg, p.num_groups, KIND == DW, has_pieces(KIND, CTAS) && p.pieces);
   if (smem_sz > kSmemMax) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s: segment tables too large", what);
   const int smem = (int)smem_sz;
   if (!g_attr[KIND][CTAS - 1][dev]) {
@@ -1310,9 +1454,8 @@ int launch(Params p, const CUtensorMap& a, const CUtensorMap& b0, const CUtensor
     if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
     g_attr[KIND][CTAS - 1][dev] = true;
   }
-  int sms = sm_count();
+  const int sms = gemm_sms();
   if (sms <= 0) return fail(MOE_ERR_CUDA, "%s: cannot query the SM count", what);
-  if (g_gemm_sm_limit > 0 && g_gemm_sm_limit < sms) sms = g_gemm_sm_limit;
   const long long units_max = sms / CTAS;
   long long units = upper < units_max ? upper : units_max;
   if (units < 1) units = 1;
@@ -1492,7 +1635,11 @@ int swiglu_impl(const void* a_src, const int32_t* gather_rows, int T, const void
   const bool pair = pair_for_rows(p.BN, R, num_seg, E);
   if (gu_scale) {  // its epilogue stores without maps (the A map fills the slots)
     p.ckpt_scale = static_cast<unsigned short*>(gu_scale);
-    return run<GATE_UP_CKPT>(pair, p, ta, tg, tu, ta, ta, s, fn);
+    p.pieces = tiles_of_pieces(pair, num_seg, E, R, p.n_tiles);
+    CUtensorMap ta32 = ta;
+    if (p.pieces)
+      if (int rc = make_tmap(&ta32, a_src, H, R, 64, 32)) return rc;
+    return run<GATE_UP_CKPT>(pair, p, ta, tg, tu, ta32, ta, s, fn);
   }
   CUtensorMap th, tgu;
   if (int rc = make_out_map(&th, h, I, R, false)) return rc;
@@ -1822,7 +1969,11 @@ int moe_grouped_gemm_down_bwd_ckpt(const void* dy_perm, const float* row_w, cons
     if (int rc = make_tmap_mn(&tb, Wd, I, (uint64_t)E * H, bn / 64 / (pair ? 2 : 1))) return rc;
     if (int rc = make_out_map(&to, dgu, 2 * I, R, false)) return rc;
     if (int rc = make_out_map(&th, h_w, I, R, false)) return rc;
-    if (int rc = run<DOWN_BWD_CKPT>(pair, p, ta, tb, tb, to, th, s, fn)) return rc;
+    CUtensorMap ta32 = tb;
+    p.pieces = tiles_of_pieces(pair, num_seg, E, R, p.n_tiles);
+    if (p.pieces)
+      if (int rc = make_tmap(&ta32, dy_perm, H, R, 64, 32)) return rc;
+    if (int rc = run<DOWN_BWD_CKPT>(pair, p, ta, tb, ta32, to, th, s, fn)) return rc;
   }
   const int n = row_of_slot ? T * k : R;
   if (n == 0) return MOE_OK;

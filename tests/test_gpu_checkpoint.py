@@ -115,6 +115,10 @@ def table(kind, R, E):
         c = rng.multinomial(R, np.where(np.arange(E) == 1, 0, 1.0) / max(1, E - 1)) if E > 1 else np.array([R])
         off = np.concatenate([[0], np.cumsum(c)])
         return E, off, None
+    if kind == "ranks":  # 8 ranks' blocks of each expert: 48, 24 and 320 segments, some of an expert that is not there
+        cut = np.sort(np.concatenate([[0, R], rng.integers(0, R, 8 * E - 1)]))
+        se = np.tile(np.arange(E), 8)
+        return 8 * E, cut, se
     cut = np.sort(rng.integers(R // 10, R - R // 10, 2 * E + 1))
     cut[3] = cut[2]
     return 2 * E, cut, np.concatenate([np.arange(E)[::-1], rng.permutation(E)])
@@ -122,7 +126,17 @@ def table(kind, R, E):
 
 CASES = [("experts", 7, 64, 64, 2), ("experts", 300, 128, 64, 8), ("experts", 700, 512, 320, 4), ("experts", 2500, 256, 128, 3),
          ("experts", 2600, 128, 256, 5), ("experts", 900, 64, 512, 2),
+         ("ranks", 3000, 128, 256, 6), ("ranks", 40, 64, 64, 3), ("ranks", 2000, 64, 64, 40), ("ranks", 5000, 64, 1024, 30),
          ("experts", 129, 64, 192, 1), ("blocks", 400, 128, 128, 3), ("blocks", 1000, 256, 768, 5)]
+
+
+def on_few_sms(call, n=3):
+    """On few SMs, tiles come in many rounds, and several segments an expert in tiles of pieces."""
+    prev = m.moe_set_gemm_sm_limit(n)
+    try:
+        call()
+    finally:
+        m.moe_set_gemm_sm_limit(prev)
 
 
 def inputs(kind, R, H, I, E):
@@ -147,6 +161,9 @@ def test_swiglu_ckpt(kind, R, H, I, E):
     m.moe_grouped_gemm_swiglu(d["x"], d["Wg"], d["Wu"], d["n"], d["o"], d["s"], R, H, I, E, h0, gu0)
     m.moe_grouped_gemm_swiglu_ckpt(d["x"], d["Wg"], d["Wu"], d["n"], d["o"], d["s"], R, H, I, E, h, q, s)
     assert torch.equal(h, h0)  # the product and h are the same
+    few = torch.empty_like(h).fill_(9.0), torch.full_like(q, 77), torch.empty_like(s).fill_(9.0)
+    on_few_sms(lambda: m.moe_grouped_gemm_swiglu_ckpt(d["x"], d["Wg"], d["Wu"], d["n"], d["o"], d["s"], R, H, I, E, *few))
+    assert torch.equal(h, few[0]) and torch.equal(q, few[1]) and torch.equal(s, few[2])
     dead = torch.tensor(~d["live"], device="cuda")
     assert (q[dead] == 77).all() and (s[dead] == 9).all()
     g, u, mag = ref.gate_up(np64(d["x"]), np64(d["Wg"]), np64(d["Wu"]), d["segs"])
@@ -185,6 +202,10 @@ def test_down_bwd_ckpt(kind, R, H, I, E, weighted):
     near(hw[~dead], b["h_w"][live], np.abs(b["h_w"][live]), "h_w")
     near(dw, b["d_w"], b["d_w_mag"], "d_w")
     assert (dgu[dead] == 9).all() and (hw[dead] == 9).all() and (dw[dead] == 0).all()
+    few = torch.empty_like(dgu).fill_(9.0), torch.empty_like(hw).fill_(9.0), e(R).fill_(9.0)
+    ws.fill_(0xFF)
+    on_few_sms(lambda: m.moe_grouped_gemm_down_bwd_ckpt(*args, *few, ws=ws))
+    assert all(torch.equal(a, b) for a, b in zip((dgu, hw, dw), few))
     k = 2
     slot = torch.randperm(R, device="cuda")[:R // k * k].to(torch.int32).view(-1, k)
     dgu2, hw2, dwt = torch.empty_like(dgu).fill_(9.0), torch.empty_like(hw).fill_(9.0), e(R // k, k)
@@ -195,6 +216,31 @@ def test_down_bwd_ckpt(kind, R, H, I, E, weighted):
         slot[0, 0] = -1
         m.moe_grouped_gemm_down_bwd_ckpt(*args, dgu2, hw2, dwt, slot, R // k, k, ws)
         assert dwt[0, 0] == 0 and m.moe_read_device_status(reset=True) == 1
+
+
+@pytest.mark.parametrize("sms", [0, 2])
+def test_segments_of_no_expert(sms):
+    """Rows of a segment whose expert is out of range are skipped and reported, by tiles and by pieces of tiles."""
+    R, H, I, E, n = 900, 64, 128, 4, 12
+    rn = gen(1)
+    dy, Wd, w = rn(R, H).to(BF), (rn(E, H, I) * 0.1).to(BF), torch.rand(R, device="cuda")
+    q, s = packed(rn(R, 2 * I).to(BF))
+    off = np.linspace(0, R, n + 1).astype(np.int64)
+    se = np.array([0, 1, 2, 3, -1, 3, 2, 4, 0, 1, 1, 1000])
+    dec = ref.unpack(q.cpu().numpy(), s.float().cpu().numpy())
+    b = ref.down_bwd(np64(dy), np64(w), dec[:, :I], dec[:, I:], np64(Wd), ref.experts(off, se))
+    live = np.repeat((se >= 0) & (se < E), np.diff(off))
+    ws = torch.full((m.moe_grouped_gemm_down_bwd_ckpt_workspace_size(R, I),), 0xFF, dtype=torch.uint8, device="cuda")
+    dgu, hw, dw = e(R, 2 * I, dt=BF).fill_(9.0), e(R, I, dt=BF).fill_(9.0), e(R).fill_(9.0)
+    o, t = torch.tensor(off, dtype=torch.int32, device="cuda"), torch.tensor(se, dtype=torch.int32, device="cuda")
+    m.moe_read_device_status(reset=True)
+    on_few_sms(lambda: m.moe_grouped_gemm_down_bwd_ckpt(dy, w, q, s, Wd, n, o, t, R, H, I, E, dgu, hw, dw, ws=ws), sms)
+    assert m.moe_read_device_status(reset=True) == 2
+    dead = torch.tensor(~live, device="cuda")
+    near(dgu[~dead], b["dgu"][live], b["dgu_mag"][live], "dgu")
+    near(hw[~dead], b["h_w"][live], np.abs(b["h_w"][live]), "h_w")
+    near(dw, b["d_w"], b["d_w_mag"], "d_w")
+    assert (dgu[dead] == 9).all() and (hw[dead] == 9).all() and (dw[dead] == 0).all()
 
 
 def test_no_rows_or_segments():
