@@ -602,7 +602,9 @@ int moe_post_norm_bwd(const void* dout, int fp32, const void* z, const float* ga
  * Activations kept in 8 bits for the backward (no counterpart on the pages).
  *
  * Each 32 columns of a row share a scale, a bf16 number:
- *   s = amax(|a|) / 127 (IEEE fp32 division), rounded up to bf16, at least 2^-126
+ *   s = amax(|a|) / 127 (IEEE fp32 division), rounded up to bf16, at least 2^-126;
+ *       2.125 * 2^120 where that is above 2^121, so that no finite a comes back
+ *       infinite in bf16
  *   q = a * (1/s) (fp32, 1/s IEEE) rounded to the nearest whole number, ties to even
  *   a ~ q s, off by at most s/2
  * q int8 [rows, cols] row-major, scale bf16 [rows, cols/32]: 1.0625 bytes an

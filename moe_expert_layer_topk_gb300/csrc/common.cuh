@@ -198,10 +198,14 @@ __device__ __forceinline__ float amax_nan(float m, float a) {
   return r;
 }
 // An amax that is infinite or NaN gives a NaN: all the group's values come back as NaN.
+// A scale above 2^121 becomes 2.125 * 2^120: the largest values, up to 256 * 2^120, then
+// have codes of at most 120, which stand for 255 * 2^120, bf16's largest, where 127 of
+// the scale 2.015625 * 2^120 would be rounded to an infinity.
 __device__ __forceinline__ float ckpt_scale(float amax) {
   const float q = __fdiv_rn(amax, 127.0f);
   const float up = __uint_as_float((__float_as_uint(q) + 0xFFFFu) & 0xFFFF0000u);
-  return !(q <= 3.402823466e+38f) ? __uint_as_float(0x7FC00000u) : (up < 1.17549435e-38f ? 1.17549435e-38f : up);
+  if (!(q <= 3.402823466e+38f)) return __uint_as_float(0x7FC00000u);
+  return up < 0x1p-126f ? 0x1p-126f : (up > 0x1p121f ? 0x1.1p121f : up);
 }
 // Four codes, lowest first: a * inv rounded to nearest even by adding 1.5 * 2^23,
 // whose lowest byte is then the two's complement code (|a * inv| is at most 127

@@ -92,6 +92,7 @@ def pack(a):
     """Codes int8 [rows, cols] and scales fp32 [rows, cols/32] of fp32 values."""
     g = np.asarray(a, np.float32).reshape(len(a), -1, 32)
     s = np.maximum(bf16_up(np.abs(g).max(2) / np.float32(127)), np.float32(2.0 ** -126))
+    s[s > 2.0 ** 121] = 2.125 * 2.0 ** 120
     q = np.rint(g * (np.float32(1) / s)[:, :, None])
     assert np.abs(q).max(initial=0) <= 127
     return q.astype(np.int8).reshape(np.shape(a)), s

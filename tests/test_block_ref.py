@@ -67,6 +67,17 @@ def test_pack_by_hand():
     assert (err <= s * (0.5 + 2.0 ** -16)).all() and (s >= np.abs(a).reshape(50, 3, 32).max(2) / 127 * (1 - 2.0 ** -23)).all()
 
 
+def test_pack_of_the_largest_values():
+    """Codes and scales of amax from 252 * 2^120 to fp32's largest number: no value of a bf16 group
+    comes back as more than bf16's largest, 255 * 2^120, and each is off by half a scale at most."""
+    top = np.array([252, 253, 253.99, 254, 254.01, 255, 255.49, 256 * (1 - 2.0 ** -24)], np.float64) * 2.0 ** 120
+    a = np.repeat(top.astype(np.float32)[:, None], 32, 1) * np.linspace(-1, 1, 32, dtype=np.float32)
+    q, s = ref.pack(a)
+    v = ref.unpack(q, s)
+    assert (np.abs(v) <= 255 * 2.0 ** 120).all()
+    assert (np.abs(v - a) <= s * (0.5 + 2.0 ** -16)).all()
+
+
 def test_down_bwd_is_the_weighted_backward():
     """dgu, dWd and d_w of y = sum_rows w_r h_r Wd^T . dy, by differences."""
     rng = np.random.default_rng(3)

@@ -81,6 +81,21 @@ def test_tiny_infinite_and_nan_groups():
     assert (q[1, 128:].cpu().numpy() == wq).all() and wq[0, 0] == 126 and (a[1, 128:] == 1).all()
 
 
+def test_the_largest_values_stay_finite():
+    top = torch.tensor([252.0, 253.0, 254.0, 255.0], device="cuda") * 2.0 ** 120  # 255 * 2^120: bf16's largest
+    x = (top[:, None] * torch.linspace(-1, 1, 64, device="cuda")).to(BF)
+    assert x[3, 63] == torch.finfo(BF).max
+    q, s = packed(x)
+    wq, ws = ref.pack(x.float().cpu().numpy())
+    assert np.array_equal(s.float().cpu().numpy(), ws) and np.array_equal(q.cpu().numpy(), wq)
+    a, xp = e(4, 64, dt=BF), e(4, 64, dt=BF)
+    m.moe_ckpt_unpack(q, s, 4, 64, a)
+    m.moe_dispatch_rows(q, s, torch.arange(4, dtype=torch.int32, device="cuda").view(4, 1), None, 4, 64, 1, xp, None)
+    half = 0.5 * s.double().repeat_interleave(32, 1) * (1 + 2.0 ** -15)
+    assert torch.isfinite(a).all() and torch.equal(a, xp)
+    assert ((a.double() - x.double()).abs() <= half + 2.0 ** -8 * a.double().abs()).all()
+
+
 @pytest.mark.parametrize("weights", [True, False])
 @pytest.mark.parametrize("codes", [True, False])
 @pytest.mark.parametrize("T,H,k", [(1, 64, 1), (5, 128, 3), (300, 2048, 8), (33, 576, 32), (1, 2048, 8)])
