@@ -130,6 +130,8 @@ def table(kind, R, E):
         c = rng.multinomial(R, np.where(np.arange(E) == 1, 0, 1.0) / max(1, E - 1)) if E > 1 else np.array([R])
         off = np.concatenate([[0], np.cumsum(c)])
         return E, off, None
+    if kind == "tails":  # segments of 512 rows and these
+        return E, np.concatenate([[0], np.cumsum(512 + np.array(TAILS))]), None
     if kind == "ranks":  # 8 ranks' blocks of each expert: 48, 24 and 320 segments, some of an expert that is not there
         cut = np.sort(np.concatenate([[0, R], rng.integers(0, R, 8 * E - 1)]))
         se = np.tile(np.arange(E), 8)
@@ -139,10 +141,12 @@ def table(kind, R, E):
     return 2 * E, cut, np.concatenate([np.arange(E)[::-1], rng.permutation(E)])
 
 
+TAILS = (1, 32, 63, 64, 65, 96, 128, 129, 255, 256)
 CASES = [("experts", 7, 64, 64, 2), ("experts", 300, 128, 64, 8), ("experts", 700, 512, 320, 4), ("experts", 2500, 256, 128, 3),
          ("experts", 2600, 128, 256, 5), ("experts", 900, 64, 512, 2),
          ("ranks", 3000, 128, 256, 6), ("ranks", 40, 64, 64, 3), ("ranks", 2000, 64, 64, 40), ("ranks", 5000, 64, 1024, 30),
-         ("experts", 129, 64, 192, 1), ("blocks", 400, 128, 128, 3), ("blocks", 1000, 256, 768, 5)]
+         ("experts", 129, 64, 192, 1), ("blocks", 400, 128, 128, 3), ("blocks", 1000, 256, 768, 5),
+         ("tails", 6209, 128, 128, 10), ("tails", 6209, 64, 256, 10), ("tails", 6209, 64, 768, 10)]
 
 
 def on_few_sms(call, n=3):
