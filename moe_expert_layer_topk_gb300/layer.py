@@ -31,6 +31,15 @@ def _ws(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(256, (nbytes + 255) // 256 * 256), dtype=torch.uint8, device=device)
 
 
+def _stream_of(stream, device):
+    """torch's stream for what the calls take as one: None (the current one), an object, or a handle."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if hasattr(stream, "cuda_stream"):
+        return stream
+    return torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+
+
 class MoELayer:
     """One layer's buffers for T tokens of hidden size H, E experts of size I, top-k.
 
@@ -237,12 +246,7 @@ class MoELayer:
         calls (a layer without dropout has none)."""
         if not self.dropout:
             return
-        if stream is None:
-            self.rng[1] += self.T * self.H // 8
-            return
-        handle = getattr(stream, "cuda_stream", stream)
-        dev = self.rng.device
-        with torch.cuda.stream(torch.cuda.ExternalStream(handle, dev) if handle else torch.cuda.default_stream(dev)):
+        with torch.cuda.stream(_stream_of(stream, self.rng.device)):
             self.rng[1] += self.T * self.H // 8
 
     def combine(self, stream=None, y=None, residual=None):
@@ -340,7 +344,7 @@ class MoELayer:
                                        stream)
         tail = stream
         if overlap:
-            main = stream if stream is not None else torch.cuda.current_stream(self.dx_perm.device)
+            main = _stream_of(stream, self.dx_perm.device)
             if self._side is None:
                 self._side = torch.cuda.Stream(self.dx_perm.device)
                 self._ev_fork, self._ev_join = torch.cuda.Event(), torch.cuda.Event()
