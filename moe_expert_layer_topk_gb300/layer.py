@@ -392,6 +392,16 @@ class MoELayer:
         return x
 
 
+class _Normed(tuple):
+    """(n, rstd) as a block leaves them for the next one.  scratch: n is memory that blocks share, which holds it only until
+    the next of them runs, forward or backward; else both stay until that block's own next forward."""
+
+    def __new__(cls, n, rstd, scratch):
+        self = super().__new__(cls, (n, rstd))
+        self.scratch = scratch
+        return self
+
+
 class MoEBlock:
     """An MoE layer between its norms, with the block's gate and the residual:
 
@@ -406,7 +416,11 @@ class MoEBlock:
     Gains are fp32 [H] or None (ones).  Blocks one after another: with
     next_norm=True a block also computes the next one's normed input on the
     way, with that one's pre_gain as next_gain, and leaves it and its rstd in
-    `next_normed`, which that one's forward takes as `normed`.
+    `next_normed`, which that one's forward takes as `normed`, before any other
+    block that shares their scratch runs.  Plain and checkpointed blocks may follow one
+    another: what a backward needs of `normed` and the block before does not
+    keep (a checkpointed block's n is scratch), and any other tensors given as
+    `normed`, are copied into the block's own.
 
     After the backward: d_pre_gain, d_post_gain (fp32 [H]), d_gate (like the
     gate), and the layer's gradients (`layer.dWg` ...).  A checkpointed
@@ -449,7 +463,20 @@ class MoEBlock:
     @property
     def next_normed(self):
         """The next block's normed input and its rstd (after a forward, with next_norm)."""
-        return self.next_n, self.next_rstd
+        return _Normed(self.next_n, self.next_rstd, scratch=self.checkpoint)
+
+    def _keep(self, normed, stream):
+        """The normed input and the rstd, where they last until the backward: n in a plain block (a
+        checkpointed one makes it again), rstd in both."""
+        n, rstd = normed
+        known = isinstance(normed, _Normed)
+        if not (self.checkpoint or (known and not normed.scratch)):
+            with torch.cuda.stream(_stream_of(stream, self.n.device)):
+                n = self.n.copy_(n)
+        if not known and rstd is not None:
+            with torch.cuda.stream(_stream_of(stream, self.rstd.device)):
+                rstd = self.rstd.copy_(rstd)
+        return n, rstd
 
     def _check_gate(self, gate):
         if (gate is None) != (self.gate is None):
@@ -460,16 +487,18 @@ class MoEBlock:
     def forward(self, x, pre_gain, post_gain, Wr, bias, Wg, Wu, Wd, gate=None, stream=None, out=None, *, normed=None,
                 next_gain=None, mask=None, seg_offsets=None):
         """out (default: the block's own) of x.  normed: (n, rstd) as the block before left them
-        (its next_normed, for this block's pre_gain); else the block norms x itself.  next_gain:
+        (its next_normed, for this block's pre_gain), or tensors like them; else the block norms x itself.  next_gain:
         the next block's pre_gain, of a block with next_norm."""
         self._check_gate(gate)
         if next_gain is not None and self.next_n is None:
             raise ValueError("next_gain belongs to a block built with next_norm")
         T, H, L = self.T, self.H, self.layer
         out = self.out if out is None else out
-        n, rstd = (self.n, self.rstd) if normed is None else normed
         if normed is None:
+            n, rstd = self.n, self.rstd
             moe_pre_norm(x, pre_gain, self.eps, T, H, n, rstd, stream)
+        else:
+            n, rstd = self._keep(normed, stream) if self.training else normed
         self._normed = n, rstd
         L.route(n, Wr, bias, stream)
         if L.balanced:
