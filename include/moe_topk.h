@@ -566,8 +566,8 @@ int moe_adapter_linear_bwd(const void* dy, long long lddy, const void* x, long l
  *   residual may be NULL (0); out may be residual.  G by gate_kind:
  *     0: 1;  1: sigmoid(gate[t]), gate fp32 [T];  2: sigmoid(gate[t,h]), gate bf16 [T,H].
  *   rstd: NULL or where z's rstd is left (norm = 1).  next_y not NULL: the next
- *   block's moe_pre_norm of out as stored is computed on the way,
- *   next_y = norm(out) next_gain, next_rstd its rstd (may be NULL).
+ *   block's moe_pre_norm of out as stored is computed on the way, with this
+ *   call's eps: next_y = norm(out) next_gain, next_rstd its rstd (may be NULL).
  * moe_combine_post_norm: the same of z[t] = sum_j topk_w[t,j] y_perm[row_of_slot[t,j]]
  *   (fp32, slots in order, as moe_combine); z NULL, or where it is kept in bf16
  *   for the backward.  H a multiple of 64, k <= 32.

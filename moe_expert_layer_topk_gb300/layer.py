@@ -393,12 +393,13 @@ class MoELayer:
 
 
 class _Normed(tuple):
-    """(n, rstd) as a block leaves them for the next one.  scratch: n is memory that blocks share, which holds it only until
-    the next of them runs, forward or backward; else both stay until that block's own next forward."""
+    """(n, rstd) as a block leaves them for the next one, and the eps that they were made with.  scratch: n is memory that
+    blocks share, which holds it only until the next of them runs, forward or backward; else both stay until that block's
+    own next forward."""
 
-    def __new__(cls, n, rstd, scratch):
+    def __new__(cls, n, rstd, eps, scratch):
         self = super().__new__(cls, (n, rstd))
-        self.scratch = scratch
+        self.eps, self.scratch = eps, scratch
         return self
 
 
@@ -417,8 +418,9 @@ class MoEBlock:
     next_norm=True a block also computes the next one's normed input on the
     way, with that one's pre_gain as next_gain, and leaves it and its rstd in
     `next_normed`, which that one's forward takes as `normed`, before any other
-    block that shares their scratch runs.  Plain and checkpointed blocks may follow one
-    another: what a backward needs of `normed` and the block before does not
+    block that shares their scratch runs.  One eps serves a block's two norms and the
+    next one's: a block refuses a next_normed made with another eps than its
+    own.  Plain and checkpointed blocks may follow one another: what a backward needs of `normed` and the block before does not
     keep (a checkpointed block's n is scratch), and any other tensors given as
     `normed`, are copied into the block's own.
 
@@ -463,7 +465,7 @@ class MoEBlock:
     @property
     def next_normed(self):
         """The next block's normed input and its rstd (after a forward, with next_norm)."""
-        return _Normed(self.next_n, self.next_rstd, scratch=self.checkpoint)
+        return _Normed(self.next_n, self.next_rstd, self.eps, self.checkpoint)
 
     def _keep(self, normed, stream):
         """The normed input and the rstd, where they last until the backward: n in a plain block (a
@@ -487,11 +489,13 @@ class MoEBlock:
     def forward(self, x, pre_gain, post_gain, Wr, bias, Wg, Wu, Wd, gate=None, stream=None, out=None, *, normed=None,
                 next_gain=None, mask=None, seg_offsets=None):
         """out (default: the block's own) of x.  normed: (n, rstd) as the block before left them
-        (its next_normed, for this block's pre_gain), or tensors like them; else the block norms x itself.  next_gain:
+        (its next_normed, for this block's pre_gain), or tensors like them, made with this block's eps; else the block norms x itself.  next_gain:
         the next block's pre_gain, of a block with next_norm."""
         self._check_gate(gate)
         if next_gain is not None and self.next_n is None:
             raise ValueError("next_gain belongs to a block built with next_norm")
+        if isinstance(normed, _Normed) and normed.eps != self.eps:
+            raise ValueError("normed was made with eps %g, this block's is %g" % (normed.eps, self.eps))
         T, H, L = self.T, self.H, self.layer
         out = self.out if out is None else out
         if normed is None:

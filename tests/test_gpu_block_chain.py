@@ -151,3 +151,20 @@ def test_mixed_stack_on_a_stream_and_in_a_graph(hand):
         g.replay()
         torch.cuda.synchronize()
         assert same(results(blocks, *left), w)
+
+
+def test_one_eps_along_a_stack():
+    """A normed input made with another eps than the block's own is refused, and nothing is left of the call."""
+    ps, (x, _) = params(2), batch()
+    (p, q) = ps
+    for training in (True, False):
+        a = m.MoEBlock(T, H, I, E, k, gate="token", eps=1e-2, fp32=True, next_norm=True, training=training)
+        other, same_eps = (m.MoEBlock(T, H, I, E, k, gate="token", eps=eps, fp32=True, training=training) for eps in (1e-6, 1e-2))
+        out = a.forward(x, *args(p), None, p["Wg"], p["Wu"], p["Wd"], p["gate"], next_gain=q["pre"])
+        rest = (*args(q), None, q["Wg"], q["Wu"], q["Wd"], q["gate"])
+        other.out.fill_(7.0)
+        with pytest.raises(ValueError, match="eps"):
+            other.forward(out, *rest, normed=a.next_normed)
+        assert (other.out == 7).all()
+        got = same_eps.forward(out, *rest, normed=a.next_normed).clone()
+        assert rel(got, same_eps.forward(out, *rest)) <= 2 ** -8  # its own norm: other orders of the sum
