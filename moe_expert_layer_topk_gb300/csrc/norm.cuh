@@ -76,9 +76,9 @@ struct RowGroup {
     return v;
   }
   // 1/sqrt(mean + eps) of the squares of a row's values, at(i, j) for element j of this
-  // lane's i-th vector (0 where it has none).  Squares beyond fp32's range are added
-  // again of values times 2^-80 (8192 of the largest, 2^48 each, add up to 2^109); eps
-  // is nothing beside those.  An infinity gives 0, a NaN NaN.
+  // lane's i-th vector (0 where it has none).  Where mean + eps, or the squares' sum, leaves
+  // fp32's range they are formed again of values times 2^-80 (8192 of the largest, 2^48 each,
+  // add up to 2^109) and eps times 2^-160.  An infinity gives 0, a NaN NaN.
   template <int NV, class At>
   __device__ __forceinline__ float rstd(float inv_h, float eps, At&& at) {
     float ss = 0.f;
@@ -87,8 +87,9 @@ struct RowGroup {
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = __fmaf_rn(at(i, j), at(i, j), ss);
     ss = sum(ss);
-    float r = __frsqrt_rn(__fmaf_rn(ss, inv_h, eps));
-    const bool big = !(ss <= 3.402823466e+38f);
+    const float ms = __fmaf_rn(ss, inv_h, eps);
+    float r = __frsqrt_rn(ms);
+    const bool big = !(ms <= 3.402823466e+38f);
     if (L ? __any_sync(0xffffffffu, big) : big) {
       float s2 = 0.f;
 #pragma unroll
@@ -99,7 +100,7 @@ struct RowGroup {
           s2 = __fmaf_rn(v, v, s2);
         }
       s2 = sum(s2);
-      if (big) r = __frsqrt_rn(s2 * inv_h) * 0x1p-80f;
+      if (big) r = __frsqrt_rn(__fmaf_rn(s2, inv_h, eps * 0x1p-80f * 0x1p-80f)) * 0x1p-80f;
     }
     return r;
   }
