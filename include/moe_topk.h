@@ -548,8 +548,8 @@ int moe_adapter_linear_bwd(const void* dy, long long lddy, const void* x, long l
  * The residual stream (x, dres, dx, residual, out, dout) is bf16 (fp32 = 0) or
  * fp32 (fp32 = 1); what enters and leaves the block (y, dy, z, dz, next_y) is
  * bf16.  gain fp32 [H], NULL: ones.  fp32 arithmetic, each output rounded once.
- * H a multiple of 8, at most 8192; eps > 0.  A row whose squares leave fp32's
- * range is summed again on a smaller scale.  Row strides ld* in elements,
+ * H a multiple of 8, at most 8192; eps > 0.  A row whose squares, with eps,
+ * come near the ends of fp32's range is summed again on another scale.  Row strides ld* in elements,
  * multiples of 8 (of 4 for fp32 rows), at least H; without one, rows are
  * contiguous.
  *

@@ -78,7 +78,9 @@ struct RowGroup {
   // 1/sqrt(mean + eps) of the squares of a row's values, at(i, j) for element j of this
   // lane's i-th vector (0 where it has none).  Where mean + eps, or the squares' sum, leaves
   // fp32's range they are formed again of values times 2^-80 (8192 of the largest, 2^48 each,
-  // add up to 2^109) and eps times 2^-160.  An infinity gives 0, a NaN NaN.
+  // add up to 2^109) and eps times 2^-160; below 2^-90, where squares of eps's size lose
+  // digits, of values times 2^64 (at most 2^51 each then) and eps times 2^128.  An infinity
+  // gives 0, a NaN NaN.
   template <int NV, class At>
   __device__ __forceinline__ float rstd(float inv_h, float eps, At&& at) {
     float ss = 0.f;
@@ -89,18 +91,19 @@ struct RowGroup {
     ss = sum(ss);
     const float ms = __fmaf_rn(ss, inv_h, eps);
     float r = __frsqrt_rn(ms);
-    const bool big = !(ms <= 3.402823466e+38f);
-    if (L ? __any_sync(0xffffffffu, big) : big) {
+    const bool again = !(ms <= 3.402823466e+38f && ms >= 0x1p-90f);
+    if (L ? __any_sync(0xffffffffu, again) : again) {
+      const float scale = ms < 0x1p-90f ? 0x1p64f : 0x1p-80f;
       float s2 = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float v = at(i, j) * 0x1p-80f;
+          const float v = at(i, j) * scale;
           s2 = __fmaf_rn(v, v, s2);
         }
       s2 = sum(s2);
-      if (big) r = __frsqrt_rn(__fmaf_rn(s2, inv_h, eps * 0x1p-80f * 0x1p-80f)) * 0x1p-80f;
+      if (again) r = __frsqrt_rn(__fmaf_rn(s2, inv_h, eps * scale * scale)) * scale;
     }
     return r;
   }

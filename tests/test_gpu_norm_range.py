@@ -71,6 +71,20 @@ def test_eps_beside_squares_beyond_the_range(H, dt):
 
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("H", WIDTHS)
+def test_squares_below_the_range(H, dt):
+    """Rows whose squares are below fp32's normal numbers, beside an eps that is no larger; the other rows of a
+    warp keep theirs."""
+    for eps in (1e-45, 1e-42, 1e-38, 1e-30):
+        x = rand(H + 3, 37, H)
+        for t, size in ((1, 1e-22), (3, 1e-20), (4, 1e-19), (6, 1e-15), (7, 1e-13), (9, 1e-30), (10, 3e-23)):
+            x[t] *= size
+        x[12] = 0
+        x[20:] *= 1e-21
+        check(x, eps, dt)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("H", WIDTHS)
 def test_backward_of_rows_beyond_the_range(H, dt):
     """With the rstd that the forward leaves for rows whose squares overflow; the gain's gradient takes those rows too."""
     T, eps = 24, 1e-5
