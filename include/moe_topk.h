@@ -549,16 +549,17 @@ int moe_adapter_linear_bwd(const void* dy, long long lddy, const void* x, long l
  * fp32 (fp32 = 1); what enters and leaves the block (y, dy, z, dz, next_y) is
  * bf16.  gain fp32 [H], NULL: ones.  fp32 arithmetic, each output rounded once.
  * H a multiple of 8, at most 8192; eps > 0.  A row whose squares, with eps,
- * come near the ends of fp32's range is summed again on another scale.  Row strides ld* in elements,
- * multiples of 8 (of 4 for fp32 rows), at least H; without one, rows are
- * contiguous.
+ * come near the ends of fp32's range is summed again on another scale.  Row
+ * strides ld* in elements, multiples of 8 (of 4 for fp32 rows), at least H;
+ * without one, rows are contiguous.
  *
  * moe_pre_norm:     rstd[t] = 1 / sqrt(mean_h x[t,h]^2 + eps)   (rstd fp32 [T], may be NULL)
  *                   y[t,h]  = x[t,h] rstd[t] gain[h]
  * moe_pre_norm_bwd: with n = x rstd and dn = dy gain,
  *                   dx[t,h]  = res_scale dres[t,h] + rstd[t] (dn[t,h] - n[t,h] mean_j dn[t,j] n[t,j])
  *                   dgain[h] = sum_t dy[t,h] n[t,h]             (fp32 [H], NULL: not computed)
- *                   dres: gradient of the residual path, or NULL (0); dx may be dres.
+ *                   dres: gradient of the residual path, or NULL (0); dx may be dres, with
+ *                   the same row stride.
  *                   y may not overlap x, nor dx overlap x or dy.
  *
  * moe_post_norm: with n = z rstd (norm = 1, rstd as above, of z) or n = z (norm = 0),

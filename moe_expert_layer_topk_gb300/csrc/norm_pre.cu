@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(256, NV == 1 ? 8 : 4) pre_norm_kernel(const S*
   }
 }
 
-// dx may be dres: each vector is read before it is written, by the same thread.
+// dx may be dres, with its row stride: each vector is read before it is written, by the same thread.
 template <typename S, int NV>
 struct PreBwd {
   static constexpr int SU = sizeof(Vec8<S>) / 16;         // units of a stream vector
@@ -307,6 +307,7 @@ int moe_pre_norm_bwd(const void* dy, long long lddy, const void* x, long long ld
   };
   if (!(fp32 ? strides(float()) : strides(__nv_bfloat16())) || !row_strides_ok(static_cast<const __nv_bfloat16*>(dy), lddy, H))
     return fail(MOE_ERR_INVALID_ARG, "%s: row strides must be at least H and whole 16-byte vectors", fn);
+  if (dx == dres && lddx != lddres && T > 1) return fail(MOE_ERR_INVALID_ARG, "%s: dx over dres needs dres's row stride", fn);
   if (!aligned16(dy) || !aligned16(x) || !aligned16(dx) || (dres && !aligned16(dres)) || (gain && !aligned16(gain)))
     return fail(MOE_ERR_ALIGNMENT, "%s: dy, x, gain, dres and dx must be 16-byte aligned", fn);
   if (int rc = check_gain_grad(fn, T, H, dgain, ws, ws_bytes)) return rc;
