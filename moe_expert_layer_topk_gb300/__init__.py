@@ -420,8 +420,10 @@ def moe_combine_dropout_bwd(dy, y_perm, topk_w, row_of_slot, T, H, k, p, rng, dy
           _ptr(rng), _ptr(dy_perm), _ptr(d_w), _stream(stream))
 
 
-def _rows(t):
-    """Pointer and row stride of a 2-D tensor whose rows may lie apart."""
+def _rows(t, dtype=None):
+    """Pointer and row stride of a 2-D tensor (of that type) whose rows may lie apart."""
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"a tensor of {t.dtype} where {dtype} is read or written")
     st = t.stride()
     if len(st) != 2 or st[1] != 1:
         raise ValueError("row tensors must be 2-D with contiguous rows")
@@ -482,11 +484,25 @@ def _gate_kind(gate, T, H) -> int:
     raise ValueError("gate must be fp32 logits of the tokens or bf16 logits of their elements")
 
 
-def _fp32(t):
-    """Pointer of an fp32 tensor (a gain, or its gradient), which a bf16 parameter is not."""
-    if t is not None and t.dtype is not torch.float32:
-        raise ValueError("gains and their gradients are fp32")
-    return _ptr(t)
+def _pointer_of(dtype, what):
+    """_ptr for tensors that are read or written as dtype."""
+    def pointer(t):
+        if t is None:
+            return None
+        try:
+            if t.dtype is dtype and t.is_cuda and t.is_contiguous():
+                return t.data_ptr()
+        except AttributeError:  # an address
+            return _ptr(t)
+        if t.dtype is not dtype:
+            raise ValueError(f"{what}, not {t.dtype}")
+        return _ptr(t)
+    return pointer
+
+
+_bf16 = _pointer_of(torch.bfloat16, "what enters and leaves a block or an expert is bf16")
+_f32 = _pointer_of(torch.float32, "rows' statistics, weights and their gradients are fp32")
+_fp32 = _pointer_of(torch.float32, "gains and their gradients are fp32")
 
 
 def _codes(q, scale):
@@ -499,8 +515,8 @@ def _codes(q, scale):
 def moe_pre_norm(x, gain, eps, T, H, y, rstd=None, stream=None):
     """y = x / rms(x) * gain; x bf16 or fp32, x and y may be row slices of wider tensors."""
     px, ldx = _rows(x)
-    py, ldy = _rows(y)
-    _call("moe_pre_norm", px, ldx, _stream_type(x), _fp32(gain), eps, T, H, py, ldy, _ptr(rstd), _stream(stream))
+    py, ldy = _rows(y, torch.bfloat16)
+    _call("moe_pre_norm", px, ldx, _stream_type(x), _fp32(gain), eps, T, H, py, ldy, _f32(rstd), _stream(stream))
 
 
 def moe_pre_norm_bwd_workspace_size(T, H) -> int:
@@ -508,11 +524,11 @@ def moe_pre_norm_bwd_workspace_size(T, H) -> int:
 
 
 def moe_pre_norm_bwd(dy, x, gain, rstd, dres, res_scale, T, H, dx, dgain=None, accumulate=0, ws=None, stream=None):
-    pd, lddy = _rows(dy)
+    pd, lddy = _rows(dy, torch.bfloat16)
     px, ldx = _rows(x)
     pr, lddres = (None, H) if dres is None else _rows(dres)
     po, lddx = _rows(dx)
-    _call("moe_pre_norm_bwd", pd, lddy, px, ldx, _stream_type(x, dres, dx), _fp32(gain), _ptr(rstd), pr, lddres, res_scale,
+    _call("moe_pre_norm_bwd", pd, lddy, px, ldx, _stream_type(x, dres, dx), _fp32(gain), _f32(rstd), pr, lddres, res_scale,
           T, H, po, lddx, _fp32(dgain), int(accumulate), _ptr(ws), _nbytes(ws), _stream(stream))
 
 
@@ -520,16 +536,16 @@ def moe_post_norm(z, residual, gain, norm, eps, gate, res_scale, out_scale, T, H
                   next_y=None, next_rstd=None, stream=None):
     """out = res_scale residual + out_scale sigmoid(gate) norm(z) gain, and the next norm of out where next_y is given;
     the stream's type is out's, the gate's kind its own (fp32 [T] or bf16 [T,H])."""
-    _call("moe_post_norm", _ptr(z), _ptr(residual), _stream_type(out, residual), _fp32(gain), int(norm), eps,
-          _gate_kind(gate, T, H), _ptr(gate), res_scale, out_scale, T, H, _ptr(out), _ptr(rstd), _fp32(next_gain),
-          _ptr(next_y), _ptr(next_rstd), _stream(stream))
+    _call("moe_post_norm", _bf16(z), _ptr(residual), _stream_type(out, residual), _fp32(gain), int(norm), eps,
+          _gate_kind(gate, T, H), _ptr(gate), res_scale, out_scale, T, H, _ptr(out), _f32(rstd), _fp32(next_gain),
+          _bf16(next_y), _f32(next_rstd), _stream(stream))
 
 
 def moe_combine_post_norm(y_perm, topk_w, row_of_slot, residual, gain, norm, eps, gate, res_scale, out_scale, T, H, k, z,
                           out, rstd=None, next_gain=None, next_y=None, next_rstd=None, stream=None):
-    _call("moe_combine_post_norm", _ptr(y_perm), _ptr(topk_w), _ptr(row_of_slot), _ptr(residual),
+    _call("moe_combine_post_norm", _bf16(y_perm), _f32(topk_w), _ptr(row_of_slot), _ptr(residual),
           _stream_type(out, residual), _fp32(gain), int(norm), eps, _gate_kind(gate, T, H), _ptr(gate), res_scale, out_scale,
-          T, H, k, _ptr(z), _ptr(out), _ptr(rstd), _fp32(next_gain), _ptr(next_y), _ptr(next_rstd), _stream(stream))
+          T, H, k, _bf16(z), _ptr(out), _f32(rstd), _fp32(next_gain), _bf16(next_y), _f32(next_rstd), _stream(stream))
 
 
 def moe_post_norm_bwd_workspace_size(T, H) -> int:
@@ -540,31 +556,31 @@ def moe_post_norm_bwd(dout, z, gain, norm, rstd, gate, out_scale, T, H, dz, dgai
                       stream=None):
     if dgate is not None and (gate is None or dgate.dtype != gate.dtype):
         raise ValueError("dgate must have the gate's type")
-    _call("moe_post_norm_bwd", _ptr(dout), _stream_type(dout), _ptr(z), _fp32(gain), int(norm), _ptr(rstd),
-          _gate_kind(gate, T, H), _ptr(gate), out_scale, T, H, _ptr(dz), _fp32(dgain), _ptr(dgate), int(accumulate), _ptr(ws),
+    _call("moe_post_norm_bwd", _ptr(dout), _stream_type(dout), _bf16(z), _fp32(gain), int(norm), _f32(rstd),
+          _gate_kind(gate, T, H), _ptr(gate), out_scale, T, H, _bf16(dz), _fp32(dgain), _ptr(dgate), int(accumulate), _ptr(ws),
           _nbytes(ws), _stream(stream))
 
 
 def moe_ckpt_pack(a, rows, cols, q, scale, stream=None):
-    _call("moe_ckpt_pack", _ptr(a), rows, cols, *_codes(q, scale), _stream(stream))
+    _call("moe_ckpt_pack", _bf16(a), rows, cols, *_codes(q, scale), _stream(stream))
 
 
 def moe_ckpt_unpack(q, scale, rows, cols, a, stream=None):
-    _call("moe_ckpt_unpack", *_codes(q, scale), rows, cols, _ptr(a), _stream(stream))
+    _call("moe_ckpt_unpack", *_codes(q, scale), rows, cols, _bf16(a), _stream(stream))
 
 
 def moe_dispatch_rows(x, scale, row_of_slot, topk_w, T, H, k, x_perm, row_w=None, stream=None):
     """x: bf16 tokens (scale None), or int8 codes with their scales."""
-    if x.element_size() != (2 if scale is None else 1):
+    if x.dtype is not torch.bfloat16 if scale is None else x.element_size() != 1:
         raise ValueError("x must be bf16 tokens, or 8-bit codes with their scales")
-    _call("moe_dispatch_rows", _ptr(x), _ptr(scale), _ptr(row_of_slot), _ptr(topk_w), T, H, k, _ptr(x_perm), _ptr(row_w),
+    _call("moe_dispatch_rows", _ptr(x), _bf16(scale), _ptr(row_of_slot), _f32(topk_w), T, H, k, _bf16(x_perm), _f32(row_w),
           _stream(stream))
 
 
 def moe_grouped_gemm_swiglu_ckpt(x_perm, Wg, Wu, num_seg, seg_offsets, seg_expert, R, H, I, E, h, gu_q, gu_scale,
                                  stream=None):
-    _call("moe_grouped_gemm_swiglu_ckpt", _ptr(x_perm), _ptr(Wg), _ptr(Wu), num_seg, _ptr(seg_offsets), _ptr(seg_expert),
-          R, H, I, E, _ptr(h), *_codes(gu_q, gu_scale), _stream(stream))
+    _call("moe_grouped_gemm_swiglu_ckpt", _bf16(x_perm), _bf16(Wg), _bf16(Wu), num_seg, _ptr(seg_offsets), _ptr(seg_expert),
+          R, H, I, E, _bf16(h), *_codes(gu_q, gu_scale), _stream(stream))
 
 
 def moe_grouped_gemm_down_bwd_ckpt_workspace_size(R, I) -> int:
@@ -573,8 +589,8 @@ def moe_grouped_gemm_down_bwd_ckpt_workspace_size(R, I) -> int:
 
 def moe_grouped_gemm_down_bwd_ckpt(dy_perm, row_w, gu_q, gu_scale, Wd, num_seg, seg_offsets, seg_expert, R, H, I, E, dgu,
                                    h_w, d_w, row_of_slot=None, T=0, k=0, ws=None, stream=None):
-    _call("moe_grouped_gemm_down_bwd_ckpt", _ptr(dy_perm), _ptr(row_w), *_codes(gu_q, gu_scale), _ptr(Wd), num_seg,
-          _ptr(seg_offsets), _ptr(seg_expert), R, H, I, E, _ptr(dgu), _ptr(h_w), _ptr(row_of_slot), T, k, _ptr(d_w), _ptr(ws),
+    _call("moe_grouped_gemm_down_bwd_ckpt", _bf16(dy_perm), _f32(row_w), *_codes(gu_q, gu_scale), _bf16(Wd), num_seg,
+          _ptr(seg_offsets), _ptr(seg_expert), R, H, I, E, _bf16(dgu), _bf16(h_w), _ptr(row_of_slot), T, k, _f32(d_w), _ptr(ws),
           _nbytes(ws), _stream(stream))
 
 
