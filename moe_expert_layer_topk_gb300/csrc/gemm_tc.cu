@@ -41,9 +41,9 @@
 // row (64 bf16 or 128 e4m3 elements), 4-stage shared-memory ring (3 for the
 // router dX kind, whose epilogue stages its addend), two 256-column
 // accumulators in TMEM so the epilogue of tile i overlaps the MMAs of tile
-// i+1.  GATE_UP_BWD_DX, and GATE_UP_FWD and DOWN_FWD in the dispatch layout
-// (one segment per expert), run as cluster pairs (tcgen05 cta_group::2,
-// 256-row tiles).  The weight-gradient kind's TMA stores carry an
+// i+1.  GATE_UP_BWD_DX, and in the dispatch layout (one segment per expert)
+// GATE_UP_FWD, GATE_UP_CKPT, DOWN_FWD, DOWN_COMBINE and DOWN_BWD_CKPT, run as
+// cluster pairs (tcgen05 cta_group::2, 256-row tiles).  The weight-gradient kind's TMA stores carry an
 // evict-last L2 policy.
 //
 // Every wait on an mbarrier is bounded (globaltimer): on timeout the CTA
@@ -60,7 +60,7 @@ namespace tc {
 
 constexpr int A_BYTES = BM * BK * 2;          // 16 KiB
 constexpr int B_BYTES_MAX = 256 * BK * 2;     // 32 KiB
-// DOWN_BWD_DX also loads the saved g, u boxes by TMA: 4 sets of (g, u) slots.
+// DENSE_ADD also loads its addend's boxes by TMA: 4 sets of two slots.
 constexpr int EP_GU_SETS = 4;
 
 enum Kind : int {
@@ -169,7 +169,8 @@ __host__ __device__ constexpr size_t seg_table_bytes(int num_seg, int num_groups
   return ((size_t)(3 * num_seg + 2 + (dw ? num_groups : 0) + (pieces ? num_seg : 0)) * 4 + 15) / 16 * 16;
 }
 // the kinds whose tiles may be made of pieces, and segments up to which they are (the order
-// by expert costs each CTA num_seg^2 / 320 comparisons)
+// by expert costs each thread of a CTA num_seg comparisons for every segment that it places:
+// num_seg^2 / 320 of them backward, num_seg^2 / 192 forward)
 __host__ __device__ constexpr bool has_pieces(int kind, int ctas) {
   return (kind == DOWN_BWD_CKPT || kind == GATE_UP_CKPT) && ctas == 1;
 }
@@ -208,7 +209,7 @@ struct Cfg {
   // SwiGLU-backward kind (heavy epilogue) and the down projections (256
   // output columns per tile from a short reduction, K = I) run eight
   // epilogue warps, two per TMEM lane quadrant sharing the columns (a
-  // one-box store ring each).
+  // one-box store ring each; the 8-bit SwiGLU backward's pairs two boxes).
   static constexpr bool EP8 = KIND == DW || is_down_bwd(KIND) || is_down_fwd(KIND);
   static constexpr int EPW = EP8 ? 8 : 4;
   // row-gathering kinds: four more warps share the row gather
@@ -220,7 +221,8 @@ struct Cfg {
   // without the segment tables
   static constexpr size_t SMEM_FIXED = 1024 + (size_t)STAGES * STAGE_BYTES + EP_TOTAL + sizeof(Ctl);
 };
-// the configurations launched (cluster pairs for GATE_UP_FWD, GATE_UP_BWD_DX, DOWN_FWD and DOWN_COMBINE)
+// the configurations launched (cluster pairs for GATE_UP_FWD, GATE_UP_CKPT, GATE_UP_BWD_DX, DOWN_FWD, DOWN_COMBINE and
+// DOWN_BWD_CKPT)
 static_assert(Cfg<GATE_UP_FWD, 1>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
                   Cfg<GATE_UP_GATHER, 1>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
                   Cfg<GATE_UP_FP8, 1>::SMEM_FIXED + kMaxTableBytes <= kSmemMax &&
@@ -1299,12 +1301,6 @@ __global__ void __launch_bounds__(Cfg<KIND, CTAS>::NTHREADS, 1)
   }
 }
 
-// Per-segment operand maps of the weight-gradient GEMM.  Thread i writes
-// map i = 2s (A) or 2s+1 (B): a copy of the MN-major template whose base
-// address is moved to segment s's first row and whose row extent is the
-// segment's length (rows clamped to [0, rows) like the kernel's own table).
-// An empty segment keeps the template unchanged; no k-block ever reads it.
-
 // d_w of the 8-bit SwiGLU backward: a row's parts added in their order, for each slot
 // (row_of_slot) or each row; 0 where no segment of an expert holds the row.
 __global__ void __launch_bounds__(256) ckpt_dw_kernel(const float* __restrict__ part, int parts, int R,
@@ -1348,6 +1344,11 @@ __global__ void __launch_bounds__(256) f32_to_bf16_kernel(const float* __restric
   }
 }
 
+// Per-segment operand maps of the weight-gradient GEMM.  Thread i writes
+// map i = 2s (A) or 2s+1 (B): a copy of the MN-major template whose base
+// address is moved to segment s's first row and whose row extent is the
+// segment's length (rows clamped to [0, rows) like the kernel's own table).
+// An empty segment keeps the template unchanged; no k-block ever reads it.
 __global__ void dw_segment_maps_kernel(const __grid_constant__ CUtensorMap tplA,
                                        const __grid_constant__ CUtensorMap tplB,
                                        const int32_t* seg_offsets, int num_seg, int rows,
@@ -1389,12 +1390,12 @@ int pick_bn(int n) { return n % 256 == 0 ? 256 : (n % 128 == 0 ? 128 : 64); }
 
 // Cluster pairs (256-row tiles) need at least 128 output columns per tile
 // (64 per CTA).  They are used where they measured faster: the gate/up
-// backward dX GEMM, and the bf16 down projection and gate/up forward GEMM
-// on permuted rows in the dispatch layout with enough rows per expert
-// (pair_for_rows).  Every other kind runs one CTA per 128-row tile.
+// backward dX GEMM, and the bf16 down projection, the gate/up forward GEMM
+// and the 8-bit SwiGLU backward on permuted rows in the dispatch layout with
+// enough rows per expert (pair_for_rows).  Every other kind runs one CTA per 128-row tile.
 bool use_pair(int bn) { return bn >= 128; }
 
-// The forward row kinds take pairs only in the dispatch layout (one segment
+// Those row kinds take pairs only in the dispatch layout (one segment
 // per expert) and with at least 384 rows per segment on average: a pair
 // tile wastes up to 255 rows of a segment's last tile, a single CTA's up to
 // 127.  Measured at T=8192 (512 rows per expert): down 187 -> 181 us as

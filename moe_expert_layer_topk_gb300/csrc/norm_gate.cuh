@@ -9,8 +9,9 @@ namespace moe {
 struct Gate {
   float g, d;
 };
-// (The approximate instructions themselves: each is off by 2^-22 or so, and what is below
-// 2^-126 is 0.)
+// e^-|x| = 2^(-|x| log2 e) by the approximate instructions: each is off by 2^-22 or so, what is
+// below 2^-126 is 0, and the rounding of the exponent adds |x| 2^-24 (1e-6 at a logit of -20;
+// at +20 it is lost beside 1).
 __device__ __forceinline__ Gate sigmoid(float x) {
   float e, t;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fabsf(x) * -1.44269504f));

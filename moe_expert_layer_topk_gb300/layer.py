@@ -81,7 +81,9 @@ class MoELayer:
     (the layers of a model run one after another on one stream), so that
     only the kept tensors, the outputs and the gradients are a layer's own.
     checkpoint_input: x is kept in 8 bits too, and the backward's x may be
-    None.  Gradients are those of the kept values: about 1% off."""
+    None.  Gradients are those of the kept values: about 1% off.  With
+    dropout, dy under the mask times 1/(1-p) is rounded to bf16 before it is
+    permuted (the plain layer rounds the permuted rows, weighted, instead)."""
 
     def __init__(self, T: int, H: int, I: int, E: int, k: int, ep_size: int = 1, *,
                  training: bool = True, fused_dispatch: bool = False, fp8: bool = False,
@@ -372,12 +374,11 @@ class MoELayer:
             main.wait_event(self._ev_join)
         return dx
 
-
     def _experts_bwd_checkpointed(self, dy, x, Wd, accumulate, stream):
         """The backward of combine and down projection from the kept codes (fills d_w, dgu and
         dWd), and the experts' rows of x made again; returns the x that the router's backward uses."""
         T, H, I, E, k, R = self.T, self.H, self.I, self.E, self.k, self.R
-        if self.dropout:
+        if self.dropout:  # rounded to bf16 here, as moe_combine_dropout_bwd rounds its rows: the products take bf16
             moe_dropout(dy, None, T * H, self.dropout, self.rng, self.tokens, stream)
             dy = self.tokens
         moe_dispatch_rows(dy, None, self.row_of_slot, self.topk_w, T, H, k, self.dy_perm, self.row_w, stream)
