@@ -518,7 +518,8 @@ class MoEBlock:
     def backward(self, dout, x, pre_gain, post_gain, Wr, Wg, Wu, Wd, gate=None, accumulate: bool = False, stream=None, dx=None,
                  overlap: bool = True, dloss=None):
         """After the forward of the same x: the gradients of the parameters and of the gate, and dx
-        (default: the block's own), which may be dout."""
+        (default: the block's own), which may be dout.  accumulate adds to the parameters' gradients;
+        d_gate, of this batch's tokens, is overwritten."""
         assert self.training, "block was built without backward buffers"
         self._check_gate(gate)
         T, H, L = self.T, self.H, self.layer
